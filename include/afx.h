@@ -71,6 +71,10 @@ typedef enum afx_status {
 #define AFX_DEV_TIMEOUT 0x10  /* a staging copy did not arrive within the kernel's wait limit; work skipped */
 #define AFX_DEV_UNDRAINED 0x20 /* with AFX_DEV_TIMEOUT: a copy into shared memory had not arrived when the
                                   warp gave up on it, and may land after the kernel's work on it ended */
+#define AFX_DEV_NO_PAGES 0x40   /* the free pages do not cover what the new lengths need; nothing was moved */
+#define AFX_DEV_BAD_LENGTH 0x80 /* a length, start or count is out of range; nothing was done */
+#define AFX_DEV_BAD_PAGE 0x100  /* a page or slot lies outside the pool; its keys and values were left out */
+#define AFX_DEV_BAD_PLAN 0x200  /* the attention workspace holds no plan for this description; nothing was done */
 
 /* Element formats a container can hold (header field at byte 108; the hi
  * section's offset is the u64 at byte 112, 0 unless FP16).  The
@@ -512,6 +516,171 @@ afx_status afx_prefill_fused_batch(const afx_desc* descs, const void* const* con
                                    const uint32_t* cols, const uint16_t* const* xs_dev, uint32_t n_tokens,
                                    float* const* ys_dev, uint32_t count, void* workspace_dev, uint64_t workspace_bytes,
                                    afx_stream_t stream, int32_t* status_dev);
+
+/* ---- serving: cache, attention, sampling ----------------------------------
+ *
+ * What a decode step does between its weight products: the pages of the
+ * key/value cache and the slots of its new tokens (afx_kv_tables), their
+ * keys and values written there (afx_kv_write), the attention over the
+ * cache of a batch whose requests share a long prefix, such as one system
+ * prompt or one document (afx_attention), and after the head the next
+ * token (afx_sample).  Lengths, tables and random numbers are read on the
+ * GPU: a step needs no host round trip between its calls and can be
+ * captured in a CUDA graph.  "Memory requirements of language model
+ * inference on a consumer GPU", section "Loading one part of the model at a
+ * time", names these steps of a request; the pages give no design for
+ * them, and the layouts here are the library's own.  Inference only: no
+ * gradients.
+ *
+ * All arrays are device memory owned by the caller.  status_dev as for the
+ * restores (nullable; AFX_DEV_* bits are OR-ed in). */
+
+#define AFX_KV_MAX_REQUESTS 16384
+
+/* The cache of one layer: two pools (keys, values) of n_pages pages of
+ * page_tokens tokens of kv_heads heads of head_dim elements.  Element
+ * (page, token, head, i) of a pool lies at page * page_stride + token *
+ * token_stride + head * head_stride + i (elements), the same for both
+ * pools; any order of the three works, strides a multiple of 8 and pools
+ * 16-byte aligned.  A slot is page * page_tokens + token. */
+typedef struct afx_kv_cache {
+    void* k_dev;
+    void* v_dev;
+    uint64_t page_stride, token_stride, head_stride;
+    uint32_t format;      /* AFX_FMT_BF16 or AFX_FMT_FP16 */
+    uint32_t n_pages;     /* n_pages * page_tokens < 2^31 */
+    uint32_t page_tokens; /* 16, 32, 64, 128 or 256 */
+    uint32_t kv_heads;
+    uint32_t head_dim;    /* 64 or 128 */
+    uint32_t reserved;
+} afx_kv_cache;
+
+/* Block tables and slots from request lengths.  Request r has
+ * old_len_dev[r] cached tokens and is to have new_len_dev[r]: more (new
+ * tokens come), fewer (draft tokens are taken back; 0: the request has
+ * ended) or as many.  table_dev [n_requests][table_cols]: the pages of each
+ * request's tokens, in order; the first ceil(old_len / page_tokens) entries
+ * of a row are in use.  Pages that shrinking requests no longer need go
+ * back first, in request order, and then growing requests take theirs, in
+ * request order: the page given back last is taken first, and the free
+ * stack (free_pages_dev[0 .. *free_count_dev), room for n_pages entries) is
+ * taken from its end.  Written: the rows' new entries (entries past a
+ * request's pages are left as they are), the stack above its old count,
+ * *free_count_out_dev (another place than free_count_dev: the old count
+ * stays, so a step can be run again), starts_dev [n_requests + 1] (the
+ * first new token of each request, then their number), and for t <
+ * max_tokens, the room the caller has for new tokens, slots_dev[t] and
+ * positions_dev[t] (slot and position in its request of new token t; -1
+ * past the last one).
+ * All or nothing: where the pages do not suffice (AFX_DEV_NO_PAGES), or a
+ * length is negative or past a table row, or the new tokens are more than
+ * max_tokens, or the count is not one of this pool (AFX_DEV_BAD_LENGTH),
+ * no page moves, starts are 0, slots and positions -1 and the count out is
+ * the count in.  A page id outside 0 .. n_pages - 1 met on the way sets
+ * AFX_DEV_BAD_PAGE and its tokens' slots to -1.
+ * One launch, asynchronous on stream.  Errors: AFX_E_ARG, AFX_E_CUDA. */
+afx_status afx_kv_tables(uint32_t page_tokens, uint32_t n_pages, const int32_t* old_len_dev,
+                         const int32_t* new_len_dev, uint32_t n_requests, int32_t* table_dev, uint32_t table_cols,
+                         int32_t* free_pages_dev, const int32_t* free_count_dev, int32_t* free_count_out_dev,
+                         int32_t* starts_dev, int32_t* slots_dev, int32_t* positions_dev, uint32_t max_tokens,
+                         afx_stream_t stream, int32_t* status_dev);
+
+/* Writes the keys and values of n_tokens new tokens into the cache: token
+ * t's head h, k_dev[t * token_stride + h * head_stride + i] (elements of
+ * the cache's format; v_dev alike, same strides), goes to slot slots_dev[t].
+ * A negative slot is skipped; one past the pool sets AFX_DEV_BAD_PAGE and
+ * is skipped.  Two tokens must not have the same slot.  Any alignment and
+ * strides (16-byte aligned rows are fastest); the sources must not overlap the
+ * cache.  One launch, asynchronous on stream.  Errors: AFX_E_ARG,
+ * AFX_E_CUDA. */
+afx_status afx_kv_write(const afx_kv_cache* cache, const void* k_dev, const void* v_dev, uint64_t token_stride,
+                        uint64_t head_stride, const int32_t* slots_dev, uint32_t n_tokens, afx_stream_t stream,
+                        int32_t* status_dev);
+
+/* Attention of a batch's new tokens over a prefix that all its requests
+ * share and each request's own cached tokens.  The new tokens of request r
+ * are the rows starts_dev[r] .. starts_dev[r + 1] - 1 of the queries (the
+ * starts of afx_kv_tables); they are the last of its lens_dev[r] own cached
+ * tokens, in order, and each sees the whole prefix and its request's tokens
+ * up to itself: row i of n sees own tokens 0 .. lens_dev[r] - n + i.
+ * Prefix token j is token j % page_tokens of page prefix_table_dev[j /
+ * page_tokens]; own token j the same through row r of table_dev. */
+typedef struct afx_attention_args {
+    afx_kv_cache cache;
+    uint32_t q_heads;     /* a multiple of cache.kv_heads; head h reads key/value head h / (q_heads / kv_heads) */
+    uint32_t n_requests;  /* 1 .. AFX_KV_MAX_REQUESTS */
+    uint32_t n_tokens;    /* rows of the queries; starts_dev[n_requests] may be lower: the rest is left alone */
+    uint32_t table_cols;
+    uint32_t prefix_len;  /* tokens of the shared prefix; 0: none */
+    float scale;          /* scores are scale * q.k, usually 1 / sqrt(head_dim) */
+    const int32_t* prefix_table_dev; /* ceil(prefix_len / page_tokens) pages */
+    const int32_t* table_dev;        /* [n_requests][table_cols] */
+    const int32_t* starts_dev;       /* [n_requests + 1] */
+    const int32_t* lens_dev;         /* [n_requests] */
+} afx_attention_args;
+
+/* Bytes of device workspace the two calls below need for this description. */
+afx_status afx_attention_workspace(const afx_attention_args* args, uint64_t* bytes);
+
+/* Lists the step's work in the workspace from the lengths on the GPU.  One
+ * call a step: every layer's afx_attention with the same starts, lens,
+ * tables' shapes and prefix length uses it (the pools and the tables'
+ * contents may differ).  Lengths that make no sense (starts that fall or pass
+ * n_tokens, lens outside a table row) set AFX_DEV_BAD_LENGTH and leave a
+ * plan without work.  workspace_dev: 256-byte aligned, of at least
+ * afx_attention_workspace bytes, contents ignored.  One launch,
+ * asynchronous on stream.  Errors: AFX_E_ARG, AFX_E_NOSPACE, AFX_E_CUDA. */
+afx_status afx_attention_plan(const afx_attention_args* args, void* workspace_dev, uint64_t workspace_bytes,
+                              afx_stream_t stream, int32_t* status_dev);
+
+/* out[t][h] = sum over the visible j of softmax_j(scale * q[t][h].k_j) v_j,
+ * and, where lse_dev is not NULL, lse_dev[t * q_heads + h] = log sum_j
+ * exp(scale * q.k_j).  q_dev and out_dev hold elements of the cache's format
+ * at t * token stride + h * head stride (out's rows must not overlap).  A row that
+ * sees nothing gets zeros and minus infinity.  Scores, maxima, sums and
+ * outputs are held in float32; the softmax weights are rounded to the
+ * cache's format for their product with the values, and the output once at
+ * the end.  Cache contents past a request's length (or the prefix's) are
+ * never used, whatever they hold; the values of tokens that a row of the
+ * same request does see must be finite for the rows that do not see them
+ * yet.  A page outside the pool sets AFX_DEV_BAD_PAGE, a workspace without
+ * this description's plan AFX_DEV_BAD_PLAN.  Pieces are joined in a fixed
+ * order: the same call gives the same bits.  Calls that overlap on the GPU
+ * need their own workspaces.  Asynchronous on stream.  Errors: AFX_E_ARG,
+ * AFX_E_NOSPACE, AFX_E_CUDA. */
+afx_status afx_attention(const afx_attention_args* args, const void* q_dev, uint64_t q_token_stride,
+                         uint64_t q_head_stride, void* out_dev, uint64_t out_token_stride, uint64_t out_head_stride,
+                         float* lse_dev, void* workspace_dev, uint64_t workspace_bytes, afx_stream_t stream,
+                         int32_t* status_dev);
+
+#define AFX_LOGITS_BF16 0u
+#define AFX_LOGITS_FP16 1u
+#define AFX_LOGITS_F32 2u
+#define AFX_SAMPLE_MAX_VOCAB 524288
+
+/* Draws one token from each of rows rows of vocab logits (row r at
+ * logits_dev + r * row_stride elements).  A NaN logit counts as minus
+ * infinity (masked).  With m the row's largest logit, y = (z - m) * (1 / T)
+ * in float32 and weights e^y, tokens ordered by z, descending, equal ones by
+ * index:
+ *   temperature  T; a row whose T is not above 0 gets the first token;
+ *   top_k        keeps the first top_k tokens (<= 0: all);
+ *   top_p        of those, keeps the ones before which less than top_p of
+ *                their weight lies (>= 1: all; the first always stays);
+ *   min_p        of those, keeps weights >= min_p (the first always stays).
+ * The token drawn is the first, by index, at which the running sum of the
+ * kept weights exceeds u_dev[r] times their sum, u in [0, 1).  Weights are
+ * summed as integers of 2^-44, so the result does not depend on any order
+ * of summation.  logprobs_dev (nullable): the logarithm of the drawn token's share of
+ * the kept weights (0 at T = 0).  A row with nothing above minus infinity
+ * gets token -1 and minus infinity.  The four parameter arrays, one value a
+ * row, may each be NULL: T = 1, no top-k, no top-p, no min-p.  vocab at
+ * most AFX_SAMPLE_MAX_VOCAB.  One launch, no workspace, asynchronous on
+ * stream.  Errors: AFX_E_ARG, AFX_E_CUDA. */
+afx_status afx_sample(const void* logits_dev, uint32_t type, uint32_t rows, uint32_t vocab, uint64_t row_stride,
+                      const float* temperature_dev, const int32_t* top_k_dev, const float* top_p_dev,
+                      const float* min_p_dev, const float* u_dev, int32_t* tokens_dev, float* logprobs_dev,
+                      afx_stream_t stream);
 
 /* ---- residency planning ------------------------------------------------
  *

@@ -31,6 +31,7 @@ AFX_OK, AFX_E_ARG, AFX_E_FORMAT, AFX_E_CORRUPT, AFX_E_CUDA, AFX_E_NOSPACE, AFX_E
 AFX_DEV_BAD_BLOCK, AFX_DEV_BAD_CHUNK, AFX_DEV_BAD_CODE, AFX_DEV_BAD_SHAPE = 0x1, 0x2, 0x4, 0x8
 AFX_DEV_TIMEOUT = 0x10
 AFX_DEV_UNDRAINED = 0x20
+AFX_DEV_NO_PAGES, AFX_DEV_BAD_LENGTH, AFX_DEV_BAD_PAGE, AFX_DEV_BAD_PLAN = 0x40, 0x80, 0x100, 0x200
 AFX_MAX_CODE_LEN = 24
 AFX_BLOCK_CAPACITY = 32768
 AFX_HEADER_BYTES = 512
@@ -150,6 +151,37 @@ _lib.afx_prefill_fused_batch.argtypes = [ctypes.POINTER(afx_desc), ctypes.POINTE
                                          ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(ctypes.c_uint32),
                                          ctypes.POINTER(ctypes.c_void_p), _u32, ctypes.POINTER(ctypes.c_void_p), _u32,
                                          _vp, _u64, _vp, _i32p]
+
+
+class afx_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
+        ("page_stride", ctypes.c_uint64), ("token_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64),
+        ("format", ctypes.c_uint32), ("n_pages", ctypes.c_uint32), ("page_tokens", ctypes.c_uint32),
+        ("kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+    ]
+
+
+class afx_attention_args(ctypes.Structure):
+    _fields_ = [
+        ("cache", afx_kv_cache),
+        ("q_heads", ctypes.c_uint32), ("n_requests", ctypes.c_uint32), ("n_tokens", ctypes.c_uint32),
+        ("table_cols", ctypes.c_uint32), ("prefix_len", ctypes.c_uint32), ("scale", ctypes.c_float),
+        ("prefix_table_dev", ctypes.c_void_p), ("table_dev", ctypes.c_void_p), ("starts_dev", ctypes.c_void_p),
+        ("lens_dev", ctypes.c_void_p),
+    ]
+
+
+AFX_KV_MAX_REQUESTS = 16384
+AFX_SAMPLE_MAX_VOCAB = 524288
+AFX_LOGITS_BF16, AFX_LOGITS_FP16, AFX_LOGITS_F32 = 0, 1, 2
+_lib.afx_kv_tables.argtypes = [_u32, _u32, _vp, _vp, _u32, _vp, _u32, _vp, _vp, _vp, _vp, _vp, _vp, _u32, _vp, _i32p]
+_lib.afx_kv_write.argtypes = [ctypes.POINTER(afx_kv_cache), _vp, _vp, _u64, _u64, _vp, _u32, _vp, _i32p]
+_lib.afx_attention_workspace.argtypes = [ctypes.POINTER(afx_attention_args), ctypes.POINTER(ctypes.c_uint64)]
+_lib.afx_attention_plan.argtypes = [ctypes.POINTER(afx_attention_args), _vp, _u64, _vp, _i32p]
+_lib.afx_attention.argtypes = [ctypes.POINTER(afx_attention_args), _vp, _u64, _u64, _vp, _u64, _u64, _vp, _vp, _u64, _vp,
+                               _i32p]
+_lib.afx_sample.argtypes = [_vp, _u32, _u32, _u32, _u64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
 _lib.afx_last_error.argtypes = []
 _lib.afx_last_error.restype = ctypes.c_char_p
 _lib.afx_status_string.argtypes = [ctypes.c_int]
@@ -159,7 +191,8 @@ for _f in (_lib.afx_build_code, _lib.afx_build_code_fmt, _lib.afx_encode_bound, 
            _lib.afx_decode_gemv_static, _lib.afx_stream_run, _lib.afx_test_restore_stalled,
            _lib.afx_plan_residency, _lib.afx_debug_bounds_report, _lib.afx_prefill, _lib.afx_prefill_batch,
            _lib.afx_tile_order, _lib.afx_prefill_fused, _lib.afx_prefill_fused_batch,
-           _lib.afx_prefill_fused_workspace):
+           _lib.afx_prefill_fused_workspace, _lib.afx_kv_tables, _lib.afx_kv_write, _lib.afx_attention_workspace,
+           _lib.afx_attention_plan, _lib.afx_attention, _lib.afx_sample):
     _f.restype = ctypes.c_int
 
 
@@ -496,6 +529,145 @@ def afx_sync(stream=None, timeout_ms: int = 0, status_dev=None) -> tuple[int, in
     if st not in (AFX_OK, AFX_E_CORRUPT, AFX_E_TIMEOUT):
         _check("afx_sync", st)
     return int(st), int(word.value)
+
+
+# ---- serving: cache, attention, sampling -------------------------------------
+
+def _int32_ptr(t, count: int, name: str) -> int:
+    """The address of a contiguous CUDA int32 tensor of at least count values."""
+    if str(t.dtype) != "torch.int32" or t.numel() < count:
+        raise ValueError(f"{name} must be an int32 tensor of at least {count} values")
+    return _dev_ptr(t)
+
+
+def _float_ptr(t, count: int, name: str) -> int:
+    if t is None:
+        return 0
+    if str(t.dtype) != "torch.float32" or t.numel() != count:
+        raise ValueError(f"{name} must be a float32 tensor of {count} values")
+    return _dev_ptr(t)
+
+
+_KV_FORMATS = {"torch.bfloat16": AFX_FMT_BF16, "torch.float16": AFX_FMT_FP16}
+
+
+def kv_cache(k_pool, v_pool) -> afx_kv_cache:
+    """The description of one layer's cache: k_pool and v_pool are CUDA
+    tensors [n_pages][page_tokens][kv_heads][head_dim], bfloat16 or float16,
+    with the same strides (any order of pages, tokens and heads in memory,
+    as a permuted view; the last dimension contiguous).  The description
+    holds their addresses: keep the tensors alive."""
+    if not (k_pool.is_cuda and v_pool.is_cuda):
+        raise ValueError("expected CUDA tensors")
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.stride() != v_pool.stride() or \
+            k_pool.dtype != v_pool.dtype or str(k_pool.dtype) not in _KV_FORMATS:
+        raise ValueError("k_pool and v_pool must be [n_pages][page_tokens][kv_heads][head_dim] tensors of one shape, "
+                         "layout and type (bfloat16 or float16)")
+    pages, page_tokens, heads, dim = k_pool.shape
+    if k_pool.stride(3) != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return afx_kv_cache(k_pool.data_ptr(), v_pool.data_ptr(), *k_pool.stride()[:3], _KV_FORMATS[str(k_pool.dtype)], pages,
+                        page_tokens, heads, dim, 0)
+
+
+def afx_kv_tables(page_tokens: int, old_len, new_len, table, free_pages, free_count, free_count_out, starts, slots,
+                  positions, stream=None, status_dev=None) -> None:
+    """Block tables and slots from request lengths (all CUDA int32 tensors): old_len, new_len [n]; table
+    [n][cols]; free_pages [n_pages]; free_count, free_count_out [1]; starts [n + 1]; slots, positions
+    [max_tokens]."""
+    n = old_len.numel()
+    if table.dim() != 2 or table.shape[0] != n or slots.numel() != positions.numel():
+        raise ValueError("table must be [requests][cols], and slots and positions of one length")
+    _check("afx_kv_tables", _lib.afx_kv_tables(
+        page_tokens, free_pages.numel(), _int32_ptr(old_len, n, "old_len"), _int32_ptr(new_len, n, "new_len"), n,
+        _int32_ptr(table, 1, "table"), table.shape[1], _int32_ptr(free_pages, 1, "free_pages"),
+        _int32_ptr(free_count, 1, "free_count"), _int32_ptr(free_count_out, 1, "free_count_out"),
+        _int32_ptr(starts, n + 1, "starts"), _int32_ptr(slots, 0, "slots"), _int32_ptr(positions, 0, "positions"),
+        slots.numel(), _stream_handle(stream), _dev_ptr(status_dev)))
+
+
+def _rows_of(x, cache: afx_kv_cache, heads: int, name: str) -> tuple:
+    """(address, token stride, head stride) of a CUDA tensor [tokens][heads][head_dim] of the cache's type."""
+    if not x.is_cuda or x.dim() != 3 or x.shape[1] != heads or x.shape[2] != cache.head_dim or \
+            _KV_FORMATS.get(str(x.dtype)) != cache.format:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens][{heads}][{cache.head_dim}] of the cache's type")
+    if x.stride(2) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return x.data_ptr(), x.stride(0), x.stride(1)
+
+
+def afx_kv_write(cache: afx_kv_cache, k, v, slots, stream=None, status_dev=None) -> None:
+    """Writes k, v ([tokens][kv_heads][head_dim], views with equal strides) into the cache at slots (int32 [tokens])."""
+    pk, token_stride, head_stride = _rows_of(k, cache, cache.kv_heads, "k")
+    pv = _rows_of(v, cache, cache.kv_heads, "v")
+    if k.shape != v.shape or pv[1:] != (token_stride, head_stride):
+        raise ValueError("k and v must have the same shape and strides")
+    _check("afx_kv_write", _lib.afx_kv_write(ctypes.byref(cache), pk, pv[0], token_stride, head_stride,
+                                              _int32_ptr(slots, k.shape[0], "slots"), k.shape[0], _stream_handle(stream),
+                                              _dev_ptr(status_dev)))
+
+
+def attention_args(cache: afx_kv_cache, q_heads: int, n_tokens: int, starts, lens, table, scale: float,
+                   prefix_table=None, prefix_len: int = 0) -> afx_attention_args:
+    """The description of a step's attention (see afx_attention_args in afx.h): starts int32 [n + 1], lens
+    int32 [n], table int32 [n][cols], prefix_table int32 [ceil(prefix_len / page_tokens)].  It holds the
+    tensors' addresses: keep them alive."""
+    n = lens.numel()
+    if table.dim() != 2 or table.shape[0] != n:
+        raise ValueError("table must be [requests][cols]")
+    if prefix_len < 0 or (prefix_len and prefix_table is None):
+        raise ValueError("a prefix needs its page table")
+    pages = -(-prefix_len // cache.page_tokens)
+    return afx_attention_args(cache, q_heads, n, n_tokens, table.shape[1], prefix_len, scale,
+                              _int32_ptr(prefix_table, pages, "prefix_table") if prefix_len else None,
+                              _int32_ptr(table, 1, "table"), _int32_ptr(starts, n + 1, "starts"),
+                              _int32_ptr(lens, n, "lens"))
+
+
+def afx_attention_workspace(args: afx_attention_args) -> int:
+    """Bytes of device workspace that the plan and the attention of this description need."""
+    v = ctypes.c_uint64(0)
+    _check("afx_attention_workspace", _lib.afx_attention_workspace(ctypes.byref(args), ctypes.byref(v)))
+    return int(v.value)
+
+
+def afx_attention_plan(args: afx_attention_args, workspace_dev, stream=None, status_dev=None) -> None:
+    """Lists the step's work in the workspace; once a step, for all its layers."""
+    _check("afx_attention_plan", _lib.afx_attention_plan(ctypes.byref(args), _dev_ptr(workspace_dev),
+                                                          workspace_dev.numel() * workspace_dev.element_size(),
+                                                          _stream_handle(stream), _dev_ptr(status_dev)))
+
+
+def afx_attention(args: afx_attention_args, q, out, workspace_dev, lse=None, stream=None, status_dev=None) -> None:
+    """out = attention of q over the shared prefix and each request's own tokens; q, out
+    [n_tokens][q_heads][head_dim] of the cache's type (views allowed), lse float32 [n_tokens][q_heads]."""
+    pq = _rows_of(q, args.cache, args.q_heads, "q")
+    po = _rows_of(out, args.cache, args.q_heads, "out")
+    if q.shape[0] != args.n_tokens or out.shape[0] != args.n_tokens:
+        raise ValueError(f"q and out must have {args.n_tokens} tokens")
+    _check("afx_attention", _lib.afx_attention(
+        ctypes.byref(args), *pq, *po, _float_ptr(lse, args.n_tokens * args.q_heads, "lse"), _dev_ptr(workspace_dev),
+        workspace_dev.numel() * workspace_dev.element_size(), _stream_handle(stream), _dev_ptr(status_dev)))
+
+
+_LOGITS = {"torch.bfloat16": AFX_LOGITS_BF16, "torch.float16": AFX_LOGITS_FP16, "torch.float32": AFX_LOGITS_F32}
+
+
+def afx_sample(logits, u, tokens, logprobs=None, temperature=None, top_k=None, top_p=None, min_p=None,
+               stream=None) -> None:
+    """Draws one token a row: logits CUDA [rows][vocab] (rows may be strided), u float32 [rows] in [0, 1), tokens
+    int32 [rows]; optional float32 [rows] logprobs, temperature, top_p, min_p and int32 [rows] top_k."""
+    if not logits.is_cuda or logits.dim() != 2 or str(logits.dtype) not in _LOGITS or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor [rows][vocab] of bfloat16, float16 or float32, rows contiguous")
+    rows = logits.shape[0]
+    if u is None:
+        raise ValueError("u must hold one number in [0, 1) a row")
+    _check("afx_sample", _lib.afx_sample(
+        logits.data_ptr(), _LOGITS[str(logits.dtype)], rows, logits.shape[1], logits.stride(0),
+        _float_ptr(temperature, rows, "temperature"), _int32_ptr(top_k, rows, "top_k") if top_k is not None else 0,
+        _float_ptr(top_p, rows, "top_p"), _float_ptr(min_p, rows, "min_p"), _float_ptr(u, rows, "u"),
+        _int32_ptr(tokens, rows, "tokens"), _float_ptr(logprobs, rows, "logprobs"), _stream_handle(stream)))
 
 
 def afx_debug_bounds_report() -> tuple[int, bool]:
