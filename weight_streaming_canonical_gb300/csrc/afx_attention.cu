@@ -16,7 +16,16 @@
 // kernel writes a step (the lengths are on the GPU, and every layer of the
 // step uses the same list), one attention kernel works off and one join
 // kernel puts together in a fixed order.
-#include "afx_serving.cuh"
+//
+// Two kernels work items off: the 16-row kernel here (mma.sync, four warps on
+// their own keys: one or a few new tokens a request, where reading the keys is
+// all) and the tile kernel (afx_attention_tile.cu: tcgen05, 256 rows).  A
+// request with 128 packed rows or more, a prompt, has tiles of its own that
+// run over the prefix and its own keys in one go; the others share tiles on
+// the prefix.
+#include <initializer_list>
+
+#include "afx_attention.cuh"
 
 namespace afx {
 namespace serve {
@@ -27,96 +36,81 @@ namespace {
 
 constexpr uint32_t kPlanThreads = 1024;
 constexpr uint32_t kMaxRequests = AFX_KV_MAX_REQUESTS;
-constexpr uint32_t kRows = 16;         // packed rows of an item
-constexpr uint32_t kKeyAlign = 64;     // item key ranges start at multiples of this
-constexpr uint32_t kMinKeys = 256;     // keys of an item, at least, where a range is cut
-constexpr uint32_t kTargetUnits = 1216;  // items x heads that the cuts aim at
-
-// The key names what the plan was made for: a workspace that holds no plan,
-// or that of another description, is refused instead of read.
-struct PlanHead {
-    uint32_t n_items, n_groups, n_tokens, n_prefix_groups;
-    uint64_t key;
-};
-
-// A tile of packed rows of one source: its pieces' results start at
-// part_row, piece s at part_row + s * rows.
-struct Group {
-    uint32_t part_row, n_pieces, rows, pad;
-};
-
-struct Item {
-    int32_t request;        // -1: the prefix
-    uint32_t row0, rows;    // packed rows of the source
-    uint32_t key0, key1;    // keys of the source
-    uint32_t part_row;      // where the results of its rows go
-    uint32_t token0;        // first token of the source
-    int32_t seen;           // token i of the source sees keys below seen + i + 1 (prefix: all)
-};
-
-struct Layout {
-    uint64_t token_request, request_group, groups, items, part_ml, part_o, total;
-    uint32_t max_groups, max_items, max_rows;
-};
-
-struct AttnArgs {
-    const void *k, *v;
-    uint64_t page_stride, token_stride, head_stride;  // elements
-    const int32_t *table, *prefix_table, *starts, *lens;
-    const void* q;
-    void* out;
-    float* lse;
-    uint64_t q_token, q_head, out_token, out_head;  // elements
-    uint8_t* ws;
-    int32_t* status;
-    Layout L;
-    uint32_t table_cols, n_requests, n_tokens, prefix_len, group, kv_heads, shift, n_pages, q_wide;
-    float scale_log2;
-    uint64_t plan_key;
-};
+constexpr uint32_t kKeyAlign = 64;     // 16-row items' key ranges start at multiples of this
+constexpr uint32_t kMinKeys = 256;     // keys of a 16-row item, at least, where a range is cut
+constexpr uint32_t kTargetUnits = 1216;  // 16-row items x heads that the cuts aim at
+constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's tiles take the prefix along
+constexpr uint32_t kMinShare = 8;      // cost of a tile CTA, at least
 
 __host__ __device__ inline uint64_t up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 
-// Keys that the last token of packed rows [row0, row0 + rows) sees.
-__device__ __forceinline__ uint32_t visible(int32_t seen, uint32_t last_row, uint32_t group) {
-    const int64_t v = static_cast<int64_t>(seen) + last_row / group + 1;
-    return v > 0 ? static_cast<uint32_t>(v) : 0u;
-}
-
 // ---- the plan ----------------------------------------------------------------------
 
-__device__ uint64_t block_sum_exclusive(uint64_t v, uint64_t* total, uint64_t* scratch) {
+template <int N>
+struct Counts {
+    uint64_t v[N];
+};
+
+// Exclusive sums over the CTA's threads; *total gets the sums.
+template <int N>
+__device__ Counts<N> block_exclusive(const Counts<N>& mine, Counts<N>* total) {
+    __shared__ Counts<N> warps[kPlanThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t inc = v;
+    Counts<N> inc = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-        if (lane >= d) inc += o;
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, inc.v[i], d);
+            if (lane >= d) inc.v[i] += o;
+        }
+    if (lane == 31) warps[warp] = inc;
+    __syncthreads();
+    Counts<N> out;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        uint64_t before = 0, all = 0;
+        for (uint32_t w = 0; w < kPlanThreads / 32; ++w) {
+            if (static_cast<int>(w) < warp) before += warps[w].v[i];
+            all += warps[w].v[i];
+        }
+        out.v[i] = before + inc.v[i] - mine.v[i];
+        total->v[i] = all;
     }
     __syncthreads();
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    uint64_t before = 0, all = 0;
-    for (uint32_t w = 0; w < kPlanThreads / 32; ++w) {
-        const uint64_t s = scratch[w];
-        if (static_cast<int>(w) < warp) before += s;
-        all += s;
-    }
-    *total = all;
-    return before + inc - v;
+    return out;
 }
 
-// One CTA.  A request's rows are cut into groups of kRows; every group's
-// keys are cut into pieces of `piece` keys, chosen so that all pieces x heads come
-// to about kTargetUnits (enough to fill the GPU, and a bound on the
-// workspace), but not below kMinKeys.
+// How a request's rows are worked off.
+struct Kind {
+    uint32_t own;    // Source
+    bool fused;      // its tiles take the prefix along (or there is none)
+};
+
+__device__ __forceinline__ Kind kind_of(const AttnArgs& a, uint32_t rows) {
+    const bool tile = a.tile_ctas && rows > kRows;
+    return Kind{rows == 0 ? kNone : tile ? kTile : kRow16, a.prefix_len == 0 || (tile && rows >= kFuseRows)};
+}
+
+__device__ __forceinline__ uint32_t tile_cost(uint32_t rows, uint32_t prefix_keys, uint32_t own_keys) {
+    const uint32_t steps = ceil_div(prefix_keys, kTileKeys) + ceil_div(own_keys, kTileKeys);
+    return rows > kTileRows ? 2 * steps : (steps + 1) / 2 * 2;
+}
+
+// One CTA.  Requests' rows are cut into groups of 16 (or 256 for the tile
+// kernel).  A 16-row group's keys are cut into pieces of `piece` keys, chosen
+// so that all pieces x heads come to about kTargetUnits (enough to fill the
+// GPU, and a bound on the workspace), but not below kMinKeys; the tile
+// groups' cost is cut into one share a CTA.
 __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const AttnArgs a) {
-    __shared__ uint64_t scratch[kPlanThreads / 32];
-    PlanHead* head = reinterpret_cast<PlanHead*>(a.ws);
-    int32_t* token_request = reinterpret_cast<int32_t*>(a.ws + a.L.token_request);
-    uint32_t* request_group = reinterpret_cast<uint32_t*>(a.ws + a.L.request_group);
-    Group* groups = reinterpret_cast<Group*>(a.ws + a.L.groups);
-    Item* items = reinterpret_cast<Item*>(a.ws + a.L.items);
+    PlanHead* head = a.at<PlanHead>(0);
+    int32_t* token_request = a.at<int32_t>(a.L.token_request);
+    uint32_t* token_packed = a.at<uint32_t>(a.L.token_packed);
+    int32_t* packed_token = a.at<int32_t>(a.L.packed_token);
+    RequestInfo* requests = a.at<RequestInfo>(a.L.requests);
+    Row16Group* groups = a.at<Row16Group>(a.L.groups16);
+    Row16Item* items = a.at<Row16Item>(a.L.items16);
+    TileGroup* tiles = a.at<TileGroup>(a.L.tiles);
     const uint32_t R = a.n_requests, G = a.group;
     const uint32_t per = ceil_div(R, kPlanThreads);
     const uint32_t r0 = min(R, threadIdx.x * per), r1 = min(R, r0 + per);
@@ -124,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
 
     // the lengths have to make sense before anything is addressed by them
     bool bad = false;
-    uint64_t keys = 0;
+    Counts<2> first{};  // keys of the 16-row groups, tokens that share tiles on the prefix
     if (threadIdx.x == 0 && a.starts[0] != 0) bad = true;
     for (uint32_t r = r0; r < r1; ++r) {
         const int32_t s = a.starts[r], e = a.starts[r + 1], len = a.lens[r];
@@ -133,113 +127,124 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
             continue;
         }
         const uint32_t rows = static_cast<uint32_t>(e - s) * G;
-        for (uint32_t row = 0; row < rows; row += kRows)
-            keys += visible(len - (e - s), min(rows, row + kRows) - 1, G);
+        const Kind k = kind_of(a, rows);
+        if (k.own == kRow16)
+            for (uint32_t row = 0; row < rows; row += kRows) first.v[0] += visible(len - (e - s), min(rows, row + kRows) - 1, G);
+        if (!k.fused) first.v[1] += e - s;
     }
     const bool refused = __syncthreads_or(bad) != 0;
     if (refused) {
         if (threadIdx.x == 0) {
             raise(a.status, AFX_DEV_BAD_LENGTH);
-            *head = PlanHead{0, 0, 0, 0, a.plan_key};
+            *head = PlanHead{a.plan_key, 0, 0, 0, 0, 0, kNone};
         }
         return;
     }
-    const uint32_t n_tokens = a.starts[R];
-    const uint32_t prefix_rows = a.prefix_len ? n_tokens * G : 0;
-    const uint32_t prefix_groups = ceil_div(prefix_rows, kRows);
-    uint64_t total_keys;
-    block_sum_exclusive(keys, &total_keys, scratch);
-    total_keys += static_cast<uint64_t>(prefix_groups) * a.prefix_len;
+    Counts<2> all;
+    uint32_t packed = static_cast<uint32_t>(block_exclusive(first, &all).v[1]);
+    const uint32_t prefix_rows = static_cast<uint32_t>(all.v[1]) * G;
+    const uint32_t prefix_kind = prefix_rows == 0 ? kNone : a.tile_ctas && prefix_rows > kRows ? kTile : kRow16;
+    const uint32_t groups_p = prefix_kind == kRow16 ? ceil_div(prefix_rows, kRows) : 0;
+    const uint32_t tiles_p = prefix_kind == kTile ? ceil_div(prefix_rows, kGroupRows) : 0;
+    const uint64_t keys = all.v[0] + static_cast<uint64_t>(groups_p) * a.prefix_len;
     const uint64_t units = kTargetUnits / a.kv_heads ? kTargetUnits / a.kv_heads : 1;
-    const uint64_t want = up((total_keys + units - 1) / units, kKeyAlign);
+    const uint64_t want = up((keys + units - 1) / units, kKeyAlign);
     const uint32_t piece = static_cast<uint32_t>(want < kMinKeys ? kMinKeys : want < (1u << 31) ? want : 1u << 31);
 
-    // the prefix: every group has the same pieces
-    const uint32_t prefix_pieces = ceil_div(a.prefix_len, piece);
-    for (uint32_t g = threadIdx.x; g < prefix_groups; g += kPlanThreads) {
-        const uint32_t row0 = g * kRows, rows = min(kRows, prefix_rows - row0);
-        groups[g] = Group{row0 * prefix_pieces, prefix_pieces, rows, 0};
+    // the prefix of the tokens that share it
+    const uint32_t pieces_p = groups_p ? ceil_div(a.prefix_len, piece) : 0;
+    for (uint32_t g = threadIdx.x; g < groups_p; g += kPlanThreads) {
+        const uint32_t row0 = g * kRows;
+        groups[g] = Row16Group{row0 * pieces_p, pieces_p, min(kRows, prefix_rows - row0), 0};
     }
-    for (uint32_t i = threadIdx.x; i < prefix_groups * prefix_pieces; i += kPlanThreads) {
+    for (uint32_t i = threadIdx.x; i < groups_p * pieces_p; i += kPlanThreads) {
         // piece by piece, so that the groups that read the same keys run together
-        const uint32_t s = i / prefix_groups, g = i % prefix_groups;
-        const uint32_t row0 = g * kRows, rows = min(kRows, prefix_rows - row0);
-        items[i] = Item{-1, row0, rows, s * piece, min(a.prefix_len, (s + 1) * piece), row0 * prefix_pieces + s * rows, 0, 0};
+        const uint32_t s = i / groups_p, row0 = (i % groups_p) * kRows, rows = min(kRows, prefix_rows - row0);
+        items[i] = Row16Item{-1, row0, rows, s * piece, min(a.prefix_len, (s + 1) * piece), row0 * pieces_p + s * rows, 0, 0};
+    }
+    const uint32_t cost_full = tile_cost(kGroupRows, a.prefix_len, 0);
+    const uint64_t tile_row0 = a.L.max_rows;  // rows of the tile kernel's first pieces start here
+    uint64_t cost_p = 0, rows_p = 0;
+    if (tiles_p) {
+        for (uint32_t g = threadIdx.x; g < tiles_p; g += kPlanThreads) {
+            const uint32_t row0 = g * kGroupRows, rows = min(kGroupRows, prefix_rows - row0);
+            tiles[g] = TileGroup{static_cast<uint64_t>(g) * cost_full * a.kv_heads, tile_row0 + static_cast<uint64_t>(row0) * a.kv_heads,
+                                 tile_cost(rows, a.prefix_len, 0), -1, row0, rows, a.prefix_len, 0, 0, 0, 0, {}};
+        }
+        const uint32_t last = prefix_rows - (tiles_p - 1) * kGroupRows;
+        cost_p = (static_cast<uint64_t>(tiles_p - 1) * cost_full + tile_cost(last, a.prefix_len, 0)) * a.kv_heads;
+        rows_p = (static_cast<uint64_t>(tiles_p - 1) * kGroupRows + (last > kTileRows ? last : 2 * last)) * a.kv_heads;
     }
 
-    // the requests' own tokens
-    uint64_t n_groups = 0, n_items = 0, n_rows = 0;
+    // the requests' own keys
+    auto walk = [&](uint32_t r, auto&& row16, auto&& tile) {
+        const uint32_t s = a.starts[r], n = a.starts[r + 1] - s, rows = n * G;
+        const int32_t seen = a.lens[r] - static_cast<int32_t>(n);
+        const Kind k = kind_of(a, rows);
+        if (k.own == kRow16)
+            for (uint32_t row = 0; row < rows; row += kRows) {
+                const uint32_t m = min(kRows, rows - row);
+                row16(row, m, visible(seen, row + m - 1, G), s, seen);
+            }
+        if (k.own == kTile)
+            for (uint32_t row = 0; row < rows; row += kGroupRows) {
+                const uint32_t m = min(kGroupRows, rows - row);
+                tile(row, m, k.fused ? a.prefix_len : 0u, visible(seen, row + m - 1, G), s, seen, k.fused);
+            }
+    };
+    Counts<6> mine{};
+    for (uint32_t r = r0; r < r1; ++r)
+        walk(
+            r,
+            [&](uint32_t, uint32_t m, uint32_t end, uint32_t, int32_t) {
+                const uint32_t pieces = ceil_div(end, piece);
+                mine.v[0] += 1;
+                mine.v[1] += pieces;
+                mine.v[2] += static_cast<uint64_t>(pieces) * m;
+            },
+            [&](uint32_t, uint32_t m, uint32_t prefix, uint32_t own, uint32_t, int32_t, bool) {
+                mine.v[3] += 1;
+                mine.v[4] += static_cast<uint64_t>(tile_cost(m, prefix, own)) * a.kv_heads;
+                mine.v[5] += static_cast<uint64_t>(m > kTileRows ? m : 2 * m) * a.kv_heads;
+            });
+    Counts<6> total;
+    const Counts<6> at = block_exclusive(mine, &total);
+    uint32_t g = static_cast<uint32_t>(at.v[0]) + groups_p, it = static_cast<uint32_t>(at.v[1]) + groups_p * pieces_p,
+             pr = static_cast<uint32_t>(at.v[2]) + (groups_p ? prefix_rows * pieces_p : 0), tg = static_cast<uint32_t>(at.v[3]) + tiles_p;
+    uint64_t cost = at.v[4] + cost_p, trow = tile_row0 + at.v[5] + rows_p;
     for (uint32_t r = r0; r < r1; ++r) {
         const uint32_t s = a.starts[r], e = a.starts[r + 1];
-        const int32_t seen = a.lens[r] - static_cast<int32_t>(e - s);
-        const uint32_t rows = (e - s) * G;
-        for (uint32_t row = 0; row < rows; row += kRows) {
-            const uint32_t n = min(kRows, rows - row), pieces = ceil_div(visible(seen, row + n - 1, G), piece);
-            ++n_groups;
-            n_items += pieces;
-            n_rows += static_cast<uint64_t>(pieces) * n;
+        const Kind k = kind_of(a, (e - s) * G);
+        requests[r] = RequestInfo{k.own, k.own == kTile ? tg : g, k.fused, 0};
+        walk(
+            r,
+            [&](uint32_t row, uint32_t m, uint32_t end, uint32_t token0, int32_t seen) {
+                const uint32_t pieces = ceil_div(end, piece);
+                groups[g++] = Row16Group{pr, pieces, m, 0};
+                for (uint32_t p = 0; p < pieces; ++p, pr += m)
+                    items[it++] = Row16Item{static_cast<int32_t>(r), row, m, p * piece, min(end, (p + 1) * piece), pr, token0, seen};
+            },
+            [&](uint32_t row, uint32_t m, uint32_t prefix, uint32_t own, uint32_t token0, int32_t seen, bool single) {
+                const uint32_t c = tile_cost(m, prefix, own);
+                tiles[tg++] = TileGroup{cost, trow, c, static_cast<int32_t>(r), row, m, prefix, own, token0, seen, single, {}};
+                cost += static_cast<uint64_t>(c) * a.kv_heads;
+                trow += static_cast<uint64_t>(m > kTileRows ? m : 2 * m) * a.kv_heads;
+            });
+        for (uint32_t t = s; t < e; ++t) {
+            token_request[t] = static_cast<int32_t>(r);
+            token_packed[t] = k.fused ? UINT32_MAX : packed;
+            if (!k.fused) packed_token[packed++] = static_cast<int32_t>(t);
         }
     }
-    uint64_t all_groups, all_items, all_rows;
-    uint32_t g = static_cast<uint32_t>(block_sum_exclusive(n_groups, &all_groups, scratch)) + prefix_groups;
-    uint32_t it = static_cast<uint32_t>(block_sum_exclusive(n_items, &all_items, scratch)) + prefix_groups * prefix_pieces;
-    uint32_t pr = static_cast<uint32_t>(block_sum_exclusive(n_rows, &all_rows, scratch)) + prefix_rows * prefix_pieces;
-    for (uint32_t r = r0; r < r1; ++r) {
-        const uint32_t s = a.starts[r], e = a.starts[r + 1];
-        const int32_t seen = a.lens[r] - static_cast<int32_t>(e - s);
-        const uint32_t rows = (e - s) * G;
-        request_group[r] = g;
-        for (uint32_t row = 0; row < rows; row += kRows) {
-            const uint32_t n = min(kRows, rows - row), end = visible(seen, row + n - 1, G), pieces = ceil_div(end, piece);
-            groups[g++] = Group{pr, pieces, n, 0};
-            for (uint32_t p = 0; p < pieces; ++p, pr += n)
-                items[it++] = Item{static_cast<int32_t>(r), row, n, p * piece, min(end, (p + 1) * piece), pr, s, seen};
-        }
-        for (uint32_t t = s; t < e; ++t) token_request[t] = static_cast<int32_t>(r);
+    if (threadIdx.x == 0) {
+        const uint64_t c = total.v[4] + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
+        const uint64_t share = up((c + ctas - 1) / ctas, 2);
+        *head = PlanHead{a.plan_key, c, share < kMinShare ? kMinShare : share, static_cast<uint32_t>(a.starts[R]),
+                         groups_p * pieces_p + static_cast<uint32_t>(total.v[1]), tiles_p + static_cast<uint32_t>(total.v[3]), prefix_kind};
     }
-    if (threadIdx.x == 0)
-        *head = PlanHead{prefix_groups * prefix_pieces + static_cast<uint32_t>(all_items),
-                         prefix_groups + static_cast<uint32_t>(all_groups), n_tokens, prefix_groups, a.plan_key};
 }
 
 // ---- 16 packed rows x a range of keys ------------------------------------------------
-
-template <typename T>
-struct Mma;
-template <>
-struct Mma<__nv_bfloat16> {
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-        uint32_t r;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-        return r;
-    }
-    static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
-};
-template <>
-struct Mma<__half> {
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-        uint32_t r;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-        return r;
-    }
-    static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
-};
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
     const uint32_t n = real ? 16u : 0u;  // 0: the 16 bytes are zeros, src is not read
@@ -262,12 +267,6 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
 constexpr int kWarps = 4;
 constexpr int kBlockKeys = 16;  // keys of one step of a warp; divides every page size
 constexpr int kStages = 3;
-// A row's reference maximum lags behind by up to this many powers of two:
-// exact all the same (numerator and denominator use the same reference), it
-// saves scaling the sums on every small rise; p stays below 2^8, which both
-// 16-bit types hold.
-constexpr float kLag = 8.0f;
-
 template <int D>
 constexpr size_t rows16_smem() {
     return static_cast<size_t>(kWarps) * kStages * 2 * kBlockKeys * D * 2;
@@ -281,14 +280,15 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
     constexpr int kChunks = D / 8;                     // 16-byte chunks of a key
     constexpr uint32_t kTile = kBlockKeys * D * 2;     // bytes of a block's keys
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PlanHead head = *reinterpret_cast<const PlanHead*>(a.ws);
+    const PlanHead head = *a.at<PlanHead>(0);
     if (head.key != a.plan_key) {
         if (threadIdx.x == 0) raise(a.status, AFX_DEV_BAD_PLAN);
         return;
     }
-    const Item* items = reinterpret_cast<const Item*>(a.ws + a.L.items);
-    float* part_o = reinterpret_cast<float*>(a.ws + a.L.part_o);
-    float2* part_ml = reinterpret_cast<float2*>(a.ws + a.L.part_ml);
+    const Row16Item* items = a.at<Row16Item>(a.L.items16);
+    const int32_t* packed = a.at<int32_t>(a.L.packed_token);
+    float* part_o = a.at<float>(a.L.part_o);
+    float2* part_ml = a.at<float2>(a.L.part_ml);
     const T* q = static_cast<const T*>(a.q);
     const T* kp = static_cast<const T*>(a.k);
     const T* vp = static_cast<const T*>(a.v);
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
     const uint32_t page_mask = (1u << a.shift) - 1;
 
     for (uint32_t unit = blockIdx.x; unit < head.n_items * a.kv_heads; unit += gridDim.x) {
-        const Item it = items[unit / a.kv_heads];
+        const Row16Item it = items[unit / a.kv_heads];
         const uint32_t h = unit % a.kv_heads;
         const int32_t* pages = it.request < 0 ? a.prefix_table : a.table + static_cast<uint64_t>(it.request) * a.table_cols;
 
@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
             const uint32_t i = lane / 4 + half * 8, row = it.row0 + i;
             const bool live = i < it.rows;
             limit[half] = it.request < 0 || !live ? UINT32_MAX : visible(it.seen, row, a.group);
-            const T* src = q + (it.token0 + row / a.group) * a.q_token + (h * a.group + row % a.group) * a.q_head + (lane % 4) * 2;
+            const uint64_t token = !live ? 0 : it.request < 0 ? packed[row / a.group] : it.token0 + row / a.group;
+            const T* src = q + token * a.q_token + (h * a.group + row % a.group) * a.q_head + (lane % 4) * 2;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
                     uint32_t v = 0;
                     if (live) {
                         const T* s = src + ks * 16 + kk * 8;
-                        if (a.q_wide)
+                        if (a.q_align >= 4)
                             v = *reinterpret_cast<const uint32_t*>(s);
                         else
                             v = *reinterpret_cast<const uint16_t*>(s) |
@@ -379,8 +380,8 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
                 uint32_t b[4];
                 const uint32_t row = (lane / 16) * 8 + lane % 8, chunk = ks * 2 + ((lane / 8) & 1);
                 ldmatrix4(b, buf + row * (D * 2) + ((chunk ^ (row & 7)) * 16));
-                Mma<T>::mma(s[0], qf[ks], b[0], b[1]);
-                Mma<T>::mma(s[1], qf[ks], b[2], b[3]);
+                Elem<T>::mma(s[0], qf[ks], b[0], b[1]);
+                Elem<T>::mma(s[1], qf[ks], b[2], b[3]);
             }
             const bool whole = key + kBlockKeys <= it.key1 && key + kBlockKeys <= min_limit;
             float top[2] = {-INFINITY, -INFINITY};
@@ -423,15 +424,15 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
                 }
             // the weights as A fragments, rounded to the cache's type for
             // the product with V (the sums above keep all their bits)
-            const uint32_t p[4] = {Mma<T>::pack(s[0][0], s[0][1]), Mma<T>::pack(s[0][2], s[0][3]),
-                                   Mma<T>::pack(s[1][0], s[1][1]), Mma<T>::pack(s[1][2], s[1][3])};
+            const uint32_t p[4] = {Elem<T>::pack(s[0][0], s[0][1]), Elem<T>::pack(s[0][2], s[0][3]),
+                                   Elem<T>::pack(s[1][0], s[1][1]), Elem<T>::pack(s[1][2], s[1][3])};
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
                 uint32_t b[4];
                 const uint32_t row = ((lane / 8) & 1) * 8 + lane % 8, chunk = n * 2 + lane / 16;
                 ldmatrix4_t(b, buf + kTile + row * (D * 2) + ((chunk ^ (row & 7)) * 16));
-                Mma<T>::mma(o[n * 2], p, b[0], b[1]);
-                Mma<T>::mma(o[n * 2 + 1], p, b[2], b[3]);
+                Elem<T>::mma(o[n * 2], p, b[0], b[1]);
+                Elem<T>::mma(o[n * 2 + 1], p, b[2], b[3]);
             }
             __syncwarp();  // the buffer is read before it is filled again
         }
@@ -488,56 +489,105 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
 
 // ---- the join ------------------------------------------------------------------------
 
-// One warp a row of the output: the pieces of its prefix group, then those
-// of its request's group, in order.
+// The pieces of one row's results: the prefix's (where the row shares it),
+// then those of its request's own keys.
+struct Pieces {
+    uint32_t n16, n_tile, ctas, rows16, group_rows;
+    uint64_t at16, step16;               // 16-row pieces: first row, distance
+    uint64_t first, further;             // tile pieces: of the first CTA, of the CTAs after it
+    uint32_t in, two;
+
+    __device__ uint32_t count() const { return n16 + n_tile; }
+    __device__ uint64_t row(uint32_t p) const {
+        if (p < n16) return at16 + p * step16;
+        p -= n16;
+        const uint32_t cta = two ? p / 2 : p, lane = two ? p % 2 : 0;
+        return cta == 0 ? first + lane * group_rows + in : further + static_cast<uint64_t>(cta - 1) * kGroupRows + lane * kTileRows + in;
+    }
+};
+
+__device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& head, uint32_t kind, uint32_t first_group, uint32_t row,
+                                            uint32_t h, bool* final) {
+    Pieces p{};
+    if (kind == kRow16) {
+        const Row16Group g = a.at<Row16Group>(a.L.groups16)[first_group + row / kRows];
+        p.n16 = g.n_pieces;
+        p.at16 = static_cast<uint64_t>(g.part_row + row % kRows) * a.kv_heads + h;
+        p.step16 = static_cast<uint64_t>(g.rows) * a.kv_heads;
+    } else if (kind == kTile) {
+        const TileGroup g = a.at<TileGroup>(a.L.tiles)[first_group + row / kGroupRows];
+        if (g.cost) {
+            uint32_t c0, c1;
+            tile_ctas(g, h, head.share, &c0, &c1);
+            p.two = g.rows <= kTileRows;
+            *final = g.single && c0 == c1 && !p.two;
+            p.n_tile = (c1 - c0 + 1) * (p.two ? 2 : 1);
+            p.group_rows = g.rows;
+            p.in = row % kGroupRows;
+            p.first = tile_part_row(g, h, c0, c0, a.L.extra_row);
+            p.further = tile_part_row(g, h, c0, c0 + 1, a.L.extra_row);
+        }
+    }
+    return p;
+}
+
+constexpr int kJoinThreads = 128;
+
+// One warp a row of the output; pieces in a fixed order.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) attention_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a) {
     constexpr int kPer = D / 32;
     const int lane = threadIdx.x & 31;
     const uint32_t q_heads = a.kv_heads * a.group;
-    const uint64_t w = static_cast<uint64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const PlanHead head = *reinterpret_cast<const PlanHead*>(a.ws);
+    const uint64_t w = static_cast<uint64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const PlanHead head = *a.at<PlanHead>(0);
     const uint32_t t = static_cast<uint32_t>(w / q_heads), qh = static_cast<uint32_t>(w % q_heads);
     if (head.key != a.plan_key || t >= head.n_tokens) return;
-    const Group* groups = reinterpret_cast<const Group*>(a.ws + a.L.groups);
-    const float* part_o = reinterpret_cast<const float*>(a.ws + a.L.part_o);
-    const float2* part_ml = reinterpret_cast<const float2*>(a.ws + a.L.part_ml);
-    const uint32_t r = reinterpret_cast<const int32_t*>(a.ws + a.L.token_request)[t];
-    const uint32_t h = qh / a.group;
-    const uint32_t row_p = t * a.group + qh % a.group;
-    const uint32_t row_r = (t - a.starts[r]) * a.group + qh % a.group;
-    Group src[2] = {Group{0, 0, 0, 0}, groups[reinterpret_cast<const uint32_t*>(a.ws + a.L.request_group)[r] + row_r / kRows]};
-    const uint32_t in[2] = {row_p % kRows, row_r % kRows};
-    if (head.n_prefix_groups) src[0] = groups[row_p / kRows];
+    const float* part_o = a.at<float>(a.L.part_o);
+    const float2* part_ml = a.at<float2>(a.L.part_ml);
+    const uint32_t r = a.at<int32_t>(a.L.token_request)[t], packed = a.at<uint32_t>(a.L.token_packed)[t];
+    const RequestInfo info = a.at<RequestInfo>(a.L.requests)[r];
+    const uint32_t h = qh / a.group, gh = qh % a.group;
+    bool final = false, unused = false;
+    const Pieces own = pieces_of(a, head, info.kind, info.first, (t - a.starts[r]) * a.group + gh, h, &final);
+    if (final) return;  // the tile kernel wrote this row's output
+    const Pieces pre = pieces_of(a, head, packed == UINT32_MAX ? static_cast<uint32_t>(kNone) : head.prefix_kind, 0, packed * a.group + gh, h, &unused);
 
-    float top = -INFINITY;
+    float top = -INFINITY, sum = 0.0f, acc[kPer] = {};
+    const uint32_t n = pre.count() + own.count();
+    for (uint32_t base = 0; base < n; base += 32) {
+        const uint32_t p = base + lane;
+        const uint64_t row = p < pre.count() ? pre.row(p) : own.row(p - pre.count());
+        const float2 ml = p < n ? part_ml[row] : make_float2(-INFINITY, 0.0f);
+        float most = fmaxf(top, ml.x);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-        for (uint32_t p = lane; p < src[k].n_pieces; p += 32)
-            top = fmaxf(top, part_ml[static_cast<uint64_t>(src[k].part_row + p * src[k].rows + in[k]) * a.kv_heads + h].x);
+        for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        if (most == -INFINITY) continue;  // none of these pieces has a key that the row sees
+        const float keep = exp2_approx(top - most);
+        top = most;
+        sum *= keep;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    float acc[kPer] = {}, sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
+        for (int j = 0; j < kPer; ++j) acc[j] *= keep;
+        const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
+        const float part = f * ml.y;
+        const uint32_t m = min(32u, n - base);
 #pragma unroll 4
-        for (uint32_t p = 0; p < src[k].n_pieces; ++p) {
-            const uint64_t at = static_cast<uint64_t>(src[k].part_row + p * src[k].rows + in[k]) * a.kv_heads + h;
-            const float2 ml = part_ml[at];
-            const float f = exp2_approx(ml.x - ref);
-            sum += f * ml.y;
+        for (uint32_t j = 0; j < m; ++j) {
+            const float fj = __shfl_sync(0xFFFFFFFFu, f, j);
+            const uint64_t rj = __shfl_sync(0xFFFFFFFFu, row, j);
+            sum += __shfl_sync(0xFFFFFFFFu, part, j);
+            if (__shfl_sync(0xFFFFFFFFu, ml.x, j) == -INFINITY) continue;  // its sums may never have been written
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) acc[j] += f * part_o[at * D + lane * kPer + j];
+            for (int k = 0; k < kPer; ++k) acc[k] += fj * part_o[rj * D + lane * kPer + k];
         }
+    }
     // a row that sees no key: zeros, and the logarithm of an empty sum
-    const float inv = sum > 0.0f ? 1.0f / sum : (top == -INFINITY ? 0.0f : 1.0f / sum);
+    const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
     T* out = static_cast<T*>(a.out) + t * a.out_token + qh * a.out_head + lane * kPer;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) out[j] = Mma<T>::from(acc[j] * inv);
+    for (int j = 0; j < kPer; ++j) out[j] = Elem<T>::from(acc[j] * inv);
     if (a.lse && lane == 0)
-        a.lse[static_cast<uint64_t>(t) * q_heads + qh] =
-            top == -INFINITY ? -INFINITY : (top + log2f(sum)) * 0.693147180559945309f;
+        a.lse[static_cast<uint64_t>(t) * q_heads + qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // ---- host side -----------------------------------------------------------------------
@@ -579,14 +629,26 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
     a->shift = shift;
     a->n_pages = c.n_pages;
     a->scale_log2 = static_cast<float>(static_cast<double>(d->scale) * 1.4426950408889634074);
-    // every group has one piece, and the cuts add at most kTargetUnits / kv_heads
-    const uint64_t rows = static_cast<uint64_t>(d->n_tokens) * a->group;
+    const int sms = current_sms();
+    if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
+    a->tile_ctas = tiles_fit(c) ? static_cast<uint32_t>(sms) : 0u;
+    // bounds on what the plan writes.  16-row groups: where tiles serve the
+    // larger ones, one a request and one on the prefix; every group has one
+    // piece, and the cuts add at most kTargetUnits / kv_heads.  Tile groups:
+    // full ones, and a last one a request; a group of 128 rows or fewer has
+    // its first piece's results twice.  Rows that share the prefix are in
+    // requests of fewer than kFuseRows rows
+    const uint64_t rows = static_cast<uint64_t>(d->n_tokens) * a->group, R = d->n_requests;
     const uint64_t extra = kTargetUnits / c.kv_heads + 1;
-    const uint64_t groups = 2 * ceil_div(static_cast<uint32_t>(rows), kRows) + d->n_requests + 1;
-    Layout& L = a->L;
-    L.max_groups = static_cast<uint32_t>(groups);
-    L.max_items = static_cast<uint32_t>(groups + extra);
-    L.max_rows = static_cast<uint32_t>(2 * rows + extra * kRows);
+    const bool tiles = a->tile_ctas != 0;
+    const uint64_t small = tiles ? (rows < kRows * R ? rows : kRows * R) + kRows : 2 * rows;
+    const uint64_t groups = tiles ? R + 1 : 2 * (rows / kRows + 1) + R;
+    const uint64_t shared = rows < kFuseRows * R ? rows : kFuseRows * R;
+    const uint64_t tile_rows = tiles ? rows + 2 * shared + 2 * kTileRows : 0;
+    AttnLayout& L = a->L;
+    L.max_rows = (small + extra * kRows) * c.kv_heads;
+    L.extra_row = L.max_rows + tile_rows * c.kv_heads;
+    const uint64_t part_rows = L.extra_row + static_cast<uint64_t>(a->tile_ctas) * kGroupRows;
     uint64_t off = up(sizeof(PlanHead), 256);
     auto take = [&](uint64_t bytes) {
         const uint64_t at = off;
@@ -594,16 +656,20 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
         return at;
     };
     L.token_request = take(4ull * d->n_tokens);
-    L.request_group = take(4ull * d->n_requests);
-    L.groups = take(sizeof(Group) * groups);
-    L.items = take(sizeof(Item) * static_cast<uint64_t>(L.max_items));
-    L.part_ml = take(8ull * L.max_rows * c.kv_heads);
-    L.part_o = take(4ull * L.max_rows * c.kv_heads * c.head_dim);
+    L.token_packed = take(4ull * d->n_tokens);
+    L.packed_token = take(4ull * d->n_tokens);
+    L.requests = take(sizeof(RequestInfo) * R);
+    L.groups16 = take(sizeof(Row16Group) * groups);
+    L.items16 = take(sizeof(Row16Item) * (groups + extra));
+    L.tiles = take(sizeof(TileGroup) * (tiles ? 2 * (rows / kGroupRows + 1) + R : 0));
+    L.part_ml = take(8ull * part_rows);
+    L.part_o = take(4ull * part_rows * c.head_dim);
     L.total = off;
     uint64_t key = 0x61667850u;
     for (uint64_t v : {L.total, static_cast<uint64_t>(d->n_tokens), static_cast<uint64_t>(d->n_requests),
                        static_cast<uint64_t>(d->prefix_len), static_cast<uint64_t>(d->table_cols),
-                       static_cast<uint64_t>(a->group), static_cast<uint64_t>(c.kv_heads), static_cast<uint64_t>(shift)})
+                       static_cast<uint64_t>(a->group), static_cast<uint64_t>(c.kv_heads), static_cast<uint64_t>(shift),
+                       static_cast<uint64_t>(a->tile_ctas)})
         key = (key ^ v) * 0x9E3779B97F4A7C15ull + 1;
     a->plan_key = key;
     return AFX_OK;
@@ -619,17 +685,21 @@ afx_status bind_workspace(AttnArgs* a, void* ws, uint64_t bytes, int32_t* status
 }
 
 template <typename T, int D>
-afx_status launch(const AttnArgs& a, cudaStream_t s) {
+afx_status launch(const AttnArgs& a, const afx_kv_cache& cache, cudaStream_t s) {
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
+    if (a.tile_ctas) {
+        const afx_status st = launch_tiles(a, cache, s);
+        if (st != AFX_OK) return st;
+    }
     const size_t smem = rows16_smem<D>();
     AFX_SERVE_TRY(cudaFuncSetAttribute(attention_rows16_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem)),
                   "cudaFuncSetAttribute");
     attention_rows16_kernel<T, D><<<sms * 2, kWarps * 32, smem, s>>>(a);
     AFX_SERVE_TRY(cudaGetLastError(), "attention_rows16_kernel launch");
-    const uint64_t warps = static_cast<uint64_t>(a.n_tokens) * a.kv_heads * a.group;
-    attention_join_kernel<T, D><<<static_cast<uint32_t>((warps + 3) / 4), 128, 0, s>>>(a);
+    const uint64_t warps = static_cast<uint64_t>(a.n_tokens) * a.kv_heads * a.group, per = kJoinThreads / 32;
+    attention_join_kernel<T, D><<<static_cast<uint32_t>((warps + per - 1) / per), kJoinThreads, 0, s>>>(a);
     AFX_SERVE_TRY(cudaGetLastError(), "attention_join_kernel launch");
     return AFX_OK;
 }
@@ -677,9 +747,10 @@ extern "C" afx_status afx_attention(const afx_attention_args* args, const void* 
     a.q_head = q_head_stride;
     a.out_token = out_token_stride;
     a.out_head = out_head_stride;
-    a.q_wide = !((reinterpret_cast<uintptr_t>(q_dev) & 3u) || (q_token_stride & 1u) || (q_head_stride & 1u));
+    const uintptr_t q_bits = reinterpret_cast<uintptr_t>(q_dev) | 2 * q_token_stride | 2 * q_head_stride;
+    a.q_align = q_bits & 3u ? 2 : q_bits & 15u ? 4 : 16;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = args->cache.format == AFX_FMT_BF16, wide = args->cache.head_dim == 128;
-    if (bf) return wide ? launch<__nv_bfloat16, 128>(a, s) : launch<__nv_bfloat16, 64>(a, s);
-    return wide ? launch<__half, 128>(a, s) : launch<__half, 64>(a, s);
+    if (bf) return wide ? launch<__nv_bfloat16, 128>(a, args->cache, s) : launch<__nv_bfloat16, 64>(a, args->cache, s);
+    return wide ? launch<__half, 128>(a, args->cache, s) : launch<__half, 64>(a, args->cache, s);
 }

@@ -1,0 +1,741 @@
+// sm_103a attention for many rows on the same keys: the tensor-core kernel
+// of afx_attention (tcgen05, tensor memory, TMA).
+//
+// A tile group is up to 256 packed query rows of one key/value head, as two
+// tiles of 128 rows, and the keys they see, in steps of 128.  A step of a
+// tile is
+//     S = Q K^T            (tcgen05, 128 x 128, float32 in tensor memory)
+//     P = 2^(S * c - ref)  (one thread a row: lane = row)
+//     O += P V             (P in tensor memory, V from shared memory)
+// with the running reference and sum of the softmax in the row's thread.
+// While one tile's threads work on their scores, the tensor cores work for
+// the other tile.  With more than 128 rows both tiles use every step's keys;
+// with fewer the two tiles hold the same rows and take the steps in turn
+// (their results are two pieces of the same rows).
+//
+// Work split: the cost of all groups x heads, laid end to end, is cut into
+// equal shares, one CTA each, whatever groups that cuts through; the join
+// puts a group's pieces together.  So every SM gets the same number of
+// steps whether there are two groups or thousands.
+//
+// Roles of a CTA's 10 warps: 0-3 and 4-7 the rows of tile 0 and 1, 8 issues
+// the products, 9 loads keys and values: each page of a step by TMA (64
+// elements x the page's tokens a box, 128-byte swizzle), into a ring of
+// slots that runs ahead over groups.  Tensor memory: S0 S1 O0 O1; P replaces S
+// in place for heads of 128, and has columns of its own for heads of 64.
+//
+// Every wait is bounded: one that runs out raises AFX_DEV_TIMEOUT and a
+// flag that all roles poll, copies and products in flight are waited for,
+// and the CTA frees its tensor memory and ends.
+#include <cstdio>
+#include <mutex>
+
+#include "afx_attention.cuh"
+
+namespace afx {
+namespace serve {
+namespace {
+
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kTileThreads = 320;
+constexpr uint32_t kWaitPolls = 1u << 22;
+
+template <int D>
+struct Shape {
+    static constexpr uint32_t kHalves = D / 64;                    // 128-byte wide column blocks of a tile
+    static constexpr uint32_t kBlock = kTileKeys * 128;            // bytes of one
+    static constexpr uint32_t kSlot = kHalves * kBlock;            // keys or values of a step
+    static constexpr uint32_t kSlots = D == 128 ? 5 : 8;
+    static constexpr uint32_t kQ = 2 * kSlot;                      // both tiles' queries
+    static constexpr uint32_t kCtl = kQ + kSlots * kSlot;
+    static constexpr uint32_t kSmem = kCtl + 1024 + 1024;          // control block, alignment
+    // tensor memory columns
+    static constexpr uint32_t kS = 0, kO = 256, kP = D == 128 ? 0 : 384;
+    static constexpr uint32_t kPStep = D == 128 ? 128 : 64;
+};
+
+struct Ctl {
+    uint64_t full[8], empty[8];
+    uint64_t tail;                     // a last step's values, before their missing rows are zeroed
+    uint64_t q_full;
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t abort_flag;
+};
+static_assert(sizeof(Ctl) <= 1024, "control block");
+
+struct TileArgs {
+    CUtensorMap k, v;
+    AttnArgs a;
+    // where token, head and page stand among the map's outer dimensions (by stride, smallest first)
+    uint32_t token_at, head_at, page_at;
+};
+
+// ---- barriers, TMA, tensor memory ------------------------------------------------
+
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_addr(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(done)
+                 : "r"(smem_addr(b)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+// Bounded, without giving up early: for what is in flight.
+__device__ __forceinline__ bool bar_drain(uint64_t* b, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitPolls; ++i)
+        if (bar_try(b, parity)) return true;
+    return false;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Ctl& ctl, int32_t* status) {
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+        if (bar_try(b, parity)) return true;
+        if ((i & 31u) == 31u && *reinterpret_cast<volatile int32_t*>(&ctl.abort_flag)) return false;
+    }
+    *reinterpret_cast<volatile int32_t*>(&ctl.abort_flag) = 1;
+    raise(status, AFX_DEV_TIMEOUT);
+    return false;
+}
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t c1, uint32_t c2, uint32_t c3,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+// Shared-memory operand of 128-byte rows with the 128-byte swizzle, 8-row
+// groups 1024 bytes apart.  lead: distance of 64-element blocks along the
+// contiguous dimension (values: 128 keys x 128 bytes; not used for queries
+// and keys, whose contiguous dimension is the product's K).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (uint64_t{1024 >> 4} << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// D = A B^T (+ D), A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+                 : "memory");
+}
+// The same with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_addr(bar)) : "memory");
+}
+
+#define AFX_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define AFX_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : AFX_R8(v, 0), AFX_R8(v, 8), AFX_R8(v, 16), AFX_R8(v, 24)
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+        "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
+        AFX_W8(v, 0), AFX_W8(v, 8), AFX_W8(v, 16), AFX_W8(v, 24)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(addr),
+                 AFX_W8(v, 0), AFX_W8(v, 8)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// ---- a CTA's share -----------------------------------------------------------------
+
+// The pieces of a CTA's share of the cost, in order; every role walks the
+// same ones.
+struct Walk {
+    const TileGroup* groups;
+    uint64_t at, end, share;
+    uint32_t n, heads, cta, g;
+
+    __device__ Walk(const AttnArgs& a, const PlanHead& head)
+        : groups(a.at<TileGroup>(a.L.tiles)), share(head.share), n(head.n_tiles), heads(a.kv_heads), cta(blockIdx.x), g(0) {
+        at = static_cast<uint64_t>(cta) * share;
+        end = at + share < head.cost ? at + share : head.cost;
+        if (at >= end) return;
+        uint32_t lo = 0, hi = n;  // the group that holds `at`
+        while (hi - lo > 1) {
+            const uint32_t mid = (lo + hi) >> 1;
+            if (groups[mid].cost_begin <= at)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        g = lo;
+    }
+    struct Piece {
+        TileGroup g;
+        uint32_t h, step0, step1;  // steps of 128 keys, prefix first
+        uint32_t prefix_steps;
+        bool both;                 // both tiles on every step
+    };
+    __device__ bool next(Piece* p) {
+        if (at >= end) return false;
+        while (at >= groups[g].cost_begin + static_cast<uint64_t>(groups[g].cost) * heads) ++g;
+        p->g = groups[g];
+        const uint64_t in = at - p->g.cost_begin;
+        p->h = static_cast<uint32_t>(in / p->g.cost);
+        const uint32_t off = static_cast<uint32_t>(in % p->g.cost);
+        const uint64_t stop = min(end, p->g.cost_begin + (static_cast<uint64_t>(p->h) + 1) * p->g.cost);
+        const uint32_t off1 = off + static_cast<uint32_t>(stop - at);
+        p->both = p->g.rows > kTileRows;
+        p->prefix_steps = ceil_div(p->g.prefix_keys, kTileKeys);
+        const uint32_t steps = p->prefix_steps + ceil_div(p->g.own_keys, kTileKeys);
+        p->step0 = p->both ? off / 2 : off;
+        p->step1 = min(steps, p->both ? off1 / 2 : off1);
+        at = stop;
+        return true;
+    }
+};
+
+// The keys of step s of a group: `first` in its source, `n` of them.
+__device__ __forceinline__ void step_keys(const Walk::Piece& p, uint32_t s, bool* prefix, uint32_t* first, uint32_t* n) {
+    *prefix = s < p.prefix_steps;
+    *first = (*prefix ? s : s - p.prefix_steps) * kTileKeys;
+    const uint32_t all = *prefix ? p.g.prefix_keys : p.g.own_keys;
+    *n = min(kTileKeys, all - *first);
+}
+
+// ---- the kernel ----------------------------------------------------------------------
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const __grid_constant__ TileArgs args) {
+    using Sh = Shape<D>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Ctl& ctl = *reinterpret_cast<Ctl*>(smem + Sh::kCtl);
+    const AttnArgs& a = args.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PlanHead head = *a.at<PlanHead>(0);
+    if (head.key != a.plan_key) {
+        if (threadIdx.x == 0) raise(a.status, AFX_DEV_BAD_PLAN);
+        return;
+    }
+    if (blockIdx.x * head.share >= head.cost) return;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < Sh::kSlots; ++i) {
+            bar_init(&ctl.full[i], 1);
+            bar_init(&ctl.empty[i], 1);
+        }
+        bar_init(&ctl.tail, 1);
+        bar_init(&ctl.q_full, kSoftWarps);
+        for (int t = 0; t < 2; ++t) {
+            bar_init(&ctl.s_full[t], 1);
+            bar_init(&ctl.p_full[t], kSoftWarps / 2);
+            bar_init(&ctl.pv_done[t], 1);
+        }
+        bar_init(&ctl.drain, 1);
+        ctl.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&ctl.tmem)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = ctl.tmem;
+    Walk walk(a, head);
+    Walk::Piece p;
+
+    if (warp == kLoadWarp) {
+        // ---- keys and values: slot 2 i of the sequence is step i's keys, 2 i + 1 its values
+        const uint32_t box = min(1u << a.shift, kTileKeys), page_mask = (1u << a.shift) - 1;
+        uint32_t seq = 0, tails = 0;
+        bool ok = true;
+        while (ok && walk.next(&p)) {
+            for (uint32_t s = p.step0; s < p.step1 && ok; ++s) {
+                bool prefix;
+                uint32_t first, n;
+                step_keys(p, s, &prefix, &first, &n);
+                const uint32_t used = ceil_div(n, box);  // boxes that hold keys of this step
+                const uint32_t key = first + lane * box;
+                uint32_t page = 0;
+                if (static_cast<uint32_t>(lane) < used) {
+                    const int32_t id = prefix ? a.prefix_table[key >> a.shift]
+                                              : a.table[static_cast<uint64_t>(p.g.request) * a.table_cols + (key >> a.shift)];
+                    if (id < 0 || static_cast<uint32_t>(id) >= a.n_pages)
+                        raise(a.status, AFX_DEV_BAD_PAGE);
+                    else
+                        page = id;
+                }
+                uint32_t at[3];
+#pragma unroll
+                for (uint32_t i = 0; i < 3; ++i) at[i] = i == args.token_at ? key & page_mask : i == args.head_at ? p.h : page;
+                for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
+                    const uint32_t slot = seq % Sh::kSlots;
+                    if (seq >= Sh::kSlots) ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.empty[slot], (seq / Sh::kSlots - 1) & 1u, ctl, a.status));
+                    if (!ok) break;
+                    // a last step's values: rows past the keys must be zeros, whatever the page holds there (0 * NaN)
+                    const bool patch = kv == 1 && n < kTileKeys;
+                    uint64_t* bar = patch ? &ctl.tail : &ctl.full[slot];
+                    const uint32_t dst = smem_addr(smem + Sh::kQ + slot * Sh::kSlot);
+                    if (lane == 0) bar_expect(bar, used * box * 128 * Sh::kHalves);
+                    __syncwarp();
+                    if (static_cast<uint32_t>(lane) < used)
+#pragma unroll
+                        for (uint32_t hf = 0; hf < Sh::kHalves; ++hf)
+                            load_box(dst + hf * Sh::kBlock + lane * box * 128, kv ? &args.v : &args.k, hf * 64, at[0], at[1], at[2], bar);
+                    if (patch) {
+                        ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.tail, tails & 1u, ctl, a.status));
+                        if (!ok) {
+                            if (!bar_drain(&ctl.tail, tails & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
+                            break;
+                        }
+                        ++tails;
+                        uint8_t* v = smem + Sh::kQ + slot * Sh::kSlot;
+                        for (uint32_t hf = 0; hf < Sh::kHalves; ++hf)
+                            for (uint32_t i = n * 8 + lane; i < kTileKeys * 8; i += 32)
+                                *reinterpret_cast<uint4*>(v + hf * Sh::kBlock + i * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&ctl.full[slot]);
+                    }
+                }
+            }
+        }
+        if (!ok) {  // copies in flight land before the CTA ends
+            for (uint32_t q = seq > Sh::kSlots ? seq - Sh::kSlots : 0; q < seq; ++q)
+                if (!bar_drain(&ctl.full[q % Sh::kSlots], (q / Sh::kSlots) & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- the products
+        if (lane == 0) {
+            // float32 accumulator, A and B of the cache's type, M = 128; values have their head elements contiguous (bit 16)
+            constexpr uint32_t kBase = (1u << 4) | (Elem<T>::kMmaType << 7) | (Elem<T>::kMmaType << 10) | ((kTileRows >> 4) << 24);
+            constexpr uint32_t kQk = kBase | ((kTileKeys >> 3) << 17), kPv = kBase | (1u << 16) | ((D >> 3) << 17);
+            const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + Sh::kQ);
+            uint32_t seq = 0, pieces = 0, p_count[2] = {0, 0};
+            bool ok = true;
+            auto slot_full = [&](uint32_t q) {
+                const bool r = bar_wait(&ctl.full[q % Sh::kSlots], (q / Sh::kSlots) & 1u, ctl, a.status);
+                fence_after();
+                return r;
+            };
+            auto scores = [&](uint32_t t, uint32_t q, bool both) {
+                const uint64_t qd = operand(q_addr + (both ? t * Sh::kSlot : 0), 16);
+                const uint64_t kd = operand(ring + (q % Sh::kSlots) * Sh::kSlot, 16);
+#pragma unroll
+                for (uint32_t ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks / 4) * (Sh::kBlock >> 4) + (ks % 4) * 2;
+                    mma_ss(tmem + Sh::kS + t * kTileKeys, qd + off, kd + off, kQk, ks != 0);
+                }
+                commit(&ctl.s_full[t]);
+            };
+            auto values = [&](uint32_t t, uint32_t q, bool first, bool release) {
+                const uint64_t vd = operand(ring + (q % Sh::kSlots) * Sh::kSlot, Sh::kBlock);
+#pragma unroll
+                for (uint32_t ks = 0; ks < kTileKeys / 16; ++ks)
+                    mma_ts(tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep + ks * 8, vd + ks * (2048 >> 4), kPv, !first || ks != 0);
+                if (release) commit(&ctl.empty[q % Sh::kSlots]);
+                commit(&ctl.pv_done[t]);  // last: the row threads wait for it before the CTA ends
+            };
+            auto weights_full = [&](uint32_t t) {
+                const bool r = bar_wait(&ctl.p_full[t], p_count[t]++ & 1u, ctl, a.status);
+                fence_after();
+                return r;
+            };
+            while (ok && walk.next(&p)) {
+                ok = bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status);
+                fence_after();
+                const uint32_t n = p.step1 - p.step0;
+                if (p.both) {
+                    // scores of step 0 for both tiles; then, a tile at a time, the values of step i and the scores of step i + 1
+                    if (ok) ok = slot_full(seq);
+                    if (ok) {
+                        scores(0, seq, true);
+                        scores(1, seq, true);
+                        commit(&ctl.empty[seq % Sh::kSlots]);
+                    }
+                    for (uint32_t i = 0; i < n && ok; ++i) {
+                        const uint32_t vq = seq + 2 * i + 1, kq = vq + 1;
+                        ok = slot_full(vq);
+                        for (uint32_t t = 0; t < 2 && ok; ++t) {
+                            ok = weights_full(t);
+                            if (!ok) break;
+                            values(t, vq, i == 0, t == 1);
+                            if (i + 1 < n) {
+                                if (t == 0) ok = slot_full(kq);
+                                if (!ok) break;
+                                scores(t, kq, true);
+                                if (t == 1) commit(&ctl.empty[kq % Sh::kSlots]);
+                            }
+                        }
+                    }
+                } else {
+                    // steps alternate between the tiles; the scores run one step ahead of the values
+                    if (ok) ok = slot_full(seq);
+                    if (ok) {
+                        scores(0, seq, false);
+                        commit(&ctl.empty[seq % Sh::kSlots]);
+                    }
+                    for (uint32_t i = 0; i < n && ok; ++i) {
+                        const uint32_t t = i & 1, vq = seq + 2 * i + 1, kq = vq + 1;
+                        // step i + 1's scores go to the other tile, whose step i - 1 has been read (its weights were full)
+                        if (i + 1 < n) {
+                            ok = slot_full(kq);
+                            if (!ok) break;
+                            scores(t ^ 1, kq, false);
+                            commit(&ctl.empty[kq % Sh::kSlots]);
+                        }
+                        ok = slot_full(vq) && weights_full(t);
+                        if (!ok) break;
+                        values(t, vq, i < 2, true);
+                    }
+                }
+                seq += 2 * n;
+            }
+            if (!ok) {  // products in flight finish before the tensor memory is freed
+                commit(&ctl.drain);
+                if (!bar_drain(&ctl.drain, 0)) raise(a.status, AFX_DEV_UNDRAINED);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- one row a thread
+        const uint32_t t = warp >> 2, in_tile = threadIdx.x & 127;
+        const uint32_t lanes = (static_cast<uint32_t>(warp & 3) * 32u) << 16;
+        const uint32_t s_col = tmem + lanes + Sh::kS + t * kTileKeys, p_col = tmem + lanes + Sh::kP + t * Sh::kPStep,
+                       o_col = tmem + lanes + Sh::kO + t * D;
+        const T* q = static_cast<const T*>(a.q);
+        const int32_t* packed = a.at<int32_t>(a.L.packed_token);
+        float* part_o = a.at<float>(a.L.part_o);
+        float2* part_ml = a.at<float2>(a.L.part_ml);
+        const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);  // not 0: masked scores stay minus infinity
+        const uint16_t flip = a.scale_log2 < 0.0f ? 0x8000u : 0u;  // a negative scale: -q instead
+        uint32_t s_count = 0, pv_count = 0, pieces = 0;
+        bool ok = true;
+        while (ok && walk.next(&p)) {
+            const TileGroup& g = p.g;
+            // the queries of this tile, 16 bytes a thread at a time, in the operand's swizzled order
+            if (p.both || t == 0) {
+                const uint32_t row_first = p.both ? t * kTileRows : 0;
+                uint8_t* dst = smem + (p.both ? t * Sh::kSlot : 0);
+                for (uint32_t i = in_tile; i < kTileRows * (D / 8); i += kTileRows) {
+                    const uint32_t r = i / (D / 8), c = i % (D / 8), row = row_first + r;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (row < g.rows) {
+                        const uint32_t pr = g.row0 + row, tok = pr / a.group;
+                        const uint64_t token = g.request < 0 ? packed[tok] : g.token0 + tok;
+                        const T* src = q + token * a.q_token + (p.h * a.group + pr % a.group) * a.q_head + c * 8;
+                        if (a.q_align == 16) {
+                            v = *reinterpret_cast<const uint4*>(src);
+                        } else {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = reinterpret_cast<const uint16_t*>(src)[2 * j] |
+                                       static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[2 * j + 1]) << 16;
+                            v = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        const uint32_t f = flip * 0x10001u;
+                        v.x ^= f;
+                        v.y ^= f;
+                        v.z ^= f;
+                        v.w ^= f;
+                    }
+                    *reinterpret_cast<uint4*>(dst + (c / 8) * Sh::kBlock + r * 128 + (((c % 8) ^ (r & 7)) * 16)) = v;
+                }
+                fence_async_shared();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ctl.q_full);
+            // all warps together: one without steps here must not run ahead into the next piece's phase
+            ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status));
+            if (!ok) break;
+
+            const uint32_t row = p.both ? t * kTileRows + in_tile : in_tile;
+            const bool live = row < g.rows;
+            const bool warp_live = (p.both ? t * kTileRows : 0) + (warp & 3) * 32 < g.rows;
+            const uint32_t limit = g.request < 0 || !live ? g.own_keys : min(g.own_keys, visible(g.seen, g.row0 + row, a.group));
+            const uint32_t all_see = g.request < 0 ? g.own_keys : visible(g.seen, g.row0, a.group);  // own keys every row sees
+            float ref = -INFINITY, sum = 0.0f;
+            const uint32_t first = p.step0 + (p.both ? 0 : t), stride = p.both ? 1 : 2;
+            uint32_t done = 0;  // steps of this tile
+            for (uint32_t s = first; s < p.step1 && ok; s += stride, ++done) {
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.s_full[t], s_count++ & 1u, ctl, a.status));
+                if (!ok) break;
+                fence_after();
+                if (warp_live) {
+                    bool prefix;
+                    uint32_t key, n;
+                    step_keys(p, s, &prefix, &key, &n);
+                    const uint32_t sees = prefix ? n : (limit > key ? min(n, limit - key) : 0u);
+                    const bool whole = n == kTileKeys && (prefix || key + kTileKeys <= all_see);
+                    uint32_t x[kTileKeys];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_load32(s_col + c * 32, x + c * 32);
+                    tmem_wait_load();
+                    if (!whole) {
+#pragma unroll
+                        for (uint32_t j = 0; j < kTileKeys; ++j)
+                            if (j >= sees) x[j] = 0xFF800000u;  // -inf
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (uint32_t j = 0; j < kTileKeys; j += 8)
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k)
+                            top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1])));
+                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                    const bool rise = most > ref + kLag;
+                    if (__any_sync(0xFFFFFFFFu, rise)) {
+                        const float next = rise ? most : ref;
+                        const float f = next == -INFINITY ? 1.0f : exp2_approx(ref - next);
+                        ref = next;
+                        sum *= f;
+                        if (done > 0) {  // scale O, once the last product into it is done
+                            ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.pv_done[t], (pv_count + done - 1) & 1u, ctl, a.status));
+                            if (!ok) break;
+                            fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_load32(o_col + c * 32, o);
+                                tmem_wait_load();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_store32(o_col + c * 32, o);
+                            }
+                        }
+                    }
+                    if (D != 128 && done > 0) {
+                        // weights have columns of their own: the product that read them must be done
+                        ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.pv_done[t], (pv_count + done - 1) & 1u, ctl, a.status));
+                        if (!ok) break;
+                        fence_after();
+                    }
+                    const float base = ref == -INFINITY ? 0.0f : ref;
+                    float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float e0 = exp2_approx(fmaf(__uint_as_float(x[c * 32 + 2 * j]), scale, -base));
+                            const float e1 = exp2_approx(fmaf(__uint_as_float(x[c * 32 + 2 * j + 1]), scale, -base));
+                            add[(2 * j) & 3] += e0;
+                            add[(2 * j + 1) & 3] += e1;
+                            // rounded to the cache's type for the product with V; the sum keeps all bits
+                            w[j] = Elem<T>::pack(e0, e1);
+                        }
+                        tmem_store16(p_col + c * 16, w);
+                    }
+                    sum += (add[0] + add[1]) + (add[2] + add[3]);
+                    tmem_wait_store();
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&ctl.p_full[t]);
+            }
+            if (!ok) break;
+            if (done > 0) {
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.pv_done[t], (pv_count + done - 1) & 1u, ctl, a.status));
+                if (!ok) break;
+                fence_after();
+            }
+            pv_count += done;
+            if (warp_live) {
+                uint32_t cta0, cta1;
+                tile_ctas(g, p.h, head.share, &cta0, &cta1);
+                const bool final = g.single && cta0 == cta1 && p.both;
+                const float total = sum;
+                const uint32_t in_piece = p.both ? row : t * (walk.cta == cta0 ? g.rows : kTileRows) + row;
+                const uint64_t pr = tile_part_row(g, p.h, cta0, walk.cta, a.L.extra_row) + in_piece;
+                uint64_t token = 0;
+                uint32_t qh = 0;
+                if (final && live) {
+                    const uint32_t prow = g.row0 + row, tok = prow / a.group;
+                    token = g.request < 0 ? packed[tok] : g.token0 + tok;
+                    qh = p.h * a.group + prow % a.group;
+                }
+                const float inv = total > 0.0f || ref != -INFINITY ? 1.0f / total : 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (done > 0) {
+                        tmem_load32(o_col + c * 32, o);
+                        tmem_wait_load();
+                    }
+                    if (live && done > 0 && final) {
+                        T* out = static_cast<T*>(a.out) + token * a.out_token + qh * a.out_head + c * 32;
+                        const bool wide = !(reinterpret_cast<uintptr_t>(out) & 15u);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = ref == -INFINITY ? 0u
+                                                        : Elem<T>::pack(__uint_as_float(o[j + 2 * k]) * inv, __uint_as_float(o[j + 2 * k + 1]) * inv);
+                            if (wide) {
+                                *reinterpret_cast<uint4*>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    reinterpret_cast<uint16_t*>(out)[j + 2 * k] = static_cast<uint16_t>(w[k]);
+                                    reinterpret_cast<uint16_t*>(out)[j + 2 * k + 1] = static_cast<uint16_t>(w[k] >> 16);
+                                }
+                            }
+                        }
+                    } else if (live && done > 0) {
+                        float4* dst = reinterpret_cast<float4*>(part_o + pr * D + c * 32);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+                                                 __uint_as_float(o[4 * j + 3]));
+                    }
+                    __syncwarp();
+                }
+                if (live) {
+                    if (!final)
+                        part_ml[pr] = make_float2(ref, total);
+                    else if (a.lse)
+                        a.lse[token * (static_cast<uint64_t>(a.kv_heads) * a.group) + qh] =
+                            ref == -INFINITY ? -INFINITY : (ref + log2f(total)) * kLn2;
+                }
+            }
+            fence_before();  // O has been read before the next piece's products, which wait for this tile's weights
+            __syncwarp();
+        }
+    }
+
+    fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+// ---- host side -----------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static std::once_flag once;
+    static EncodeFn fn = nullptr;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeFn>(f);
+    });
+    return fn;
+}
+
+struct PoolDim {
+    uint64_t size, stride;  // elements
+    uint32_t box, which;    // 0 token, 1 head, 2 page
+};
+
+// The pool's outer dimensions, smallest stride first; a dimension of one
+// element may have any stride and goes last.
+void pool_dims(const afx_kv_cache& c, PoolDim (&d)[3]) {
+    d[0] = PoolDim{c.page_tokens, c.token_stride, c.page_tokens < kTileKeys ? c.page_tokens : kTileKeys, 0};
+    d[1] = PoolDim{c.kv_heads, c.kv_heads > 1 ? c.head_stride : 0, 1, 1};
+    d[2] = PoolDim{c.n_pages, c.n_pages > 1 ? c.page_stride : 0, 1, 2};
+    auto after = [](const PoolDim& x, const PoolDim& y) { return x.size == 1 ? y.size != 1 : y.size != 1 && x.stride > y.stride; };
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (after(d[j], d[j + 1])) {
+                const PoolDim x = d[j];
+                d[j] = d[j + 1];
+                d[j + 1] = x;
+            }
+    for (int i = 0; i < 3; ++i)
+        if (d[i].size == 1) d[i].stride = i ? d[i - 1].stride * d[i - 1].size : c.head_dim;
+}
+
+// A box is 64 elements of up to 128 tokens of a page's head.
+afx_status pool_map(CUtensorMap* map, void* pool, const afx_kv_cache& c, const PoolDim (&d)[3]) {
+    const EncodeFn enc = encode_fn();
+    if (!enc) return afx_fail(AFX_E_CUDA, "cuTensorMapEncodeTiled is not available from the driver", 0);
+    const cuuint64_t dims[4] = {c.head_dim, d[0].size, d[1].size, d[2].size};
+    const cuuint64_t strides[3] = {2 * d[0].stride, 2 * d[1].stride, 2 * d[2].stride};
+    const cuuint32_t box[4] = {64, d[0].box, d[1].box, d[2].box};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, c.format == AFX_FMT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, pool, dims,
+                           strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        char msg[96];
+        snprintf(msg, sizeof msg, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+        return afx_fail(AFX_E_CUDA, msg, 0);
+    }
+    return AFX_OK;
+}
+
+template <typename T, int D>
+afx_status launch(const TileArgs& args, cudaStream_t s) {
+    AFX_SERVE_TRY(cudaFuncSetAttribute(attention_tile_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(Shape<D>::kSmem)),
+                  "cudaFuncSetAttribute");
+    attention_tile_kernel<T, D><<<args.a.tile_ctas, kTileThreads, Shape<D>::kSmem, s>>>(args);
+    AFX_SERVE_TRY(cudaGetLastError(), "attention_tile_kernel launch");
+    return AFX_OK;
+}
+
+}  // namespace
+
+bool tiles_fit(const afx_kv_cache& cache) {
+    PoolDim d[3];
+    pool_dims(cache, d);
+    // a tensor map wants each stride to be a multiple of the one before it, and below 2^40 bytes
+    return d[0].stride >= cache.head_dim && d[1].stride % d[0].stride == 0 && d[2].stride % d[1].stride == 0 &&
+           2 * d[2].stride < (uint64_t{1} << 40);
+}
+
+afx_status launch_tiles(const AttnArgs& a, const afx_kv_cache& cache, cudaStream_t s) {
+    TileArgs args;
+    args.a = a;
+    PoolDim d[3];
+    pool_dims(cache, d);
+    for (uint32_t i = 0; i < 3; ++i) (d[i].which == 0 ? args.token_at : d[i].which == 1 ? args.head_at : args.page_at) = i;
+    afx_status st = pool_map(&args.k, cache.k_dev, cache, d);
+    if (st == AFX_OK) st = pool_map(&args.v, cache.v_dev, cache, d);
+    if (st != AFX_OK) return st;
+    if (cache.format == AFX_FMT_BF16)
+        return cache.head_dim == 128 ? launch<__nv_bfloat16, 128>(args, s) : launch<__nv_bfloat16, 64>(args, s);
+    return cache.head_dim == 128 ? launch<__half, 128>(args, s) : launch<__half, 64>(args, s);
+}
+
+}  // namespace serve
+}  // namespace afx
