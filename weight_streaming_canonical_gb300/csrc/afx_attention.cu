@@ -54,30 +54,37 @@ struct Counts {
 // Exclusive sums over the CTA's threads; *total gets the sums.
 template <int N>
 __device__ Counts<N> block_exclusive(const Counts<N>& mine, Counts<N>* total) {
-    __shared__ Counts<N> warps[kPlanThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ uint64_t warps[N][32], sums[N];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
     Counts<N> inc = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1)
+    for (int i = 0; i < N; ++i) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int d = 1; d < 32; d <<= 1) {
             const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, inc.v[i], d);
             if (lane >= d) inc.v[i] += o;
         }
-    if (lane == 31) warps[warp] = inc;
+        if (lane == 31) warps[i][warp] = inc.v[i];
+    }
+    __syncthreads();
+    for (int i = warp; i < N; i += n_warps) {  // a warp a sum: the warps' totals
+        const uint64_t x = lane < n_warps ? warps[i][lane] : 0;
+        uint64_t y = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, y, d);
+            if (lane >= d) y += o;
+        }
+        warps[i][lane] = y - x;
+        if (lane == 31) sums[i] = y;
+    }
     __syncthreads();
     Counts<N> out;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        uint64_t before = 0, all = 0;
-        for (uint32_t w = 0; w < kPlanThreads / 32; ++w) {
-            if (static_cast<int>(w) < warp) before += warps[w].v[i];
-            all += warps[w].v[i];
-        }
-        out.v[i] = before + inc.v[i] - mine.v[i];
-        total->v[i] = all;
+        out.v[i] = warps[i][warp] + inc.v[i] - mine.v[i];
+        total->v[i] = sums[i];
     }
-    __syncthreads();
     return out;
 }
 
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     Row16Item* items = a.at<Row16Item>(a.L.items16);
     TileGroup* tiles = a.at<TileGroup>(a.L.tiles);
     const uint32_t R = a.n_requests, G = a.group;
-    const uint32_t per = ceil_div(R, kPlanThreads);
+    const uint32_t threads = blockDim.x, per = ceil_div(R, threads);
     const uint32_t r0 = min(R, threadIdx.x * per), r1 = min(R, r0 + per);
     const uint64_t max_len = static_cast<uint64_t>(a.table_cols) << a.shift;
 
@@ -153,11 +160,11 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
 
     // the prefix of the tokens that share it
     const uint32_t pieces_p = groups_p ? ceil_div(a.prefix_len, piece) : 0;
-    for (uint32_t g = threadIdx.x; g < groups_p; g += kPlanThreads) {
+    for (uint32_t g = threadIdx.x; g < groups_p; g += threads) {
         const uint32_t row0 = g * kRows;
         groups[g] = Row16Group{row0 * pieces_p, pieces_p, min(kRows, prefix_rows - row0), 0};
     }
-    for (uint32_t i = threadIdx.x; i < groups_p * pieces_p; i += kPlanThreads) {
+    for (uint32_t i = threadIdx.x; i < groups_p * pieces_p; i += threads) {
         // piece by piece, so that the groups that read the same keys run together
         const uint32_t s = i / groups_p, row0 = (i % groups_p) * kRows, rows = min(kRows, prefix_rows - row0);
         items[i] = Row16Item{-1, row0, rows, s * piece, min(a.prefix_len, (s + 1) * piece), row0 * pieces_p + s * rows, 0, 0};
@@ -166,7 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     const uint64_t tile_row0 = a.L.max_rows;  // rows of the tile kernel's first pieces start here
     uint64_t cost_p = 0, rows_p = 0;
     if (tiles_p) {
-        for (uint32_t g = threadIdx.x; g < tiles_p; g += kPlanThreads) {
+        for (uint32_t g = threadIdx.x; g < tiles_p; g += threads) {
             const uint32_t row0 = g * kGroupRows, rows = min(kGroupRows, prefix_rows - row0);
             tiles[g] = TileGroup{static_cast<uint64_t>(g) * cost_full * a.kv_heads, tile_row0 + static_cast<uint64_t>(row0) * a.kv_heads,
                                  tile_cost(rows, a.prefix_len, 0), -1, row0, rows, a.prefix_len, 0, 0, 0, 0, {}};
@@ -531,63 +538,130 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& h
     return p;
 }
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
-// One warp a row of the output; pieces in a fixed order.
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a) {
+// Rows base .. base + span - 1 of the output a warp; kSplit: one row a CTA, whose
+// warps share its pieces (few rows, each of many pieces).  Pieces are added
+// in a fixed order.
+template <typename T, int D, bool kSplit>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, uint32_t span) {
     constexpr int kPer = D / 32;
-    const int lane = threadIdx.x & 31;
+    __shared__ float sh_acc[kSplit ? kJoinWarps : 1][D];
+    __shared__ float2 sh_ml[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t q_heads = a.kv_heads * a.group;
-    const uint64_t w = static_cast<uint64_t>(blockIdx.x) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const uint64_t base = kSplit ? blockIdx.x : (static_cast<uint64_t>(blockIdx.x) * kJoinWarps + warp) * span;
     const PlanHead head = *a.at<PlanHead>(0);
-    const uint32_t t = static_cast<uint32_t>(w / q_heads), qh = static_cast<uint32_t>(w % q_heads);
-    if (head.key != a.plan_key || t >= head.n_tokens) return;
-    const float* part_o = a.at<float>(a.L.part_o);
-    const float2* part_ml = a.at<float2>(a.L.part_ml);
-    const uint32_t r = a.at<int32_t>(a.L.token_request)[t], packed = a.at<uint32_t>(a.L.token_packed)[t];
-    const RequestInfo info = a.at<RequestInfo>(a.L.requests)[r];
-    const uint32_t h = qh / a.group, gh = qh % a.group;
-    bool final = false, unused = false;
-    const Pieces own = pieces_of(a, head, info.kind, info.first, (t - a.starts[r]) * a.group + gh, h, &final);
-    if (final) return;  // the tile kernel wrote this row's output
-    const Pieces pre = pieces_of(a, head, packed == UINT32_MAX ? static_cast<uint32_t>(kNone) : head.prefix_kind, 0, packed * a.group + gh, h, &unused);
+    const uint64_t n_rows = head.key == a.plan_key ? static_cast<uint64_t>(head.n_tokens) * q_heads : 0;
+    if (base >= n_rows) return;
 
-    float top = -INFINITY, sum = 0.0f, acc[kPer] = {};
-    const uint32_t n = pre.count() + own.count();
-    for (uint32_t base = 0; base < n; base += 32) {
-        const uint32_t p = base + lane;
-        const uint64_t row = p < pre.count() ? pre.row(p) : own.row(p - pre.count());
-        const float2 ml = p < n ? part_ml[row] : make_float2(-INFINITY, 0.0f);
-        float most = fmaxf(top, ml.x);
+    struct Sources {
+        Pieces pre, own;
+        uint32_t t, qh;
+        bool final;  // the tile kernel wrote this row's output
+    };
+    auto sources = [&](uint64_t w) {
+        Sources s;
+        s.t = static_cast<uint32_t>(w / q_heads);
+        s.qh = static_cast<uint32_t>(w % q_heads);
+        const uint32_t r = a.at<int32_t>(a.L.token_request)[s.t], packed = a.at<uint32_t>(a.L.token_packed)[s.t];
+        const RequestInfo info = a.at<RequestInfo>(a.L.requests)[r];
+        const uint32_t h = s.qh / a.group, gh = s.qh % a.group;
+        bool unused = false;
+        s.final = false;
+        s.own = pieces_of(a, head, info.kind, info.first, (s.t - a.starts[r]) * a.group + gh, h, &s.final);
+        s.pre = pieces_of(a, head, packed == UINT32_MAX ? static_cast<uint32_t>(kNone) : head.prefix_kind, 0, packed * a.group + gh, h, &unused);
+        return s;
+    };
+    auto join = [&](const Sources& s) {
+        const float* part_o = a.at<float>(a.L.part_o);
+        const float2* part_ml = a.at<float2>(a.L.part_ml);
+        float top = -INFINITY, sum = 0.0f, acc[kPer] = {};
+        const uint32_t n = s.pre.count() + s.own.count();
+        constexpr uint32_t kStep = kSplit ? kJoinWarps : 1;
+        const uint32_t off = kSplit ? warp : 0;  // this warp's pieces: off, off + kStep, ...
+        for (uint32_t b = off; b < n; b += 32 * kStep) {
+            const uint32_t p = b + lane * kStep;
+            const uint64_t row = p >= n ? 0 : p < s.pre.count() ? s.pre.row(p) : s.own.row(p - s.pre.count());
+            const float2 ml = p < n ? part_ml[row] : make_float2(-INFINITY, 0.0f);
+            float most = fmaxf(top, ml.x);
 #pragma unroll
-        for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-        if (most == -INFINITY) continue;  // none of these pieces has a key that the row sees
-        const float keep = exp2_approx(top - most);
-        top = most;
-        sum *= keep;
+            for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+            if (most == -INFINITY) continue;  // none of these pieces has a key that the row sees
+            const float keep = exp2_approx(top - most);
+            top = most;
+            sum *= keep;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) acc[j] *= keep;
-        const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
-        const float part = f * ml.y;
-        const uint32_t m = min(32u, n - base);
-#pragma unroll 4
-        for (uint32_t j = 0; j < m; ++j) {
-            const float fj = __shfl_sync(0xFFFFFFFFu, f, j);
-            const uint64_t rj = __shfl_sync(0xFFFFFFFFu, row, j);
-            sum += __shfl_sync(0xFFFFFFFFu, part, j);
-            if (__shfl_sync(0xFFFFFFFFu, ml.x, j) == -INFINITY) continue;  // its sums may never have been written
+            for (int j = 0; j < kPer; ++j) acc[j] *= keep;
+            const bool real = ml.x != -INFINITY;  // else its sums may never have been written
+            const float f = real ? exp2_approx(ml.x - top) : 0.0f;
+            float part = f * ml.y;
+            const uint32_t m = min(32u, ceil_div(n - b, kStep));
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) acc[k] += fj * part_o[rj * D + lane * kPer + k];
+            for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
+            sum += part;
+            const uint32_t live = __ballot_sync(0xFFFFFFFFu, real);
+#pragma unroll 8
+            for (uint32_t j = 0; j < m; ++j) {
+                const float fj = __shfl_sync(0xFFFFFFFFu, f, j);
+                const uint64_t rj = __shfl_sync(0xFFFFFFFFu, row, j);
+                float v[kPer] = {};
+                if (live >> j & 1) {
+                    if constexpr (kPer == 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(part_o + rj * D + lane * 4);
+                        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2*>(part_o + rj * D + lane * 2);
+                        v[0] = x.x, v[1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) acc[k] += fj * v[k];
+            }
         }
-    }
-    // a row that sees no key: zeros, and the logarithm of an empty sum
-    const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
-    T* out = static_cast<T*>(a.out) + t * a.out_token + qh * a.out_head + lane * kPer;
+        if constexpr (kSplit) {
+            if (lane == 0) sh_ml[warp] = make_float2(top, sum);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) out[j] = Elem<T>::from(acc[j] * inv);
-    if (a.lse && lane == 0)
-        a.lse[static_cast<uint64_t>(t) * q_heads + qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+            for (int j = 0; j < kPer; ++j) sh_acc[warp][lane * kPer + j] = acc[j];
+            __syncthreads();
+            if (warp) return;
+            top = -INFINITY;
+            sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sh_ml[w].x);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) acc[j] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float f = sh_ml[w].x == -INFINITY ? 0.0f : exp2_approx(sh_ml[w].x - top);
+                sum += f * sh_ml[w].y;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) acc[j] += f * sh_acc[w][lane * kPer + j];
+            }
+        }
+        // a row that sees no key: zeros, and the logarithm of an empty sum
+        const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
+        T* out = static_cast<T*>(a.out) + s.t * a.out_token + s.qh * a.out_head + lane * kPer;
+        if (reinterpret_cast<uintptr_t>(out) & (kPer * 2 - 1)) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) out[j] = Elem<T>::from(acc[j] * inv);
+        } else if constexpr (kPer == 4) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pack(acc[0] * inv, acc[1] * inv), Elem<T>::pack(acc[2] * inv, acc[3] * inv));
+        } else {
+            *reinterpret_cast<uint32_t*>(out) = Elem<T>::pack(acc[0] * inv, acc[1] * inv);
+        }
+        if (a.lse && lane == 0)
+            a.lse[static_cast<uint64_t>(s.t) * q_heads + s.qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+    };
+    if (kSplit || span == 1) {
+        const Sources s = sources(base);
+        if (!s.final) join(s);
+        return;
+    }
+    // which of the warp's rows are left to do: mostly none behind the tile kernel
+    bool todo = false;
+    if (static_cast<uint32_t>(lane) < span && base + lane < n_rows) todo = !sources(base + lane).final;
+    for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, todo); rest; rest &= rest - 1) join(sources(base + __ffs(rest) - 1));
 }
 
 // ---- host side -----------------------------------------------------------------------
@@ -675,6 +749,13 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
     return AFX_OK;
 }
 
+// A thread a request, up to the most a CTA has; with fewer the sums over the
+// CTA cost less.
+uint32_t plan_threads(uint32_t requests) {
+    const uint32_t n = (requests + 31) / 32 * 32;
+    return n < 128 ? 128 : n > kPlanThreads ? kPlanThreads : n;
+}
+
 afx_status bind_workspace(AttnArgs* a, void* ws, uint64_t bytes, int32_t* status) {
     if (bytes < a->L.total) return afx_fail(AFX_E_NOSPACE, "the attention workspace is smaller than afx_attention_workspace", 0);
     if (!device_ptr(ws, 256)) return afx_fail(AFX_E_ARG, "the workspace must be 256-byte aligned device memory", 0);
@@ -698,8 +779,13 @@ afx_status launch(const AttnArgs& a, const afx_kv_cache& cache, cudaStream_t s) 
                   "cudaFuncSetAttribute");
     attention_rows16_kernel<T, D><<<sms * 2, kWarps * 32, smem, s>>>(a);
     AFX_SERVE_TRY(cudaGetLastError(), "attention_rows16_kernel launch");
-    const uint64_t warps = static_cast<uint64_t>(a.n_tokens) * a.kv_heads * a.group, per = kJoinThreads / 32;
-    attention_join_kernel<T, D><<<static_cast<uint32_t>((warps + per - 1) / per), kJoinThreads, 0, s>>>(a);
+    const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.kv_heads * a.group;
+    if (rows <= static_cast<uint64_t>(sms) * 8) {  // a CTA a row while they all run at once
+        attention_join_kernel<T, D, true><<<static_cast<uint32_t>(rows), kJoinThreads, 0, s>>>(a, 1);
+    } else {
+        const uint64_t span = rows <= static_cast<uint64_t>(sms) * 256 ? 1 : 32, per = span * kJoinWarps;
+        attention_join_kernel<T, D, false><<<static_cast<uint32_t>((rows + per - 1) / per), kJoinThreads, 0, s>>>(a, static_cast<uint32_t>(span));
+    }
     AFX_SERVE_TRY(cudaGetLastError(), "attention_join_kernel launch");
     return AFX_OK;
 }
@@ -725,7 +811,7 @@ extern "C" afx_status afx_attention_plan(const afx_attention_args* args, void* w
     afx_status st = prepare(args, &a);
     if (st == AFX_OK) st = bind_workspace(&a, workspace_dev, workspace_bytes, status_dev);
     if (st != AFX_OK) return st;
-    attention_plan_kernel<<<1, kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    attention_plan_kernel<<<1, plan_threads(args->n_requests), 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
     AFX_SERVE_TRY(cudaGetLastError(), "attention_plan_kernel launch");
     return AFX_OK;
 }

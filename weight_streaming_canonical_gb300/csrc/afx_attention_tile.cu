@@ -18,8 +18,10 @@
 // puts a group's pieces together.  So every SM gets the same number of
 // steps whether there are two groups or thousands.
 //
-// Roles of a CTA's 10 warps: 0-3 and 4-7 the rows of tile 0 and 1, 8 issues
-// the products, 9 loads keys and values: each page of a step by TMA (64
+// Roles of a CTA's 12 warps: 0-3 and 4-7 the rows of tile 0 and 1 (a row's
+// 128 scores stay in its thread's registers: these warps take registers from
+// the others), 8 issues the products, 9 loads keys and values, 10 and 11 only
+// make up a warpgroup: each page of a step by TMA (64
 // elements x the page's tokens a box, 128-byte swizzle), into a ring of
 // slots that runs ahead over groups.  Tensor memory: S0 S1 O0 O1; P replaces S
 // in place for heads of 128, and has columns of its own for heads of 64.
@@ -38,7 +40,11 @@ namespace {
 
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kTileThreads = 320;
+constexpr int kTileThreads = 384;
+// registers a thread: as launched, then of the row warps and of the others
+// (what the row warps add is what the others gave up)
+constexpr int kRegsLaunch = 168, kRegsRows = 208, kRegsOther = 88;
+static_assert(256 * kRegsRows + 128 * kRegsOther <= kTileThreads * kRegsLaunch, "register shares");
 constexpr uint32_t kWaitPolls = 1u << 22;
 
 template <int D>
@@ -272,8 +278,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
     const uint32_t tmem = ctl.tmem;
     Walk walk(a, head);
     Walk::Piece p;
-
-    if (warp == kLoadWarp) {
+    if (warp >= kSoftWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsOther));
+      if (warp == kLoadWarp) {
         // ---- keys and values: slot 2 i of the sequence is step i's keys, 2 i + 1 its values
         const uint32_t box = min(1u << a.shift, kTileKeys), page_mask = (1u << a.shift) - 1;
         uint32_t seq = 0, tails = 0;
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             for (uint32_t q = seq > Sh::kSlots ? seq - Sh::kSlots : 0; q < seq; ++q)
                 if (!bar_drain(&ctl.full[q % Sh::kSlots], (q / Sh::kSlots) & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
         }
-    } else if (warp == kMmaWarp) {
+      } else if (warp == kMmaWarp) {
         // ---- the products
         if (lane == 0) {
             // float32 accumulator, A and B of the cache's type, M = 128; values have their head elements contiguous (bit 16)
@@ -426,7 +433,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             }
         }
         __syncwarp();
+      }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsRows));
         // ---- one row a thread
         const uint32_t t = warp >> 2, in_tile = threadIdx.x & 127;
         const uint32_t lanes = (static_cast<uint32_t>(warp & 3) * 32u) << 16;
@@ -442,35 +451,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         bool ok = true;
         while (ok && walk.next(&p)) {
             const TileGroup& g = p.g;
-            // the queries of this tile, 16 bytes a thread at a time, in the operand's swizzled order
+            // this thread's row of the queries, in the operand's swizzled order
             if (p.both || t == 0) {
-                const uint32_t row_first = p.both ? t * kTileRows : 0;
-                uint8_t* dst = smem + (p.both ? t * Sh::kSlot : 0);
-                for (uint32_t i = in_tile; i < kTileRows * (D / 8); i += kTileRows) {
-                    const uint32_t r = i / (D / 8), c = i % (D / 8), row = row_first + r;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (row < g.rows) {
-                        const uint32_t pr = g.row0 + row, tok = pr / a.group;
-                        const uint64_t token = g.request < 0 ? packed[tok] : g.token0 + tok;
-                        const T* src = q + token * a.q_token + (p.h * a.group + pr % a.group) * a.q_head + c * 8;
-                        if (a.q_align == 16) {
-                            v = *reinterpret_cast<const uint4*>(src);
-                        } else {
-                            uint32_t w[4];
+                const uint32_t q_row = (p.both ? t * kTileRows : 0) + in_tile;
+                uint8_t* dst = smem + (p.both ? t * Sh::kSlot : 0) + in_tile * 128;
+                uint4 v[D / 8];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[j] = reinterpret_cast<const uint16_t*>(src)[2 * j] |
-                                       static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[2 * j + 1]) << 16;
-                            v = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                        const uint32_t f = flip * 0x10001u;
-                        v.x ^= f;
-                        v.y ^= f;
-                        v.z ^= f;
-                        v.w ^= f;
+                for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+                if (q_row < g.rows) {
+                    const uint32_t pr = g.row0 + q_row, tok = pr / a.group;
+                    const uint64_t token = g.request < 0 ? packed[tok] : g.token0 + tok;
+                    const T* src = q + token * a.q_token + (p.h * a.group + pr % a.group) * a.q_head;
+                    if (a.q_align == 16) {
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) v[c] = *reinterpret_cast<const uint4*>(src + c * 8);
+                    } else {
+                        const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c)
+                            v[c] = make_uint4(e[c * 8] | static_cast<uint32_t>(e[c * 8 + 1]) << 16, e[c * 8 + 2] | static_cast<uint32_t>(e[c * 8 + 3]) << 16,
+                                              e[c * 8 + 4] | static_cast<uint32_t>(e[c * 8 + 5]) << 16, e[c * 8 + 6] | static_cast<uint32_t>(e[c * 8 + 7]) << 16);
                     }
-                    *reinterpret_cast<uint4*>(dst + (c / 8) * Sh::kBlock + r * 128 + (((c % 8) ^ (r & 7)) * 16)) = v;
                 }
+                const uint32_t f = flip * 0x10001u;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint4*>(dst + (c / 8) * Sh::kBlock + (((c % 8) ^ (in_tile & 7)) * 16)) =
+                        make_uint4(v[c].x ^ f, v[c].y ^ f, v[c].z ^ f, v[c].w ^ f);
                 fence_async_shared();
             }
             __syncwarp();
@@ -705,6 +712,17 @@ afx_status pool_map(CUtensorMap* map, void* pool, const afx_kv_cache& c, const P
 
 template <typename T, int D>
 afx_status launch(const TileArgs& args, cudaStream_t s) {
+    // the row warps wait for the registers that they ask for: they must be there
+    static std::once_flag once;
+    static int regs = 0;
+    std::call_once(once, [] {
+        cudaFuncAttributes at{};
+        if (cudaFuncGetAttributes(&at, attention_tile_kernel<T, D>) == cudaSuccess)
+            regs = at.numRegs;
+        else
+            cudaGetLastError();
+    });
+    if (regs < kRegsLaunch) return afx_fail(AFX_E_CUDA, "attention_tile_kernel was built with too few registers", 0);
     AFX_SERVE_TRY(cudaFuncSetAttribute(attention_tile_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(Shape<D>::kSmem)),
                   "cudaFuncSetAttribute");
