@@ -151,6 +151,13 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
 #define AFX_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
 #define AFX_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
 
@@ -341,96 +348,110 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 if (!bar_drain(&ctl.full[q % Sh::kSlots], (q / Sh::kSlots) & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
         }
       } else if (warp == kMmaWarp) {
-        // ---- the products
-        if (lane == 0) {
-            // float32 accumulator, A and B of the cache's type, M = 128; values have their head elements contiguous (bit 16)
-            constexpr uint32_t kBase = (1u << 4) | (Elem<T>::kMmaType << 7) | (Elem<T>::kMmaType << 10) | ((kTileRows >> 4) << 24);
-            constexpr uint32_t kQk = kBase | ((kTileKeys >> 3) << 17), kPv = kBase | (1u << 16) | ((D >> 3) << 17);
-            const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + Sh::kQ);
-            uint32_t seq = 0, pieces = 0, p_count[2] = {0, 0};
-            bool ok = true;
-            auto slot_full = [&](uint32_t q) {
-                const bool r = bar_wait(&ctl.full[q % Sh::kSlots], (q / Sh::kSlots) & 1u, ctl, a.status);
-                fence_after();
-                return r;
-            };
-            auto scores = [&](uint32_t t, uint32_t q, bool both) {
-                const uint64_t qd = operand(q_addr + (both ? t * Sh::kSlot : 0), 16);
-                const uint64_t kd = operand(ring + (q % Sh::kSlots) * Sh::kSlot, 16);
+        // ---- the products.  The whole warp walks the steps and waits; one
+        // lane, the same throughout, issues (descriptors stay warp-uniform)
+        // float32 accumulator, A and B of the cache's type, M = 128; values have their head elements contiguous (bit 16)
+        constexpr uint32_t kBase = (1u << 4) | (Elem<T>::kMmaType << 7) | (Elem<T>::kMmaType << 10) | ((kTileRows >> 4) << 24);
+        constexpr uint32_t kQk = kBase | ((kTileKeys >> 3) << 17), kPv = kBase | (1u << 16) | ((D >> 3) << 17);
+        const bool leader = elect();
+        const uint64_t q_desc = operand(smem_addr(smem), 16), k_desc = operand(smem_addr(smem + Sh::kQ), 16),
+                       v_desc = operand(smem_addr(smem + Sh::kQ), Sh::kBlock);
+        uint32_t pieces = 0, p_count[2] = {0, 0};
+        uint32_t k_slot = 0, k_phase = 0;  // ring position of the next keys or values to use
+        bool ok = true;
+        auto uniform = [&](bool r) { return __all_sync(0xFFFFFFFFu, r); };
+        auto slot_full = [&](uint32_t slot, uint32_t phase) {
+            const bool r = uniform(bar_wait(&ctl.full[slot], phase, ctl, a.status));
+            fence_after();
+            return r;
+        };
+        auto step_on = [&](uint32_t& slot, uint32_t& phase) {
+            if (++slot == Sh::kSlots) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        };
+        auto scores = [&](uint32_t t, uint32_t slot, bool own_q, bool release) {
+            const uint64_t qd = q_desc + (own_q ? t * (Sh::kSlot >> 4) : 0), kd = k_desc + slot * (Sh::kSlot >> 4);
+            if (leader) {
 #pragma unroll
                 for (uint32_t ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = (ks / 4) * (Sh::kBlock >> 4) + (ks % 4) * 2;
                     mma_ss(tmem + Sh::kS + t * kTileKeys, qd + off, kd + off, kQk, ks != 0);
                 }
+                if (release) commit(&ctl.empty[slot]);
                 commit(&ctl.s_full[t]);
-            };
-            auto values = [&](uint32_t t, uint32_t q, bool first, bool release) {
-                const uint64_t vd = operand(ring + (q % Sh::kSlots) * Sh::kSlot, Sh::kBlock);
+            }
+            __syncwarp();
+        };
+        auto values = [&](uint32_t t, uint32_t slot, bool first, bool release) {
+            const uint64_t vd = v_desc + slot * (Sh::kSlot >> 4);
+            if (leader) {
+                mma_ts(tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep, vd, kPv, !first);
 #pragma unroll
-                for (uint32_t ks = 0; ks < kTileKeys / 16; ++ks)
-                    mma_ts(tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep + ks * 8, vd + ks * (2048 >> 4), kPv, !first || ks != 0);
-                if (release) commit(&ctl.empty[q % Sh::kSlots]);
+                for (uint32_t ks = 1; ks < kTileKeys / 16; ++ks)
+                    mma_ts(tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep + ks * 8, vd + ks * (2048 >> 4), kPv, true);
+                if (release) commit(&ctl.empty[slot]);
                 commit(&ctl.pv_done[t]);  // last: the row threads wait for it before the CTA ends
-            };
-            auto weights_full = [&](uint32_t t) {
-                const bool r = bar_wait(&ctl.p_full[t], p_count[t]++ & 1u, ctl, a.status);
-                fence_after();
-                return r;
-            };
-            while (ok && walk.next(&p)) {
-                ok = bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status);
-                fence_after();
-                const uint32_t n = p.step1 - p.step0;
-                if (p.both) {
-                    // scores of step 0 for both tiles; then, a tile at a time, the values of step i and the scores of step i + 1
-                    if (ok) ok = slot_full(seq);
-                    if (ok) {
-                        scores(0, seq, true);
-                        scores(1, seq, true);
-                        commit(&ctl.empty[seq % Sh::kSlots]);
-                    }
-                    for (uint32_t i = 0; i < n && ok; ++i) {
-                        const uint32_t vq = seq + 2 * i + 1, kq = vq + 1;
-                        ok = slot_full(vq);
-                        for (uint32_t t = 0; t < 2 && ok; ++t) {
-                            ok = weights_full(t);
-                            if (!ok) break;
-                            values(t, vq, i == 0, t == 1);
-                            if (i + 1 < n) {
-                                if (t == 0) ok = slot_full(kq);
-                                if (!ok) break;
-                                scores(t, kq, true);
-                                if (t == 1) commit(&ctl.empty[kq % Sh::kSlots]);
-                            }
-                        }
-                    }
-                } else {
-                    // steps alternate between the tiles; the scores run one step ahead of the values
-                    if (ok) ok = slot_full(seq);
-                    if (ok) {
-                        scores(0, seq, false);
-                        commit(&ctl.empty[seq % Sh::kSlots]);
-                    }
-                    for (uint32_t i = 0; i < n && ok; ++i) {
-                        const uint32_t t = i & 1, vq = seq + 2 * i + 1, kq = vq + 1;
-                        // step i + 1's scores go to the other tile, whose step i - 1 has been read (its weights were full)
-                        if (i + 1 < n) {
-                            ok = slot_full(kq);
-                            if (!ok) break;
-                            scores(t ^ 1, kq, false);
-                            commit(&ctl.empty[kq % Sh::kSlots]);
-                        }
-                        ok = slot_full(vq) && weights_full(t);
+            }
+            __syncwarp();
+        };
+        auto weights_full = [&](uint32_t t) {
+            const bool r = uniform(bar_wait(&ctl.p_full[t], p_count[t]++ & 1u, ctl, a.status));
+            fence_after();
+            return r;
+        };
+        while (ok && walk.next(&p)) {
+            ok = uniform(bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status));
+            fence_after();
+            const uint32_t n = p.step1 - p.step0;
+            if (ok) ok = slot_full(k_slot, k_phase);
+            if (!ok) break;
+            if (p.both) {
+                // scores of step 0 for both tiles; then, a tile at a time, the values of step i and the scores of step i + 1
+                scores(0, k_slot, true, false);
+                scores(1, k_slot, true, true);
+                for (uint32_t i = 0; i < n; ++i) {
+                    step_on(k_slot, k_phase);
+                    const uint32_t v_slot = k_slot;
+                    ok = slot_full(k_slot, k_phase) && weights_full(0);
+                    if (!ok) break;
+                    step_on(k_slot, k_phase);
+                    const bool more = i + 1 < n;
+                    values(0, v_slot, i == 0, false);
+                    if (more) {
+                        ok = slot_full(k_slot, k_phase);
                         if (!ok) break;
-                        values(t, vq, i < 2, true);
+                        scores(0, k_slot, true, false);
                     }
+                    ok = weights_full(1);
+                    if (!ok) break;
+                    values(1, v_slot, i == 0, true);
+                    if (more) scores(1, k_slot, true, true);
                 }
-                seq += 2 * n;
+            } else {
+                // steps alternate between the tiles; the scores run one step ahead of the values
+                scores(0, k_slot, false, true);
+                for (uint32_t i = 0; i < n; ++i) {
+                    const uint32_t t = i & 1;
+                    step_on(k_slot, k_phase);
+                    const uint32_t v_slot = k_slot, v_phase = k_phase;
+                    step_on(k_slot, k_phase);
+                    // step i + 1's scores go to the other tile, whose step i - 1 has been read (its weights were full)
+                    if (i + 1 < n) {
+                        ok = slot_full(k_slot, k_phase);
+                        if (!ok) break;
+                        scores(t ^ 1, k_slot, false, true);
+                    }
+                    ok = slot_full(v_slot, v_phase) && weights_full(t);
+                    if (!ok) break;
+                    values(t, v_slot, i < 2, true);
+                }
             }
-            if (!ok) {  // products in flight finish before the tensor memory is freed
-                commit(&ctl.drain);
-                if (!bar_drain(&ctl.drain, 0)) raise(a.status, AFX_DEV_UNDRAINED);
-            }
+        }
+        if (!ok && leader) {  // products in flight finish before the tensor memory is freed
+            commit(&ctl.drain);
+            if (!bar_drain(&ctl.drain, 0)) raise(a.status, AFX_DEV_UNDRAINED);
         }
         __syncwarp();
       }
@@ -451,33 +472,46 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         bool ok = true;
         while (ok && walk.next(&p)) {
             const TileGroup& g = p.g;
-            // this thread's row of the queries, in the operand's swizzled order
+            // the warp's 32 rows of the queries, in the operand's swizzled order: a lane works out where its
+            // row lies, then 16 bytes a lane of two (or four) rows at a time
+            const uint32_t row = (p.both ? t * kTileRows : 0) + in_tile;
+            const bool live = row < g.rows;
+            const bool warp_live = (p.both ? t * kTileRows : 0) + (warp & 3) * 32 < g.rows;
+            uint32_t token = 0, qh = 0;
+            if (live) {
+                const uint32_t pr = g.row0 + row, tok = pr / a.group;
+                token = g.request < 0 ? packed[tok] : g.token0 + tok;
+                qh = p.h * a.group + (pr - tok * a.group);
+            }
             if (p.both || t == 0) {
-                const uint32_t q_row = (p.both ? t * kTileRows : 0) + in_tile;
-                uint8_t* dst = smem + (p.both ? t * Sh::kSlot : 0) + in_tile * 128;
-                uint4 v[D / 8];
+                constexpr uint32_t kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
+                const uint64_t src = reinterpret_cast<uint64_t>(q + token * a.q_token + qh * a.q_head);
+                const uint32_t c = lane % kChunks, flip2 = flip * 0x10001u;
+                uint8_t* dst = smem + (p.both ? t * Sh::kSlot : 0) + (c / 8) * Sh::kBlock;
+                uint4 v[32 / kRowsAtOnce];  // all loads, then all stores
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
-                if (q_row < g.rows) {
-                    const uint32_t pr = g.row0 + q_row, tok = pr / a.group;
-                    const uint64_t token = g.request < 0 ? packed[tok] : g.token0 + tok;
-                    const T* src = q + token * a.q_token + (p.h * a.group + pr % a.group) * a.q_head;
-                    if (a.q_align == 16) {
+                for (uint32_t i = 0; i < 32 / kRowsAtOnce; ++i) {
+                    const uint32_t r = i * kRowsAtOnce + lane / kChunks;
+                    const uint4* from = reinterpret_cast<const uint4*>(__shfl_sync(0xFFFFFFFFu, src, r)) + c;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if ((p.both ? t * kTileRows : 0) + (warp & 3) * 32 + r < g.rows) {
+                        if (a.q_align == 16) {
+                            v[i] = __ldg(from);
+                        } else {
+                            const uint16_t* e = reinterpret_cast<const uint16_t*>(from);
+                            uint32_t w[4];
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c) v[c] = *reinterpret_cast<const uint4*>(src + c * 8);
-                    } else {
-                        const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
-#pragma unroll
-                        for (int c = 0; c < D / 8; ++c)
-                            v[c] = make_uint4(e[c * 8] | static_cast<uint32_t>(e[c * 8 + 1]) << 16, e[c * 8 + 2] | static_cast<uint32_t>(e[c * 8 + 3]) << 16,
-                                              e[c * 8 + 4] | static_cast<uint32_t>(e[c * 8 + 5]) << 16, e[c * 8 + 6] | static_cast<uint32_t>(e[c * 8 + 7]) << 16);
+                            for (int k = 0; k < 4; ++k) w[k] = __ldg(e + 2 * k) | static_cast<uint32_t>(__ldg(e + 2 * k + 1)) << 16;
+                            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
                     }
                 }
-                const uint32_t f = flip * 0x10001u;
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4*>(dst + (c / 8) * Sh::kBlock + (((c % 8) ^ (in_tile & 7)) * 16)) =
-                        make_uint4(v[c].x ^ f, v[c].y ^ f, v[c].z ^ f, v[c].w ^ f);
+                for (uint32_t i = 0; i < 32 / kRowsAtOnce; ++i) {
+                    const uint32_t tile_row = (warp & 3) * 32 + i * kRowsAtOnce + lane / kChunks;
+                    *reinterpret_cast<uint4*>(dst + tile_row * 128 + (((c % 8) ^ (tile_row & 7)) * 16)) =
+                        make_uint4(v[i].x ^ flip2, v[i].y ^ flip2, v[i].z ^ flip2, v[i].w ^ flip2);
+                }
                 fence_async_shared();
             }
             __syncwarp();
@@ -486,9 +520,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status));
             if (!ok) break;
 
-            const uint32_t row = p.both ? t * kTileRows + in_tile : in_tile;
-            const bool live = row < g.rows;
-            const bool warp_live = (p.both ? t * kTileRows : 0) + (warp & 3) * 32 < g.rows;
             const uint32_t limit = g.request < 0 || !live ? g.own_keys : min(g.own_keys, visible(g.seen, g.row0 + row, a.group));
             const uint32_t all_see = g.request < 0 ? g.own_keys : visible(g.seen, g.row0, a.group);  // own keys every row sees
             float ref = -INFINITY, sum = 0.0f;
@@ -581,59 +612,66 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 uint32_t cta0, cta1;
                 tile_ctas(g, p.h, head.share, &cta0, &cta1);
                 const bool final = g.single && cta0 == cta1 && p.both;
-                const float total = sum;
                 const uint32_t in_piece = p.both ? row : t * (walk.cta == cta0 ? g.rows : kTileRows) + row;
                 const uint64_t pr = tile_part_row(g, p.h, cta0, walk.cta, a.L.extra_row) + in_piece;
-                uint64_t token = 0;
-                uint32_t qh = 0;
-                if (final && live) {
-                    const uint32_t prow = g.row0 + row, tok = prow / a.group;
-                    token = g.request < 0 ? packed[tok] : g.token0 + tok;
-                    qh = p.h * a.group + prow % a.group;
-                }
-                const float inv = total > 0.0f || ref != -INFINITY ? 1.0f / total : 0.0f;
+                const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
+                T* out = static_cast<T*>(a.out) + token * a.out_token + qh * a.out_head;
+                // 32 columns at a time through this warp's 4 KB of the tile's queries (no product reads them any
+                // more, and the warp's next queries go there too), so that rows go out in runs of 128 (64) bytes;
+                // 16-byte chunks swizzled against bank conflicts
+                uint8_t* stage = smem + t * Sh::kSlot + (warp & 3) * 4096;
+                auto chunk = [&](uint32_t r, uint32_t k) { return reinterpret_cast<uint4*>(stage + r * 128 + ((k ^ (r & 7)) * 16)); };
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (uint32_t c = 0; done > 0 && c < D / 32; ++c) {
                     uint32_t o[32];
-                    if (done > 0) {
-                        tmem_load32(o_col + c * 32, o);
-                        tmem_wait_load();
-                    }
-                    if (live && done > 0 && final) {
-                        T* out = static_cast<T*>(a.out) + token * a.out_token + qh * a.out_head + c * 32;
-                        const bool wide = !(reinterpret_cast<uintptr_t>(out) & 15u);
+                    tmem_load32(o_col + c * 32, o);
+                    tmem_wait_load();
+                    __syncwarp();
+                    if (final) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint32_t w[4];
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = ref == -INFINITY ? 0u : Elem<T>::pack(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = ref == -INFINITY ? 0u
-                                                        : Elem<T>::pack(__uint_as_float(o[j + 2 * k]) * inv, __uint_as_float(o[j + 2 * k + 1]) * inv);
-                            if (wide) {
-                                *reinterpret_cast<uint4*>(out + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                            } else {
+                        for (int j = 0; j < 4; ++j)
+                            *chunk(lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                        __syncwarp();
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    reinterpret_cast<uint16_t*>(out)[j + 2 * k] = static_cast<uint16_t>(w[k]);
-                                    reinterpret_cast<uint16_t*>(out)[j + 2 * k + 1] = static_cast<uint16_t>(w[k] >> 16);
+                        for (uint32_t i = 0; i < 4; ++i) {
+                            const uint32_t r = i * 8 + lane / 4;
+                            T* to = reinterpret_cast<T*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(out), r)) + c * 32 + (lane % 4) * 8;
+                            const uint4 v = *chunk(r, lane % 4);
+                            if ((p.both ? t * kTileRows : 0) + (warp & 3) * 32 + r < g.rows) {
+                                if (reinterpret_cast<uintptr_t>(to) & 15u) {
+                                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k) reinterpret_cast<uint16_t*>(to)[k] = static_cast<uint16_t>(x[k / 2] >> (16 * (k & 1)));
+                                } else {
+                                    *reinterpret_cast<uint4*>(to) = v;
                                 }
                             }
                         }
-                    } else if (live && done > 0) {
-                        float4* dst = reinterpret_cast<float4*>(part_o + pr * D + c * 32);
+                    } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
-                                                 __uint_as_float(o[4 * j + 3]));
+                            *chunk(lane, j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        __syncwarp();
+                        const uint64_t pr0 = __shfl_sync(0xFFFFFFFFu, pr, 0);  // the warp's rows follow one another
+#pragma unroll
+                        for (uint32_t i = 0; i < 8; ++i) {
+                            const uint32_t r = i * 4 + lane / 8;
+                            const uint4 v = *chunk(r, lane % 8);
+                            if ((p.both ? t * kTileRows : 0) + (warp & 3) * 32 + r < g.rows)
+                                *reinterpret_cast<uint4*>(part_o + (pr0 + r) * D + c * 32 + (lane % 8) * 4) = v;
+                        }
                     }
-                    __syncwarp();
                 }
                 if (live) {
                     if (!final)
-                        part_ml[pr] = make_float2(ref, total);
+                        part_ml[pr] = make_float2(ref, sum);
                     else if (a.lse)
                         a.lse[token * (static_cast<uint64_t>(a.kv_heads) * a.group) + qh] =
-                            ref == -INFINITY ? -INFINITY : (ref + log2f(total)) * kLn2;
+                            ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * kLn2;
                 }
             }
             fence_before();  // O has been read before the next piece's products, which wait for this tile's weights
