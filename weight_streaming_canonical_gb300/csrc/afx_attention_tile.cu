@@ -20,8 +20,8 @@
 //
 // Roles of a CTA's 12 warps: 0-3 and 4-7 the rows of tile 0 and 1 (a row's
 // 128 scores stay in its thread's registers: these warps take registers from
-// the others), 8 issues the products, 9 loads keys and values, 10 and 11 only
-// make up a warpgroup: each page of a step by TMA (64
+// the others), 8 issues the products, 9 loads keys and 10 values, 11 only
+// makes up a warpgroup: each page of a step by TMA (64
 // elements x the page's tokens a box, 128-byte swizzle), into a ring of
 // slots that runs ahead over groups.  Tensor memory: S0 S1 O0 O1; P replaces S
 // in place for heads of 128, and has columns of its own for heads of 64.
@@ -39,13 +39,14 @@ namespace serve {
 namespace {
 
 constexpr int kSoftWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;  // keys; values: the warp after it
 constexpr int kTileThreads = 384;
 // registers a thread: as launched, then of the row warps and of the others
 // (what the row warps add is what the others gave up)
 constexpr int kRegsLaunch = 168, kRegsRows = 208, kRegsOther = 88;
 static_assert(256 * kRegsRows + 128 * kRegsOther <= kTileThreads * kRegsLaunch, "register shares");
 constexpr uint32_t kWaitPolls = 1u << 22;
+constexpr float kHigh = 14.0f;  // weights stay below 2^14: FP16 holds them, and their sums are far from float32's end
 
 template <int D>
 struct Shape {
@@ -65,7 +66,7 @@ struct Ctl {
     uint64_t full[8], empty[8];
     uint64_t tail;                     // a last step's values, before their missing rows are zeroed
     uint64_t q_full;
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2], p_full[2][2], pv_done[2];
     uint64_t drain;
     uint32_t tmem;
     int32_t abort_flag;
@@ -151,6 +152,24 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_addr(bar)) : "memory");
 }
 
+// Two float32 operations an instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float* lo, float* hi) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(*lo), "=f"(*hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect() {
     uint32_t r;
@@ -176,11 +195,6 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
         "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
         AFX_W8(v, 0), AFX_W8(v, 8), AFX_W8(v, 16), AFX_W8(v, 24)
         : "memory");
-}
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(addr),
-                 AFX_W8(v, 0), AFX_W8(v, 8)
-                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
@@ -268,7 +282,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         bar_init(&ctl.q_full, kSoftWarps);
         for (int t = 0; t < 2; ++t) {
             bar_init(&ctl.s_full[t], 1);
-            bar_init(&ctl.p_full[t], kSoftWarps / 2);
+            bar_init(&ctl.p_full[t][0], kSoftWarps / 2);
+            bar_init(&ctl.p_full[t][1], kSoftWarps / 2);
             bar_init(&ctl.pv_done[t], 1);
         }
         bar_init(&ctl.drain, 1);
@@ -287,10 +302,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
     Walk::Piece p;
     if (warp >= kSoftWarps) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsOther));
-      if (warp == kLoadWarp) {
-        // ---- keys and values: slot 2 i of the sequence is step i's keys, 2 i + 1 its values
+      if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+        // ---- keys and values: slot 2 i of the sequence is step i's keys, 2 i + 1 its values.  A lane a page looks
+        // the page up; one lane issues all copies, from values that are the same in the whole warp (a copy from each
+        // lane on its own took 180 cycles a copy, one after the other)
+        const uint32_t kv = warp - kLoadWarp;
+        const CUtensorMap* map = kv ? &args.v : &args.k;
         const uint32_t box = min(1u << a.shift, kTileKeys), page_mask = (1u << a.shift) - 1;
-        uint32_t seq = 0, tails = 0;
+        const bool leader = elect();
+        uint32_t slot = kv, phase = 0, seq = kv, tails = 0;
         bool ok = true;
         while (ok && walk.next(&p)) {
             for (uint32_t s = p.step0; s < p.step1 && ok; ++s) {
@@ -298,53 +318,60 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 uint32_t first, n;
                 step_keys(p, s, &prefix, &first, &n);
                 const uint32_t used = ceil_div(n, box);  // boxes that hold keys of this step
-                const uint32_t key = first + lane * box;
                 uint32_t page = 0;
                 if (static_cast<uint32_t>(lane) < used) {
-                    const int32_t id = prefix ? a.prefix_table[key >> a.shift]
-                                              : a.table[static_cast<uint64_t>(p.g.request) * a.table_cols + (key >> a.shift)];
+                    const uint32_t col = (first + lane * box) >> a.shift;
+                    const int32_t id = prefix ? __ldg(a.prefix_table + col) : __ldg(a.table + static_cast<uint64_t>(p.g.request) * a.table_cols + col);
                     if (id < 0 || static_cast<uint32_t>(id) >= a.n_pages)
                         raise(a.status, AFX_DEV_BAD_PAGE);
                     else
                         page = id;
                 }
-                uint32_t at[3];
-#pragma unroll
-                for (uint32_t i = 0; i < 3; ++i) at[i] = i == args.token_at ? key & page_mask : i == args.head_at ? p.h : page;
-                for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
-                    const uint32_t slot = seq % Sh::kSlots;
-                    if (seq >= Sh::kSlots) ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.empty[slot], (seq / Sh::kSlots - 1) & 1u, ctl, a.status));
+                if (seq >= Sh::kSlots) {
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.empty[slot], phase ^ 1u, ctl, a.status));
                     if (!ok) break;
-                    // a last step's values: rows past the keys must be zeros, whatever the page holds there (0 * NaN)
-                    const bool patch = kv == 1 && n < kTileKeys;
-                    uint64_t* bar = patch ? &ctl.tail : &ctl.full[slot];
-                    const uint32_t dst = smem_addr(smem + Sh::kQ + slot * Sh::kSlot);
-                    if (lane == 0) bar_expect(bar, used * box * 128 * Sh::kHalves);
-                    __syncwarp();
-                    if (static_cast<uint32_t>(lane) < used)
+                }
+                // a last step's values: rows past the keys must be zeros, whatever the page holds there (0 * NaN)
+                const bool patch = kv == 1 && n < kTileKeys;
+                uint64_t* bar = patch ? &ctl.tail : &ctl.full[slot];
+                const uint32_t dst = smem_addr(smem + Sh::kQ) + slot * Sh::kSlot;
+                if (leader) bar_expect(bar, used * box * 128 * Sh::kHalves);
+                for (uint32_t b = 0; b < used; ++b) {
+                    const uint32_t id = __shfl_sync(0xFFFFFFFFu, page, b), token = first & page_mask;  // 0 but for pages of 256
+                    const uint32_t c1 = args.token_at == 0 ? token : args.head_at == 0 ? p.h : id, c2 = args.token_at == 1 ? token : args.head_at == 1 ? p.h : id,
+                                   c3 = args.token_at == 2 ? token : args.head_at == 2 ? p.h : id;
+                    if (leader) {
 #pragma unroll
-                        for (uint32_t hf = 0; hf < Sh::kHalves; ++hf)
-                            load_box(dst + hf * Sh::kBlock + lane * box * 128, kv ? &args.v : &args.k, hf * 64, at[0], at[1], at[2], bar);
-                    if (patch) {
-                        ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.tail, tails & 1u, ctl, a.status));
-                        if (!ok) {
-                            if (!bar_drain(&ctl.tail, tails & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
-                            break;
-                        }
-                        ++tails;
-                        uint8_t* v = smem + Sh::kQ + slot * Sh::kSlot;
-                        for (uint32_t hf = 0; hf < Sh::kHalves; ++hf)
-                            for (uint32_t i = n * 8 + lane; i < kTileKeys * 8; i += 32)
-                                *reinterpret_cast<uint4*>(v + hf * Sh::kBlock + i * 16) = make_uint4(0, 0, 0, 0);
-                        fence_async_shared();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(&ctl.full[slot]);
+                        for (uint32_t hf = 0; hf < Sh::kHalves; ++hf) load_box(dst + hf * Sh::kBlock + b * box * 128, map, hf * 64, c1, c2, c3, bar);
                     }
+                }
+                __syncwarp();
+                if (patch) {
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.tail, tails & 1u, ctl, a.status));
+                    if (!ok) {
+                        if (!bar_drain(&ctl.tail, tails & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
+                        break;
+                    }
+                    ++tails;
+                    uint8_t* v = smem + Sh::kQ + slot * Sh::kSlot;
+                    for (uint32_t hf = 0; hf < Sh::kHalves; ++hf)
+                        for (uint32_t i = n * 8 + lane; i < kTileKeys * 8; i += 32)
+                            *reinterpret_cast<uint4*>(v + hf * Sh::kBlock + i * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (leader) bar_arrive(&ctl.full[slot]);
+                }
+                seq += 2;
+                slot += 2;
+                if (slot >= Sh::kSlots) {
+                    slot -= Sh::kSlots;
+                    phase ^= 1u;
                 }
             }
         }
-        if (!ok) {  // copies in flight land before the CTA ends
-            for (uint32_t q = seq > Sh::kSlots ? seq - Sh::kSlots : 0; q < seq; ++q)
+        if (!ok) {  // this warp's copies in flight land before the CTA ends
+            uint32_t q = seq > Sh::kSlots ? seq - Sh::kSlots : 0;
+            for (q += (q & 1u) != kv; q < seq; q += 2)
                 if (!bar_drain(&ctl.full[q % Sh::kSlots], (q / Sh::kSlots) & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
         }
       } else if (warp == kMmaWarp) {
@@ -384,22 +411,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             }
             __syncwarp();
         };
+        // the weights come in two halves of 64 keys; false: a wait gave up
         auto values = [&](uint32_t t, uint32_t slot, bool first, bool release) {
             const uint64_t vd = v_desc + slot * (Sh::kSlot >> 4);
-            if (leader) {
-                mma_ts(tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep, vd, kPv, !first);
+            const uint32_t phase = p_count[t]++ & 1u;
 #pragma unroll
-                for (uint32_t ks = 1; ks < kTileKeys / 16; ++ks)
-                    mma_ts(tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep + ks * 8, vd + ks * (2048 >> 4), kPv, true);
-                if (release) commit(&ctl.empty[slot]);
-                commit(&ctl.pv_done[t]);  // last: the row threads wait for it before the CTA ends
+            for (uint32_t half = 0; half < 2; ++half) {
+                if (!uniform(bar_wait(&ctl.p_full[t][half], phase, ctl, a.status))) return false;
+                fence_after();
+                if (leader) {
+#pragma unroll
+                    for (uint32_t ks = half * 4; ks < half * 4 + 4; ++ks)
+                        mma_ts(tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep + ks * 8, vd + ks * (2048 >> 4), kPv, !first || ks != 0);
+                    if (half) {
+                        if (release) commit(&ctl.empty[slot]);
+                        commit(&ctl.pv_done[t]);  // last: the row threads wait for it before the CTA ends
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
-        };
-        auto weights_full = [&](uint32_t t) {
-            const bool r = uniform(bar_wait(&ctl.p_full[t], p_count[t]++ & 1u, ctl, a.status));
-            fence_after();
-            return r;
+            return true;
         };
         while (ok && walk.next(&p)) {
             ok = uniform(bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status));
@@ -411,28 +442,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 // scores of step 0 for both tiles; then, a tile at a time, the values of step i and the scores of step i + 1
                 scores(0, k_slot, true, false);
                 scores(1, k_slot, true, true);
-                for (uint32_t i = 0; i < n; ++i) {
+                for (uint32_t i = 0; i < n && ok; ++i) {
                     step_on(k_slot, k_phase);
                     const uint32_t v_slot = k_slot;
-                    ok = slot_full(k_slot, k_phase) && weights_full(0);
-                    if (!ok) break;
+                    ok = slot_full(k_slot, k_phase);
                     step_on(k_slot, k_phase);
                     const bool more = i + 1 < n;
-                    values(0, v_slot, i == 0, false);
-                    if (more) {
-                        ok = slot_full(k_slot, k_phase);
-                        if (!ok) break;
-                        scores(0, k_slot, true, false);
+                    if (more) ok = ok && slot_full(k_slot, k_phase);
+                    if (!ok || !values(0, v_slot, i == 0, false)) {
+                        ok = false;
+                        break;
                     }
-                    ok = weights_full(1);
-                    if (!ok) break;
-                    values(1, v_slot, i == 0, true);
-                    if (more) scores(1, k_slot, true, true);
+                    if (more) scores(0, k_slot, true, false);
+                    ok = values(1, v_slot, i == 0, true);
+                    if (ok && more) scores(1, k_slot, true, true);
                 }
             } else {
                 // steps alternate between the tiles; the scores run one step ahead of the values
                 scores(0, k_slot, false, true);
-                for (uint32_t i = 0; i < n; ++i) {
+                for (uint32_t i = 0; i < n && ok; ++i) {
                     const uint32_t t = i & 1;
                     step_on(k_slot, k_phase);
                     const uint32_t v_slot = k_slot, v_phase = k_phase;
@@ -443,9 +471,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                         if (!ok) break;
                         scores(t ^ 1, k_slot, false, true);
                     }
-                    ok = slot_full(v_slot, v_phase) && weights_full(t);
-                    if (!ok) break;
-                    values(t, v_slot, i < 2, true);
+                    ok = slot_full(v_slot, v_phase) && values(t, v_slot, i < 2, true);
                 }
             }
         }
@@ -522,9 +548,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
 
             const uint32_t limit = g.request < 0 || !live ? g.own_keys : min(g.own_keys, visible(g.seen, g.row0 + row, a.group));
             const uint32_t all_see = g.request < 0 ? g.own_keys : visible(g.seen, g.row0, a.group);  // own keys every row sees
-            float ref = -INFINITY, sum = 0.0f;
+            float ref = -INFINITY, sum = 0.0f, seen_most = -INFINITY;
             const uint32_t first = p.step0 + (p.both ? 0 : t), stride = p.both ? 1 : 2;
             uint32_t done = 0;  // steps of this tile
+            // a new reference: the sums so far are scaled to it (the scores' barrier of this step says that the
+            // product with the last step's weights is done too)
+            auto rebase = [&](float most) {
+                const float next = most > ref + kLag ? most : ref;
+                const float f = next == -INFINITY ? 1.0f : exp2_approx(ref - next);
+                ref = next;
+                sum *= f;
+                if (done > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_load32(o_col + c * 32, o);
+                        tmem_wait_load();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_store32(o_col + c * 32, o);
+                    }
+                }
+            };
             for (uint32_t s = first; s < p.step1 && ok; s += stride, ++done) {
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.s_full[t], s_count++ & 1u, ctl, a.status));
                 if (!ok) break;
@@ -536,70 +581,80 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     const uint32_t sees = prefix ? n : (limit > key ? min(n, limit - key) : 0u);
                     const bool whole = n == kTileKeys && (prefix || key + kTileKeys <= all_see);
                     uint32_t x[kTileKeys];
+                    auto mask = [&](uint32_t half) {
+                        if (whole) return;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_load32(s_col + c * 32, x + c * 32);
+                        for (uint32_t j = 0; j < 64; ++j)
+                            if (half * 64 + j >= sees) x[half * 64 + j] = 0xFF800000u;  // -inf
+                    };
+                    auto half_most = [&](uint32_t half) {
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (uint32_t j = 0; j < 64; j += 2)
+                            top[(j / 2) & 3] = fmaxf(top[(j / 2) & 3], fmaxf(__uint_as_float(x[half * 64 + j]), __uint_as_float(x[half * 64 + j + 1])));
+                        return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+                    };
+                    uint64_t add[2];
+                    uint32_t w[32];
+                    auto weigh = [&](const uint32_t* from) {
+                        const uint64_t factor = pack2(scale, scale), base = ref == -INFINITY ? 0 : pack2(-ref, -ref);
+                        add[0] = add[1] = 0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            float e0, e1;
+                            unpack2(fma2(pack2(__uint_as_float(from[2 * j]), __uint_as_float(from[2 * j + 1])), factor, base), &e0, &e1);
+                            e0 = exp2_approx(e0);
+                            e1 = exp2_approx(e1);
+                            add[j & 1] = add2(add[j & 1], pack2(e0, e1));
+                            w[j] = Elem<T>::pack(e0, e1);  // rounded to the cache's type for the product with V; the sum keeps all bits
+                        }
+                    };
+                    auto publish = [&](uint32_t half) {
+                        tmem_store32(p_col + half * 32, w);
+                        tmem_wait_store();
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&ctl.p_full[t][half]);
+                    };
+                    auto added = [&]() {
+                        float s0, s1;
+                        unpack2(add2(add[0], add[1]), &s0, &s1);
+                        return s0 + s1;
+                    };
+                    // The weights of the first half with the reference as it stands, while the second half is on its
+                    // way; the maximum of the step is the next step's reference.  Only where it would lift a weight
+                    // past 2^kHigh is the reference moved first and the half done again.
+                    tmem_load32(s_col, x);
+                    tmem_load32(s_col + 32, x + 32);
                     tmem_wait_load();
-                    if (!whole) {
-#pragma unroll
-                        for (uint32_t j = 0; j < kTileKeys; ++j)
-                            if (j >= sees) x[j] = 0xFF800000u;  // -inf
+                    if (done > 0 && __any_sync(0xFFFFFFFFu, seen_most > ref + kLag)) rebase(seen_most);
+                    tmem_load32(s_col + 64, x + 64);
+                    tmem_load32(s_col + 96, x + 96);
+                    mask(0);
+                    float most = half_most(0);
+                    if (done == 0) ref = most;
+                    weigh(x);
+                    tmem_wait_load();
+                    mask(1);
+                    most = fmaxf(most, half_most(1));
+                    if (__any_sync(0xFFFFFFFFu, most > ref + kHigh)) {
+                        rebase(most);
+                        weigh(x);
                     }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (uint32_t j = 0; j < kTileKeys; j += 8)
-#pragma unroll
-                        for (uint32_t k = 0; k < 4; ++k)
-                            top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1])));
-                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
-                    const bool rise = most > ref + kLag;
-                    if (__any_sync(0xFFFFFFFFu, rise)) {
-                        const float next = rise ? most : ref;
-                        const float f = next == -INFINITY ? 1.0f : exp2_approx(ref - next);
-                        ref = next;
-                        sum *= f;
-                        if (done > 0) {  // scale O, once the last product into it is done
-                            ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.pv_done[t], (pv_count + done - 1) & 1u, ctl, a.status));
-                            if (!ok) break;
-                            fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_load32(o_col + c * 32, o);
-                                tmem_wait_load();
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_store32(o_col + c * 32, o);
-                            }
-                        }
+                    seen_most = most;
+                    publish(0);
+                    sum += added();
+                    weigh(x + 64);
+                    publish(1);
+                    sum += added();
+                } else {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(&ctl.p_full[t][0]);
+                        bar_arrive(&ctl.p_full[t][1]);
                     }
-                    if (D != 128 && done > 0) {
-                        // weights have columns of their own: the product that read them must be done
-                        ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.pv_done[t], (pv_count + done - 1) & 1u, ctl, a.status));
-                        if (!ok) break;
-                        fence_after();
-                    }
-                    const float base = ref == -INFINITY ? 0.0f : ref;
-                    float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float e0 = exp2_approx(fmaf(__uint_as_float(x[c * 32 + 2 * j]), scale, -base));
-                            const float e1 = exp2_approx(fmaf(__uint_as_float(x[c * 32 + 2 * j + 1]), scale, -base));
-                            add[(2 * j) & 3] += e0;
-                            add[(2 * j + 1) & 3] += e1;
-                            // rounded to the cache's type for the product with V; the sum keeps all bits
-                            w[j] = Elem<T>::pack(e0, e1);
-                        }
-                        tmem_store16(p_col + c * 16, w);
-                    }
-                    sum += (add[0] + add[1]) + (add[2] + add[3]);
-                    tmem_wait_store();
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&ctl.p_full[t]);
             }
             if (!ok) break;
             if (done > 0) {
