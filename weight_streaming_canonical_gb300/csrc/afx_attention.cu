@@ -41,6 +41,10 @@ constexpr uint32_t kMinKeys = 256;     // keys of a 16-row item, at least, where
 constexpr uint32_t kTargetUnits = 1216;  // 16-row items x heads that the cuts aim at
 constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's tiles take the prefix along
 constexpr uint32_t kMinShare = 8;      // cost of a tile CTA, at least
+constexpr uint32_t kFewTokens = 8, kManyMax = 512;
+// token_packed of tokens that do not share the prefix's tiles: in tiles of
+// their request's own, or (no prefix) in 16-row items
+constexpr uint32_t kInTiles = 0xFFFFFFFEu, kAlone = 0xFFFFFFFFu;
 
 __host__ __device__ inline uint64_t up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 
@@ -123,6 +127,9 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     const uint32_t r0 = min(R, threadIdx.x * per), r1 = min(R, r0 + per);
     const uint64_t max_len = static_cast<uint64_t>(a.table_cols) << a.shift;
 
+    __shared__ uint32_t n_many;
+    __shared__ uint2 many[kManyMax];  // requests of more than a few tokens, and their tokens' mark
+    if (threadIdx.x == 0) n_many = 0;
     // the lengths have to make sense before anything is addressed by them
     bool bad = false;
     Counts<2> first{};  // keys of the 16-row groups, tokens that share tiles on the prefix
@@ -183,6 +190,11 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         rows_p = (static_cast<uint64_t>(tiles_p - 1) * kGroupRows + (last > kTileRows ? last : 2 * last)) * a.kv_heads;
     }
 
+    auto write_token = [&](uint32_t r, uint32_t t, uint32_t mark, uint32_t i) {
+        token_request[t] = static_cast<int32_t>(r);
+        token_packed[t] = mark >= kInTiles ? mark : mark + i;
+        if (mark < kInTiles) packed_token[mark + i] = static_cast<int32_t>(t);
+    };
     // the requests' own keys
     auto walk = [&](uint32_t r, auto&& row16, auto&& tile) {
         const uint32_t s = a.starts[r], n = a.starts[r + 1] - s, rows = n * G;
@@ -237,11 +249,23 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
                 cost += static_cast<uint64_t>(c) * a.kv_heads;
                 trow += static_cast<uint64_t>(m > kTileRows ? m : 2 * m) * a.kv_heads;
             });
-        for (uint32_t t = s; t < e; ++t) {
-            token_request[t] = static_cast<int32_t>(r);
-            token_packed[t] = k.fused ? UINT32_MAX : packed;
-            if (!k.fused) packed_token[packed++] = static_cast<int32_t>(t);
+        // its tokens: a few here, more by a warp below
+        const uint32_t mark = k.fused ? (k.own == kTile ? kInTiles : kAlone) : packed;
+        if (e - s <= kFewTokens) {
+            for (uint32_t t = s; t < e; ++t) write_token(r, t, mark, t - s);
+        } else {
+            const uint32_t i = atomicAdd(&n_many, 1u);
+            if (i < kManyMax)
+                many[i] = make_uint2(r, mark);
+            else
+                for (uint32_t t = s; t < e; ++t) write_token(r, t, mark, t - s);
         }
+        if (!k.fused) packed += e - s;
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x / 32; i < min(n_many, kManyMax); i += threads / 32) {
+        const uint32_t r = many[i].x, s = a.starts[r], e = a.starts[r + 1];
+        for (uint32_t t = s + threadIdx.x % 32; t < e; t += 32) write_token(r, t, many[i].y, t - s);
     }
     if (threadIdx.x == 0) {
         const uint64_t c = total.v[4] + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
@@ -514,7 +538,7 @@ struct Pieces {
 };
 
 __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& head, uint32_t kind, uint32_t first_group, uint32_t row,
-                                            uint32_t h, bool* final) {
+                                            uint32_t h) {
     Pieces p{};
     if (kind == kRow16) {
         const Row16Group g = a.at<Row16Group>(a.L.groups16)[first_group + row / kRows];
@@ -527,7 +551,6 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& h
             uint32_t c0, c1;
             tile_ctas(g, h, head.share, &c0, &c1);
             p.two = g.rows <= kTileRows;
-            *final = g.single && c0 == c1 && !p.two;
             p.n_tile = (c1 - c0 + 1) * (p.two ? 2 : 1);
             p.group_rows = g.rows;
             p.in = row % kGroupRows;
@@ -540,11 +563,110 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& h
 
 constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
-// Rows base .. base + span - 1 of the output a warp; kSplit: one row a CTA, whose
-// warps share its pieces (few rows, each of many pieces).  Pieces are added
-// in a fixed order.
+// A lane's elements of an output row, in one store where its address allows.
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* out, const float (&v)[N]) {
+    if (reinterpret_cast<uintptr_t>(out) & (N * 2 - 1)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) out[j] = Elem<T>::from(v[j]);
+    } else if constexpr (N == 4) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]));
+    } else {
+        *reinterpret_cast<uint32_t*>(out) = Elem<T>::pack(v[0], v[1]);
+    }
+}
+
+// Rows in tiles of their request's own: mostly the tile kernel has written
+// the output; where a CTA's share ended within a group's head, or the group's two
+// tiles took steps in turn, its pieces are put together here, a warp 8 rows.
+template <typename T, int D>
+__device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t block, uint32_t blocks) {
+    constexpr int kPer = D / 32;
+    const int lane = threadIdx.x & 31;
+    const uint32_t q_heads = a.kv_heads * a.group;
+    const float* part_o = a.at<float>(a.L.part_o);
+    const float2* part_ml = a.at<float2>(a.L.part_ml);
+    constexpr uint32_t kUnit = 8, kAtOnce = 4;  // rows of a warp, pieces it takes at a time: lane = 8 piece + row
+    const uint64_t units = static_cast<uint64_t>(head.n_tiles) * a.kv_heads * (kGroupRows / kUnit);
+    for (uint64_t u = static_cast<uint64_t>(block) * kJoinWarps + (threadIdx.x >> 5); u < units;
+         u += static_cast<uint64_t>(blocks) * kJoinWarps) {
+        const uint32_t row0 = static_cast<uint32_t>(u % (kGroupRows / kUnit)) * kUnit;
+        const uint64_t gh = u / (kGroupRows / kUnit);
+        const TileGroup& g = a.at<TileGroup>(a.L.tiles)[gh / a.kv_heads];
+        const uint32_t h = static_cast<uint32_t>(gh % a.kv_heads), rows = g.rows;
+        if (!g.single || row0 >= rows) continue;
+        uint32_t c0 = 0, c1 = 0;
+        const bool two = rows <= kTileRows, keys = g.cost != 0;
+        if (keys) tile_ctas(g, h, head.share, &c0, &c1);
+        if (keys && c0 == c1 && !two) continue;
+        const uint32_t lanes = two ? 2 : 1, n = keys ? (c1 - c0 + 1) * lanes : 0;
+        const uint32_t slot = lane / kUnit, mine = min(row0 + lane % kUnit, rows - 1);
+        float top = -INFINITY, sum = 0.0f, acc[kUnit][kPer] = {};
+        for (uint32_t base = 0; base < n; base += kAtOnce) {
+            const uint32_t p = min(base + slot, n - 1), c = c0 + p / lanes;
+            const uint64_t row = tile_part_row(g, h, c0, c, a.L.extra_row) + (p % lanes) * (c == c0 ? rows : kTileRows) + mine;
+            const float2 ml = base + slot < n ? part_ml[row] : make_float2(-INFINITY, 0.0f);
+            float most = fmaxf(top, ml.x);
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
+            const float ref = most == -INFINITY ? 0.0f : most, keep = exp2_approx(top - ref), f = exp2_approx(ml.x - ref);
+            top = most;
+            float part = f * ml.y;
+            part += __shfl_xor_sync(0xFFFFFFFFu, part, 8);
+            part += __shfl_xor_sync(0xFFFFFFFFu, part, 16);
+            sum = sum * keep + part;
+            const uint32_t real = __ballot_sync(0xFFFFFFFFu, ml.x != -INFINITY);  // of the others the sums may never have been written
+#pragma unroll
+            for (uint32_t r = 0; r < kUnit; ++r) {
+                const float k = __shfl_sync(0xFFFFFFFFu, keep, r);
+                float v[kAtOnce][kPer] = {};
+#pragma unroll
+                for (uint32_t q = 0; q < kAtOnce; ++q) {
+                    const uint64_t at = __shfl_sync(0xFFFFFFFFu, row, q * kUnit + r);
+                    if (real >> (q * kUnit + r) & 1) {
+                        if constexpr (kPer == 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(part_o + at * D + lane * 4);
+                            v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
+                        } else {
+                            const float2 x = *reinterpret_cast<const float2*>(part_o + at * D + lane * 2);
+                            v[q][0] = x.x, v[q][1] = x.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) acc[r][j] *= k;
+#pragma unroll
+                for (uint32_t q = 0; q < kAtOnce; ++q) {
+                    const float fr = __shfl_sync(0xFFFFFFFFu, f, q * kUnit + r);
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) acc[r][j] += fr * v[q][j];
+                }
+            }
+        }
+        const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
+        const uint32_t pr = g.row0 + mine, tok = pr / a.group, token = g.token0 + tok, qh = h * a.group + (pr - tok * a.group);
+        if (a.lse && lane < static_cast<int>(kUnit) && row0 + lane < rows)
+            a.lse[static_cast<uint64_t>(token) * q_heads + qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+        const uint64_t dst = token * a.out_token + qh * a.out_head;
+#pragma unroll
+        for (uint32_t r = 0; r < kUnit; ++r) {
+            const float scale = __shfl_sync(0xFFFFFFFFu, inv, r);
+            const uint64_t to = __shfl_sync(0xFFFFFFFFu, dst, r);
+            if (row0 + r < rows) {
+                float o[kPer];
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) o[j] = acc[r][j] * scale;
+                store_row<T, kPer>(static_cast<T*>(a.out) + to + lane * kPer, o);
+            }
+        }
+    }
+}
+
+// The first row_blocks CTAs: rows base .. base + span - 1 of the output a warp;
+// kSplit: one row a CTA, whose warps share its pieces (few rows, each of many
+// pieces).  The others: join_tiles.  Pieces are added in a fixed order.
 template <typename T, int D, bool kSplit>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, uint32_t span) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, uint32_t span, uint32_t row_blocks) {
     constexpr int kPer = D / 32;
     __shared__ float sh_acc[kSplit ? kJoinWarps : 1][D];
     __shared__ float2 sh_ml[kJoinWarps];
@@ -552,13 +674,17 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     const uint32_t q_heads = a.kv_heads * a.group;
     const uint64_t base = kSplit ? blockIdx.x : (static_cast<uint64_t>(blockIdx.x) * kJoinWarps + warp) * span;
     const PlanHead head = *a.at<PlanHead>(0);
-    const uint64_t n_rows = head.key == a.plan_key ? static_cast<uint64_t>(head.n_tokens) * q_heads : 0;
+    if (head.key != a.plan_key) return;
+    if (blockIdx.x >= row_blocks) {
+        join_tiles<T, D>(a, head, blockIdx.x - row_blocks, gridDim.x - row_blocks);
+        return;
+    }
+    const uint64_t n_rows = static_cast<uint64_t>(head.n_tokens) * q_heads;
     if (base >= n_rows) return;
 
     struct Sources {
         Pieces pre, own;
         uint32_t t, qh;
-        bool final;  // the tile kernel wrote this row's output
     };
     auto sources = [&](uint64_t w) {
         Sources s;
@@ -567,10 +693,8 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         const uint32_t r = a.at<int32_t>(a.L.token_request)[s.t], packed = a.at<uint32_t>(a.L.token_packed)[s.t];
         const RequestInfo info = a.at<RequestInfo>(a.L.requests)[r];
         const uint32_t h = s.qh / a.group, gh = s.qh % a.group;
-        bool unused = false;
-        s.final = false;
-        s.own = pieces_of(a, head, info.kind, info.first, (s.t - a.starts[r]) * a.group + gh, h, &s.final);
-        s.pre = pieces_of(a, head, packed == UINT32_MAX ? static_cast<uint32_t>(kNone) : head.prefix_kind, 0, packed * a.group + gh, h, &unused);
+        s.own = pieces_of(a, head, info.kind, info.first, (s.t - a.starts[r]) * a.group + gh, h);
+        s.pre = pieces_of(a, head, packed >= kInTiles ? static_cast<uint32_t>(kNone) : head.prefix_kind, 0, packed * a.group + gh, h);
         return s;
     };
     auto join = [&](const Sources& s) {
@@ -642,25 +766,21 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         // a row that sees no key: zeros, and the logarithm of an empty sum
         const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
         T* out = static_cast<T*>(a.out) + s.t * a.out_token + s.qh * a.out_head + lane * kPer;
-        if (reinterpret_cast<uintptr_t>(out) & (kPer * 2 - 1)) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) out[j] = Elem<T>::from(acc[j] * inv);
-        } else if constexpr (kPer == 4) {
-            *reinterpret_cast<uint2*>(out) = make_uint2(Elem<T>::pack(acc[0] * inv, acc[1] * inv), Elem<T>::pack(acc[2] * inv, acc[3] * inv));
-        } else {
-            *reinterpret_cast<uint32_t*>(out) = Elem<T>::pack(acc[0] * inv, acc[1] * inv);
-        }
+        for (int j = 0; j < kPer; ++j) acc[j] *= inv;
+        store_row<T, kPer>(out, acc);
         if (a.lse && lane == 0)
             a.lse[static_cast<uint64_t>(s.t) * q_heads + s.qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
     };
+    const uint32_t* marks = a.at<uint32_t>(a.L.token_packed);
     if (kSplit || span == 1) {
-        const Sources s = sources(base);
-        if (!s.final) join(s);
+        if (marks[base / q_heads] == kInTiles) return;
+        join(sources(base));
         return;
     }
-    // which of the warp's rows are left to do: mostly none behind the tile kernel
+    // which of the warp's rows are this kernel's: of a batch of prompts, none
     bool todo = false;
-    if (static_cast<uint32_t>(lane) < span && base + lane < n_rows) todo = !sources(base + lane).final;
+    if (static_cast<uint32_t>(lane) < span && base + lane < n_rows) todo = marks[(base + lane) / q_heads] != kInTiles;
     for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, todo); rest; rest &= rest - 1) join(sources(base + __ffs(rest) - 1));
 }
 
@@ -780,11 +900,16 @@ afx_status launch(const AttnArgs& a, const afx_kv_cache& cache, cudaStream_t s) 
     attention_rows16_kernel<T, D><<<sms * 2, kWarps * 32, smem, s>>>(a);
     AFX_SERVE_TRY(cudaGetLastError(), "attention_rows16_kernel launch");
     const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.kv_heads * a.group;
+    // a request can have tiles of its own from kFuseRows rows on, without a prefix from kRows + 1
+    const bool own_tiles = a.tile_ctas && static_cast<uint64_t>(a.n_tokens) * a.group > (a.prefix_len ? kFuseRows - 1 : kRows);
+    const uint32_t tile_blocks = own_tiles ? sms * 8 : 0;
     if (rows <= static_cast<uint64_t>(sms) * 8) {  // a CTA a row while they all run at once
-        attention_join_kernel<T, D, true><<<static_cast<uint32_t>(rows), kJoinThreads, 0, s>>>(a, 1);
+        const uint32_t n = static_cast<uint32_t>(rows);
+        attention_join_kernel<T, D, true><<<n + tile_blocks, kJoinThreads, 0, s>>>(a, 1, n);
     } else {
         const uint64_t span = rows <= static_cast<uint64_t>(sms) * 256 ? 1 : 32, per = span * kJoinWarps;
-        attention_join_kernel<T, D, false><<<static_cast<uint32_t>((rows + per - 1) / per), kJoinThreads, 0, s>>>(a, static_cast<uint32_t>(span));
+        const uint32_t n = static_cast<uint32_t>((rows + per - 1) / per);
+        attention_join_kernel<T, D, false><<<n + tile_blocks, kJoinThreads, 0, s>>>(a, static_cast<uint32_t>(span), n);
     }
     AFX_SERVE_TRY(cudaGetLastError(), "attention_join_kernel launch");
     return AFX_OK;

@@ -199,6 +199,19 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// Multiplies 8 n columns of this thread's lane by f.  Rare: kept out of the
+// row warps' loop, whose code is long enough.
+__device__ __noinline__ void scale_columns(uint32_t addr, int n, float f) {
+    for (int c = 0; c < n; ++c) {
+        uint32_t v[8];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n" : AFX_R8(v, 0) : "r"(addr + c * 8) : "memory");
+        tmem_wait_load();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(addr + c * 8), AFX_W8(v, 0) : "memory");
+    }
+}
+
 // ---- a CTA's share -----------------------------------------------------------------
 
 // The pieces of a CTA's share of the cost, in order; every role walks the
@@ -558,17 +571,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 const float f = next == -INFINITY ? 1.0f : exp2_approx(ref - next);
                 ref = next;
                 sum *= f;
-                if (done > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_load32(o_col + c * 32, o);
-                        tmem_wait_load();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_store32(o_col + c * 32, o);
-                    }
-                }
+                if (done > 0) scale_columns(o_col, D / 8, f);
             };
             for (uint32_t s = first; s < p.step1 && ok; s += stride, ++done) {
                 ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.s_full[t], s_count++ & 1u, ctl, a.status));
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     const bool whole = n == kTileKeys && (prefix || key + kTileKeys <= all_see);
                     uint32_t x[kTileKeys];
                     auto mask = [&](uint32_t half) {
-                        if (whole) return;
+                        if (__builtin_expect(whole, 1)) return;
 #pragma unroll
                         for (uint32_t j = 0; j < 64; ++j)
                             if (half * 64 + j >= sees) x[half * 64 + j] = 0xFF800000u;  // -inf
@@ -627,19 +630,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     tmem_load32(s_col, x);
                     tmem_load32(s_col + 32, x + 32);
                     tmem_wait_load();
-                    if (done > 0 && __any_sync(0xFFFFFFFFu, seen_most > ref + kLag)) rebase(seen_most);
+                    if (__builtin_expect(done > 0 && __any_sync(0xFFFFFFFFu, seen_most > ref + kLag), 0)) rebase(seen_most);
                     tmem_load32(s_col + 64, x + 64);
                     tmem_load32(s_col + 96, x + 96);
                     mask(0);
                     float most = half_most(0);
                     if (done == 0) ref = most;
-                    weigh(x);
-                    tmem_wait_load();
-                    mask(1);
-                    most = fmaxf(most, half_most(1));
-                    if (__any_sync(0xFFFFFFFFu, most > ref + kHigh)) {
-                        rebase(most);
+#pragma unroll 1
+                    for (bool again = false;; again = true) {
                         weigh(x);
+                        if (again) break;
+                        tmem_wait_load();
+                        mask(1);
+                        most = fmaxf(most, half_most(1));
+                        if (__builtin_expect(!__any_sync(0xFFFFFFFFu, most > ref + kHigh), 1)) break;
+                        rebase(most);
                     }
                     seen_most = most;
                     publish(0);
