@@ -101,11 +101,13 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
 }
 // Bounded, without giving up early: for what is in flight.
 __device__ __forceinline__ bool bar_drain(uint64_t* b, uint32_t parity) {
+#pragma unroll 1
     for (uint32_t i = 0; i < kWaitPolls; ++i)
         if (bar_try(b, parity)) return true;
     return false;
 }
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Ctl& ctl, int32_t* status) {
+#pragma unroll 1
     for (uint32_t i = 0; i < kWaitPolls; ++i) {
         if (bar_try(b, parity)) return true;
         if ((i & 31u) == 31u && *reinterpret_cast<volatile int32_t*>(&ctl.abort_flag)) return false;
@@ -227,6 +229,7 @@ struct Walk {
         end = at + share < head.cost ? at + share : head.cost;
         if (at >= end) return;
         uint32_t lo = 0, hi = n;  // the group that holds `at`
+#pragma unroll 1
         while (hi - lo > 1) {
             const uint32_t mid = (lo + hi) >> 1;
             if (groups[mid].cost_begin <= at)
@@ -244,6 +247,7 @@ struct Walk {
     };
     __device__ bool next(Piece* p) {
         if (at >= end) return false;
+#pragma unroll 1
         while (at >= groups[g].cost_begin + static_cast<uint64_t>(groups[g].cost) * heads) ++g;
         p->g = groups[g];
         const uint64_t in = at - p->g.cost_begin;
@@ -349,6 +353,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 uint64_t* bar = patch ? &ctl.tail : &ctl.full[slot];
                 const uint32_t dst = smem_addr(smem + Sh::kQ) + slot * Sh::kSlot;
                 if (leader) bar_expect(bar, used * box * 128 * Sh::kHalves);
+#pragma unroll 1
                 for (uint32_t b = 0; b < used; ++b) {
                     const uint32_t id = __shfl_sync(0xFFFFFFFFu, page, b), token = first & page_mask;  // 0 but for pages of 256
                     const uint32_t c1 = args.token_at == 0 ? token : args.head_at == 0 ? p.h : id, c2 = args.token_at == 1 ? token : args.head_at == 1 ? p.h : id,
@@ -368,6 +373,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     ++tails;
                     uint8_t* v = smem + Sh::kQ + slot * Sh::kSlot;
                     for (uint32_t hf = 0; hf < Sh::kHalves; ++hf)
+#pragma unroll 1
                         for (uint32_t i = n * 8 + lane; i < kTileKeys * 8; i += 32)
                             *reinterpret_cast<uint4*>(v + hf * Sh::kBlock + i * 16) = make_uint4(0, 0, 0, 0);
                     fence_async_shared();
@@ -449,43 +455,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             ok = uniform(bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status));
             fence_after();
             const uint32_t n = p.step1 - p.step0;
+            const bool both = p.both;
             if (ok) ok = slot_full(k_slot, k_phase);
             if (!ok) break;
-            if (p.both) {
-                // scores of step 0 for both tiles; then, a tile at a time, the values of step i and the scores of step i + 1
-                scores(0, k_slot, true, false);
-                scores(1, k_slot, true, true);
-                for (uint32_t i = 0; i < n && ok; ++i) {
+            // scores of step 0; then, with both tiles on every step, a tile at a time the values of step i and the
+            // scores of step i + 1 (whose place in tensor memory the weights of step i held); with the tiles taking
+            // turns the scores of step i + 1, of the other tile, first
+#pragma unroll 1
+            for (uint32_t t = 0; t < (both ? 2u : 1u); ++t) scores(t, k_slot, both, !both || t == 1);
+            uint32_t v_slot = 0;
+#pragma unroll 1
+            for (uint32_t u = 0; u < (both ? 2 * n : n) && ok; ++u) {
+                const uint32_t t = u & 1, i = both ? u >> 1 : u;
+                const bool more = i + 1 < n, last = !both || t == 1;
+                if (!both || t == 0) {  // on to step i's values and step i + 1's keys
                     step_on(k_slot, k_phase);
-                    const uint32_t v_slot = k_slot;
-                    ok = slot_full(k_slot, k_phase);
+                    v_slot = k_slot;
+                    const uint32_t v_phase = k_phase;
                     step_on(k_slot, k_phase);
-                    const bool more = i + 1 < n;
-                    if (more) ok = ok && slot_full(k_slot, k_phase);
-                    if (!ok || !values(0, v_slot, i == 0, false)) {
-                        ok = false;
-                        break;
-                    }
-                    if (more) scores(0, k_slot, true, false);
-                    ok = values(1, v_slot, i == 0, true);
-                    if (ok && more) scores(1, k_slot, true, true);
+                    ok = !more || slot_full(k_slot, k_phase);
+                    if (ok && more && !both) scores(t ^ 1, k_slot, false, true);
+                    ok = ok && slot_full(v_slot, v_phase);
                 }
-            } else {
-                // steps alternate between the tiles; the scores run one step ahead of the values
-                scores(0, k_slot, false, true);
-                for (uint32_t i = 0; i < n && ok; ++i) {
-                    const uint32_t t = i & 1;
-                    step_on(k_slot, k_phase);
-                    const uint32_t v_slot = k_slot, v_phase = k_phase;
-                    step_on(k_slot, k_phase);
-                    // step i + 1's scores go to the other tile, whose step i - 1 has been read (its weights were full)
-                    if (i + 1 < n) {
-                        ok = slot_full(k_slot, k_phase);
-                        if (!ok) break;
-                        scores(t ^ 1, k_slot, false, true);
-                    }
-                    ok = slot_full(v_slot, v_phase) && values(t, v_slot, i < 2, true);
-                }
+                ok = ok && values(t, v_slot, both ? i == 0 : i < 2, last);
+                if (ok && more && both) scores(t, k_slot, true, last);
             }
         }
         if (!ok && leader) {  // products in flight finish before the tensor memory is freed
