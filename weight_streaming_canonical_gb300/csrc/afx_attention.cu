@@ -42,9 +42,6 @@ constexpr uint32_t kTargetUnits = 1216;  // 16-row items x heads that the cuts a
 constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's tiles take the prefix along
 constexpr uint32_t kMinShare = 8;      // cost of a tile CTA, at least
 constexpr uint32_t kFewTokens = 8, kManyMax = 512;
-// token_packed of tokens that do not share the prefix's tiles: in tiles of
-// their request's own, or (no prefix) in 16-row items
-constexpr uint32_t kInTiles = 0xFFFFFFFEu, kAlone = 0xFFFFFFFFu;
 
 __host__ __device__ inline uint64_t up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 
@@ -92,6 +89,11 @@ __device__ Counts<N> block_exclusive(const Counts<N>& mine, Counts<N>* total) {
     return out;
 }
 
+struct Many {
+    uint32_t request, mark;
+    RequestInfo own;
+};
+
 // How a request's rows are worked off.
 struct Kind {
     uint32_t own;    // Source
@@ -115,10 +117,8 @@ __device__ __forceinline__ uint32_t tile_cost(uint32_t rows, uint32_t prefix_key
 // groups' cost is cut into one share a CTA.
 __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const AttnArgs a) {
     PlanHead* head = a.at<PlanHead>(0);
-    int32_t* token_request = a.at<int32_t>(a.L.token_request);
-    uint32_t* token_packed = a.at<uint32_t>(a.L.token_packed);
+    TokenInfo* tokens = a.at<TokenInfo>(a.L.tokens);
     int32_t* packed_token = a.at<int32_t>(a.L.packed_token);
-    RequestInfo* requests = a.at<RequestInfo>(a.L.requests);
     Row16Group* groups = a.at<Row16Group>(a.L.groups16);
     Row16Item* items = a.at<Row16Item>(a.L.items16);
     TileGroup* tiles = a.at<TileGroup>(a.L.tiles);
@@ -127,8 +127,10 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     const uint32_t r0 = min(R, threadIdx.x * per), r1 = min(R, r0 + per);
     const uint64_t max_len = static_cast<uint64_t>(a.table_cols) << a.shift;
 
+    wait_for_earlier();
+    let_next_start();
     __shared__ uint32_t n_many;
-    __shared__ uint2 many[kManyMax];  // requests of more than a few tokens, and their tokens' mark
+    __shared__ Many many[kManyMax];  // requests of more than a few tokens
     if (threadIdx.x == 0) n_many = 0;
     // the lengths have to make sense before anything is addressed by them
     bool bad = false;
@@ -190,9 +192,8 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         rows_p = (static_cast<uint64_t>(tiles_p - 1) * kGroupRows + (last > kTileRows ? last : 2 * last)) * a.kv_heads;
     }
 
-    auto write_token = [&](uint32_t r, uint32_t t, uint32_t mark, uint32_t i) {
-        token_request[t] = static_cast<int32_t>(r);
-        token_packed[t] = mark >= kInTiles ? mark : mark + i;
+    auto write_token = [&](uint32_t r, uint32_t t, uint32_t mark, uint32_t i, const RequestInfo& own) {
+        tokens[t] = TokenInfo{r, i * G, mark >= kInTiles ? mark : mark + i, 0, own};
         if (mark < kInTiles) packed_token[mark + i] = static_cast<int32_t>(t);
     };
     // the requests' own keys
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     for (uint32_t r = r0; r < r1; ++r) {
         const uint32_t s = a.starts[r], e = a.starts[r + 1];
         const Kind k = kind_of(a, (e - s) * G);
-        requests[r] = RequestInfo{k.own, k.own == kTile ? tg : g, k.fused, 0};
+        const RequestInfo own{k.own, k.own == kTile ? tg : g, k.fused, 0};
         walk(
             r,
             [&](uint32_t row, uint32_t m, uint32_t end, uint32_t token0, int32_t seen) {
@@ -252,20 +253,21 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         // its tokens: a few here, more by a warp below
         const uint32_t mark = k.fused ? (k.own == kTile ? kInTiles : kAlone) : packed;
         if (e - s <= kFewTokens) {
-            for (uint32_t t = s; t < e; ++t) write_token(r, t, mark, t - s);
+            for (uint32_t t = s; t < e; ++t) write_token(r, t, mark, t - s, own);
         } else {
             const uint32_t i = atomicAdd(&n_many, 1u);
             if (i < kManyMax)
-                many[i] = make_uint2(r, mark);
+                many[i] = Many{r, mark, own};
             else
-                for (uint32_t t = s; t < e; ++t) write_token(r, t, mark, t - s);
+                for (uint32_t t = s; t < e; ++t) write_token(r, t, mark, t - s, own);
         }
         if (!k.fused) packed += e - s;
     }
     __syncthreads();
     for (uint32_t i = threadIdx.x / 32; i < min(n_many, kManyMax); i += threads / 32) {
-        const uint32_t r = many[i].x, s = a.starts[r], e = a.starts[r + 1];
-        for (uint32_t t = s + threadIdx.x % 32; t < e; t += 32) write_token(r, t, many[i].y, t - s);
+        const Many m = many[i];
+        const uint32_t s = a.starts[m.request], e = a.starts[m.request + 1];
+        for (uint32_t t = s + threadIdx.x % 32; t < e; t += 32) write_token(m.request, t, m.mark, t - s, m.own);
     }
     if (threadIdx.x == 0) {
         const uint64_t c = total.v[4] + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
@@ -311,11 +313,14 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
     constexpr int kChunks = D / 8;                     // 16-byte chunks of a key
     constexpr uint32_t kTile = kBlockKeys * D * 2;     // bytes of a block's keys
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // The plan was done before the tile kernel, which let this one start, and
+    // the two kernels' results do not meet: they run side by side, and only
+    // the end of this one waits for the end of that one.
+    if (!a.tile_ctas) wait_for_earlier();
+    let_next_start();
     const PlanHead head = *a.at<PlanHead>(0);
-    if (head.key != a.plan_key) {
-        if (threadIdx.x == 0) raise(a.status, AFX_DEV_BAD_PLAN);
-        return;
-    }
+    if (head.key != a.plan_key && threadIdx.x == 0) raise(a.status, AFX_DEV_BAD_PLAN);
+    const uint32_t n_units = head.key == a.plan_key ? head.n_items * a.kv_heads : 0;
     const Row16Item* items = a.at<Row16Item>(a.L.items16);
     const int32_t* packed = a.at<int32_t>(a.L.packed_token);
     float* part_o = a.at<float>(a.L.part_o);
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
     const uint32_t mine_addr = smem_addr(mine);
     const uint32_t page_mask = (1u << a.shift) - 1;
 
-    for (uint32_t unit = blockIdx.x; unit < head.n_items * a.kv_heads; unit += gridDim.x) {
+    for (uint32_t unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
         const Row16Item it = items[unit / a.kv_heads];
         const uint32_t h = unit % a.kv_heads;
         const int32_t* pages = it.request < 0 ? a.prefix_table : a.table + static_cast<uint64_t>(it.request) * a.table_cols;
@@ -516,6 +521,7 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
         }
         __syncthreads();
     }
+    if (a.tile_ctas) wait_for_earlier();
 }
 
 // ---- the join ------------------------------------------------------------------------
@@ -672,29 +678,29 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     __shared__ float2 sh_ml[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t q_heads = a.kv_heads * a.group;
-    const uint64_t base = kSplit ? blockIdx.x : (static_cast<uint64_t>(blockIdx.x) * kJoinWarps + warp) * span;
+    wait_for_earlier();
+    const uint32_t base = kSplit ? blockIdx.x : (blockIdx.x * kJoinWarps + warp) * span;  // n_tokens * q_heads is below 2^31
     const PlanHead head = *a.at<PlanHead>(0);
     if (head.key != a.plan_key) return;
     if (blockIdx.x >= row_blocks) {
         join_tiles<T, D>(a, head, blockIdx.x - row_blocks, gridDim.x - row_blocks);
         return;
     }
-    const uint64_t n_rows = static_cast<uint64_t>(head.n_tokens) * q_heads;
+    const uint32_t n_rows = head.n_tokens * q_heads;
     if (base >= n_rows) return;
 
     struct Sources {
         Pieces pre, own;
         uint32_t t, qh;
     };
-    auto sources = [&](uint64_t w) {
+    auto sources = [&](uint32_t w) {
         Sources s;
-        s.t = static_cast<uint32_t>(w / q_heads);
-        s.qh = static_cast<uint32_t>(w % q_heads);
-        const uint32_t r = a.at<int32_t>(a.L.token_request)[s.t], packed = a.at<uint32_t>(a.L.token_packed)[s.t];
-        const RequestInfo info = a.at<RequestInfo>(a.L.requests)[r];
-        const uint32_t h = s.qh / a.group, gh = s.qh % a.group;
-        s.own = pieces_of(a, head, info.kind, info.first, (s.t - a.starts[r]) * a.group + gh, h);
-        s.pre = pieces_of(a, head, packed >= kInTiles ? static_cast<uint32_t>(kNone) : head.prefix_kind, 0, packed * a.group + gh, h);
+        s.t = w / q_heads;
+        s.qh = w - s.t * q_heads;
+        const TokenInfo info = a.at<TokenInfo>(a.L.tokens)[s.t];
+        const uint32_t h = s.qh / a.group, gh = s.qh - h * a.group;
+        s.own = pieces_of(a, head, info.own.kind, info.own.first, info.row + gh, h);
+        s.pre = pieces_of(a, head, info.packed >= kInTiles ? static_cast<uint32_t>(kNone) : head.prefix_kind, 0, info.packed * a.group + gh, h);
         return s;
     };
     auto join = [&](const Sources& s) {
@@ -772,15 +778,15 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         if (a.lse && lane == 0)
             a.lse[static_cast<uint64_t>(s.t) * q_heads + s.qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
     };
-    const uint32_t* marks = a.at<uint32_t>(a.L.token_packed);
+    const TokenInfo* tokens = a.at<TokenInfo>(a.L.tokens);
     if (kSplit || span == 1) {
-        if (marks[base / q_heads] == kInTiles) return;
+        if (tokens[base / q_heads].packed == kInTiles) return;
         join(sources(base));
         return;
     }
     // which of the warp's rows are this kernel's: of a batch of prompts, none
     bool todo = false;
-    if (static_cast<uint32_t>(lane) < span && base + lane < n_rows) todo = marks[(base + lane) / q_heads] != kInTiles;
+    if (static_cast<uint32_t>(lane) < span && base + lane < n_rows) todo = tokens[(base + lane) / q_heads].packed != kInTiles;
     for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, todo); rest; rest &= rest - 1) join(sources(base + __ffs(rest) - 1));
 }
 
@@ -849,10 +855,8 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
         off = up(off + bytes, 256);
         return at;
     };
-    L.token_request = take(4ull * d->n_tokens);
-    L.token_packed = take(4ull * d->n_tokens);
+    L.tokens = take(sizeof(TokenInfo) * static_cast<uint64_t>(d->n_tokens));
     L.packed_token = take(4ull * d->n_tokens);
-    L.requests = take(sizeof(RequestInfo) * R);
     L.groups16 = take(sizeof(Row16Group) * groups);
     L.items16 = take(sizeof(Row16Item) * (groups + extra));
     L.tiles = take(sizeof(TileGroup) * (tiles ? 2 * (rows / kGroupRows + 1) + R : 0));
@@ -897,21 +901,20 @@ afx_status launch(const AttnArgs& a, const afx_kv_cache& cache, cudaStream_t s) 
     AFX_SERVE_TRY(cudaFuncSetAttribute(attention_rows16_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem)),
                   "cudaFuncSetAttribute");
-    attention_rows16_kernel<T, D><<<sms * 2, kWarps * 32, smem, s>>>(a);
-    AFX_SERVE_TRY(cudaGetLastError(), "attention_rows16_kernel launch");
+    AFX_SERVE_TRY(launch_early(attention_rows16_kernel<T, D>, sms * 2, kWarps * 32, smem, s, a), "attention_rows16_kernel launch");
     const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.kv_heads * a.group;
     // a request can have tiles of its own from kFuseRows rows on, without a prefix from kRows + 1
     const bool own_tiles = a.tile_ctas && static_cast<uint64_t>(a.n_tokens) * a.group > (a.prefix_len ? kFuseRows - 1 : kRows);
     const uint32_t tile_blocks = own_tiles ? sms * 8 : 0;
     if (rows <= static_cast<uint64_t>(sms) * 8) {  // a CTA a row while they all run at once
         const uint32_t n = static_cast<uint32_t>(rows);
-        attention_join_kernel<T, D, true><<<n + tile_blocks, kJoinThreads, 0, s>>>(a, 1, n);
+        AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, true>, n + tile_blocks, kJoinThreads, 0, s, a, 1u, n), "attention_join_kernel launch");
     } else {
         const uint64_t span = rows <= static_cast<uint64_t>(sms) * 256 ? 1 : 32, per = span * kJoinWarps;
         const uint32_t n = static_cast<uint32_t>((rows + per - 1) / per);
-        attention_join_kernel<T, D, false><<<n + tile_blocks, kJoinThreads, 0, s>>>(a, static_cast<uint32_t>(span), n);
+        AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, false>, n + tile_blocks, kJoinThreads, 0, s, a, static_cast<uint32_t>(span), n),
+                      "attention_join_kernel launch");
     }
-    AFX_SERVE_TRY(cudaGetLastError(), "attention_join_kernel launch");
     return AFX_OK;
 }
 
@@ -936,8 +939,8 @@ extern "C" afx_status afx_attention_plan(const afx_attention_args* args, void* w
     afx_status st = prepare(args, &a);
     if (st == AFX_OK) st = bind_workspace(&a, workspace_dev, workspace_bytes, status_dev);
     if (st != AFX_OK) return st;
-    attention_plan_kernel<<<1, plan_threads(args->n_requests), 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    AFX_SERVE_TRY(cudaGetLastError(), "attention_plan_kernel launch");
+    AFX_SERVE_TRY(launch_early(attention_plan_kernel, 1, plan_threads(args->n_requests), 0, reinterpret_cast<cudaStream_t>(stream), a),
+                  "attention_plan_kernel launch");
     return AFX_OK;
 }
 

@@ -30,17 +30,29 @@ enum Source : uint32_t { kNone = 0, kRow16 = 1, kTile = 2 };
 
 // A request's own keys (with the prefix before them where fused): its rows'
 // first group, of kRows or kGroupRows rows each.
-struct RequestInfo {
+struct alignas(16) RequestInfo {
     uint32_t kind, first, fused, pad;
 };
 
+// A token of the queries: its request, its first packed row among the
+// request's, its place among the tokens that share the prefix's groups (or
+// kInTiles, kAlone), and its request's own groups.
+struct alignas(16) TokenInfo {
+    uint32_t request, row, packed, pad;
+    RequestInfo own;
+};
+
+// TokenInfo::packed of tokens that do not share the prefix's groups: in
+// tiles of their request's own, or (no prefix) in 16-row items.
+constexpr uint32_t kInTiles = 0xFFFFFFFEu, kAlone = 0xFFFFFFFFu;
+
 // 16 packed rows of one source: its pieces' results start at part_row, piece
 // s at part_row + s * rows.
-struct Row16Group {
+struct alignas(16) Row16Group {
     uint32_t part_row, n_pieces, rows, pad;
 };
 
-struct Row16Item {
+struct alignas(16) Row16Item {
     int32_t request;        // -1: the prefix
     uint32_t row0, rows;    // packed rows of the source
     uint32_t key0, key1;    // keys of the source
@@ -53,7 +65,7 @@ struct Row16Item {
 // then `own_keys` of the request.  cost: 2 a step of 128 keys for more than
 // 128 rows (both tiles work on every step), else 1 (the tiles take turns),
 // rounded up to even.
-struct TileGroup {
+struct alignas(16) TileGroup {
     uint64_t cost_begin;    // of head 0; head h begins h * cost later
     uint64_t part_row;      // where the results of the first piece of head 0 go
     uint32_t cost;
@@ -67,7 +79,7 @@ struct TileGroup {
 };
 
 struct AttnLayout {
-    uint64_t token_request, token_packed, packed_token, requests, groups16, items16, tiles, part_ml, part_o, total;
+    uint64_t tokens, packed_token, groups16, items16, tiles, part_ml, part_o, total;
     uint64_t extra_row;     // rows of the tile kernel's further pieces: 256 a CTA
     uint64_t max_rows;
 };

@@ -283,13 +283,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
     Ctl& ctl = *reinterpret_cast<Ctl*>(smem + Sh::kCtl);
     const AttnArgs& a = args.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PlanHead head = *a.at<PlanHead>(0);
-    if (head.key != a.plan_key) {
-        if (threadIdx.x == 0) raise(a.status, AFX_DEV_BAD_PLAN);
-        return;
-    }
-    if (blockIdx.x * head.share >= head.cost) return;
-
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < Sh::kSlots; ++i) {
             bar_init(&ctl.full[i], 1);
@@ -315,6 +308,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
     __syncthreads();
     fence_after();
     const uint32_t tmem = ctl.tmem;
+    wait_for_earlier();
+    let_next_start();  // the plan is done, which is all that the 16-row kernel needs
+    PlanHead head = *a.at<PlanHead>(0);
+    if (head.key != a.plan_key) {
+        if (threadIdx.x == 0) raise(a.status, AFX_DEV_BAD_PLAN);
+        head.cost = 0;
+    }
     Walk walk(a, head);
     Walk::Piece p;
     if (warp >= kSoftWarps) {
@@ -817,8 +817,7 @@ afx_status launch(const TileArgs& args, cudaStream_t s) {
     AFX_SERVE_TRY(cudaFuncSetAttribute(attention_tile_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(Shape<D>::kSmem)),
                   "cudaFuncSetAttribute");
-    attention_tile_kernel<T, D><<<args.a.tile_ctas, kTileThreads, Shape<D>::kSmem, s>>>(args);
-    AFX_SERVE_TRY(cudaGetLastError(), "attention_tile_kernel launch");
+    AFX_SERVE_TRY(launch_early(attention_tile_kernel<T, D>, args.a.tile_ctas, kTileThreads, Shape<D>::kSmem, s, args), "attention_tile_kernel launch");
     return AFX_OK;
 }
 

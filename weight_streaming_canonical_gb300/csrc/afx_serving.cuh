@@ -41,6 +41,29 @@ inline int current_sms() {
     return sms;
 }
 
+// Launches a kernel that may start while the one before it on the stream is
+// still running: it has to call wait_for_earlier() before it touches memory
+// that earlier work writes or reads.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), uint32_t grid, uint32_t block, size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Returns once all work before this kernel on the stream is done and visible.
+__device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// From here on (in every CTA) the next kernel on the stream may start.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 __device__ __forceinline__ void raise(int32_t* status, int32_t bits) {
     if (status) atomicOr(status, bits);
 }
