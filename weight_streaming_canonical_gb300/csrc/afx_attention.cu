@@ -17,8 +17,7 @@
 // step uses the same list), one attention kernel works off and one join
 // kernel puts together in a fixed order.
 //
-// Two kernels work items off: the 16-row kernel here (mma.sync, four warps on
-// their own keys: one or a few new tokens a request, where reading the keys is
+// Two kernels work items off: the 16-row kernel here (mma.sync, every warp on its own: one or a few new tokens a request, where reading the keys is
 // all) and the tile kernel (afx_attention_tile.cu: tcgen05, 256 rows).  A
 // request with 128 packed rows or more, a prompt, has tiles of its own that
 // run over the prefix and its own keys in one go; the others share tiles on
@@ -300,18 +299,22 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {
 constexpr int kWarps = 4;
 constexpr int kBlockKeys = 16;  // keys of one step of a warp; divides every page size
 constexpr int kStages = 3;
+
 template <int D>
 constexpr size_t rows16_smem() {
     return static_cast<size_t>(kWarps) * kStages * 2 * kBlockKeys * D * 2;
 }
 
-// The four warps of a CTA take every fourth block of 16 keys of the item,
-// each with its own copies, maxima and sums, and meet once at the end.
+// A unit is an item's rows and keys of one key/value head; every warp takes
+// units on its own, steps of 16 keys, with no barrier anywhere.  Its copies
+// run kStages - 1 steps ahead, over the ends of units, so that memory stays
+// busy while a unit's results are written and the next one's queries loaded.
+// Two CTAs an SM: 8 warps with 16 KB each in flight.
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int kChunks = D / 8;                     // 16-byte chunks of a key
-    constexpr uint32_t kTile = kBlockKeys * D * 2;     // bytes of a block's keys
+    constexpr uint32_t kTile = kBlockKeys * D * 2;     // bytes of a step's keys
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // The plan was done before the tile kernel, which let this one start, and
     // the two kernels' results do not meet: they run side by side, and only
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
     let_next_start();
     const PlanHead head = *a.at<PlanHead>(0);
     if (head.key != a.plan_key && threadIdx.x == 0) raise(a.status, AFX_DEV_BAD_PLAN);
-    const uint32_t n_units = head.key == a.plan_key ? head.n_items * a.kv_heads : 0;
+    const uint32_t n_units = head.key == a.plan_key ? head.n_items * a.kv_heads : 0, step = gridDim.x * kWarps;
     const Row16Item* items = a.at<Row16Item>(a.L.items16);
     const int32_t* packed = a.at<int32_t>(a.L.packed_token);
     float* part_o = a.at<float>(a.L.part_o);
@@ -328,15 +331,70 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
     const T* q = static_cast<const T*>(a.q);
     const T* kp = static_cast<const T*>(a.k);
     const T* vp = static_cast<const T*>(a.v);
-    uint8_t* mine = smem + warp * (kStages * 2 * kTile);
-    const uint32_t mine_addr = smem_addr(mine);
+    const uint32_t mine = smem_addr(smem) + warp * (kStages * 2 * kTile);
     const uint32_t page_mask = (1u << a.shift) - 1;
 
-    for (uint32_t unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
+    // the copies: unit c_unit's step c_block goes into stage c_stage
+    uint32_t c_unit = blockIdx.x * kWarps + warp, c_block = 0, c_blocks = 0, c_key0 = 0, c_key1 = 0, c_stage = 0;
+    uint64_t c_head = 0;
+    const int32_t* c_pages = nullptr;
+    uint32_t c_page = 0;  // lane l: the page of step c_block / 32 * 32 + l
+    auto open = [&]() {
+        if (c_unit >= n_units) return;
+        const Row16Item& it = items[c_unit / a.kv_heads];
+        c_key0 = it.key0;
+        c_key1 = it.key1;
+        c_blocks = ceil_div(c_key1 - c_key0, kBlockKeys);
+        c_block = 0;
+        c_head = (c_unit % a.kv_heads) * a.head_stride;
+        c_pages = it.request < 0 ? a.prefix_table : a.table + static_cast<uint64_t>(it.request) * a.table_cols;
+    };
+    auto copy_next = [&]() {
+        if (c_unit < n_units) {
+            if (c_block % 32 == 0) {  // 32 steps' pages at a time
+                const uint32_t i = c_block + lane;
+                const int32_t id = i < c_blocks ? __ldg(c_pages + ((c_key0 + i * kBlockKeys) >> a.shift)) : 0;
+                c_page = id;
+                if (id < 0 || static_cast<uint32_t>(id) >= a.n_pages) {
+                    raise(a.status, AFX_DEV_BAD_PAGE);
+                    c_page = 0;
+                }
+            }
+            const uint32_t key = c_key0 + c_block * kBlockKeys;
+            const uint64_t page = __shfl_sync(0xFFFFFFFFu, c_page, c_block % 32);
+            // a lane copies every (32 / kChunks)-th key from its own on, the same 16 bytes of each
+            const uint32_t row0 = lane / kChunks, chunk = lane % kChunks;
+            const uint64_t from = page * a.page_stride + c_head + ((key & page_mask) + row0) * a.token_stride + chunk * 8;
+            const T* k_from = kp + from;
+            const T* v_from = vp + from;
+            const uint64_t hop = (32 / kChunks) * a.token_stride;
+            const uint32_t buf = mine + c_stage * 2 * kTile;
+#pragma unroll
+            for (int c = 0; c < kBlockKeys * kChunks / 32; ++c) {
+                const uint32_t row = c * (32 / kChunks) + row0;
+                const bool real = key + row < c_key1;  // past the range: zeros, whatever the page holds there
+                const uint32_t dst = buf + row * (D * 2) + ((chunk ^ (row & 7)) * 16);
+                copy16(dst, k_from, real);
+                copy16(dst + kTile, v_from, real);
+                k_from += hop;
+                v_from += hop;
+            }
+            if (++c_block == c_blocks) {
+                c_unit += step;
+                open();
+            }
+            c_stage = c_stage + 1 == kStages ? 0 : c_stage + 1;
+        }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    open();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) copy_next();
+
+    uint32_t stage = 0;
+    for (uint32_t unit = blockIdx.x * kWarps + warp; unit < n_units; unit += step) {
         const Row16Item it = items[unit / a.kv_heads];
         const uint32_t h = unit % a.kv_heads;
-        const int32_t* pages = it.request < 0 ? a.prefix_table : a.table + static_cast<uint64_t>(it.request) * a.table_cols;
-
         // the queries as A fragments: rows lane / 4 and lane / 4 + 8
         uint32_t qf[D / 16][4];
         uint32_t limit[2];  // keys the row sees
@@ -365,36 +423,6 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
         }
         const uint32_t min_limit = it.request < 0 ? UINT32_MAX : visible(it.seen, it.row0, a.group);
 
-        const uint32_t n_blocks = ceil_div(it.key1 - it.key0, kBlockKeys);
-        const uint32_t n_mine = n_blocks > static_cast<uint32_t>(warp) ? ceil_div(n_blocks - warp, kWarps) : 0;
-        int32_t page_of = 0;  // lane l: the page of this warp's block base + l
-        auto issue = [&](uint32_t i) {
-            if (i < n_mine) {
-                if (i % 32 == 0) {  // 32 blocks' pages at a time
-                    const uint32_t key = it.key0 + (warp + kWarps * (i + lane)) * kBlockKeys;
-                    page_of = i + lane < n_mine ? pages[key >> a.shift] : 0;
-                    if (page_of < 0 || static_cast<uint32_t>(page_of) >= a.n_pages) {
-                        raise(a.status, AFX_DEV_BAD_PAGE);
-                        page_of = 0;
-                    }
-                }
-                const uint32_t key = it.key0 + (warp + kWarps * i) * kBlockKeys;
-                const uint64_t page = static_cast<uint32_t>(__shfl_sync(0xFFFFFFFFu, page_of, i % 32));
-                const uint64_t base = page * a.page_stride + h * a.head_stride;
-                const uint32_t buf = mine_addr + (i % kStages) * 2 * kTile;
-#pragma unroll
-                for (int c = 0; c < kBlockKeys * kChunks / 32; ++c) {
-                    const uint32_t idx = c * 32 + lane, row = idx / kChunks, chunk = idx % kChunks;
-                    const bool real = key + row < it.key1;  // past the range: zeros, whatever the page holds there
-                    const uint64_t off = base + ((key + row) & page_mask) * a.token_stride + chunk * 8;
-                    const uint32_t dst = buf + row * (D * 2) + ((chunk ^ (row & 7)) * 16);
-                    copy16(dst, kp + off, real);
-                    copy16(dst + kTile, vp + off, real);
-                }
-            }
-            asm volatile("cp.async.commit_group;\n" ::: "memory");
-        };
-
         float o[D / 8][4];
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
@@ -402,14 +430,12 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
             for (int j = 0; j < 4; ++j) o[n][j] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) issue(s);
-        for (uint32_t i = 0; i < n_mine; ++i) {
-            issue(i + kStages - 1);
+        for (uint32_t key = it.key0; key < it.key1; key += kBlockKeys) {
+            copy_next();
             asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
             __syncwarp();
-            const uint32_t buf = mine_addr + (i % kStages) * 2 * kTile;
-            const uint32_t key = it.key0 + (warp + kWarps * i) * kBlockKeys;
+            const uint32_t buf = mine + stage * 2 * kTile;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
             float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
@@ -470,57 +496,23 @@ __global__ void __launch_bounds__(kWarps * 32) attention_rows16_kernel(const Att
                 Elem<T>::mma(o[n * 2], p, b[0], b[1]);
                 Elem<T>::mma(o[n * 2 + 1], p, b[2], b[3]);
             }
-            __syncwarp();  // the buffer is read before it is filled again
+            __syncwarp();  // the stage is read before it is filled again
         }
-        asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 1);
             l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 2);
-        }
-
-        // the warps' sums meet: each scales its own to the common maximum
-        __syncthreads();
-        float* sm_ml = reinterpret_cast<float*>(smem);                       // [warp][16][2]
-        float* sm_o = reinterpret_cast<float*>(smem) + kWarps * 16 * 2;      // [warp][16][D]
-        static_assert(rows16_smem<D>() >= (kWarps * 16 * 2 + kWarps * 16 * D) * sizeof(float), "the sums fit the copies' space");
+            const uint32_t row = lane / 4 + half * 8;
+            if (row < it.rows) {
+                const uint64_t at = static_cast<uint64_t>(it.part_row + row) * a.kv_heads + h;
+                if (lane % 4 == 0) part_ml[at] = make_float2(m[half], l[half]);
+                float2* to = reinterpret_cast<float2*>(part_o + at * D + (lane % 4) * 2);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = lane / 4 + half * 8;
-            if (lane % 4 == 0) {
-                sm_ml[(warp * 16 + row) * 2] = m[half];
-                sm_ml[(warp * 16 + row) * 2 + 1] = l[half];
+                for (int n = 0; n < D / 8; ++n) to[n * 4] = make_float2(o[n][half * 2], o[n][half * 2 + 1]);
             }
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-                *reinterpret_cast<float2*>(sm_o + (warp * 16 + row) * D + n * 8 + (lane % 4) * 2) =
-                    make_float2(o[n][half * 2], o[n][half * 2 + 1]);
         }
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < it.rows * (D / 4); i += kWarps * 32) {
-            const uint32_t row = i / (D / 4), c = i % (D / 4);
-            float top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_ml[(w * 16 + row) * 2]);
-            const float ref = top == -INFINITY ? 0.0f : top;
-            float4 acc = make_float4(0, 0, 0, 0);
-            float sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2_approx(sm_ml[(w * 16 + row) * 2] - ref);
-                const float4 x = *reinterpret_cast<const float4*>(sm_o + (w * 16 + row) * D + c * 4);
-                sum += f * sm_ml[(w * 16 + row) * 2 + 1];
-                acc.x += f * x.x;
-                acc.y += f * x.y;
-                acc.z += f * x.z;
-                acc.w += f * x.w;
-            }
-            const uint64_t at = static_cast<uint64_t>(it.part_row + row) * a.kv_heads + h;
-            *reinterpret_cast<float4*>(part_o + at * D + c * 4) = acc;
-            if (c == 0) part_ml[at] = make_float2(top, sum);
-        }
-        __syncthreads();
     }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     if (a.tile_ctas) wait_for_earlier();
 }
 
