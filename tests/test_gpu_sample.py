@@ -145,6 +145,16 @@ def test_infinite_logits(afx):
         assert _run(afx, z, [0.2, 0.7], **params)[0] == [17, 5]
 
 
+@pytest.mark.parametrize("temperature", [1e-30, 1.0, 1e30, math.inf])
+def test_infinite_logits_at_temperatures_far_out(afx, temperature):
+    import torch
+    z = torch.randn((2, 3000), device="cuda")
+    z[0, 17], z[0, 2000] = math.inf, math.inf
+    z[1, 5], z[1, 9] = math.inf, -math.inf
+    for params in ({}, {"top_k": [3] * 2}, {"top_k": [2000] * 2}, {"top_p": [0.9] * 2}, {"min_p": [0.5] * 2}):
+        assert _run(afx, z, [0.7, 0.7], temperature=[temperature] * 2, **params)[0] == [2000, 5]
+
+
 def test_rows_of_the_types_lowest_value(afx):
     import torch
     for dtype in (torch.float32, torch.bfloat16, torch.float16):

@@ -14,17 +14,27 @@
 //
 // A row belongs to a cluster of CTAs; each keeps a slice of it in shared
 // memory, so the logits are read from memory once however many passes the
-// choice takes:
-//   1. load, maximum (ties: lowest index; at temperature 0 that is all);
-//   2. top-k or top-p: a histogram of counts and masses over 1024 equal
-//      steps of z between m and the last token with any mass, summed over
-//      the cluster; the step where the count (the mass) is reached holds
-//      the last token kept, which a pass over that step's tokens finds;
-//   3. the kept mass of every warp's run, their running sums over the
-//      cluster, and the run in which the aim falls, walked to the token.
+// choice takes.  Pass 1 gives every thread's and the row's maximum.  Then, by
+// what the row asks for:
+//   - temperature 0: the lowest index of the maximum;
+//   - top-k up to 1024 (with or without top-p and min-p): the k-th largest of
+//     the threads' maxima bounds the k-th largest logit from below, so the
+//     tokens from that bound on, a few more than k, go to one CTA, which
+//     sorts them and does the rest.  Only the threads whose maximum reaches
+//     the bound look at their tokens again;
+//   - no top-k, top-p 1: one pass of weights (min-p is a condition on each),
+//     then the run of tokens in which the aim falls, walked to the token;
+//   - top-p alone: the row's mass, a histogram of counts over equal steps of
+//     z (of the tokens that can matter: below y = ln((1 - p) S / V) lies too little
+//     mass), which tells within a step where the mass is reached; the exact mass above
+//     three steps around it, and those steps' tokens sorted in one CTA, give the last token kept;
+//   - anything else, and rows where a list above is too long (thousands of
+//     ties): a histogram of counts and masses refined until a list fits.
 // Bound: the read of the logits for many rows; for few rows the chain of
 // cluster barriers.
 #include <cooperative_groups.h>
+
+#include <utility>
 
 #include "afx_serving.cuh"
 
@@ -34,10 +44,13 @@ namespace afx {
 namespace serve {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;      // two CTAs an SM
 constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kBins = 1024;       // one a thread
-constexpr uint32_t kListMax = 1024;    // tokens whose order is worked out pair by pair
+constexpr uint32_t kBinBits = 9, kBins = 1u << kBinBits;  // one a thread
+static_assert(kBins == kThreads, "a bin a thread");
+constexpr uint32_t kListMax = 2048;    // tokens that one CTA sorts
+constexpr uint32_t kPer = kListMax / kThreads;
+constexpr uint32_t kTopMax = 1024;     // top-k that goes by the threads' maxima
 constexpr uint32_t kMaxCluster = 16;
 constexpr float kRange = 30.5f;        // e^-30.5 < 2^-44: no mass below m - 30.5 T
 constexpr float kMassOne = 17592186044416.0f;  // 2^44
@@ -49,24 +62,28 @@ struct SampleArgs {
     const int32_t* top_k;
     int32_t* tokens;
     float* logprobs;
-    uint32_t vocab, slice, wide;
+    uint32_t vocab, slice, run, wide;  // run: tokens of a warp
 };
 
-struct Shared {
-    uint64_t mass[kBins];          // this CTA's histogram
-    uint64_t all_mass[kBins];      // the cluster's
-    uint64_t list[kListMax];       // on rank 0: tokens of one step
-    uint64_t list_mass[kListMax];
+struct alignas(16) Shared {
+    // a list is made when the histograms of masses have been used
+    union {
+        struct {
+            uint64_t mass[kBins];      // this CTA's histogram
+            uint64_t all_mass[kBins];  // the cluster's
+        };
+        uint64_t list[kListMax];       // on rank 0: tokens to be sorted
+    };
     uint32_t count[kBins];
     uint32_t all_count[kBins];
     uint64_t scan[kWarps];
     uint32_t scan_count[kWarps];
-    uint64_t best[kMaxCluster];    // every rank's maximum
-    uint64_t lo[kMaxCluster], hi[kMaxCluster];  // every rank's smallest and largest key of a step
-    uint64_t total[kMaxCluster];   // every rank's kept mass
-    uint64_t threshold, kept_mass; // results of a selection
+    float top[kMaxCluster];            // every rank's maximum
+    uint64_t lo[kMaxCluster], hi[kMaxCluster];  // every rank's smallest and largest place of a step, or two masses
+    uint64_t total[kMaxCluster];       // every rank's kept mass
+    uint64_t threshold, kept_mass;     // results of a selection
     uint64_t found_mass;
-    uint32_t found_bin, found_count, list_n;
+    uint32_t found_bin, found_count, list_n, first;
 };
 
 // The order of float32 as unsigned integers.
@@ -128,8 +145,44 @@ __device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16* 
 template <>
 __device__ __forceinline__ float load_logit<__half>(const __half* p) { return __half2float(*p); }
 
-// NaN counts as masked; -0 and +0 are one value.
-__device__ __forceinline__ float clean(float z) { return z != z ? -INFINITY : z + 0.0f; }
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load4(const __half* p, float (&x)[4]) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+    x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+}
+
+// NaN counts as masked (a maximum passes over it); -0 and +0 are one value.
+__device__ __forceinline__ float clean(float z) { return fmaxf(z, -INFINITY) + 0.0f; }
+
+// Sums the CTAs' histograms into every CTA's all_count (and all_mass), which
+// nobody may be reading; before it, a cluster barrier behind the counting.
+// Rank r sums the bins r, r + ranks, ...: a group of `ranks` lanes a bin, each lane reads one
+// rank's count and hands the sum to one rank.
+__device__ void combine(cg::cluster_group& cluster, Shared& sh, bool masses) {
+    const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const uint32_t peer = threadIdx.x % ranks;
+    Shared* other = cluster.map_shared_rank(&sh, peer);
+    for (uint32_t b = rank + threadIdx.x / ranks * ranks; b < kBins; b += kThreads) {
+        uint32_t c = other->count[b];
+        uint64_t w = masses ? other->mass[b] : 0;
+        for (uint32_t d = 1; d < ranks; d <<= 1) {
+            c += __shfl_xor_sync(0xFFFFFFFFu, c, d);
+            if (masses) w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
+        }
+        other->all_count[b] = c;
+        if (masses) other->all_mass[b] = w;
+    }
+    cluster.sync();
+}
 
 // The cluster's histogram of the tokens with lo <= place <= hi in the bins
 // that bin_of gives, in every CTA's all_count and all_mass.
@@ -149,34 +202,22 @@ __device__ void histogram(cg::cluster_group& cluster, Shared& sh, const float* z
         if (w) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[b]), static_cast<unsigned long long>(w));
     }
     cluster.sync();
-    // rank r sums every ranks-th bin over the cluster and hands it to all
-    for (uint32_t b = rank + ranks * (threadIdx.x / ranks), peer = threadIdx.x % ranks; b < kBins && threadIdx.x / ranks < ceil_div(kBins, ranks);
-         b += ranks * (kThreads / ranks)) {
-        uint32_t c = 0;
-        uint64_t w = 0;
-        for (uint32_t r = 0; r < ranks; ++r) {
-            const Shared* other = cluster.map_shared_rank(&sh, r);
-            c += other->count[b];
-            w += other->mass[b];
-        }
-        Shared* to = cluster.map_shared_rank(&sh, peer);
-        to->all_count[b] = c;
-        to->all_mass[b] = w;
-    }
-    cluster.sync();
+    combine(cluster, sh, true);
 }
 
 // The first bin at which the running count (by_mass: mass) from `before`
-// reaches `aim`; found_count / found_mass: what runs before it.
-__device__ void find_bin(Shared& sh, uint64_t before_count, uint64_t before_mass, uint64_t aim, bool by_mass) {
+// reaches `aim`; found_count / found_mass: what runs before it (masses: there
+// is a histogram of them).
+__device__ void find_bin(Shared& sh, uint64_t before_count, uint64_t before_mass, uint64_t aim, bool by_mass, bool masses = true) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t c = sh.all_count[threadIdx.x], w = sh.all_mass[threadIdx.x];
+    const uint64_t c = sh.all_count[threadIdx.x], w = masses ? sh.all_mass[threadIdx.x] : 0;
     const uint64_t ic = warp_inclusive(c), iw = warp_inclusive(w);
     __syncthreads();
     if (lane == 31) {
         sh.scan[warp] = iw;
         sh.scan_count[warp] = static_cast<uint32_t>(ic);
     }
+    if (threadIdx.x == 0) sh.found_bin = kBins - 1;  // where the aim is not reached
     __syncthreads();
     uint64_t bc = before_count, bw = before_mass;
     for (int i = 0; i < warp; ++i) {
@@ -184,12 +225,85 @@ __device__ void find_bin(Shared& sh, uint64_t before_count, uint64_t before_mass
         bw += sh.scan[i];
     }
     const uint64_t from = by_mass ? bw + iw - w : bc + ic - c, to = by_mass ? bw + iw : bc + ic;
+    __syncthreads();
     if (from < aim && to >= aim) {
         sh.found_bin = threadIdx.x;
         sh.found_count = static_cast<uint32_t>(bc + ic - c);
         sh.found_mass = bw + iw - w;
     }
     __syncthreads();
+}
+
+// Sorts list[0 .. n), n <= kListMax, descending (kUp: ascending), by the
+// whole CTA.
+template <bool kUp>
+__device__ void sort_list(Shared& sh, uint32_t n) {
+    uint32_t size = 32;
+    while (size < n) size <<= 1;
+    for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = kUp ? ~uint64_t{0} : 0;
+    __syncthreads();
+    for (uint32_t span = 2; span <= size; span <<= 1)
+        for (uint32_t d = span >> 1; d; d >>= 1) {
+            for (uint32_t i = threadIdx.x; i < size / 2; i += kThreads) {
+                const uint32_t x = ((i & ~(d - 1)) << 1) | (i & (d - 1)), y = x + d;
+                const uint64_t p = sh.list[x], q = sh.list[y];
+                const bool up = ((x & span) == 0) == kUp;
+                if ((p > q) == up) {
+                    sh.list[x] = q;
+                    sh.list[y] = p;
+                }
+            }
+            if (size > 64)
+                __syncthreads();
+            else  // one warp has it all
+                __syncwarp();
+        }
+    __syncthreads();
+}
+
+// Exclusive running sums over the CTA's threads; *total gets the sum.
+__device__ uint64_t block_exclusive(Shared& sh, uint64_t v, uint64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint64_t inc = warp_inclusive(v);
+    __syncthreads();
+    if (lane == 31) sh.scan[warp] = inc;
+    __syncthreads();
+    const uint64_t run = warp_inclusive(lane < kWarps ? sh.scan[lane] : 0);
+    *total = __shfl_sync(0xFFFFFFFFu, run, 31);
+    const uint64_t before = warp ? __shfl_sync(0xFFFFFFFFu, run, warp - 1) : 0;
+    return before + inc - v;
+}
+
+__device__ __forceinline__ float place_value(uint64_t p) { return key_value(static_cast<uint32_t>(p >> 32)); }
+
+// Rank 0: list[0 .. n) holds the tokens around a boundary, before_count and
+// before_mass what comes before them.  Every rank's threshold gets the place
+// of the last token kept, kept_mass the mass kept with it.
+__device__ void last_kept(cg::cluster_group& cluster, Shared& sh, const Row& row, uint32_t n, uint64_t before_count, uint64_t before_mass,
+                          uint64_t aim, bool by_mass) {
+    sort_list<false>(sh, n);
+    uint64_t p[kPer], w[kPer], sum = 0, total;
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+        const uint32_t i = kPer * threadIdx.x + j;
+        p[j] = i < n ? sh.list[i] : 0;
+        w[j] = i < n ? row.mass(row.weight(place_value(p[j]))) : 0;
+        sum += w[j];
+    }
+    uint64_t mass = before_mass + block_exclusive(sh, sum, &total);
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+        const uint32_t i = kPer * threadIdx.x + j;
+        const uint64_t ahead = before_count + i;
+        const uint64_t from = by_mass ? mass : ahead, to = by_mass ? mass + w[j] : ahead + 1;
+        if (i < n && from < aim && to >= aim)
+            for (uint32_t r = 0; r < cluster.num_blocks(); ++r) {
+                Shared* other = cluster.map_shared_rank(&sh, r);
+                other->threshold = p[j];
+                other->kept_mass = mass + w[j];
+            }
+        mass += w[j];
+    }
 }
 
 // The place of the last token kept when the order's first tokens are kept
@@ -218,13 +332,13 @@ __device__ void select(cg::cluster_group& cluster, Shared& sh, const float* z, u
             b = warp_max(b);
             __syncthreads();
             if (threadIdx.x % 32 == 0) {
-                sh.list[threadIdx.x / 32] = a;
-                sh.list_mass[threadIdx.x / 32] = b;
+                sh.scan[threadIdx.x / 32] = a;
+                sh.mass[threadIdx.x / 32] = b;  // between two histograms
             }
             __syncthreads();
             if (threadIdx.x < 32) {
-                a = ~warp_max(~sh.list[threadIdx.x]);
-                b = warp_max(sh.list_mass[threadIdx.x]);
+                a = ~warp_max(threadIdx.x < kWarps ? ~sh.scan[threadIdx.x] : 0);
+                b = warp_max(threadIdx.x < kWarps ? sh.mass[threadIdx.x] : 0);
                 if (threadIdx.x < ranks) {
                     Shared* to = cluster.map_shared_rank(&sh, threadIdx.x);
                     to->lo[rank] = a;
@@ -238,9 +352,9 @@ __device__ void select(cg::cluster_group& cluster, Shared& sh, const float* z, u
             }
             by_bin = false;
         }
-        // [lo, hi] in up to 1024 equal steps of a power of two places
+        // [lo, hi] in up to kBins equal steps of a power of two places
         const uint64_t span = hi - lo;
-        const int shift = span >> 10 ? 64 - __clzll(static_cast<long long>(span >> 10)) : 0;
+        const int shift = span >> kBinBits ? 64 - __clzll(static_cast<long long>(span >> kBinBits)) : 0;
         histogram(cluster, sh, z, n, base, row, lo, hi, [&](float, uint64_t p) { return static_cast<uint32_t>((hi - p) >> shift); });
         find_bin(sh, before_count, before_mass, aim, by_mass);
         bin = sh.found_bin;
@@ -261,38 +375,94 @@ __device__ void select(cg::cluster_group& cluster, Shared& sh, const float* z, u
         const uint64_t p = place(z[i], base + i);
         if (by_bin ? row.bin(z[i]) != bin : (p < lo || p > hi)) continue;
         const uint32_t at = atomicAdd(&zero->list_n, 1u);
-        if (at < kListMax) {
-            zero->list[at] = p;
-            zero->list_mass[at] = row.mass(row.weight(z[i]));
-        }
+        if (at < kListMax) zero->list[at] = p;
     }
     cluster.sync();
     if (rank == 0) {
-        const uint32_t m = min(sh.list_n, kListMax);
-        if (threadIdx.x < m) {
-            const uint64_t p = sh.list[threadIdx.x], w = sh.list_mass[threadIdx.x];
-            uint64_t ahead = before_count, mass = before_mass;
-            for (uint32_t j = 0; j < m; ++j)
-                if (sh.list[j] > p) {
-                    ++ahead;
-                    mass += sh.list_mass[j];
-                }
-            const uint64_t from = by_mass ? mass : ahead, to = by_mass ? mass + w : ahead + 1;
-            if (from < aim && to >= aim)
-                for (uint32_t r = 0; r < ranks; ++r) {
-                    Shared* other = cluster.map_shared_rank(&sh, r);
-                    other->threshold = p;
-                    other->kept_mass = mass + w;
-                }
-        }
+        last_kept(cluster, sh, row, min(sh.list_n, kListMax), before_count, before_mass, aim, by_mass);
     }
     cluster.sync();
     *threshold = sh.threshold;
     *kept = sh.kept_mass;
 }
 
+struct Want {  // a row's parameters
+    uint32_t k;      // 0: no top-k
+    float p, least;  // p >= 1: no top-p
+    double u;
+};
+
+// floor(u * total), below total.
+__device__ __forceinline__ uint64_t aim_of(double u, uint64_t total) {
+    const double scaled = u > 0.0 ? u * static_cast<double>(total) : 0.0;
+    return scaled < static_cast<double>(total) ? min(static_cast<uint64_t>(scaled), total - 1) : total - 1;
+}
+// ceil(p * mass), from 1 to mass: what has to be reached.
+__device__ __forceinline__ uint64_t limit_of(float p, uint64_t mass) {
+    const double aim = ceil(static_cast<double>(p) * static_cast<double>(mass));
+    const uint64_t limit = aim >= 1.0 ? static_cast<uint64_t>(aim) : 1;
+    return limit < mass ? limit : mass;
+}
+
+__device__ __forceinline__ void write_token(const SampleArgs& a, uint32_t r, const Row& row, uint32_t token, float z, uint64_t total) {
+    a.tokens[r] = static_cast<int32_t>(token);
+    if (a.logprobs) a.logprobs[r] = row.scaled(z) - logf(static_cast<float>(total) * (1.0f / kMassOne));
+}
+
+// list[0 .. n) holds all tokens that can be kept: the rest of the row's
+// choice, by one CTA.
+__device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, const Row& row, const Want& want, uint32_t n) {
+    sort_list<false>(sh, n);
+    const uint32_t first = kPer * threadIdx.x, top = min(n, want.k);
+    uint64_t w[kPer], sum = 0, all;
+    float weight[kPer];
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+        weight[j] = first + j < top ? row.weight(place_value(sh.list[first + j])) : 0.0f;
+        w[j] = row.mass(weight[j]);
+        sum += w[j];
+    }
+    uint64_t before = block_exclusive(sh, sum, &all);
+    const uint64_t limit = want.p < 1.0f ? limit_of(want.p, all) : ~uint64_t{0};
+    // the kept tokens are the first ones of the sorted list
+    uint32_t kept = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+        kept += __syncthreads_count(first + j < top && before < limit && weight[j] >= want.least);
+        before += w[j];
+    }
+    // in the order of their indexes
+    uint64_t p[kPer];
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+        const uint64_t q = first + j < kept ? sh.list[first + j] : 0;
+        if (first + j < kept) sh.list[first + j] = static_cast<uint64_t>(0xFFFFFFFFu - static_cast<uint32_t>(q)) << 32 | (q >> 32);
+    }
+    __syncthreads();
+    sort_list<true>(sh, kept);
+    sum = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+        p[j] = first + j < kept ? sh.list[first + j] : 0;
+        w[j] = first + j < kept ? row.mass(row.weight(key_value(static_cast<uint32_t>(p[j])))) : 0;
+        sum += w[j];
+    }
+    uint64_t total;
+    before = block_exclusive(sh, sum, &total);
+    const uint64_t aim = aim_of(want.u, total);
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+        if (before <= aim && aim < before + w[j])
+            write_token(a, r, row, static_cast<uint32_t>(p[j] >> 32), key_value(static_cast<uint32_t>(p[j])), total);
+        before += w[j];
+    }
+}
+
+// A warp's run of the slice is contiguous; a lane has four tokens at a time.
+__device__ __forceinline__ uint32_t run_index(uint32_t run0, uint32_t i) { return run0 + i * 128 + (threadIdx.x & 31) * 4; }
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& sh = *reinterpret_cast<Shared*>(raw);
     float* z = reinterpret_cast<float*>(raw + sizeof(Shared));
@@ -301,106 +471,246 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
     const uint32_t r = blockIdx.x / ranks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = min(a.vocab, rank * a.slice), n = min(a.vocab - base, a.slice);
+    // this warp's run: a multiple of 128 tokens long, so that a lane's four are aligned
+    const uint32_t run0 = min(n, warp * a.run), run1 = min(n, run0 + a.run);
     const T* src = static_cast<const T*>(a.logits) + r * a.row_stride + base;
+    auto started = cluster.barrier_arrive();  // a rank's memory may be written once its CTA runs
+    wait_for_earlier();
+    let_next_start();
 
-    uint64_t best = 0;
-    if (a.wide) {
-        constexpr uint32_t kPer = 16 / sizeof(T);
-        for (uint32_t i = threadIdx.x * kPer; i < n; i += kThreads * kPer) {
-            if (i + kPer <= n) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + i));
-                const T* e = reinterpret_cast<const T*>(&v);
+    // pass 1: the slice into shared memory, NaN as minus infinity and -0 as 0; the thread's maximum
+    float mine = -INFINITY;
+    constexpr uint32_t kBatch = 5;  // loads in flight a lane
+    for (uint32_t i0 = 0; run0 + i0 * 128 < run1; i0 += kBatch) {
+        float x[kBatch][4];
 #pragma unroll
-                for (uint32_t j = 0; j < kPer; ++j) {
-                    const float x = clean(static_cast<float>(e[j]));
-                    z[i + j] = x;
-                    const uint64_t p = place(x, base + i + j);
-                    best = p > best ? p : best;
-                }
+        for (uint32_t j = 0; j < kBatch; ++j) {
+            const uint32_t at = run_index(run0, i0 + j);
+            if (a.wide && at + 4 <= run1) {
+                load4(src + at, x[j]);
             } else {
-                for (uint32_t j = i; j < n; ++j) {
-                    z[j] = clean(load_logit(src + j));
-                    const uint64_t p = place(z[j], base + j);
-                    best = p > best ? p : best;
-                }
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c) x[j][c] = at + c < run1 ? load_logit(src + at + c) : -INFINITY;
             }
         }
-    } else {
-        for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-            z[i] = clean(load_logit(src + i));
-            const uint64_t p = place(z[i], base + i);
-            best = p > best ? p : best;
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; ++j) {
+            const uint32_t at = run_index(run0, i0 + j);
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) x[j][c] = clean(x[j][c]);
+            mine = fmaxf(mine, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
+            if (at < run1) *reinterpret_cast<float4*>(z + at) = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
         }
     }
-    best = warp_max(best);
-    if (lane == 0) sh.scan[warp] = best;
-    __syncthreads();
-    if (warp == 0) {
-        best = warp_max(sh.scan[lane]);
-        if (lane < static_cast<int>(ranks)) cluster.map_shared_rank(&sh, lane)->best[rank] = best;
+    {
+        float top = mine;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        float* warps = reinterpret_cast<float*>(sh.scan);
+        if (lane == 0) warps[warp] = top;
+        sh.count[threadIdx.x] = 0;
+        if (threadIdx.x == 0) {
+            sh.list_n = 0;
+            sh.first = 0xFFFFFFFFu;
+        }
+        __syncthreads();
+        cluster.barrier_wait(std::move(started));
+        if (warp == 0) {
+            top = lane < kWarps ? warps[lane] : -INFINITY;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            if (lane < static_cast<int>(ranks)) cluster.map_shared_rank(&sh, lane)->top[rank] = top;
+        }
     }
     cluster.sync();
-    for (uint32_t i = 0; i < ranks; ++i) best = (i == 0 || sh.best[i] > best) ? sh.best[i] : best;
     Row row;
-    row.top = key_value(static_cast<uint32_t>(best >> 32));
+    row.top = sh.top[0];
+    for (uint32_t i = 1; i < ranks; ++i) row.top = fmaxf(row.top, sh.top[i]);
     const float temp = a.temperature ? a.temperature[r] : 1.0f;
-    if (row.top == -INFINITY || !(temp > 0.0f)) {  // nothing to draw from, or the maximum itself
+    if (row.top == -INFINITY) {  // nothing to draw from
         if (rank == 0 && threadIdx.x == 0) {
-            const bool none = row.top == -INFINITY;
-            a.tokens[r] = none ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-            if (a.logprobs) a.logprobs[r] = none ? -INFINITY : 0.0f;
+            a.tokens[r] = -1;
+            if (a.logprobs) a.logprobs[r] = -INFINITY;
         }
         return;  // the whole cluster: no rank reads another's memory any more
     }
-    row.inv_t = 1.0f / temp;
+    Shared* zero = cluster.map_shared_rank(&sh, 0);
+    auto each = [&](auto&& f) {  // this thread's tokens
+        for (uint32_t i = 0; run0 + i * 128 < run1; ++i) {
+            const uint32_t at = run_index(run0, i);
+            if (at >= run1) break;
+            const float4 v = *reinterpret_cast<const float4*>(z + at);
+            f(at, v.x);
+            if (at + 1 < run1) f(at + 1, v.y);
+            if (at + 2 < run1) f(at + 2, v.z);
+            if (at + 3 < run1) f(at + 3, v.w);
+        }
+    };
+    if (!(temp > 0.0f)) {  // the maximum itself
+        if (mine == row.top)
+            each([&](uint32_t i, float x) {
+                if (x == row.top) atomicMin(&zero->first, base + i);
+            });
+        cluster.sync();
+        if (rank == 0 && threadIdx.x == 0) {
+            a.tokens[r] = static_cast<int32_t>(sh.first);
+            if (a.logprobs) a.logprobs[r] = 0.0f;
+        }
+        return;
+    }
+    row.inv_t = temp == INFINITY ? 1.17549435e-38f : 1.0f / temp;  // not 0: masked logits stay minus infinity
     row.step = static_cast<float>(kBins) / (kRange * temp);
-
+    Want want;
     const int32_t k = a.top_k ? a.top_k[r] : 0;
-    const float p = a.top_p ? a.top_p[r] : 1.0f;
+    want.k = k > 0 && static_cast<uint32_t>(k) < a.vocab ? k : 0;
+    want.p = a.top_p ? a.top_p[r] : 1.0f;
+    if (!(want.p < 1.0f)) want.p = 1.0f;
     const float min_p = a.min_p ? a.min_p[r] : 0.0f;
-    const float least = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
-    const bool by_k = k > 0 && static_cast<uint32_t>(k) < a.vocab, by_p = p < 1.0f;
+    want.least = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
+    want.u = static_cast<double>(a.u[r]);
+    // a bound below every logit of the first `bins` steps, and of every token with mass
+    auto lower_bound = [&](uint32_t bins) {
+        if (row.top == INFINITY) return row.top;
+        const float span = __fmul_ru(__fdiv_ru(static_cast<float>(bins), row.step), 1.000002f);
+        return __fsub_rd(row.top, span);
+    };
+
     uint64_t threshold = 0;  // places from here on are kept
-    if (by_k || by_p) {
+    bool general = true;
+    if (want.k && want.k <= kTopMax) {
+        // the k-th largest of the threads' maxima: at least k tokens are as large (with fewer maxima: all that have mass)
+        if (mine > -INFINITY) atomicAdd(&sh.count[row.bin(mine)], 1u);
+        cluster.sync();
+        combine(cluster, sh, false);
+        find_bin(sh, 0, 0, want.k, false, false);
+        const uint32_t bin = sh.found_bin;
+        const float low = lower_bound(min(bin + 1, kBins));
+        if (mine >= low)
+            each([&](uint32_t i, float x) {
+                if (x >= low) {
+                    const uint32_t at = atomicAdd(&zero->list_n, 1u);
+                    if (at < kListMax) zero->list[at] = place(x, base + i);
+                }
+            });
+        cluster.sync();
+        const uint32_t listed = zero->list_n;
+        cluster.sync();  // every rank has read it: rank 0 may end
+        if (listed <= kListMax) {
+            if (rank == 0) draw_from_list(a, r, sh, row, want, listed);
+            return;
+        }
+    } else if (!want.k) {
+        general = false;
+        if (want.p < 1.0f) {
+            // the row's mass
+            uint64_t mass = 0;
+            each([&](uint32_t, float x) { mass += row.mass(row.weight(x)); });
+            uint64_t slice_mass, all = 0;
+            block_exclusive(sh, mass, &slice_mass);
+            if (threadIdx.x < ranks) cluster.map_shared_rank(&sh, threadIdx.x)->total[rank] = slice_mass;
+            cluster.sync();
+            for (uint32_t i = 0; i < ranks; ++i) all += sh.total[i];
+            const uint64_t limit = limit_of(want.p, all);
+            // Tokens of weight below (1 - p) S / V have less than (1 - p) S together: the limit is reached
+            // before them (half of it, for the rounding of this float32 line)
+            const float floor_w = fminf(0.5f * (1.0f - fmaxf(want.p, 0.0f)) * (static_cast<float>(all) * (1.0f / kMassOne)) / static_cast<float>(a.vocab), 0.5f);
+            const float low = fmaxf(lower_bound(kBins), __fsub_rd(row.top, __fmul_ru(-logf(fmaxf(floor_w, 1e-30f)), temp)));
+            if (mine >= low)
+                each([&](uint32_t, float x) {
+                    if (x >= low) atomicAdd(&sh.count[row.bin(x)], 1u);
+                });
+            cluster.sync();
+            combine(cluster, sh, false);
+            // where the limit is reached, by counts and the weight of a step's middle
+            {
+                const float middle = __expf((static_cast<float>(threadIdx.x) + 0.5f) * (-kRange / kBins));
+                const uint64_t about = static_cast<uint64_t>(static_cast<float>(sh.all_count[threadIdx.x]) * middle * kMassOne);
+                uint64_t sum;
+                const uint64_t before = block_exclusive(sh, about, &sum);
+                if (threadIdx.x == 0) sh.found_bin = kBins - 1;
+                __syncthreads();
+                if (before < limit && before + about >= limit) sh.found_bin = threadIdx.x;
+                __syncthreads();
+            }
+            const uint32_t bin = sh.found_bin, b0 = bin ? bin - 1 : 0, b1 = min(bin + 1, kBins - 1);
+            uint32_t listed = 0;
+            for (uint32_t b = b0; b <= b1; ++b) listed += sh.all_count[b];
+            // the exact masses before and of those steps
+            uint64_t above = 0, inside = 0;
+            const float low2 = lower_bound(b1 + 1);
+            if (mine >= low2)
+                each([&](uint32_t i, float x) {
+                    if (x < low2) return;
+                    const uint32_t b = row.bin(x);
+                    if (b > b1 || x < low) return;
+                    const uint64_t w = row.mass(row.weight(x));
+                    if (b < b0) {
+                        above += w;
+                    } else {
+                        inside += w;
+                        if (listed <= kListMax) {
+                            const uint32_t at = atomicAdd(&zero->list_n, 1u);
+                            if (at < kListMax) zero->list[at] = place(x, base + i);
+                        }
+                    }
+                });
+            uint64_t slice_above, slice_inside;
+            block_exclusive(sh, above, &slice_above);
+            block_exclusive(sh, inside, &slice_inside);
+            if (threadIdx.x < ranks) {
+                Shared* other = cluster.map_shared_rank(&sh, threadIdx.x);
+                other->lo[rank] = slice_above;
+                other->hi[rank] = slice_inside;
+            }
+            cluster.sync();
+            above = inside = 0;
+            for (uint32_t i = 0; i < ranks; ++i) {
+                above += sh.lo[i];
+                inside += sh.hi[i];
+            }
+            if (listed <= kListMax && above < limit && limit <= above + inside) {
+                if (rank == 0) last_kept(cluster, sh, row, listed, 0, above, limit, true);
+                cluster.sync();
+                threshold = sh.threshold;
+            } else {
+                general = true;
+            }
+        }
+    }
+    if (general) {
+        cluster.sync();  // the histograms and lists above are done with
         histogram(cluster, sh, z, n, base, row, 0, ~uint64_t{0}, [&](float x, uint64_t) { return row.bin(x); });
         uint64_t kept = 0;
         const uint32_t mine_c = sh.all_count[threadIdx.x];
         const uint64_t mine_w = sh.all_mass[threadIdx.x];
-        if (by_k) {
-            select(cluster, sh, z, n, base, row, static_cast<uint64_t>(k), false, &threshold, &kept);
+        if (want.k) {
+            select(cluster, sh, z, n, base, row, want.k, false, &threshold, &kept);
         } else {
-            const uint64_t w = warp_sum(sh.all_mass[threadIdx.x]);
-            if (lane == 0) sh.scan[warp] = w;
-            __syncthreads();
-            for (int i = 0; i < kWarps; ++i) kept += sh.scan[i];
-            __syncthreads();
+            block_exclusive(sh, mine_w, &kept);
         }
-        if (by_p) {
-            const double aim = ceil(static_cast<double>(p) * static_cast<double>(kept));
-            const uint64_t limit = aim >= 1.0 ? static_cast<uint64_t>(aim) : 1;
+        if (want.p < 1.0f) {
+            __syncthreads();
             sh.all_count[threadIdx.x] = mine_c;  // a selection may have refined the histogram
             sh.all_mass[threadIdx.x] = mine_w;
             __syncthreads();
             uint64_t t2, unused;
-            select(cluster, sh, z, n, base, row, limit < kept ? limit : kept, true, &t2, &unused);
+            select(cluster, sh, z, n, base, row, limit_of(want.p, kept), true, &t2, &unused);
             threshold = t2 > threshold ? t2 : threshold;
         }
     }
 
-    // the kept mass of every warp's run of the slice
-    const uint32_t run = ceil_div(a.slice, kWarps), i0 = min(n, warp * run), i1 = min(n, i0 + run);
-    auto kept_mass = [&](uint32_t i) -> uint64_t {
-        if (i >= i1) return 0;
-        const float x = z[i];
-        if (place(x, base + i) < threshold) return 0;
+    // the kept mass of every warp's run
+    const float low = threshold ? place_value(threshold) : lower_bound(kBins);
+    auto kept_mass = [&](uint32_t i, float x) -> uint64_t {
+        if (x < low || place(x, base + i) < threshold) return 0;
         const float w = row.weight(x);
-        return w >= least ? row.mass(w) : 0;
+        return w >= want.least ? row.mass(w) : 0;
     };
-    uint64_t mine = 0;
-    for (uint32_t i = i0 + lane; i < i1; i += 32) mine += kept_mass(i);
-    mine = warp_sum(mine);
+    uint64_t mass = 0;
+    if (mine >= low) each([&](uint32_t i, float x) { mass += kept_mass(i, x); });
+    mass = warp_sum(mass);
     __syncthreads();
-    if (lane == 0) sh.scan[warp] = mine;
+    if (lane == 0) sh.scan[warp] = mass;
     __syncthreads();
     uint64_t before = 0, slice_total = 0;
     for (int i = 0; i < kWarps; ++i) {
@@ -415,18 +725,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
         if (i < rank) before += sh.total[i];
         total += sh.total[i];
     }
-    const double u = static_cast<double>(a.u[r]);
-    const double scaled = u > 0.0 ? u * static_cast<double>(total) : 0.0;
-    const uint64_t aim = scaled < static_cast<double>(total) ? min(static_cast<uint64_t>(scaled), total - 1) : total - 1;
-    if (before <= aim && aim < before + mine) {  // the aim falls into this warp's run
-        for (uint32_t i = i0; i < i1; i += 32) {
-            const uint64_t w = kept_mass(i + lane), inc = warp_inclusive(w);
-            const bool here = before + inc - w <= aim && aim < before + inc;
-            if (here) {
-                a.tokens[r] = static_cast<int32_t>(base + i + lane);
-                if (a.logprobs)
-                    a.logprobs[r] = row.scaled(z[i + lane]) - logf(static_cast<float>(total) * (1.0f / kMassOne));
-            }
+    const uint64_t aim = aim_of(want.u, total);
+    if (before <= aim && aim < before + mass) {  // the aim falls into this warp's run
+        for (uint32_t i = run0; i < run1; i += 32) {
+            const uint32_t at = i + lane;
+            const uint64_t w = at < run1 ? kept_mass(at, z[at]) : 0, inc = warp_inclusive(w);
+            if (before + inc - w <= aim && aim < before + inc) write_token(a, r, row, base + at, z[at], total);
             before += __shfl_sync(0xFFFFFFFFu, inc, 31);
             if (before > aim) break;
         }
@@ -447,12 +751,14 @@ afx_status launch(const SampleArgs& a, uint32_t rows, uint32_t ranks, cudaStream
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ranks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
     AFX_SERVE_TRY(cudaLaunchKernelEx(&cfg, sample_kernel<T>, a), "sample_kernel launch");
     return AFX_OK;
 }
@@ -490,8 +796,16 @@ extern "C" afx_status afx_sample(const void* logits_dev, uint32_t type, uint32_t
     a.tokens = tokens_dev;
     a.logprobs = logprobs_dev;
     a.vocab = vocab;
-    const uint32_t ranks = vocab > 65536 ? 16 : vocab > 8192 ? 8 : 1;
+    // CTAs a row: as few as hold it in 32,768 tokens each (the barriers cost
+    // less), more while the GPU has two CTAs an SM to give and 4096 tokens are left for each
+    const int sms = current_sms();
+    if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
+    uint32_t ranks = 1;
+    while (ranks < kMaxCluster &&
+           (vocab / ranks > 32768 - 128 || (vocab / ranks > 4096 && static_cast<uint64_t>(rows) * ranks * 2 <= static_cast<uint64_t>(sms) * 2)))
+        ranks *= 2;
     a.slice = ceil_div(ceil_div(vocab, ranks), 128) * 128;
+    a.run = ceil_div(a.slice, kWarps * 128) * 128;
     a.wide = !((reinterpret_cast<uintptr_t>(logits_dev) | (rows > 1 ? row_stride * size : 0)) & 15u);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (type == AFX_LOGITS_F32) return launch<float>(a, rows, ranks, s);
