@@ -18,16 +18,16 @@
 // what the row asks for:
 //   - temperature 0: the lowest index of the maximum;
 //   - top-k up to 1024 (with or without top-p and min-p): the k-th largest of
-//     the threads' maxima bounds the k-th largest logit from below, so the
+//     the warps' (for larger k the threads') maxima bounds the k-th largest logit from below, so the
 //     tokens from that bound on, a few more than k, go to one CTA, which
-//     sorts them and does the rest.  Only the threads whose maximum reaches
+//     orders them and does the rest.  Only the threads whose maximum reaches
 //     the bound look at their tokens again;
 //   - no top-k, top-p 1: one pass of weights (min-p is a condition on each),
 //     then the run of tokens in which the aim falls, walked to the token;
-//   - top-p alone: the row's mass, a histogram of counts over equal steps of
-//     z (of the tokens that can matter: below y = ln((1 - p) S / V) lies too little
-//     mass), which tells within a step where the mass is reached; the exact mass above
-//     three steps around it, and those steps' tokens sorted in one CTA, give the last token kept;
+//   - top-p alone: the row's mass and the mass above a few cuts in y; a histogram of masses over equal steps of
+//     z between two cuts, whose masses say which step the boundary is in; the
+//     tokens of that step, ordered in one CTA, give the last token kept (where
+//     few tokens lie above the cut, they go to one CTA at once);
 //   - anything else, and rows where a list above is too long (thousands of
 //     ties): a histogram of counts and masses refined until a list fits.
 // Bound: the read of the logits for many rows; for few rows the chain of
@@ -46,12 +46,14 @@ namespace {
 
 constexpr int kThreads = 512;      // two CTAs an SM
 constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kBinBits = 9, kBins = 1u << kBinBits;  // one a thread
+constexpr uint32_t kBinBits = kThreads == 512 ? 9 : 8, kBins = 1u << kBinBits;  // one a thread
 static_assert(kBins == kThreads, "a bin a thread");
 constexpr uint32_t kListMax = 2048;    // tokens that one CTA sorts
 constexpr uint32_t kPer = kListMax / kThreads;
 constexpr uint32_t kTopMax = 1024;     // top-k that goes by the threads' maxima
 constexpr uint32_t kMaxCluster = 16;
+constexpr uint32_t kShort = 256;       // tokens that are ordered pair by pair
+constexpr int kCuts = 5;               // weights above e^-2, e^-4, ..., e^-10 tell how far down top-p reaches
 constexpr float kRange = 30.5f;        // e^-30.5 < 2^-44: no mass below m - 30.5 T
 constexpr float kMassOne = 17592186044416.0f;  // 2^44
 
@@ -74,16 +76,22 @@ struct alignas(16) Shared {
         };
         uint64_t list[kListMax];       // on rank 0: tokens to be sorted
     };
-    uint32_t count[kBins];
-    uint32_t all_count[kBins];
+    uint32_t count[kBins], coarse[kBins], fine[kBins];  // this CTA's counts, and masses in 2^-22 and 2^-44
+    uint32_t all_count[kBins];         // the cluster's
     uint64_t scan[kWarps];
     uint32_t scan_count[kWarps];
-    float top[kMaxCluster];            // every rank's maximum
-    uint64_t lo[kMaxCluster], hi[kMaxCluster];  // every rank's smallest and largest place of a step, or two masses
+    float top[kMaxCluster * kWarps];   // every warp's maximum, rank by rank
+    uint64_t lo[kMaxCluster], hi[kMaxCluster];  // every rank's smallest and largest place of a step
+    uint64_t part[kMaxCluster];        // every rank's mass above the steps
     uint64_t total[kMaxCluster];       // every rank's kept mass
     uint64_t threshold, kept_mass;     // results of a selection
     uint64_t found_mass;
-    uint32_t found_bin, found_count, list_n, first;
+    uint64_t bins[kBins];              // masses by steps, of the cluster or of a list
+    uint64_t short_key[kShort], short_mass[kShort];
+    uint64_t found_key, found_before;
+    uint32_t found_bin, found_count, list_n, first, short_n;
+    float bound;
+    float above[kCuts][kMaxCluster];   // every rank's weight above the cuts
 };
 
 // The order of float32 as unsigned integers.
@@ -101,8 +109,8 @@ __device__ __forceinline__ uint64_t place(float z, uint32_t index) {
 
 struct Row {
     float top, inv_t, step;  // m, 1 / T, bins a unit of z
-    // y and w of a logit; w as an integer of 2^-44
-    __device__ float scaled(float z) const { return z == top ? 0.0f : (z == -INFINITY ? -INFINITY : (z - top) * inv_t); }
+    // y and w of a logit (top is finite, inv_t above 0); w as an integer of 2^-44
+    __device__ float scaled(float z) const { return (z - top) * inv_t; }
     __device__ float weight(float z) const { return expf(scaled(z)); }
     __device__ uint64_t mass(float w) const { return static_cast<uint64_t>(w * kMassOne); }
     // 0 for the maximum, never smaller for a smaller z
@@ -110,6 +118,27 @@ struct Row {
         if (z == top) return 0;
         const float b = (top - z) * step;
         return b < static_cast<float>(kBins - 1) ? static_cast<uint32_t>(b) : kBins - 1;
+    }
+};
+
+// A sum of weights as integers of 2^-44, without a conversion a weight: adding
+// 2 leaves the weight's multiple of 2^-22 in the sum's last bits; what is
+// left, at most 2^-23, added to 1.5 * 2^-21 and rounded down, leaves its
+// multiple of 2^-44 there.  The bits are added up as they are and the
+// constants taken off at the end (up to 1023 weights).
+struct MassSum {
+    uint32_t hi = 0, lo = 0, n = 0;
+    static constexpr float kHi = 2.0f, kLo = 1.5f / 2097152.0f;
+    __device__ __forceinline__ void add(float w) {
+        const float t = __fadd_rn(w, kHi);
+        hi += __float_as_uint(t);
+        lo += __float_as_uint(__fadd_rd(__fsub_rn(w, __fsub_rn(t, kHi)), kLo));
+        ++n;
+    }
+    __device__ __forceinline__ uint64_t total() const {
+        const uint32_t h = hi - n * __float_as_uint(kHi);
+        const int32_t l = static_cast<int32_t>(lo - n * __float_as_uint(kLo));
+        return (static_cast<uint64_t>(h) << 22) + static_cast<uint64_t>(static_cast<int64_t>(l));
     }
 };
 
@@ -163,23 +192,25 @@ __device__ __forceinline__ void load4(const __half* p, float (&x)[4]) {
 // NaN counts as masked (a maximum passes over it); -0 and +0 are one value.
 __device__ __forceinline__ float clean(float z) { return fmaxf(z, -INFINITY) + 0.0f; }
 
-// Sums the CTAs' histograms into every CTA's all_count (and all_mass), which
+// Sums the CTAs' histograms into every CTA's all_count (all_mass, or bins from
+// coarse and fine), which
 // nobody may be reading; before it, a cluster barrier behind the counting.
 // Rank r sums the bins r, r + ranks, ...: a group of `ranks` lanes a bin, each lane reads one
 // rank's count and hands the sum to one rank.
-__device__ void combine(cg::cluster_group& cluster, Shared& sh, bool masses) {
+__device__ void combine(cg::cluster_group& cluster, Shared& sh, bool masses, bool parts = false) {
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t peer = threadIdx.x % ranks;
     Shared* other = cluster.map_shared_rank(&sh, peer);
     for (uint32_t b = rank + threadIdx.x / ranks * ranks; b < kBins; b += kThreads) {
         uint32_t c = other->count[b];
-        uint64_t w = masses ? other->mass[b] : 0;
+        uint64_t w = masses ? other->mass[b] : parts ? (static_cast<uint64_t>(other->coarse[b]) << 22) + other->fine[b] : 0;
         for (uint32_t d = 1; d < ranks; d <<= 1) {
             c += __shfl_xor_sync(0xFFFFFFFFu, c, d);
-            if (masses) w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
+            if (masses || parts) w += __shfl_xor_sync(0xFFFFFFFFu, w, d);
         }
         other->all_count[b] = c;
         if (masses) other->all_mass[b] = w;
+        if (parts) other->bins[b] = w;
     }
     cluster.sync();
 }
@@ -234,33 +265,6 @@ __device__ void find_bin(Shared& sh, uint64_t before_count, uint64_t before_mass
     __syncthreads();
 }
 
-// Sorts list[0 .. n), n <= kListMax, descending (kUp: ascending), by the
-// whole CTA.
-template <bool kUp>
-__device__ void sort_list(Shared& sh, uint32_t n) {
-    uint32_t size = 32;
-    while (size < n) size <<= 1;
-    for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = kUp ? ~uint64_t{0} : 0;
-    __syncthreads();
-    for (uint32_t span = 2; span <= size; span <<= 1)
-        for (uint32_t d = span >> 1; d; d >>= 1) {
-            for (uint32_t i = threadIdx.x; i < size / 2; i += kThreads) {
-                const uint32_t x = ((i & ~(d - 1)) << 1) | (i & (d - 1)), y = x + d;
-                const uint64_t p = sh.list[x], q = sh.list[y];
-                const bool up = ((x & span) == 0) == kUp;
-                if ((p > q) == up) {
-                    sh.list[x] = q;
-                    sh.list[y] = p;
-                }
-            }
-            if (size > 64)
-                __syncthreads();
-            else  // one warp has it all
-                __syncwarp();
-        }
-    __syncthreads();
-}
-
 // Exclusive running sums over the CTA's threads; *total gets the sum.
 __device__ uint64_t block_exclusive(Shared& sh, uint64_t v, uint64_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -274,35 +278,137 @@ __device__ uint64_t block_exclusive(Shared& sh, uint64_t v, uint64_t* total) {
     return before + inc - v;
 }
 
+// Up to kShort elements are ordered by counting: several threads an element
+// compare it with all others.
+struct Element {
+    uint32_t e, part, parts;  // this thread's element, and which part of the others it looks at
+    __device__ explicit Element(uint32_t n) {
+        uint32_t size = 64;
+        while (size < n) size <<= 1;
+        parts = kThreads / size;
+        e = threadIdx.x / parts;
+        part = threadIdx.x % parts;
+    }
+    __device__ uint64_t over_parts(uint64_t v) const {
+        for (uint32_t d = 1; d < parts; d <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+        return v;
+    }
+};
+
+// Which of a list's elements (kPer a thread: key and mass, no two keys alike)
+// is the last needed when they are taken by falling key until their mass,
+// from `before` on, reaches aim; aim is reached by all of them.  found_key gets its key and found_before the mass
+// before it.  bin_of: the step a key falls into, never smaller for a smaller key.
+template <typename BinOf>
+__device__ void reach(Shared& sh, const uint64_t (&key)[kPer], const uint64_t (&mass)[kPer], uint64_t before, uint64_t aim, BinOf bin_of) {
+    __syncthreads();
+    sh.bins[threadIdx.x] = 0;
+    sh.count[threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        sh.short_n = sh.found_bin = 0;
+        sh.found_before = before;
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j)
+        if (mass[j]) {
+            const uint32_t b = bin_of(key[j]);
+            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[b]), static_cast<unsigned long long>(mass[j]));
+            atomicAdd(&sh.count[b], 1u);
+        }
+    __syncthreads();
+    uint64_t all;
+    const uint64_t mine = sh.bins[threadIdx.x], from = before + block_exclusive(sh, mine, &all);
+    if (from < aim && aim <= from + mine) {
+        sh.found_bin = threadIdx.x;
+        sh.found_before = from;
+    }
+    __syncthreads();
+    const uint32_t bin = sh.found_bin, n = sh.count[bin];
+    if (n > kShort) {
+        // (ties) bit by bit: the largest key from which on the mass reaches the aim
+        uint64_t t = 0;
+        for (uint64_t bit = uint64_t{1} << 63; bit; bit >>= 1) {
+            uint64_t sum = 0, total;
+#pragma unroll
+            for (uint32_t j = 0; j < kPer; ++j) sum += key[j] >= (t | bit) ? mass[j] : 0;
+            block_exclusive(sh, sum, &total);
+            if (before + total >= aim) t |= bit;
+        }
+        uint64_t sum = 0, total;
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) sum += key[j] > t ? mass[j] : 0;
+        block_exclusive(sh, sum, &total);
+        if (threadIdx.x == 0) {
+            sh.found_key = t;
+            sh.found_before = before + total;
+        }
+        __syncthreads();
+        return;
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j)
+        if (mass[j] && bin_of(key[j]) == bin) {
+            const uint32_t at = atomicAdd(&sh.short_n, 1u);
+            sh.short_key[at] = key[j];
+            sh.short_mass[at] = mass[j];
+        }
+    __syncthreads();
+    const Element el(n);
+    const uint64_t own = el.e < n ? sh.short_key[el.e] : 0;
+    uint64_t ahead = 0;
+    for (uint32_t j = el.part; j < n; j += el.parts)
+        if (sh.short_key[j] > own) ahead += sh.short_mass[j];
+    ahead = sh.found_before + el.over_parts(ahead);
+    __syncthreads();
+    if (el.e < n && el.part == 0 && ahead < aim && aim <= ahead + sh.short_mass[el.e]) {
+        sh.found_key = own;
+        sh.found_before = ahead;
+    }
+    __syncthreads();
+}
+
 __device__ __forceinline__ float place_value(uint64_t p) { return key_value(static_cast<uint32_t>(p >> 32)); }
+
+// Steps of z that cover the list's n tokens, as a Row's are.
+__device__ void list_steps(Shared& sh, Row& row, const uint64_t (&p)[kPer], uint32_t n) {
+    uint64_t least = ~uint64_t{0};
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j)
+        if (threadIdx.x + j * kThreads < n) least = p[j] < least ? p[j] : least;
+    least = ~warp_max(~least);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sh.scan[threadIdx.x / 32] = ~least;
+    __syncthreads();
+    least = ~warp_max(threadIdx.x % 32 < kWarps ? sh.scan[threadIdx.x % 32] : 0);
+    const float span = row.top - place_value(least);
+    if (span > 0.0f && span < INFINITY) row.step = static_cast<float>(kBins) / span;
+}
 
 // Rank 0: list[0 .. n) holds the tokens around a boundary, before_count and
 // before_mass what comes before them.  Every rank's threshold gets the place
 // of the last token kept, kept_mass the mass kept with it.
-__device__ void last_kept(cg::cluster_group& cluster, Shared& sh, const Row& row, uint32_t n, uint64_t before_count, uint64_t before_mass,
+__device__ void last_kept(cg::cluster_group& cluster, Shared& sh, Row row, uint32_t n, uint64_t before_count, uint64_t before_mass,
                           uint64_t aim, bool by_mass) {
-    sort_list<false>(sh, n);
-    uint64_t p[kPer], w[kPer], sum = 0, total;
+    uint64_t p[kPer], w[kPer], mass[kPer];
 #pragma unroll
     for (uint32_t j = 0; j < kPer; ++j) {
-        const uint32_t i = kPer * threadIdx.x + j;
+        const uint32_t i = threadIdx.x + j * kThreads;
         p[j] = i < n ? sh.list[i] : 0;
         w[j] = i < n ? row.mass(row.weight(place_value(p[j]))) : 0;
-        sum += w[j];
+        mass[j] = by_mass ? w[j] : i < n ? 1 : 0;
     }
-    uint64_t mass = before_mass + block_exclusive(sh, sum, &total);
+    list_steps(sh, row, p, n);
+    reach(sh, p, mass, by_mass ? before_mass : before_count, aim, [&](uint64_t q) { return row.bin(place_value(q)); });
+    const uint64_t last = sh.found_key;
+    uint64_t kept = 0, total;
 #pragma unroll
-    for (uint32_t j = 0; j < kPer; ++j) {
-        const uint32_t i = kPer * threadIdx.x + j;
-        const uint64_t ahead = before_count + i;
-        const uint64_t from = by_mass ? mass : ahead, to = by_mass ? mass + w[j] : ahead + 1;
-        if (i < n && from < aim && to >= aim)
-            for (uint32_t r = 0; r < cluster.num_blocks(); ++r) {
-                Shared* other = cluster.map_shared_rank(&sh, r);
-                other->threshold = p[j];
-                other->kept_mass = mass + w[j];
-            }
-        mass += w[j];
+    for (uint32_t j = 0; j < kPer; ++j) kept += p[j] >= last ? w[j] : 0;
+    block_exclusive(sh, kept, &total);
+    if (threadIdx.x < cluster.num_blocks()) {
+        Shared* other = cluster.map_shared_rank(&sh, threadIdx.x);
+        other->threshold = last;
+        other->kept_mass = before_mass + total;
     }
 }
 
@@ -386,6 +492,12 @@ __device__ void select(cg::cluster_group& cluster, Shared& sh, const float* z, u
     *kept = sh.kept_mass;
 }
 
+// e^-2 .. e^-10
+__device__ __forceinline__ constexpr float cut_weight(int c) {
+    constexpr float w[kCuts] = {0.135335283f, 0.0183156389f, 0.00247875218f, 0.000335462628f, 4.53999298e-05f};
+    return w[c];
+}
+
 struct Want {  // a row's parameters
     uint32_t k;      // 0: no top-k
     float p, least;  // p >= 1: no top-p
@@ -410,52 +522,80 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, uint32_t r, con
 }
 
 // list[0 .. n) holds all tokens that can be kept: the rest of the row's
-// choice, by one CTA.
-__device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, const Row& row, const Want& want, uint32_t n) {
-    sort_list<false>(sh, n);
-    const uint32_t first = kPer * threadIdx.x, top = min(n, want.k);
-    uint64_t w[kPer], sum = 0, all;
-    float weight[kPer];
+// choice, by one CTA.  row_mass: what top-p is a share of, 0 for the mass of
+// what top-k keeps.
+__device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row row, const Want& want, uint32_t n, uint64_t row_mass) {
+    const uint32_t k = want.k ? want.k : n;
+    if (n <= kShort) {
+        const Element el(n);
+        const bool real = el.e < n, one = real && el.part == 0;
+        const uint64_t mine = real ? sh.list[el.e] : 0;
+        const float weight = real ? row.weight(place_value(mine)) : 0.0f;
+        const uint64_t w = real ? row.mass(weight) : 0;
+        if (one) sh.short_mass[el.e] = w;
+        __syncthreads();
+        uint64_t ahead = 0, before = 0, all, total;
+        for (uint32_t j = el.part; j < n; j += el.parts)
+            if (sh.list[j] > mine) {
+                ++ahead;
+                before += sh.short_mass[j];
+            }
+        ahead = el.over_parts(ahead);
+        before = el.over_parts(before);
+        const bool by_k = real && ahead < k;
+        block_exclusive(sh, by_k && one ? w : 0, &all);
+        const uint64_t limit = want.p < 1.0f ? limit_of(want.p, row_mass ? row_mass : all) : ~uint64_t{0};
+        const uint64_t kept = by_k && before < limit && weight >= want.least ? w : 0;
+        if (one) sh.bins[el.e] = kept;
+        block_exclusive(sh, one ? kept : 0, &total);  // a barrier as well
+        before = 0;
+        for (uint32_t j = el.part; j < n; j += el.parts)  // lower indexes have larger low halves
+            if (static_cast<uint32_t>(sh.list[j]) > static_cast<uint32_t>(mine)) before += sh.bins[j];
+        before = el.over_parts(before);
+        const uint64_t aim = aim_of(want.u, total);
+        if (one && before <= aim && aim < before + kept)
+            write_token(a, r, row, 0xFFFFFFFFu - static_cast<uint32_t>(mine), place_value(mine), total);
+        return;
+    }
+    uint64_t p[kPer] = {}, mass[kPer], threshold = 0, sum = 0, all;
+    auto weight = [&](uint32_t j) { return row.weight(place_value(p[j])); };
 #pragma unroll
     for (uint32_t j = 0; j < kPer; ++j) {
-        weight[j] = first + j < top ? row.weight(place_value(sh.list[first + j])) : 0.0f;
-        w[j] = row.mass(weight[j]);
-        sum += w[j];
+        const uint32_t i = threadIdx.x + j * kThreads;
+        p[j] = i < n ? sh.list[i] : 0;
+        mass[j] = i < n ? 1 : 0;
     }
-    uint64_t before = block_exclusive(sh, sum, &all);
-    const uint64_t limit = want.p < 1.0f ? limit_of(want.p, all) : ~uint64_t{0};
-    // the kept tokens are the first ones of the sorted list
-    uint32_t kept = 0;
+    list_steps(sh, row, p, n);
+    auto step_of = [&](uint64_t q) { return row.bin(place_value(q)); };
+    if (n > k) {
+        reach(sh, p, mass, 0, k, step_of);
+        threshold = sh.found_key;
+    }
 #pragma unroll
     for (uint32_t j = 0; j < kPer; ++j) {
-        kept += __syncthreads_count(first + j < top && before < limit && weight[j] >= want.least);
-        before += w[j];
+        mass[j] = mass[j] && p[j] >= threshold ? row.mass(weight(j)) : 0;
+        sum += mass[j];
     }
-    // in the order of their indexes
-    uint64_t p[kPer];
-#pragma unroll
-    for (uint32_t j = 0; j < kPer; ++j) {
-        const uint64_t q = first + j < kept ? sh.list[first + j] : 0;
-        if (first + j < kept) sh.list[first + j] = static_cast<uint64_t>(0xFFFFFFFFu - static_cast<uint32_t>(q)) << 32 | (q >> 32);
+    block_exclusive(sh, sum, &all);
+    if (want.p < 1.0f) {
+        reach(sh, p, mass, 0, limit_of(want.p, row_mass ? row_mass : all), step_of);
+        threshold = sh.found_key > threshold ? sh.found_key : threshold;
     }
-    __syncthreads();
-    sort_list<true>(sh, kept);
     sum = 0;
 #pragma unroll
     for (uint32_t j = 0; j < kPer; ++j) {
-        p[j] = first + j < kept ? sh.list[first + j] : 0;
-        w[j] = first + j < kept ? row.mass(row.weight(key_value(static_cast<uint32_t>(p[j])))) : 0;
-        sum += w[j];
+        mass[j] = p[j] >= threshold && mass[j] && weight(j) >= want.least ? mass[j] : 0;
+        sum += mass[j];
+        p[j] = (p[j] & 0xFFFFFFFFu) << 32 | (p[j] >> 32);  // by index, the lowest first
     }
     uint64_t total;
-    before = block_exclusive(sh, sum, &total);
-    const uint64_t aim = aim_of(want.u, total);
+    block_exclusive(sh, sum, &total);
+    const uint32_t share = ceil_div(a.vocab, kBins);
+    reach(sh, p, mass, 0, aim_of(want.u, total) + 1, [&](uint64_t q) { return (0xFFFFFFFFu - static_cast<uint32_t>(q >> 32)) / share; });
 #pragma unroll
-    for (uint32_t j = 0; j < kPer; ++j) {
-        if (before <= aim && aim < before + w[j])
-            write_token(a, r, row, static_cast<uint32_t>(p[j] >> 32), key_value(static_cast<uint32_t>(p[j])), total);
-        before += w[j];
-    }
+    for (uint32_t j = 0; j < kPer; ++j)
+        if (mass[j] && p[j] == sh.found_key)
+            write_token(a, r, row, 0xFFFFFFFFu - static_cast<uint32_t>(p[j] >> 32), key_value(static_cast<uint32_t>(p[j])), total);
 }
 
 // A warp's run of the slice is contiguous; a lane has four tokens at a time.
@@ -508,24 +648,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         float* warps = reinterpret_cast<float*>(sh.scan);
         if (lane == 0) warps[warp] = top;
-        sh.count[threadIdx.x] = 0;
+        sh.count[threadIdx.x] = sh.coarse[threadIdx.x] = sh.fine[threadIdx.x] = 0;
         if (threadIdx.x == 0) {
             sh.list_n = 0;
             sh.first = 0xFFFFFFFFu;
         }
         __syncthreads();
         cluster.barrier_wait(std::move(started));
-        if (warp == 0) {
-            top = lane < kWarps ? warps[lane] : -INFINITY;
-#pragma unroll
-            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            if (lane < static_cast<int>(ranks)) cluster.map_shared_rank(&sh, lane)->top[rank] = top;
-        }
+        // a warp's maximum to a rank: kWarps * ranks <= kThreads
+        if (threadIdx.x < kWarps * ranks)
+            cluster.map_shared_rank(&sh, threadIdx.x / kWarps)->top[rank * kWarps + threadIdx.x % kWarps] = warps[threadIdx.x % kWarps];
     }
     cluster.sync();
     Row row;
-    row.top = sh.top[0];
-    for (uint32_t i = 1; i < ranks; ++i) row.top = fmaxf(row.top, sh.top[i]);
+    row.top = -INFINITY;
+    for (uint32_t i = lane; i < kWarps * ranks; i += 32) row.top = fmaxf(row.top, sh.top[i]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) row.top = fmaxf(row.top, __shfl_xor_sync(0xFFFFFFFFu, row.top, d));
     const float temp = a.temperature ? a.temperature[r] : 1.0f;
     if (row.top == -INFINITY) {  // nothing to draw from
         if (rank == 0 && threadIdx.x == 0) {
@@ -559,6 +698,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         return;
     }
     row.inv_t = temp == INFINITY ? 1.17549435e-38f : 1.0f / temp;  // not 0: masked logits stay minus infinity
+    const bool infinite = row.top == INFINITY;
+    if (infinite) {  // infinite logits share everything: as zeros among masked ones
+        each([&](uint32_t i, float x) { z[i] = x == INFINITY ? 0.0f : -INFINITY; });
+        mine = mine == INFINITY ? 0.0f : -INFINITY;
+        row.top = 0.0f;
+        __syncthreads();
+    }
     row.step = static_cast<float>(kBins) / (kRange * temp);
     Want want;
     const int32_t k = a.top_k ? a.top_k[r] : 0;
@@ -570,105 +716,160 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     want.u = static_cast<double>(a.u[r]);
     // a bound below every logit of the first `bins` steps, and of every token with mass
     auto lower_bound = [&](uint32_t bins) {
-        if (row.top == INFINITY) return row.top;
         const float span = __fmul_ru(__fdiv_ru(static_cast<float>(bins), row.step), 1.000002f);
         return __fsub_rd(row.top, span);
     };
 
-    uint64_t threshold = 0;  // places from here on are kept
-    bool general = true;
-    if (want.k && want.k <= kTopMax) {
-        // the k-th largest of the threads' maxima: at least k tokens are as large (with fewer maxima: all that have mass)
-        if (mine > -INFINITY) atomicAdd(&sh.count[row.bin(mine)], 1u);
-        cluster.sync();
-        combine(cluster, sh, false);
-        find_bin(sh, 0, 0, want.k, false, false);
-        const uint32_t bin = sh.found_bin;
-        const float low = lower_bound(min(bin + 1, kBins));
+    // the places of this row's tokens that `pick` takes, all at least low, into rank 0's list, if they fit: one
+    // reservation a CTA
+    auto push = [&](float low, auto&& pick) {
+        uint32_t picked = 0;
         if (mine >= low)
+            each([&](uint32_t, float x) { picked += pick(x); });
+        uint64_t of_cta;
+        uint32_t at = static_cast<uint32_t>(block_exclusive(sh, picked, &of_cta));
+        if (threadIdx.x == 0) sh.short_n = of_cta ? atomicAdd(&zero->list_n, static_cast<uint32_t>(of_cta)) : 0;
+        __syncthreads();
+        at += sh.short_n;
+        if (picked && sh.short_n + of_cta <= kListMax)
             each([&](uint32_t i, float x) {
-                if (x >= low) {
-                    const uint32_t at = atomicAdd(&zero->list_n, 1u);
-                    if (at < kListMax) zero->list[at] = place(x, base + i);
-                }
+                if (pick(x)) zero->list[at++] = place(x, base + i);
             });
         cluster.sync();
+    };
+    // after a push: draws from the list and tells whether the row is done
+    auto draw = [&](uint64_t row_mass) {
         const uint32_t listed = zero->list_n;
-        cluster.sync();  // every rank has read it: rank 0 may end
-        if (listed <= kListMax) {
-            if (rank == 0) draw_from_list(a, r, sh, row, want, listed);
-            return;
+        auto read = cluster.barrier_arrive();  // every rank has read it once this barrier is through
+        if (listed <= kListMax && rank) return true;
+        if (listed <= kListMax) draw_from_list(a, r, sh, row, want, listed, row_mass);
+        cluster.barrier_wait(std::move(read));
+        return listed <= kListMax;
+    };
+    uint64_t threshold = 0;  // places from here on are kept
+    bool general = true;
+    const uint32_t n_warps = kWarps * ranks;
+    if (want.k && want.k <= kTopMax) {
+        // the k-th largest of maxima of k groups or more: at least k tokens are as large
+        float low;
+        if (want.k <= n_warps - n_warps / 4 && !infinite) {
+            // of the warps'; a warp without tokens has minus infinity, and ends the count below k
+            if (threadIdx.x < n_warps) {
+                const float x = sh.top[threadIdx.x];
+                uint32_t larger = 0, as_large = 0;
+                for (uint32_t i = 0; i < n_warps; ++i) {
+                    larger += sh.top[i] > x;
+                    as_large += sh.top[i] >= x;
+                }
+                if (larger < want.k && as_large >= want.k) sh.bound = x;  // the same value in every thread that finds it
+            }
+            __syncthreads();
+            low = fmaxf(sh.bound, lower_bound(kBins));
+        } else {
+            // of the threads' (with fewer maxima: all that have mass)
+            if (mine > -INFINITY) atomicAdd(&sh.count[row.bin(mine)], 1u);
+            cluster.sync();
+            combine(cluster, sh, false);
+            find_bin(sh, 0, 0, want.k, false, false);
+            low = lower_bound(min(sh.found_bin + 1, kBins));
         }
+        push(low, [&](float x) { return x >= low; });
+        if (draw(0)) return;
     } else if (!want.k) {
         general = false;
         if (want.p < 1.0f) {
             // the row's mass
-            uint64_t mass = 0;
-            each([&](uint32_t, float x) { mass += row.mass(row.weight(x)); });
+            MassSum sums;
+            float cut[kCuts] = {};
+            each([&](uint32_t, float x) {
+                const float w = row.weight(x);
+                sums.add(w);
+#pragma unroll
+                for (int c = 0; c < kCuts; ++c) cut[c] += w > cut_weight(c) ? w : 0.0f;
+            });
             uint64_t slice_mass, all = 0;
-            block_exclusive(sh, mass, &slice_mass);
-            if (threadIdx.x < ranks) cluster.map_shared_rank(&sh, threadIdx.x)->total[rank] = slice_mass;
-            cluster.sync();
-            for (uint32_t i = 0; i < ranks; ++i) all += sh.total[i];
-            const uint64_t limit = limit_of(want.p, all);
-            // Tokens of weight below (1 - p) S / V have less than (1 - p) S together: the limit is reached
-            // before them (half of it, for the rounding of this float32 line)
-            const float floor_w = fminf(0.5f * (1.0f - fmaxf(want.p, 0.0f)) * (static_cast<float>(all) * (1.0f / kMassOne)) / static_cast<float>(a.vocab), 0.5f);
-            const float low = fmaxf(lower_bound(kBins), __fsub_rd(row.top, __fmul_ru(-logf(fmaxf(floor_w, 1e-30f)), temp)));
-            if (mine >= low)
-                each([&](uint32_t, float x) {
-                    if (x >= low) atomicAdd(&sh.count[row.bin(x)], 1u);
-                });
-            cluster.sync();
-            combine(cluster, sh, false);
-            // where the limit is reached, by counts and the weight of a step's middle
-            {
-                const float middle = __expf((static_cast<float>(threadIdx.x) + 0.5f) * (-kRange / kBins));
-                const uint64_t about = static_cast<uint64_t>(static_cast<float>(sh.all_count[threadIdx.x]) * middle * kMassOne);
-                uint64_t sum;
-                const uint64_t before = block_exclusive(sh, about, &sum);
-                if (threadIdx.x == 0) sh.found_bin = kBins - 1;
-                __syncthreads();
-                if (before < limit && before + about >= limit) sh.found_bin = threadIdx.x;
-                __syncthreads();
+            float* of_warps = reinterpret_cast<float*>(sh.bins);
+#pragma unroll
+            for (int c = 0; c < kCuts; ++c) {
+#pragma unroll
+                for (int d = 16; d; d >>= 1) cut[c] += __shfl_xor_sync(0xFFFFFFFFu, cut[c], d);
+                if (lane == 0) of_warps[c * kWarps + warp] = cut[c];
             }
-            const uint32_t bin = sh.found_bin, b0 = bin ? bin - 1 : 0, b1 = min(bin + 1, kBins - 1);
-            uint32_t listed = 0;
-            for (uint32_t b = b0; b <= b1; ++b) listed += sh.all_count[b];
-            // the exact masses before and of those steps
-            uint64_t above = 0, inside = 0;
-            const float low2 = lower_bound(b1 + 1);
-            if (mine >= low2)
-                each([&](uint32_t i, float x) {
-                    if (x < low2) return;
-                    const uint32_t b = row.bin(x);
-                    if (b > b1 || x < low) return;
-                    const uint64_t w = row.mass(row.weight(x));
-                    if (b < b0) {
-                        above += w;
-                    } else {
-                        inside += w;
-                        if (listed <= kListMax) {
-                            const uint32_t at = atomicAdd(&zero->list_n, 1u);
-                            if (at < kListMax) zero->list[at] = place(x, base + i);
-                        }
-                    }
-                });
-            uint64_t slice_above, slice_inside;
-            block_exclusive(sh, above, &slice_above);
-            block_exclusive(sh, inside, &slice_inside);
+            block_exclusive(sh, sums.total(), &slice_mass);
             if (threadIdx.x < ranks) {
                 Shared* other = cluster.map_shared_rank(&sh, threadIdx.x);
-                other->lo[rank] = slice_above;
-                other->hi[rank] = slice_inside;
+                other->total[rank] = slice_mass;
+                for (int c = 0; c < kCuts; ++c) {
+                    float sum = 0.0f;
+                    for (int w = 0; w < kWarps; ++w) sum += of_warps[c * kWarps + w];
+                    other->above[c][rank] = sum;
+                }
             }
             cluster.sync();
-            above = inside = 0;
-            for (uint32_t i = 0; i < ranks; ++i) {
-                above += sh.lo[i];
-                inside += sh.hi[i];
+            for (uint32_t i = 0; i < ranks; ++i) all += sh.total[i];
+            // a cut above which there is more than top-p needs: if few tokens are there, they are all that matters
+            int far = kCuts;
+            for (int c = kCuts - 1; c >= 0; --c) {
+                float sum = 0.0f;
+                for (uint32_t i = 0; i < ranks; ++i) sum += sh.above[c][i];
+                if (sum >= want.p * 1.0002f * static_cast<float>(all) * (1.0f / kMassOne)) far = c;
             }
-            if (listed <= kListMax && above < limit && limit <= above + inside) {
+            if (far < kCuts) {
+                const float low = __fsub_rd(row.top, __fmul_ru(2.00001f * static_cast<float>(far + 1), temp));
+                push(low, [&](float x) { return x >= low; });
+                if (draw(all)) return;
+                if (rank == 0 && threadIdx.x == 0) sh.list_n = 0;  // barriers follow before the next push
+            }
+            const uint64_t limit = limit_of(want.p, all);
+            // Otherwise steps of z between the cut before that and that one.  Past the last cut: tokens of weight
+            // below (1 - p) S / V have less than (1 - p) S together, so the limit is reached before them (half of it,
+            // for the rounding of this float32 line)
+            const float floor_w = fminf(0.5f * (1.0f - fmaxf(want.p, 0.0f)) * (static_cast<float>(all) * (1.0f / kMassOne)) / static_cast<float>(a.vocab), 0.5f);
+            const float low = far < kCuts ? __fsub_rd(row.top, __fmul_ru(2.00001f * static_cast<float>(far + 1), temp))
+                                          : fmaxf(lower_bound(kBins), __fsub_rd(row.top, __fmul_ru(-logf(fmaxf(floor_w, 1e-30f)), temp)));
+            const float high = far ? fmaxf(low, row.top - 2.0f * static_cast<float>(far) * temp) : row.top;
+            const float span = high - low, step = span > 0.0f && span < INFINITY ? static_cast<float>(kBins) / span : 1.0f;
+            auto step_of = [&](float x) {  // of low <= x <= high
+                const float b = (high - x) * step;
+                return b < static_cast<float>(kBins - 1) ? static_cast<uint32_t>(b) : kBins - 1;
+            };
+            // the exact mass above the steps, and of each step in two parts of 22 bits (right for up to 1023 tokens)
+            MassSum over;
+            if (mine >= low)
+                each([&](uint32_t, float x) {
+                    if (x < low) return;
+                    const float w = row.weight(x);
+                    if (x > high) {
+                        over.add(w);
+                    } else {
+                        const uint32_t b = step_of(x);
+                        const uint64_t m = row.mass(w);
+                        atomicAdd(&sh.count[b], 1u);
+                        atomicAdd(&sh.coarse[b], static_cast<uint32_t>(m >> 22));
+                        atomicAdd(&sh.fine[b], static_cast<uint32_t>(m) & 0x3FFFFFu);
+                    }
+                });
+            block_exclusive(sh, over.total(), &slice_mass);
+            if (threadIdx.x < ranks) cluster.map_shared_rank(&sh, threadIdx.x)->part[rank] = slice_mass;
+            cluster.sync();
+            combine(cluster, sh, false, true);
+            uint64_t above = 0, unused;
+            for (uint32_t i = 0; i < ranks; ++i) above += sh.part[i];
+            const uint64_t inside = sh.bins[threadIdx.x], from = above + block_exclusive(sh, inside, &unused);
+            if (threadIdx.x == 0) sh.found_bin = kBins;
+            __syncthreads();
+            if (from < limit && limit <= from + inside) {
+                sh.found_bin = threadIdx.x;
+                sh.found_mass = from;
+            }
+            __syncthreads();
+            // the tokens of the step where the limit is reached
+            const uint32_t bin = sh.found_bin;
+            const bool right = !__syncthreads_or(threadIdx.x <= bin && sh.all_count[threadIdx.x] > 1023);
+            const uint32_t listed = bin < kBins && right ? sh.all_count[bin] : kListMax + 1;
+            if (listed <= kListMax) {
+                above = sh.found_mass;
+                push(low, [&](float x) { return x >= low && x <= high && step_of(x) == bin; });
                 if (rank == 0) last_kept(cluster, sh, row, listed, 0, above, limit, true);
                 cluster.sync();
                 threshold = sh.threshold;
@@ -706,9 +907,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const float w = row.weight(x);
         return w >= want.least ? row.mass(w) : 0;
     };
-    uint64_t mass = 0;
-    if (mine >= low) each([&](uint32_t i, float x) { mass += kept_mass(i, x); });
-    mass = warp_sum(mass);
+    MassSum sums;
+    if (threshold == 0) {
+        each([&](uint32_t, float x) {
+            const float w = row.weight(x);
+            sums.add(w >= want.least ? w : 0.0f);
+        });
+    } else if (mine >= low) {
+        each([&](uint32_t i, float x) {
+            if (x < low || place(x, base + i) < threshold) return;
+            const float w = row.weight(x);
+            sums.add(w >= want.least ? w : 0.0f);
+        });
+    }
+    uint64_t mass = warp_sum(sums.total());
     __syncthreads();
     if (lane == 0) sh.scan[warp] = mass;
     __syncthreads();
