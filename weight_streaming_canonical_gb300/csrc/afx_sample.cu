@@ -52,8 +52,10 @@ constexpr uint32_t kListMax = 2048;    // tokens that one CTA sorts
 constexpr uint32_t kPer = kListMax / kThreads;
 constexpr uint32_t kTopMax = 1024;     // top-k that goes by the threads' maxima
 constexpr uint32_t kMaxCluster = 16;
+constexpr uint32_t kTooMany = 1u << 26;
 constexpr uint32_t kShort = 256;       // tokens that are ordered pair by pair
 constexpr int kCuts = 5;               // weights above e^-2, e^-4, ..., e^-10 tell how far down top-p reaches
+constexpr uint32_t kQueue = 160;       // tokens a warp has found and not yet dealt with: 31 and 128 more
 constexpr float kRange = 30.5f;        // e^-30.5 < 2^-44: no mass below m - 30.5 T
 constexpr float kMassOne = 17592186044416.0f;  // 2^44
 
@@ -86,13 +88,20 @@ struct alignas(16) Shared {
     uint64_t total[kMaxCluster];       // every rank's kept mass
     uint64_t threshold, kept_mass;     // results of a selection
     uint64_t found_mass;
-    uint64_t bins[kBins];              // masses by steps, of the cluster or of a list
-    uint64_t short_key[kShort], short_mass[kShort];
+    union {  // a warp's queue is empty when the others are used
+        struct {
+            uint64_t bins[kBins];      // masses by steps, of the cluster or of a list
+            uint64_t short_key[kShort], short_mass[kShort];
+        };
+        uint16_t queue[kWarps][kQueue];
+    };
     uint64_t found_key, found_before;
     uint32_t found_bin, found_count, list_n, first, short_n;
     float bound;
     float above[kCuts][kMaxCluster];   // every rank's weight above the cuts
 };
+
+static_assert(2 * (sizeof(Shared) + 19008 * sizeof(float) + 1024) <= 228 * 1024, "two CTAs an SM at 152,064 tokens over eight");
 
 // The order of float32 as unsigned integers.
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -203,6 +212,7 @@ __device__ void combine(cg::cluster_group& cluster, Shared& sh, bool masses, boo
     Shared* other = cluster.map_shared_rank(&sh, peer);
     for (uint32_t b = rank + threadIdx.x / ranks * ranks; b < kBins; b += kThreads) {
         uint32_t c = other->count[b];
+        if (parts && c > 1023) c = kTooMany;  // its parts may have wrapped
         uint64_t w = masses ? other->mass[b] : parts ? (static_cast<uint64_t>(other->coarse[b]) << 22) + other->fine[b] : 0;
         for (uint32_t d = 1; d < ranks; d <<= 1) {
             c += __shfl_xor_sync(0xFFFFFFFFu, c, d);
@@ -675,15 +685,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     Shared* zero = cluster.map_shared_rank(&sh, 0);
     auto each = [&](auto&& f) {  // this thread's tokens
-        for (uint32_t i = 0; run0 + i * 128 < run1; ++i) {
-            const uint32_t at = run_index(run0, i);
-            if (at >= run1) break;
+        uint32_t at = run_index(run0, 0), i = run0;
+        for (; i + 128 <= run1; i += 128, at += 128) {
             const float4 v = *reinterpret_cast<const float4*>(z + at);
             f(at, v.x);
-            if (at + 1 < run1) f(at + 1, v.y);
-            if (at + 2 < run1) f(at + 2, v.z);
-            if (at + 3 < run1) f(at + 3, v.w);
+            f(at + 1, v.y);
+            f(at + 2, v.z);
+            f(at + 3, v.w);
         }
+        for (uint32_t c = 0; c < 4 && at + c < run1; ++c) f(at + c, z[at + c]);
+    };
+    // f for the warp's tokens that pick takes, all at least low: they are collected first, so that the lanes work
+    // together where only a few tokens are meant
+    auto few = [&](float low, auto&& pick, auto&& f) {
+        if (!__any_sync(0xFFFFFFFFu, mine >= low)) return;
+        uint16_t* q = sh.queue[warp];
+        uint32_t n_q = 0;
+        for (uint32_t i = run0; i < run1; i += 128) {
+            const uint32_t at = i + lane * 4;
+            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (at < run1) v = *reinterpret_cast<const float4*>(z + at);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) {
+                const bool take = at + c < run1 && pick(x[c]);
+                const uint32_t taken = __ballot_sync(0xFFFFFFFFu, take);
+                if (take) q[n_q + __popc(taken & ((1u << lane) - 1))] = static_cast<uint16_t>(at + c);
+                n_q += __popc(taken);
+            }
+            __syncwarp();
+            while (n_q >= 32) {
+                n_q -= 32;
+                const uint32_t j = q[n_q + lane];
+                f(j, z[j]);
+                __syncwarp();
+            }
+        }
+        if (lane < static_cast<int>(n_q)) f(q[lane], z[q[lane]]);
+        __syncwarp();
     };
     if (!(temp > 0.0f)) {  // the maximum itself
         if (mine == row.top)
@@ -754,15 +793,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         float low;
         if (want.k <= n_warps - n_warps / 4 && !infinite) {
             // of the warps'; a warp without tokens has minus infinity, and ends the count below k
-            if (threadIdx.x < n_warps) {
-                const float x = sh.top[threadIdx.x];
-                uint32_t larger = 0, as_large = 0;
-                for (uint32_t i = 0; i < n_warps; ++i) {
-                    larger += sh.top[i] > x;
-                    as_large += sh.top[i] >= x;
-                }
-                if (larger < want.k && as_large >= want.k) sh.bound = x;  // the same value in every thread that finds it
+            const uint32_t parts = kThreads / n_warps, e = threadIdx.x / parts;  // threads a maximum
+            const float x = sh.top[e];
+            uint32_t larger = 0, as_large = 0;
+            for (uint32_t i = threadIdx.x % parts; i < n_warps; i += parts) {
+                larger += sh.top[i] > x;
+                as_large += sh.top[i] >= x;
             }
+            for (uint32_t d = 1; d < parts; d <<= 1) {
+                larger += __shfl_xor_sync(0xFFFFFFFFu, larger, d);
+                as_large += __shfl_xor_sync(0xFFFFFFFFu, as_large, d);
+            }
+            if (larger < want.k && as_large >= want.k) sh.bound = x;  // the same value in every thread that finds it
             __syncthreads();
             low = fmaxf(sh.bound, lower_bound(kBins));
         } else {
@@ -785,7 +827,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 const float w = row.weight(x);
                 sums.add(w);
 #pragma unroll
-                for (int c = 0; c < kCuts; ++c) cut[c] += w > cut_weight(c) ? w : 0.0f;
+                for (int c = 0; c < kCuts; ++c)
+                    if (w > cut_weight(c)) cut[c] += w;
             });
             uint64_t slice_mass, all = 0;
             float* of_warps = reinterpret_cast<float*>(sh.bins);
@@ -835,20 +878,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             };
             // the exact mass above the steps, and of each step in two parts of 22 bits (right for up to 1023 tokens)
             MassSum over;
-            if (mine >= low)
-                each([&](uint32_t, float x) {
-                    if (x < low) return;
-                    const float w = row.weight(x);
-                    if (x > high) {
-                        over.add(w);
-                    } else {
-                        const uint32_t b = step_of(x);
-                        const uint64_t m = row.mass(w);
-                        atomicAdd(&sh.count[b], 1u);
-                        atomicAdd(&sh.coarse[b], static_cast<uint32_t>(m >> 22));
-                        atomicAdd(&sh.fine[b], static_cast<uint32_t>(m) & 0x3FFFFFu);
-                    }
-                });
+            few(low, [&](float x) { return x >= low; }, [&](uint32_t, float x) {
+                const float w = row.weight(x);
+                if (x > high) {
+                    over.add(w);
+                } else {
+                    const uint32_t b = step_of(x);
+                    const uint64_t m = row.mass(w);
+                    atomicAdd(&sh.count[b], 1u);
+                    atomicAdd(&sh.coarse[b], static_cast<uint32_t>(m >> 22));
+                    atomicAdd(&sh.fine[b], static_cast<uint32_t>(m) & 0x3FFFFFu);
+                }
+            });
             block_exclusive(sh, over.total(), &slice_mass);
             if (threadIdx.x < ranks) cluster.map_shared_rank(&sh, threadIdx.x)->part[rank] = slice_mass;
             cluster.sync();
@@ -865,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             __syncthreads();
             // the tokens of the step where the limit is reached
             const uint32_t bin = sh.found_bin;
-            const bool right = !__syncthreads_or(threadIdx.x <= bin && sh.all_count[threadIdx.x] > 1023);
+            const bool right = !__syncthreads_or(threadIdx.x <= bin && sh.all_count[threadIdx.x] >= kTooMany);
             const uint32_t listed = bin < kBins && right ? sh.all_count[bin] : kListMax + 1;
             if (listed <= kListMax) {
                 above = sh.found_mass;
@@ -913,9 +954,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             const float w = row.weight(x);
             sums.add(w >= want.least ? w : 0.0f);
         });
-    } else if (mine >= low) {
-        each([&](uint32_t i, float x) {
-            if (x < low || place(x, base + i) < threshold) return;
+    } else {
+        few(low, [&](float x) { return x >= low; }, [&](uint32_t i, float x) {
+            if (place(x, base + i) < threshold) return;
             const float w = row.weight(x);
             sums.add(w >= want.least ? w : 0.0f);
         });
