@@ -37,6 +37,7 @@ struct TablesArgs {
     int32_t *starts, *slots, *positions;
     int32_t* status;
     uint32_t n, cols, n_pages, max_tokens, shift;  // P = 1 << shift
+    uint32_t wide;  // slots and positions are 16-byte aligned
 };
 
 struct Sums {
@@ -60,20 +61,22 @@ __device__ Sums block_exclusive(Sums v, Sums* total) {
     }
     if (lane == 31) warp_sums[warp] = inc;
     __syncthreads();
-    Sums before{0, 0, 0}, all{0, 0, 0};
-    for (int w = 0; w < kTabThreads / 32; ++w) {
-        const Sums s = warp_sums[w];
-        if (w < warp) {
-            before.add += s.add;
-            before.grow += s.grow;
-            before.drop += s.drop;
+    Sums w = lane < (static_cast<int>(blockDim.x) >> 5) ? warp_sums[lane] : Sums{0, 0, 0};
+    const Sums own = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t a = __shfl_up_sync(0xFFFFFFFFu, w.add, d), g = __shfl_up_sync(0xFFFFFFFFu, w.grow, d),
+                       f = __shfl_up_sync(0xFFFFFFFFu, w.drop, d);
+        if (lane >= d) {
+            w.add += a;
+            w.grow += g;
+            w.drop += f;
         }
-        all.add += s.add;
-        all.grow += s.grow;
-        all.drop += s.drop;
     }
-    *total = all;
-    return Sums{before.add + inc.add - v.add, before.grow + inc.grow - v.grow, before.drop + inc.drop - v.drop};
+    *total = Sums{__shfl_sync(0xFFFFFFFFu, w.add, 31), __shfl_sync(0xFFFFFFFFu, w.grow, 31), __shfl_sync(0xFFFFFFFFu, w.drop, 31)};
+    const uint64_t before_add = __shfl_sync(0xFFFFFFFFu, w.add - own.add, warp), before_grow = __shfl_sync(0xFFFFFFFFu, w.grow - own.grow, warp),
+                   before_drop = __shfl_sync(0xFFFFFFFFu, w.drop - own.drop, warp);
+    return Sums{before_add + inc.add - v.add, before_grow + inc.grow - v.grow, before_drop + inc.drop - v.drop};
 }
 
 // The last r with first[r] <= x (first[0] = 0, nondecreasing, n entries):
@@ -114,7 +117,10 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TablesArgs
     uint32_t* d0 = g0 + a.n + 1;
     const uint32_t page_mask = (1u << a.shift) - 1;
     const uint64_t max_len = static_cast<uint64_t>(a.cols) << a.shift;
-    const uint32_t per = ceil_div(a.n, kTabThreads);
+    wait_for_earlier();
+    let_next_start();
+    const int32_t have = *a.count;
+    const uint32_t threads = blockDim.x, per = ceil_div(a.n, threads);
     const uint32_t r0 = min(a.n, threadIdx.x * per), r1 = min(a.n, r0 + per);
 
     Sums mine{0, 0, 0};
@@ -133,7 +139,6 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TablesArgs
     Sums total;
     Sums at = block_exclusive(mine, &total);
     // all of it or nothing: a call that cannot be served changes no page
-    const int32_t have = *a.count;
     if (total.add > a.max_tokens) bad |= AFX_DEV_BAD_LENGTH;
     if (have < 0 || static_cast<uint32_t>(have) > a.n_pages || have + total.drop > a.n_pages + total.grow)
         bad |= AFX_DEV_BAD_LENGTH;  // the count is not one of this pool, or pages came back twice
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TablesArgs
         bad |= AFX_DEV_NO_PAGES;
     const bool refused = __syncthreads_or(bad) != 0;
     if (bad && blockIdx.x == 0) raise(a.status, bad);
-    const uint32_t gid = blockIdx.x * kTabThreads + threadIdx.x, stride = gridDim.x * kTabThreads;
+    const uint32_t gid = blockIdx.x * threads + threadIdx.x, stride = gridDim.x * threads;
     if (refused) {
         for (uint32_t i = gid; i <= a.n; i += stride) a.starts[i] = 0;
         for (uint32_t i = gid; i < a.max_tokens; i += stride) a.slots[i] = a.positions[i] = -1;
@@ -172,23 +177,49 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TablesArgs
         a.table[static_cast<uint64_t>(r) * a.cols + mv.pages(a.old_len[r]) + (j - g0[r])] = page;
     }
     for (uint32_t f = gid; f + n_grow < n_drop; f += stride) a.stack[have + f] = mv.freed(f);
-    for (uint32_t t = gid; t < a.max_tokens; t += stride) {
-        int32_t slot = -1, pos = -1;
-        if (t < n_add) {
-            const uint32_t r = owner(t0, a.n, t);
-            const uint32_t held = a.old_len[r], at_pos = held + (t - t0[r]);
-            const uint32_t col = at_pos >> a.shift, first_new = mv.pages(held);
-            // a page the request already has is in its row; a new one is
-            // being written there by another thread, so it is worked out
-            const int32_t page = col < first_new ? a.table[static_cast<uint64_t>(r) * a.cols + col] : mv.taken(g0[r] + col - first_new);
-            pos = static_cast<int32_t>(at_pos);
-            if (page < 0 || static_cast<uint32_t>(page) >= a.n_pages)
-                raise(a.status, AFX_DEV_BAD_PAGE);
-            else
-                slot = static_cast<int32_t>((static_cast<uint32_t>(page) << a.shift) | (at_pos & page_mask));
+    // four tokens a thread: their request is looked up once, their page where it changes
+    for (uint32_t t = 4 * gid; t < a.max_tokens; t += 4 * stride) {
+        int32_t slot[4], pos[4];
+        uint32_t r = t < n_add ? owner(t0, a.n, t) : 0, held = 0, seen_col = UINT32_MAX;
+        int32_t page = -1;
+        bool load = true;
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            slot[j] = pos[j] = -1;
+            if (t + j >= n_add) continue;
+            while (r + 1 < a.n && t0[r + 1] <= t + j) {
+                ++r;
+                load = true;
+            }
+            if (load) {
+                held = a.old_len[r];
+                load = false;
+                seen_col = UINT32_MAX;
+            }
+            const uint32_t at_pos = held + (t + j - t0[r]), col = at_pos >> a.shift;
+            if (col != seen_col) {
+                // a page the request already has is in its row; a new one is
+                // being written there by another thread, so it is worked out
+                const uint32_t first_new = mv.pages(held);
+                page = col < first_new ? a.table[static_cast<uint64_t>(r) * a.cols + col] : mv.taken(g0[r] + col - first_new);
+                seen_col = col;
+                if (page < 0 || static_cast<uint32_t>(page) >= a.n_pages) raise(a.status, AFX_DEV_BAD_PAGE);
+            }
+            pos[j] = static_cast<int32_t>(at_pos);
+            if (page >= 0 && static_cast<uint32_t>(page) < a.n_pages)
+                slot[j] = static_cast<int32_t>((static_cast<uint32_t>(page) << a.shift) | (at_pos & page_mask));
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
+        if (a.wide && t + 4 <= a.max_tokens) {
+            *reinterpret_cast<int4*>(a.slots + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            *reinterpret_cast<int4*>(a.positions + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+                if (t + j < a.max_tokens) {
+                    a.slots[t + j] = slot[j];
+                    a.positions[t + j] = pos[j];
+                }
+        }
     }
 }
 
@@ -208,25 +239,38 @@ constexpr int kWriteThreads = 256;
 // strides are not multiples of 16).
 template <typename V>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const WriteArgs a) {
+    wait_for_earlier();
+    let_next_start();
     const uint32_t per_row = a.row_bytes / sizeof(V), per_token = per_row * a.heads;
     const uint64_t units = static_cast<uint64_t>(a.n_tokens) * per_token;
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * kWriteThreads;
-    for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kWriteThreads + threadIdx.x; u < units; u += step) {
-        const uint32_t t = static_cast<uint32_t>(u / per_token), i = static_cast<uint32_t>(u % per_token);
-        const uint32_t h = i / per_row, c = i % per_row;
-        const int32_t slot = a.slots[t];
-        if (slot < 0) continue;  // padding
-        if (static_cast<uint32_t>(slot) >= a.n_slots) {
-            raise(a.status, AFX_DEV_BAD_PAGE);
-            continue;
-        }
-        const uint64_t from = t * a.src_token + h * a.src_head + c * sizeof(V);
-        const uint64_t to = (static_cast<uint32_t>(slot) >> a.shift) * a.dst_page +
-                            (static_cast<uint32_t>(slot) & ((1u << a.shift) - 1)) * a.dst_token + h * a.dst_head +
-                            c * sizeof(V);
+    constexpr int kAtOnce = 2;  // of keys and of values each
+    for (uint64_t u0 = static_cast<uint64_t>(blockIdx.x) * kWriteThreads + threadIdx.x; u0 < units; u0 += kAtOnce * step) {
+        V v[kAtOnce][2];
+        uint64_t to[kAtOnce];
+        bool real[kAtOnce];
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-            *reinterpret_cast<V*>(a.dst[p] + to) = __ldg(reinterpret_cast<const V*>(a.src[p] + from));
+        for (int i = 0; i < kAtOnce; ++i) {
+            const uint64_t u = u0 + i * step;
+            real[i] = u < units;
+            if (!real[i]) continue;
+            const uint32_t t = static_cast<uint32_t>(u / per_token), in = static_cast<uint32_t>(u - static_cast<uint64_t>(t) * per_token);
+            const uint32_t h = in / per_row, c = in - h * per_row;
+            const int32_t slot = __ldg(a.slots + t);
+            const uint64_t from = t * a.src_token + h * a.src_head + c * sizeof(V);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) v[i][p] = __ldg(reinterpret_cast<const V*>(a.src[p] + from));
+            if (slot >= 0 && static_cast<uint32_t>(slot) >= a.n_slots) raise(a.status, AFX_DEV_BAD_PAGE);
+            real[i] = slot >= 0 && static_cast<uint32_t>(slot) < a.n_slots;  // negative: padding
+            to[i] = (static_cast<uint32_t>(slot) >> a.shift) * a.dst_page +
+                    (static_cast<uint32_t>(slot) & ((1u << a.shift) - 1)) * a.dst_token + h * a.dst_head + c * sizeof(V);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (real[i]) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) *reinterpret_cast<V*>(a.dst[p] + to[i]) = v[i][p];
+            }
     }
 }
 
@@ -303,14 +347,17 @@ extern "C" afx_status afx_kv_tables(uint32_t page_tokens, uint32_t n_pages, cons
     a.max_tokens = max_tokens;
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
-    const uint32_t want = ceil_div(max_tokens / 4 + n_requests, kTabThreads);
+    a.wide = !((reinterpret_cast<uintptr_t>(slots_dev) | reinterpret_cast<uintptr_t>(positions_dev)) & 15u);
+    // a thread a request (the sums over fewer threads cost less), and enough CTAs for four tokens a thread
+    uint32_t threads = (n_requests + 31) / 32 * 32;
+    threads = threads < 128 ? 128 : threads > kTabThreads ? kTabThreads : threads;
+    const uint32_t want = ceil_div(ceil_div(max_tokens, 4) + n_requests, threads);
     const uint32_t grid = want < 1 ? 1 : want > static_cast<uint32_t>(sms) ? sms : want;
     const size_t smem = 3 * sizeof(uint32_t) * (static_cast<size_t>(n_requests) + 1);
     AFX_SERVE_TRY(cudaFuncSetAttribute(kv_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(3 * sizeof(uint32_t) * (kMaxRequests + 1))),
                   "cudaFuncSetAttribute");
-    kv_tables_kernel<<<grid, kTabThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    AFX_SERVE_TRY(cudaGetLastError(), "kv_tables_kernel launch");
+    AFX_SERVE_TRY(launch_early(kv_tables_kernel, grid, threads, smem, reinterpret_cast<cudaStream_t>(stream), a), "kv_tables_kernel launch");
     return AFX_OK;
 }
 
@@ -347,10 +394,8 @@ extern "C" afx_status afx_kv_write(const afx_kv_cache* cache, const void* k_dev,
     const uint64_t want = (units + kWriteThreads - 1) / kWriteThreads, most = static_cast<uint64_t>(sms) * 8;
     const uint32_t grid = static_cast<uint32_t>(want < most ? want : most);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (wide)
-        kv_write_kernel<uint4><<<grid, kWriteThreads, 0, s>>>(a);
-    else
-        kv_write_kernel<unsigned short><<<grid, kWriteThreads, 0, s>>>(a);
-    AFX_SERVE_TRY(cudaGetLastError(), "kv_write_kernel launch");
+    AFX_SERVE_TRY(wide ? launch_early(kv_write_kernel<uint4>, grid, kWriteThreads, 0, s, a)
+                       : launch_early(kv_write_kernel<unsigned short>, grid, kWriteThreads, 0, s, a),
+                  "kv_write_kernel launch");
     return AFX_OK;
 }

@@ -367,6 +367,7 @@ __device__ void reach(Shared& sh, const uint64_t (&key)[kPer], const uint64_t (&
     const Element el(n);
     const uint64_t own = el.e < n ? sh.short_key[el.e] : 0;
     uint64_t ahead = 0;
+#pragma unroll 4
     for (uint32_t j = el.part; j < n; j += el.parts)
         if (sh.short_key[j] > own) ahead += sh.short_mass[j];
     ahead = sh.found_before + el.over_parts(ahead);
@@ -545,6 +546,7 @@ __device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row 
         if (one) sh.short_mass[el.e] = w;
         __syncthreads();
         uint64_t ahead = 0, before = 0, all, total;
+#pragma unroll 4
         for (uint32_t j = el.part; j < n; j += el.parts)
             if (sh.list[j] > mine) {
                 ++ahead;
@@ -559,6 +561,7 @@ __device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row 
         if (one) sh.bins[el.e] = kept;
         block_exclusive(sh, one ? kept : 0, &total);  // a barrier as well
         before = 0;
+#pragma unroll 4
         for (uint32_t j = el.part; j < n; j += el.parts)  // lower indexes have larger low halves
             if (static_cast<uint32_t>(sh.list[j]) > static_cast<uint32_t>(mine)) before += sh.bins[j];
         before = el.over_parts(before);
@@ -628,6 +631,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     wait_for_earlier();
     let_next_start();
 
+    // the row's parameters, under way with the logits
+    const float temp = a.temperature ? __ldg(a.temperature + r) : 1.0f;
+    const int32_t top_k = a.top_k ? __ldg(a.top_k + r) : 0;
+    const float top_p = a.top_p ? __ldg(a.top_p + r) : 1.0f, min_p = a.min_p ? __ldg(a.min_p + r) : 0.0f, u = __ldg(a.u + r);
+
     // pass 1: the slice into shared memory, NaN as minus infinity and -0 as 0; the thread's maximum
     float mine = -INFINITY;
     constexpr uint32_t kBatch = 5;  // loads in flight a lane
@@ -675,7 +683,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     for (uint32_t i = lane; i < kWarps * ranks; i += 32) row.top = fmaxf(row.top, sh.top[i]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) row.top = fmaxf(row.top, __shfl_xor_sync(0xFFFFFFFFu, row.top, d));
-    const float temp = a.temperature ? a.temperature[r] : 1.0f;
     if (row.top == -INFINITY) {  // nothing to draw from
         if (rank == 0 && threadIdx.x == 0) {
             a.tokens[r] = -1;
@@ -746,13 +753,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     }
     row.step = static_cast<float>(kBins) / (kRange * temp);
     Want want;
-    const int32_t k = a.top_k ? a.top_k[r] : 0;
-    want.k = k > 0 && static_cast<uint32_t>(k) < a.vocab ? k : 0;
-    want.p = a.top_p ? a.top_p[r] : 1.0f;
-    if (!(want.p < 1.0f)) want.p = 1.0f;
-    const float min_p = a.min_p ? a.min_p[r] : 0.0f;
+    want.k = top_k > 0 && static_cast<uint32_t>(top_k) < a.vocab ? top_k : 0;
+    want.p = top_p < 1.0f ? top_p : 1.0f;
     want.least = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
-    want.u = static_cast<double>(a.u[r]);
+    want.u = static_cast<double>(u);
     // a bound below every logit of the first `bins` steps, and of every token with mass
     auto lower_bound = [&](uint32_t bins) {
         const float span = __fmul_ru(__fdiv_ru(static_cast<float>(bins), row.step), 1.000002f);
@@ -796,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             const uint32_t parts = kThreads / n_warps, e = threadIdx.x / parts;  // threads a maximum
             const float x = sh.top[e];
             uint32_t larger = 0, as_large = 0;
+#pragma unroll 8
             for (uint32_t i = threadIdx.x % parts; i < n_warps; i += parts) {
                 larger += sh.top[i] > x;
                 as_large += sh.top[i] >= x;
