@@ -54,7 +54,7 @@ constexpr uint32_t kTopMax = 1024;     // top-k that goes by the threads' maxima
 constexpr uint32_t kMaxCluster = 16;
 constexpr uint32_t kTooMany = 1u << 26;
 constexpr uint32_t kShort = 256;       // tokens that are ordered pair by pair
-constexpr int kCuts = 5;               // weights above e^-2, e^-4, ..., e^-10 tell how far down top-p reaches
+constexpr int kCuts = 2;               // weights above e^-4 and e^-8 tell how far down top-p reaches
 constexpr uint32_t kQueue = 160;       // tokens a warp has found and not yet dealt with: 31 and 128 more
 constexpr float kRange = 30.5f;        // e^-30.5 < 2^-44: no mass below m - 30.5 T
 constexpr float kMassOne = 17592186044416.0f;  // 2^44
@@ -503,9 +503,9 @@ __device__ void select(cg::cluster_group& cluster, Shared& sh, const float* z, u
     *kept = sh.kept_mass;
 }
 
-// e^-2 .. e^-10
-__device__ __forceinline__ constexpr float cut_weight(int c) {
-    constexpr float w[kCuts] = {0.135335283f, 0.0183156389f, 0.00247875218f, 0.000335462628f, 4.53999298e-05f};
+constexpr float kCutStep = 4.0f;
+__device__ __forceinline__ constexpr float cut_weight(int c) {  // e^-4, e^-8
+    constexpr float w[kCuts] = {0.0183156389f, 0.000335462628f};
     return w[c];
 }
 
@@ -639,11 +639,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     // pass 1: the slice into shared memory, NaN as minus infinity and -0 as 0; the thread's maximum
     float mine = -INFINITY;
     constexpr uint32_t kBatch = 5;  // loads in flight a lane
-    for (uint32_t i0 = 0; run0 + i0 * 128 < run1; i0 += kBatch) {
+    uint32_t done = run0;
+    if (a.wide)
+        for (; done + kBatch * 128 <= run1; done += kBatch * 128) {
+            float x[kBatch][4];
+            const T* from = src + run_index(done, 0);
+            float* to = z + run_index(done, 0);
+#pragma unroll
+            for (uint32_t j = 0; j < kBatch; ++j) load4(from + j * 128, x[j]);
+#pragma unroll
+            for (uint32_t j = 0; j < kBatch; ++j) {
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c) x[j][c] = clean(x[j][c]);
+                mine = fmaxf(mine, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
+                *reinterpret_cast<float4*>(to + j * 128) = make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
+            }
+        }
+    for (; done < run1; done += kBatch * 128) {
         float x[kBatch][4];
 #pragma unroll
         for (uint32_t j = 0; j < kBatch; ++j) {
-            const uint32_t at = run_index(run0, i0 + j);
+            const uint32_t at = run_index(done, j);
             if (a.wide && at + 4 <= run1) {
                 load4(src + at, x[j]);
             } else {
@@ -653,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
 #pragma unroll
         for (uint32_t j = 0; j < kBatch; ++j) {
-            const uint32_t at = run_index(run0, i0 + j);
+            const uint32_t at = run_index(done, j);
 #pragma unroll
             for (uint32_t c = 0; c < 4; ++c) x[j][c] = clean(x[j][c]);
             mine = fmaxf(mine, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
@@ -796,21 +812,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         // the k-th largest of maxima of k groups or more: at least k tokens are as large
         float low;
         if (want.k <= n_warps - n_warps / 4 && !infinite) {
-            // of the warps'; a warp without tokens has minus infinity, and ends the count below k
-            const uint32_t parts = kThreads / n_warps, e = threadIdx.x / parts;  // threads a maximum
-            const float x = sh.top[e];
+            // of the warps' (one without tokens has minus infinity): the warp whose it is tells every rank
+            const float x = sh.top[rank * kWarps + warp];
             uint32_t larger = 0, as_large = 0;
-#pragma unroll 8
-            for (uint32_t i = threadIdx.x % parts; i < n_warps; i += parts) {
-                larger += sh.top[i] > x;
-                as_large += sh.top[i] >= x;
-            }
-            for (uint32_t d = 1; d < parts; d <<= 1) {
-                larger += __shfl_xor_sync(0xFFFFFFFFu, larger, d);
-                as_large += __shfl_xor_sync(0xFFFFFFFFu, as_large, d);
-            }
-            if (larger < want.k && as_large >= want.k) sh.bound = x;  // the same value in every thread that finds it
-            __syncthreads();
+#pragma unroll
+            for (uint32_t i = 0; i < kMaxCluster * kWarps; i += 32)
+                if (i < n_warps) {
+                    const float y = i + lane < n_warps ? sh.top[i + lane] : -INFINITY;
+                    larger += __popc(__ballot_sync(0xFFFFFFFFu, y > x));
+                    as_large += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < n_warps && y >= x));
+                }
+            if (larger < want.k && as_large >= want.k && lane < static_cast<int>(ranks)) cluster.map_shared_rank(&sh, lane)->bound = x;
+            cluster.sync();
             low = fmaxf(sh.bound, lower_bound(kBins));
         } else {
             // of the threads' (with fewer maxima: all that have mass)
@@ -863,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 if (sum >= want.p * 1.0002f * static_cast<float>(all) * (1.0f / kMassOne)) far = c;
             }
             if (far < kCuts) {
-                const float low = __fsub_rd(row.top, __fmul_ru(2.00001f * static_cast<float>(far + 1), temp));
+                const float low = __fsub_rd(row.top, __fmul_ru(1.00001f * kCutStep * static_cast<float>(far + 1), temp));
                 push(low, [&](float x) { return x >= low; });
                 if (draw(all)) return;
                 if (rank == 0 && threadIdx.x == 0) sh.list_n = 0;  // barriers follow before the next push
@@ -873,9 +886,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             // below (1 - p) S / V have less than (1 - p) S together, so the limit is reached before them (half of it,
             // for the rounding of this float32 line)
             const float floor_w = fminf(0.5f * (1.0f - fmaxf(want.p, 0.0f)) * (static_cast<float>(all) * (1.0f / kMassOne)) / static_cast<float>(a.vocab), 0.5f);
-            const float low = far < kCuts ? __fsub_rd(row.top, __fmul_ru(2.00001f * static_cast<float>(far + 1), temp))
+            const float low = far < kCuts ? __fsub_rd(row.top, __fmul_ru(1.00001f * kCutStep * static_cast<float>(far + 1), temp))
                                           : fmaxf(lower_bound(kBins), __fsub_rd(row.top, __fmul_ru(-logf(fmaxf(floor_w, 1e-30f)), temp)));
-            const float high = far ? fmaxf(low, row.top - 2.0f * static_cast<float>(far) * temp) : row.top;
+            const float high = far ? fmaxf(low, row.top - kCutStep * static_cast<float>(far) * temp) : row.top;
             const float span = high - low, step = span > 0.0f && span < INFINITY ? static_cast<float>(kBins) / span : 1.0f;
             auto step_of = [&](float x) {  // of low <= x <= high
                 const float b = (high - x) * step;
