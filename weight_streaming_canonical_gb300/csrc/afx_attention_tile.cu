@@ -117,11 +117,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Ctl& ctl,
     return false;
 }
 
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t c1, uint32_t c2, uint32_t c3,
-                                         uint64_t* bar) {
+__device__ __forceinline__ void load_box(uint32_t lane, uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t c1, uint32_t c2,
+                                         uint32_t c3, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+        "{\n .reg .pred q;\n setp.ne.u32 q, %7, 0;\n"
+        " @q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n}\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "r"(lane)
         : "memory");
 }
 
@@ -138,20 +139,32 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
            (uint64_t{1024 >> 4} << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
 }
 
+// The instructions below are issued by one lane of a converged warp: the
+// predicate is in the instruction, not in a branch around it, so that
+// descriptors and addresses stay in uniform registers.
+
 // D = A B^T (+ D), A and B in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
-                 : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t lane, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lane)
+        : "memory");
 }
 // The same with A in tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
-                 : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t lane, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lane)
+        : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ void commit(uint32_t lane, uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
+        "r"(lane)
+        : "memory");
 }
 
 // Two float32 operations an instruction.
@@ -358,10 +371,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     const uint32_t id = __shfl_sync(0xFFFFFFFFu, page, b), token = first & page_mask;  // 0 but for pages of 256
                     const uint32_t c1 = args.token_at == 0 ? token : args.head_at == 0 ? p.h : id, c2 = args.token_at == 1 ? token : args.head_at == 1 ? p.h : id,
                                    c3 = args.token_at == 2 ? token : args.head_at == 2 ? p.h : id;
-                    if (leader) {
 #pragma unroll
-                        for (uint32_t hf = 0; hf < Sh::kHalves; ++hf) load_box(dst + hf * Sh::kBlock + b * box * 128, map, hf * 64, c1, c2, c3, bar);
-                    }
+                    for (uint32_t hf = 0; hf < Sh::kHalves; ++hf)
+                        load_box(leader, dst + hf * Sh::kBlock + b * box * 128, map, hf * 64, c1, c2, c3, smem_addr(bar));
                 }
                 __syncwarp();
                 if (patch) {
@@ -419,16 +431,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         };
         auto scores = [&](uint32_t t, uint32_t slot, bool own_q, bool release) {
             const uint64_t qd = q_desc + (own_q ? t * (Sh::kSlot >> 4) : 0), kd = k_desc + slot * (Sh::kSlot >> 4);
-            if (leader) {
 #pragma unroll
-                for (uint32_t ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks / 4) * (Sh::kBlock >> 4) + (ks % 4) * 2;
-                    mma_ss(tmem + Sh::kS + t * kTileKeys, qd + off, kd + off, kQk, ks != 0);
-                }
-                if (release) commit(&ctl.empty[slot]);
-                commit(&ctl.s_full[t]);
+            for (uint32_t ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (ks / 4) * (Sh::kBlock >> 4) + (ks % 4) * 2;
+                mma_ss(leader, tmem + Sh::kS + t * kTileKeys, qd + off, kd + off, kQk, ks != 0);
             }
-            __syncwarp();
+            if (release) commit(leader, &ctl.empty[slot]);
+            commit(leader, &ctl.s_full[t]);
         };
         // the weights come in two halves of 64 keys; false: a wait gave up
         auto values = [&](uint32_t t, uint32_t slot, bool first, bool release) {
@@ -438,17 +447,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             for (uint32_t half = 0; half < 2; ++half) {
                 if (!uniform(bar_wait(&ctl.p_full[t][half], phase, ctl, a.status))) return false;
                 fence_after();
-                if (leader) {
 #pragma unroll
-                    for (uint32_t ks = half * 4; ks < half * 4 + 4; ++ks)
-                        mma_ts(tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep + ks * 8, vd + ks * (2048 >> 4), kPv, !first || ks != 0);
-                    if (half) {
-                        if (release) commit(&ctl.empty[slot]);
-                        commit(&ctl.pv_done[t]);  // last: the row threads wait for it before the CTA ends
-                    }
-                }
-                __syncwarp();
+                for (uint32_t ks = half * 4; ks < half * 4 + 4; ++ks)
+                    mma_ts(leader, tmem + Sh::kO + t * D, tmem + Sh::kP + t * Sh::kPStep + ks * 8, vd + ks * (2048 >> 4), kPv, !first || ks != 0);
             }
+            if (release) commit(leader, &ctl.empty[slot]);
+            commit(leader, &ctl.pv_done[t]);  // last: the row threads wait for it before the CTA ends
             return true;
         };
         while (ok && walk.next(&p)) {
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             }
         }
         if (!ok && leader) {  // products in flight finish before the tensor memory is freed
-            commit(&ctl.drain);
+            commit(1, &ctl.drain);
             if (!bar_drain(&ctl.drain, 0)) raise(a.status, AFX_DEV_UNDRAINED);
         }
         __syncwarp();
