@@ -39,7 +39,11 @@ constexpr uint32_t kKeyAlign = 64;     // 16-row items' key ranges start at mult
 constexpr uint32_t kMinKeys = 256;     // keys of a 16-row item, at least, where a range is cut
 constexpr uint32_t kTargetUnits = 1216;  // 16-row items x heads that the cuts aim at
 constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's tiles take the prefix along
-constexpr uint32_t kMinShare = 8;      // cost of a tile CTA, at least
+constexpr uint32_t kMinShare = 4 * kStepBoth;  // cost of a tile CTA, at least
+// What a tile group costs besides its steps (filling and emptying the pipe,
+// masked steps, the output), where CTAs take several whole groups each; where a
+// group is cut over several CTAs, all have that cost alike.
+constexpr uint32_t kGroupCost = 18;
 constexpr uint32_t kFewTokens = 8, kManyMax = 512;
 
 __host__ __device__ inline uint64_t up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
@@ -105,8 +109,7 @@ __device__ __forceinline__ Kind kind_of(const AttnArgs& a, uint32_t rows) {
 }
 
 __device__ __forceinline__ uint32_t tile_cost(uint32_t rows, uint32_t prefix_keys, uint32_t own_keys) {
-    const uint32_t steps = ceil_div(prefix_keys, kTileKeys) + ceil_div(own_keys, kTileKeys);
-    return rows > kTileRows ? 2 * steps : (steps + 1) / 2 * 2;
+    return step_cost(rows) * (ceil_div(prefix_keys, kTileKeys) + ceil_div(own_keys, kTileKeys));
 }
 
 // One CTA.  Requests' rows are cut into groups of 16 (or 256 for the tile
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     if (refused) {
         if (threadIdx.x == 0) {
             raise(a.status, AFX_DEV_BAD_LENGTH);
-            *head = PlanHead{a.plan_key, 0, 0, 0, 0, 0, kNone};
+            *head = PlanHead{a.plan_key, 0, 0, 0, 0, 0, kNone, 0, 0};
         }
         return;
     }
@@ -177,24 +180,12 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         const uint32_t s = i / groups_p, row0 = (i % groups_p) * kRows, rows = min(kRows, prefix_rows - row0);
         items[i] = Row16Item{-1, row0, rows, s * piece, min(a.prefix_len, (s + 1) * piece), row0 * pieces_p + s * rows, 0, 0};
     }
-    const uint32_t cost_full = tile_cost(kGroupRows, a.prefix_len, 0);
-    const uint64_t tile_row0 = a.L.max_rows;  // rows of the tile kernel's first pieces start here
-    uint64_t cost_p = 0, rows_p = 0;
-    if (tiles_p) {
-        for (uint32_t g = threadIdx.x; g < tiles_p; g += threads) {
-            const uint32_t row0 = g * kGroupRows, rows = min(kGroupRows, prefix_rows - row0);
-            tiles[g] = TileGroup{static_cast<uint64_t>(g) * cost_full * a.kv_heads, tile_row0 + static_cast<uint64_t>(row0) * a.kv_heads,
-                                 tile_cost(rows, a.prefix_len, 0), -1, row0, rows, a.prefix_len, 0, 0, 0, 0, {}};
-        }
-        const uint32_t last = prefix_rows - (tiles_p - 1) * kGroupRows;
-        cost_p = (static_cast<uint64_t>(tiles_p - 1) * cost_full + tile_cost(last, a.prefix_len, 0)) * a.kv_heads;
-        rows_p = (static_cast<uint64_t>(tiles_p - 1) * kGroupRows + (last > kTileRows ? last : 2 * last)) * a.kv_heads;
-    }
-
     auto write_token = [&](uint32_t r, uint32_t t, uint32_t mark, uint32_t i, const RequestInfo& own) {
         tokens[t] = TokenInfo{r, i * G, mark >= kInTiles ? mark : mark + i, 0, own};
         if (mark < kInTiles) packed_token[mark + i] = static_cast<int32_t>(t);
     };
+    // not written by the tile kernel: two tiles' sums, or none
+    auto rests = [](uint32_t m, uint32_t keys, bool single) { return single && (m <= kTileRows || keys == 0); };
     // the requests' own keys
     auto walk = [&](uint32_t r, auto&& row16, auto&& tile) {
         const uint32_t s = a.starts[r], n = a.starts[r + 1] - s, rows = n * G;
@@ -211,8 +202,11 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
                 tile(row, m, k.fused ? a.prefix_len : 0u, visible(seen, row + m - 1, G), s, seen, k.fused);
             }
     };
-    Counts<6> mine{};
-    for (uint32_t r = r0; r < r1; ++r)
+    Counts<8> mine{};
+    for (uint32_t r = r0; r < r1; ++r) {
+        const uint32_t n = a.starts[r + 1] - a.starts[r];
+        const Kind k = kind_of(a, n * G);
+        if (!(k.fused && k.own == kTile)) mine.v[7] += n;
         walk(
             r,
             [&](uint32_t, uint32_t m, uint32_t end, uint32_t, int32_t) {
@@ -221,16 +215,35 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
                 mine.v[1] += pieces;
                 mine.v[2] += static_cast<uint64_t>(pieces) * m;
             },
-            [&](uint32_t, uint32_t m, uint32_t prefix, uint32_t own, uint32_t, int32_t, bool) {
+            [&](uint32_t, uint32_t m, uint32_t prefix, uint32_t own, uint32_t, int32_t, bool single) {
                 mine.v[3] += 1;
                 mine.v[4] += static_cast<uint64_t>(tile_cost(m, prefix, own)) * a.kv_heads;
                 mine.v[5] += static_cast<uint64_t>(m > kTileRows ? m : 2 * m) * a.kv_heads;
+                mine.v[6] += rests(m, prefix + own, single);
             });
-    Counts<6> total;
-    const Counts<6> at = block_exclusive(mine, &total);
+    }
+    Counts<8> total;
+    const Counts<8> at = block_exclusive(mine, &total);
+    const uint32_t n_tiles = tiles_p + static_cast<uint32_t>(total.v[3]);
+    const uint32_t lead = static_cast<uint64_t>(n_tiles) * a.kv_heads >= a.tile_ctas ? kGroupCost : 0;
+    const uint32_t cost_full = lead + tile_cost(kGroupRows, a.prefix_len, 0);
+    const uint64_t tile_row0 = a.L.max_rows;  // rows of the tile kernel's first pieces start here
+    uint64_t cost_p = 0, rows_p = 0;
+    if (tiles_p) {
+        for (uint32_t g = threadIdx.x; g < tiles_p; g += threads) {
+            const uint32_t row0 = g * kGroupRows, rows = min(kGroupRows, prefix_rows - row0);
+            tiles[g] = TileGroup{static_cast<uint64_t>(g) * cost_full * a.kv_heads, tile_row0 + static_cast<uint64_t>(row0) * a.kv_heads,
+                                 lead + tile_cost(rows, a.prefix_len, 0), -1, row0, rows, a.prefix_len, 0, 0, 0, 0, lead, {}};
+        }
+        const uint32_t last = prefix_rows - (tiles_p - 1) * kGroupRows;
+        cost_p = (static_cast<uint64_t>(tiles_p - 1) * cost_full + lead + tile_cost(last, a.prefix_len, 0)) * a.kv_heads;
+        rows_p = (static_cast<uint64_t>(tiles_p - 1) * kGroupRows + (last > kTileRows ? last : 2 * last)) * a.kv_heads;
+    }
+    const uint64_t leads = static_cast<uint64_t>(lead) * a.kv_heads;
     uint32_t g = static_cast<uint32_t>(at.v[0]) + groups_p, it = static_cast<uint32_t>(at.v[1]) + groups_p * pieces_p,
              pr = static_cast<uint32_t>(at.v[2]) + (groups_p ? prefix_rows * pieces_p : 0), tg = static_cast<uint32_t>(at.v[3]) + tiles_p;
-    uint64_t cost = at.v[4] + cost_p, trow = tile_row0 + at.v[5] + rows_p;
+    uint32_t* rest = a.at<uint32_t>(a.L.rest) + at.v[6];
+    uint64_t cost = at.v[4] + at.v[3] * leads + cost_p, trow = tile_row0 + at.v[5] + rows_p;
     for (uint32_t r = r0; r < r1; ++r) {
         const uint32_t s = a.starts[r], e = a.starts[r + 1];
         const Kind k = kind_of(a, (e - s) * G);
@@ -244,8 +257,9 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
                     items[it++] = Row16Item{static_cast<int32_t>(r), row, m, p * piece, min(end, (p + 1) * piece), pr, token0, seen};
             },
             [&](uint32_t row, uint32_t m, uint32_t prefix, uint32_t own, uint32_t token0, int32_t seen, bool single) {
-                const uint32_t c = tile_cost(m, prefix, own);
-                tiles[tg++] = TileGroup{cost, trow, c, static_cast<int32_t>(r), row, m, prefix, own, token0, seen, single, {}};
+                const uint32_t c = lead + tile_cost(m, prefix, own);
+                if (rests(m, prefix + own, single)) *rest++ = tg;
+                tiles[tg++] = TileGroup{cost, trow, c, static_cast<int32_t>(r), row, m, prefix, own, token0, seen, single, lead, {}};
                 cost += static_cast<uint64_t>(c) * a.kv_heads;
                 trow += static_cast<uint64_t>(m > kTileRows ? m : 2 * m) * a.kv_heads;
             });
@@ -269,19 +283,14 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         for (uint32_t t = s + threadIdx.x % 32; t < e; t += 32) write_token(m.request, t, m.mark, t - s, m.own);
     }
     if (threadIdx.x == 0) {
-        const uint64_t c = total.v[4] + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
-        const uint64_t share = up((c + ctas - 1) / ctas, 2);
+        const uint64_t c = total.v[4] + total.v[3] * leads + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
+        const uint64_t share = (c + ctas - 1) / ctas;
         *head = PlanHead{a.plan_key, c, share < kMinShare ? kMinShare : share, static_cast<uint32_t>(a.starts[R]),
-                         groups_p * pieces_p + static_cast<uint32_t>(total.v[1]), tiles_p + static_cast<uint32_t>(total.v[3]), prefix_kind};
+                         groups_p * pieces_p + static_cast<uint32_t>(total.v[1]), n_tiles, prefix_kind, static_cast<uint32_t>(total.v[6]), static_cast<uint32_t>(total.v[7])};
     }
 }
 
 // ---- 16 packed rows x a range of keys ------------------------------------------------
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
-    const uint32_t n = real ? 16u : 0u;  // 0: the 16 bytes are zeros, src is not read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -545,7 +554,7 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& h
         p.step16 = static_cast<uint64_t>(g.rows) * a.kv_heads;
     } else if (kind == kTile) {
         const TileGroup g = a.at<TileGroup>(a.L.tiles)[first_group + row / kGroupRows];
-        if (g.cost) {
+        if (g.cost > g.lead) {
             uint32_t c0, c1;
             tile_ctas(g, h, head.share, &c0, &c1);
             p.two = g.rows <= kTileRows;
@@ -560,6 +569,7 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& h
 }
 
 constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
+constexpr uint32_t kJoinRows = 8;  // rows of a tile group that a warp puts together at a time
 
 // A lane's elements of an output row, in one store where its address allows.
 template <typename T, int N>
@@ -574,93 +584,107 @@ __device__ __forceinline__ void store_row(T* out, const float (&v)[N]) {
     }
 }
 
-// Rows in tiles of their request's own: mostly the tile kernel has written
-// the output; where a CTA's share ended within a group's head, or the group's two
-// tiles took steps in turn, its pieces are put together here, a warp 8 rows.
+// Eight rows of a tile group's head, put together from its pieces by a warp.
 template <typename T, int D>
-__device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t block, uint32_t blocks) {
+__device__ void join_group_rows(const AttnArgs& a, const TileGroup& g, uint32_t h, uint32_t row0, uint32_t c0, uint32_t c1) {
     constexpr int kPer = D / 32;
     const int lane = threadIdx.x & 31;
-    const uint32_t q_heads = a.kv_heads * a.group;
+    const uint32_t q_heads = a.kv_heads * a.group, rows = g.rows;
     const float* part_o = a.at<float>(a.L.part_o);
     const float2* part_ml = a.at<float2>(a.L.part_ml);
-    constexpr uint32_t kUnit = 8, kAtOnce = 4;  // rows of a warp, pieces it takes at a time: lane = 8 piece + row
-    const uint64_t units = static_cast<uint64_t>(head.n_tiles) * a.kv_heads * (kGroupRows / kUnit);
-    for (uint64_t u = static_cast<uint64_t>(block) * kJoinWarps + (threadIdx.x >> 5); u < units;
-         u += static_cast<uint64_t>(blocks) * kJoinWarps) {
-        const uint32_t row0 = static_cast<uint32_t>(u % (kGroupRows / kUnit)) * kUnit;
-        const uint64_t gh = u / (kGroupRows / kUnit);
-        const TileGroup& g = a.at<TileGroup>(a.L.tiles)[gh / a.kv_heads];
-        const uint32_t h = static_cast<uint32_t>(gh % a.kv_heads), rows = g.rows;
-        if (!g.single || row0 >= rows) continue;
-        uint32_t c0 = 0, c1 = 0;
-        const bool two = rows <= kTileRows, keys = g.cost != 0;
-        if (keys) tile_ctas(g, h, head.share, &c0, &c1);
-        if (keys && c0 == c1 && !two) continue;
-        const uint32_t lanes = two ? 2 : 1, n = keys ? (c1 - c0 + 1) * lanes : 0;
-        const uint32_t slot = lane / kUnit, mine = min(row0 + lane % kUnit, rows - 1);
-        float top = -INFINITY, sum = 0.0f, acc[kUnit][kPer] = {};
-        for (uint32_t base = 0; base < n; base += kAtOnce) {
-            const uint32_t p = min(base + slot, n - 1), c = c0 + p / lanes;
-            const uint64_t row = tile_part_row(g, h, c0, c, a.L.extra_row) + (p % lanes) * (c == c0 ? rows : kTileRows) + mine;
-            const float2 ml = base + slot < n ? part_ml[row] : make_float2(-INFINITY, 0.0f);
-            float most = fmaxf(top, ml.x);
-            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
-            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
-            const float ref = most == -INFINITY ? 0.0f : most, keep = exp2_approx(top - ref), f = exp2_approx(ml.x - ref);
-            top = most;
-            float part = f * ml.y;
-            part += __shfl_xor_sync(0xFFFFFFFFu, part, 8);
-            part += __shfl_xor_sync(0xFFFFFFFFu, part, 16);
-            sum = sum * keep + part;
-            const uint32_t real = __ballot_sync(0xFFFFFFFFu, ml.x != -INFINITY);  // of the others the sums may never have been written
+    constexpr uint32_t kAtOnce = 4;  // pieces taken at a time: lane = 8 piece + row
+    const uint32_t lanes = rows <= kTileRows ? 2 : 1, n = g.cost > g.lead ? (c1 - c0 + 1) * lanes : 0;
+    const uint32_t slot = lane / kJoinRows, mine = min(row0 + lane % kJoinRows, rows - 1);
+    float top = -INFINITY, sum = 0.0f, acc[kJoinRows][kPer] = {};
+    for (uint32_t base = 0; base < n; base += kAtOnce) {
+        const uint32_t p = min(base + slot, n - 1), c = c0 + p / lanes;
+        const uint64_t row = tile_part_row(g, h, c0, c, a.L.extra_row) + (p % lanes) * (c == c0 ? rows : kTileRows) + mine;
+        const float2 ml = base + slot < n ? part_ml[row] : make_float2(-INFINITY, 0.0f);
+        float most = fmaxf(top, ml.x);
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
+        const float ref = most == -INFINITY ? 0.0f : most, keep = exp2_approx(top - ref), f = exp2_approx(ml.x - ref);
+        top = most;
+        float part = f * ml.y;
+        part += __shfl_xor_sync(0xFFFFFFFFu, part, 8);
+        part += __shfl_xor_sync(0xFFFFFFFFu, part, 16);
+        sum = sum * keep + part;
+        const uint32_t real = __ballot_sync(0xFFFFFFFFu, ml.x != -INFINITY);  // of the others the sums may never have been written
 #pragma unroll
-            for (uint32_t r = 0; r < kUnit; ++r) {
-                const float k = __shfl_sync(0xFFFFFFFFu, keep, r);
-                float v[kAtOnce][kPer] = {};
+        for (uint32_t r = 0; r < kJoinRows; ++r) {
+            const float k = __shfl_sync(0xFFFFFFFFu, keep, r);
+            float v[kAtOnce][kPer] = {};
 #pragma unroll
-                for (uint32_t q = 0; q < kAtOnce; ++q) {
-                    const uint64_t at = __shfl_sync(0xFFFFFFFFu, row, q * kUnit + r);
-                    if (real >> (q * kUnit + r) & 1) {
-                        if constexpr (kPer == 4) {
-                            const float4 x = *reinterpret_cast<const float4*>(part_o + at * D + lane * 4);
-                            v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
-                        } else {
-                            const float2 x = *reinterpret_cast<const float2*>(part_o + at * D + lane * 2);
-                            v[q][0] = x.x, v[q][1] = x.y;
-                        }
+            for (uint32_t q = 0; q < kAtOnce; ++q) {
+                const uint64_t at = __shfl_sync(0xFFFFFFFFu, row, q * kJoinRows + r);
+                if (real >> (q * kJoinRows + r) & 1) {
+                    if constexpr (kPer == 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(part_o + at * D + lane * 4);
+                        v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2*>(part_o + at * D + lane * 2);
+                        v[q][0] = x.x, v[q][1] = x.y;
                     }
                 }
+            }
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) acc[r][j] *= k;
+            for (int j = 0; j < kPer; ++j) acc[r][j] *= k;
 #pragma unroll
-                for (uint32_t q = 0; q < kAtOnce; ++q) {
-                    const float fr = __shfl_sync(0xFFFFFFFFu, f, q * kUnit + r);
+            for (uint32_t q = 0; q < kAtOnce; ++q) {
+                const float fr = __shfl_sync(0xFFFFFFFFu, f, q * kJoinRows + r);
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) acc[r][j] += fr * v[q][j];
-                }
+                for (int j = 0; j < kPer; ++j) acc[r][j] += fr * v[q][j];
             }
         }
-        const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
-        const uint32_t pr = g.row0 + mine, tok = pr / a.group, token = g.token0 + tok, qh = h * a.group + (pr - tok * a.group);
-        if (a.lse && lane < static_cast<int>(kUnit) && row0 + lane < rows)
-            a.lse[static_cast<uint64_t>(token) * q_heads + qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
-        const uint64_t dst = token * a.out_token + qh * a.out_head;
+    }
+    const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
+    const uint32_t pr = g.row0 + mine, tok = pr / a.group, token = g.token0 + tok, qh = h * a.group + (pr - tok * a.group);
+    if (a.lse && lane < static_cast<int>(kJoinRows) && row0 + lane < rows)
+        a.lse[static_cast<uint64_t>(token) * q_heads + qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+    const uint64_t dst = token * a.out_token + qh * a.out_head;
 #pragma unroll
-        for (uint32_t r = 0; r < kUnit; ++r) {
-            const float scale = __shfl_sync(0xFFFFFFFFu, inv, r);
-            const uint64_t to = __shfl_sync(0xFFFFFFFFu, dst, r);
-            if (row0 + r < rows) {
-                float o[kPer];
+    for (uint32_t r = 0; r < kJoinRows; ++r) {
+        const float scale = __shfl_sync(0xFFFFFFFFu, inv, r);
+        const uint64_t to = __shfl_sync(0xFFFFFFFFu, dst, r);
+        if (row0 + r < rows) {
+            float o[kPer];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) o[j] = acc[r][j] * scale;
-                store_row<T, kPer>(static_cast<T*>(a.out) + to + lane * kPer, o);
-            }
+            for (int j = 0; j < kPer; ++j) o[j] = acc[r][j] * scale;
+            store_row<T, kPer>(static_cast<T*>(a.out) + to + lane * kPer, o);
         }
     }
 }
 
-// The first row_blocks CTAs: rows base .. base + span - 1 of the output a warp;
+// Rows in tiles of their request's own: mostly the tile kernel has written
+// the output.  What is left are group heads that the border between two CTAs'
+// shares cuts, found from the borders, those without keys, and those of 128
+// rows or fewer, whose two tiles took steps in turn.
+template <typename T, int D>
+__device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t block, uint32_t blocks) {
+    const TileGroup* tiles = a.at<TileGroup>(a.L.tiles);
+    const uint32_t warps = blocks * kJoinWarps, me = block * kJoinWarps + (threadIdx.x >> 5);
+    const uint32_t borders = head.cost ? static_cast<uint32_t>((head.cost - 1) / head.share) : 0;
+    constexpr uint32_t kUnits = kGroupRows / kJoinRows;
+    for (uint32_t u = me; u < borders * kUnits; u += warps) {
+        const uint32_t b = u / kUnits + 1, row0 = u % kUnits * kJoinRows;
+        const TileGroup& g = tiles[a.at<uint32_t>(a.L.tile_first)[b]];
+        if (!g.single || g.rows <= kTileRows || row0 >= g.rows || g.cost <= g.lead) continue;
+        const uint32_t h = static_cast<uint32_t>((b * head.share - g.cost_begin) / g.cost);
+        uint32_t c0, c1;
+        tile_ctas(g, h, head.share, &c0, &c1);
+        if (c0 + 1 == b && c1 >= b) join_group_rows<T, D>(a, g, h, row0, c0, c1);
+    }
+    for (uint32_t u = me; u < head.n_rest * a.kv_heads * kUnits; u += warps) {
+        const uint32_t row0 = u % kUnits * kJoinRows, gh = u / kUnits, h = gh % a.kv_heads;
+        const TileGroup& g = tiles[a.at<uint32_t>(a.L.rest)[gh / a.kv_heads]];
+        if (row0 >= g.rows) continue;
+        uint32_t c0 = 0, c1 = 0;
+        if (g.cost > g.lead) tile_ctas(g, h, head.share, &c0, &c1);
+        join_group_rows<T, D>(a, g, h, row0, c0, c1);
+    }
+}
+
+// The last row_blocks CTAs: rows base .. base + span - 1 of the output a warp;
 // kSplit: one row a CTA, whose warps share its pieces (few rows, each of many
 // pieces).  The others: join_tiles.  Pieces are added in a fixed order.
 template <typename T, int D, bool kSplit>
@@ -671,13 +695,15 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t q_heads = a.kv_heads * a.group;
     wait_for_earlier();
-    const uint32_t base = kSplit ? blockIdx.x : (blockIdx.x * kJoinWarps + warp) * span;  // n_tokens * q_heads is below 2^31
     const PlanHead head = *a.at<PlanHead>(0);
     if (head.key != a.plan_key) return;
-    if (blockIdx.x >= row_blocks) {
-        join_tiles<T, D>(a, head, blockIdx.x - row_blocks, gridDim.x - row_blocks);
+    const uint32_t tile_blocks = gridDim.x - row_blocks;
+    if (blockIdx.x < tile_blocks) {
+        join_tiles<T, D>(a, head, blockIdx.x, tile_blocks);
         return;
     }
+    if (head.n_by_row == 0) return;
+    const uint32_t block = blockIdx.x - tile_blocks, base = kSplit ? block : (block * kJoinWarps + warp) * span;  // n_tokens * q_heads is below 2^31
     const uint32_t n_rows = head.n_tokens * q_heads;
     if (base >= n_rows) return;
 
@@ -852,6 +878,8 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
     L.groups16 = take(sizeof(Row16Group) * groups);
     L.items16 = take(sizeof(Row16Item) * (groups + extra));
     L.tiles = take(sizeof(TileGroup) * (tiles ? 2 * (rows / kGroupRows + 1) + R : 0));
+    L.tile_first = take(4ull * a->tile_ctas);
+    L.rest = take(4ull * (tiles ? 2 * (rows / kGroupRows + 1) + R : 0));
     L.part_ml = take(8ull * part_rows);
     L.part_o = take(4ull * part_rows * c.head_dim);
     L.total = off;

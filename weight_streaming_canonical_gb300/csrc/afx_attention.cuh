@@ -19,11 +19,13 @@ constexpr uint32_t kGroupRows = 2 * kTileRows;
 struct PlanHead {
     uint64_t key;
     uint64_t cost;          // of all tile groups x heads
-    uint64_t share;         // cost of one CTA of the tile kernel, even
+    uint64_t share;         // cost of one CTA of the tile kernel
     uint32_t n_tokens;      // live rows of the queries
     uint32_t n_items;       // row-16 items
     uint32_t n_tiles;       // tile groups
     uint32_t prefix_kind;   // Source of the packed rows' prefix part
+    uint32_t n_rest;        // tile groups whose output the join writes whatever CTAs had them
+    uint32_t n_by_row;      // tokens that are not in tiles of their request's own
 };
 
 enum Source : uint32_t { kNone = 0, kRow16 = 1, kTile = 2 };
@@ -62,9 +64,8 @@ struct alignas(16) Row16Item {
 };
 
 // Up to 256 packed rows and the keys they see: `prefix_keys` of the prefix,
-// then `own_keys` of the request.  cost: 2 a step of 128 keys for more than
-// 128 rows (both tiles work on every step), else 1 (the tiles take turns),
-// rounded up to even.
+// then `own_keys` of the request.  cost: step_cost a step of 128 keys, after
+// `lead` for what a group costs besides.
 struct alignas(16) TileGroup {
     uint64_t cost_begin;    // of head 0; head h begins h * cost later
     uint64_t part_row;      // where the results of the first piece of head 0 go
@@ -75,11 +76,12 @@ struct alignas(16) TileGroup {
     uint32_t token0;
     int32_t seen;
     uint32_t single;        // nothing else contributes to these rows
-    uint32_t pad[3];
+    uint32_t lead;
+    uint32_t pad[2];
 };
 
 struct AttnLayout {
-    uint64_t tokens, packed_token, groups16, items16, tiles, part_ml, part_o, total;
+    uint64_t tokens, packed_token, groups16, items16, tiles, tile_first, rest, part_ml, part_o, total;
     uint64_t extra_row;     // rows of the tile kernel's further pieces: 256 a CTA
     uint64_t max_rows;
 };
@@ -111,10 +113,17 @@ __device__ __forceinline__ uint32_t visible(int32_t seen, uint32_t row, uint32_t
     return v > 0 ? static_cast<uint32_t>(v) : 0u;
 }
 
-// The CTAs [first, last] of the tile kernel that hold pieces of a group's head.
+// More than 128 rows: both tiles work on every step's keys.  Fewer: the tiles
+// take the steps in turn, and half the products need as many keys (measured:
+// 3330 cycles a step for both, 2010 for one).
+constexpr uint32_t kStepBoth = 8, kStepOne = 5;
+__host__ __device__ __forceinline__ uint32_t step_cost(uint32_t rows) { return rows > kTileRows ? kStepBoth : kStepOne; }
+
+// The CTAs [first, last] of the tile kernel that hold pieces of a group's
+// head; for a group with keys.
 __device__ __forceinline__ void tile_ctas(const TileGroup& g, uint32_t h, uint64_t share, uint32_t* first, uint32_t* last) {
     const uint64_t begin = g.cost_begin + static_cast<uint64_t>(h) * g.cost;
-    *first = static_cast<uint32_t>(begin / share);
+    *first = static_cast<uint32_t>((begin + g.lead + step_cost(g.rows) - 1) / share);
     *last = static_cast<uint32_t>((begin + g.cost - 1) / share);
 }
 
@@ -123,6 +132,12 @@ __device__ __forceinline__ void tile_ctas(const TileGroup& g, uint32_t h, uint64
 __device__ __forceinline__ uint64_t tile_part_row(const TileGroup& g, uint32_t h, uint32_t first_cta, uint32_t cta, uint64_t extra_row) {
     const uint32_t rows = g.rows > kTileRows ? g.rows : 2 * g.rows;
     return cta == first_cta ? g.part_row + static_cast<uint64_t>(h) * rows : extra_row + static_cast<uint64_t>(cta) * kGroupRows;
+}
+
+// 16 bytes to shared memory; zeros where not real, and src is not read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+    const uint32_t n = real ? 16u : 0u;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
 template <typename T>

@@ -40,6 +40,7 @@ namespace {
 
 constexpr int kSoftWarps = 8;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;  // keys; values: the warp after it
+constexpr int kQueryWarp = 11;
 constexpr int kTileThreads = 384;
 // registers a thread: as launched, then of the row warps and of the others
 // (what the row warps add is what the others gave up)
@@ -65,7 +66,7 @@ struct Shape {
 struct Ctl {
     uint64_t full[8], empty[8];
     uint64_t tail;                     // a last step's values, before their missing rows are zeroed
-    uint64_t q_full;
+    uint64_t q_full[2], q_empty[2];    // a tile's queries
     uint64_t s_full[2], p_full[2][2], pv_done[2];
     uint64_t drain;
     uint32_t tmem;
@@ -214,6 +215,13 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* v) {
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// 32 bytes, a whole sector, to a 32-byte-aligned address.
+__device__ __forceinline__ void store_sector(void* to, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Multiplies 8 n columns of this thread's lane by f.  Rare: kept out of the
 // row warps' loop, whose code is long enough.
 __device__ __noinline__ void scale_columns(uint32_t addr, int n, float f) {
@@ -259,22 +267,25 @@ struct Walk {
         bool both;                 // both tiles on every step
     };
     __device__ bool next(Piece* p) {
-        if (at >= end) return false;
 #pragma unroll 1
-        while (at >= groups[g].cost_begin + static_cast<uint64_t>(groups[g].cost) * heads) ++g;
-        p->g = groups[g];
-        const uint64_t in = at - p->g.cost_begin;
-        p->h = static_cast<uint32_t>(in / p->g.cost);
-        const uint32_t off = static_cast<uint32_t>(in % p->g.cost);
-        const uint64_t stop = min(end, p->g.cost_begin + (static_cast<uint64_t>(p->h) + 1) * p->g.cost);
-        const uint32_t off1 = off + static_cast<uint32_t>(stop - at);
-        p->both = p->g.rows > kTileRows;
-        p->prefix_steps = ceil_div(p->g.prefix_keys, kTileKeys);
-        const uint32_t steps = p->prefix_steps + ceil_div(p->g.own_keys, kTileKeys);
-        p->step0 = p->both ? off / 2 : off;
-        p->step1 = min(steps, p->both ? off1 / 2 : off1);
-        at = stop;
-        return true;
+        while (at < end) {
+#pragma unroll 1
+            while (at >= groups[g].cost_begin + static_cast<uint64_t>(groups[g].cost) * heads) ++g;
+            p->g = groups[g];
+            const uint64_t in = at - p->g.cost_begin;
+            p->h = static_cast<uint32_t>(in / p->g.cost);
+            const uint32_t off = static_cast<uint32_t>(in % p->g.cost);
+            const uint64_t stop = min(end, p->g.cost_begin + (static_cast<uint64_t>(p->h) + 1) * p->g.cost);
+            const uint32_t off1 = off + static_cast<uint32_t>(stop - at), lead = p->g.lead, each = step_cost(p->g.rows);
+            p->both = p->g.rows > kTileRows;
+            p->prefix_steps = ceil_div(p->g.prefix_keys, kTileKeys);
+            const uint32_t steps = p->prefix_steps + ceil_div(p->g.own_keys, kTileKeys);
+            p->step0 = off > lead ? (off - lead) / each : 0;
+            p->step1 = off1 > lead ? min(steps, (off1 - lead) / each) : 0;
+            at = stop;
+            if (p->step0 < p->step1) return true;  // else the share ends before the group's first step
+        }
+        return false;
     }
 };
 
@@ -302,8 +313,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             bar_init(&ctl.empty[i], 1);
         }
         bar_init(&ctl.tail, 1);
-        bar_init(&ctl.q_full, kSoftWarps);
         for (int t = 0; t < 2; ++t) {
+            bar_init(&ctl.q_full[t], 1);
+            bar_init(&ctl.q_empty[t], 1);
             bar_init(&ctl.s_full[t], 1);
             bar_init(&ctl.p_full[t][0], kSoftWarps / 2);
             bar_init(&ctl.p_full[t][1], kSoftWarps / 2);
@@ -330,6 +342,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
     }
     Walk walk(a, head);
     Walk::Piece p;
+    if (threadIdx.x == 0 && walk.at < walk.end) a.at<uint32_t>(a.L.tile_first)[blockIdx.x] = walk.g;  // for the join
     if (warp >= kSoftWarps) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsOther));
       if (warp == kLoadWarp || warp == kLoadWarp + 1) {
@@ -405,6 +418,71 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             for (q += (q & 1u) != kv; q < seq; q += 2)
                 if (!bar_drain(&ctl.full[q % Sh::kSlots], (q / Sh::kSlots) & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
         }
+      } else if (warp == kQueryWarp) {
+        // ---- the queries, in the operand's swizzled order: a lane works out where a row lies, then 16 bytes a lane of
+        // two (or four) rows at a time.  A tile's next ones are fetched while its rows finish with the last scores
+        constexpr uint32_t kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
+        const T* q = static_cast<const T*>(a.q);
+        const int32_t* packed = a.at<int32_t>(a.L.packed_token);
+        const uint32_t c = lane % kChunks;
+        uint32_t phases = 0, used = 0;  // a bit a tile
+        bool ok = true;
+        while (ok && walk.next(&p)) {
+            const TileGroup& g = p.g;
+            // lane l's rows: l, l + 32, ...; all into L2 while the products still use the rows before
+            uint64_t at[kGroupRows / 32];
+#pragma unroll
+            for (uint32_t j = 0; j < kGroupRows / 32; ++j) {
+                const uint32_t pr = g.row0 + min(j * 32 + lane, g.rows - 1), tok = pr / a.group;
+                const uint32_t token = g.request < 0 ? __ldg(packed + tok) : g.token0 + tok;
+                at[j] = reinterpret_cast<uint64_t>(q + token * a.q_token + (p.h * a.group + (pr - tok * a.group)) * a.q_head);
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < kGroupRows / 32; ++j)
+                if (j * 32 + lane < g.rows)
+#pragma unroll
+                    for (uint32_t b = 0; b < D * 2; b += 128) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(at[j] + b));
+#pragma unroll 1
+            for (uint32_t t = 0; t < (p.both ? 2u : 1u); ++t) {
+                if (used >> t & 1) {
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.q_empty[t], phases >> t & 1, ctl, a.status));
+                    if (!ok) break;
+                    phases ^= 1u << t;
+                }
+                used |= 1u << t;
+                const uint32_t dst = smem_addr(smem) + t * Sh::kSlot + (c / 8) * Sh::kBlock;
+#pragma unroll 1
+                for (uint32_t r0 = 0; r0 < kTileRows; r0 += 32) {
+                    const uint64_t src = at[0];
+#pragma unroll
+                    for (uint32_t j = 0; j + 1 < kGroupRows / 32; ++j) at[j] = at[j + 1];
+                    auto each = [&](auto&& copy) {
+#pragma unroll
+                        for (uint32_t i = 0; i < 32 / kRowsAtOnce; ++i) {
+                            const uint32_t in32 = i * kRowsAtOnce + lane / kChunks, in_tile = r0 + in32;
+                            copy(dst + in_tile * 128 + (((c % 8) ^ (in_tile & 7)) * 16), __shfl_sync(0xFFFFFFFFu, src, in32) + c * 16,
+                                 t * kTileRows + in_tile < g.rows);
+                        }
+                    };
+                    if (a.q_align == 16) {
+                        each([](uint32_t to, uint64_t from, bool real) { copy16(to, reinterpret_cast<const void*>(from), real); });
+                    } else {
+                        each([](uint32_t to, uint64_t from, bool real) {
+                            const uint16_t* e = reinterpret_cast<const uint16_t*>(from);
+                            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (real) w[k] = __ldg(e + 2 * k) | static_cast<uint32_t>(__ldg(e + 2 * k + 1)) << 16;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                        });
+                    }
+                }
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&ctl.q_full[t]);
+            }
+        }
       } else if (warp == kMmaWarp) {
         // ---- the products.  The whole warp walks the steps and waits; one
         // lane, the same throughout, issues (descriptors stay warp-uniform)
@@ -414,7 +492,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         const bool leader = elect();
         const uint64_t q_desc = operand(smem_addr(smem), 16), k_desc = operand(smem_addr(smem + Sh::kQ), 16),
                        v_desc = operand(smem_addr(smem + Sh::kQ), Sh::kBlock);
-        uint32_t pieces = 0, p_count[2] = {0, 0};
+        const uint32_t qk = kQk | (a.scale_log2 < 0.0f ? 1u << 13 : 0u);  // a negative scale: -q instead
+        uint32_t q_phase = 0, p_count[2] = {0, 0};
         uint32_t k_slot = 0, k_phase = 0;  // ring position of the next keys or values to use
         bool ok = true;
         auto uniform = [&](bool r) { return __all_sync(0xFFFFFFFFu, r); };
@@ -429,15 +508,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 phase ^= 1u;
             }
         };
-        auto scores = [&](uint32_t t, uint32_t slot, bool own_q, bool release) {
+        auto scores = [&](uint32_t t, uint32_t slot, bool own_q, bool release, bool last_q) {
             const uint64_t qd = q_desc + (own_q ? t * (Sh::kSlot >> 4) : 0), kd = k_desc + slot * (Sh::kSlot >> 4);
 #pragma unroll
             for (uint32_t ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = (ks / 4) * (Sh::kBlock >> 4) + (ks % 4) * 2;
-                mma_ss(leader, tmem + Sh::kS + t * kTileKeys, qd + off, kd + off, kQk, ks != 0);
+                mma_ss(leader, tmem + Sh::kS + t * kTileKeys, qd + off, kd + off, qk, ks != 0);
             }
             if (release) commit(leader, &ctl.empty[slot]);
             commit(leader, &ctl.s_full[t]);
+            if (last_q) commit(leader, &ctl.q_empty[own_q ? t : 0]);
         };
         // the weights come in two halves of 64 keys; false: a wait gave up
         auto values = [&](uint32_t t, uint32_t slot, bool first, bool release) {
@@ -456,17 +536,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             return true;
         };
         while (ok && walk.next(&p)) {
-            ok = uniform(bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status));
-            fence_after();
             const uint32_t n = p.step1 - p.step0;
             const bool both = p.both;
-            if (ok) ok = slot_full(k_slot, k_phase);
-            if (!ok) break;
+            ok = slot_full(k_slot, k_phase);
             // scores of step 0; then, with both tiles on every step, a tile at a time the values of step i and the
             // scores of step i + 1 (whose place in tensor memory the weights of step i held); with the tiles taking
             // turns the scores of step i + 1, of the other tile, first
 #pragma unroll 1
-            for (uint32_t t = 0; t < (both ? 2u : 1u); ++t) scores(t, k_slot, both, !both || t == 1);
+            for (uint32_t t = 0; t < (both ? 2u : 1u) && ok; ++t) {
+                ok = uniform(bar_wait(&ctl.q_full[t], q_phase >> t & 1, ctl, a.status));
+                q_phase ^= 1u << t;
+                fence_after();
+                if (ok) scores(t, k_slot, both, !both || t == 1, n == 1);
+            }
             uint32_t v_slot = 0;
 #pragma unroll 1
             for (uint32_t u = 0; u < (both ? 2 * n : n) && ok; ++u) {
@@ -478,11 +560,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     const uint32_t v_phase = k_phase;
                     step_on(k_slot, k_phase);
                     ok = !more || slot_full(k_slot, k_phase);
-                    if (ok && more && !both) scores(t ^ 1, k_slot, false, true);
+                    if (ok && more && !both) scores(t ^ 1, k_slot, false, true, i + 2 == n);
                     ok = ok && slot_full(v_slot, v_phase);
                 }
                 ok = ok && values(t, v_slot, both ? i == 0 : i < 2, last);
-                if (ok && more && both) scores(t, k_slot, true, last);
+                if (ok && more && both) scores(t, k_slot, true, last, i + 2 == n);
             }
         }
         if (!ok && leader) {  // products in flight finish before the tensor memory is freed
@@ -498,64 +580,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         const uint32_t lanes = (static_cast<uint32_t>(warp & 3) * 32u) << 16;
         const uint32_t s_col = tmem + lanes + Sh::kS + t * kTileKeys, p_col = tmem + lanes + Sh::kP + t * Sh::kPStep,
                        o_col = tmem + lanes + Sh::kO + t * D;
-        const T* q = static_cast<const T*>(a.q);
-        const int32_t* packed = a.at<int32_t>(a.L.packed_token);
         float* part_o = a.at<float>(a.L.part_o);
         float2* part_ml = a.at<float2>(a.L.part_ml);
         const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);  // not 0: masked scores stay minus infinity
-        const uint16_t flip = a.scale_log2 < 0.0f ? 0x8000u : 0u;  // a negative scale: -q instead
-        uint32_t s_count = 0, pv_count = 0, pieces = 0;
+        uint32_t s_count = 0, pv_count = 0;
         bool ok = true;
         while (ok && walk.next(&p)) {
             const TileGroup& g = p.g;
-            // the warp's 32 rows of the queries, in the operand's swizzled order: a lane works out where its
-            // row lies, then 16 bytes a lane of two (or four) rows at a time
             const uint32_t row = (p.both ? t * kTileRows : 0) + in_tile;
             const bool live = row < g.rows;
             const bool warp_live = (p.both ? t * kTileRows : 0) + (warp & 3) * 32 < g.rows;
-            uint32_t token = 0, qh = 0;
-            if (live) {
-                const uint32_t pr = g.row0 + row, tok = pr / a.group;
-                token = g.request < 0 ? packed[tok] : g.token0 + tok;
-                qh = p.h * a.group + (pr - tok * a.group);
-            }
-            if (p.both || t == 0) {
-                constexpr uint32_t kChunks = D / 8, kRowsAtOnce = 32 / kChunks;
-                const uint64_t src = reinterpret_cast<uint64_t>(q + token * a.q_token + qh * a.q_head);
-                const uint32_t c = lane % kChunks, flip2 = flip * 0x10001u;
-                uint8_t* dst = smem + (p.both ? t * Sh::kSlot : 0) + (c / 8) * Sh::kBlock;
-                uint4 v[32 / kRowsAtOnce];  // all loads, then all stores
-#pragma unroll
-                for (uint32_t i = 0; i < 32 / kRowsAtOnce; ++i) {
-                    const uint32_t r = i * kRowsAtOnce + lane / kChunks;
-                    const uint4* from = reinterpret_cast<const uint4*>(__shfl_sync(0xFFFFFFFFu, src, r)) + c;
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if ((p.both ? t * kTileRows : 0) + (warp & 3) * 32 + r < g.rows) {
-                        if (a.q_align == 16) {
-                            v[i] = __ldg(from);
-                        } else {
-                            const uint16_t* e = reinterpret_cast<const uint16_t*>(from);
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) w[k] = __ldg(e + 2 * k) | static_cast<uint32_t>(__ldg(e + 2 * k + 1)) << 16;
-                            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (uint32_t i = 0; i < 32 / kRowsAtOnce; ++i) {
-                    const uint32_t tile_row = (warp & 3) * 32 + i * kRowsAtOnce + lane / kChunks;
-                    *reinterpret_cast<uint4*>(dst + tile_row * 128 + (((c % 8) ^ (tile_row & 7)) * 16)) =
-                        make_uint4(v[i].x ^ flip2, v[i].y ^ flip2, v[i].z ^ flip2, v[i].w ^ flip2);
-                }
-                fence_async_shared();
-            }
-            __syncwarp();
-            if (lane == 0) bar_arrive(&ctl.q_full);
-            // all warps together: one without steps here must not run ahead into the next piece's phase
-            ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.q_full, pieces++ & 1u, ctl, a.status));
-            if (!ok) break;
-
             const uint32_t limit = g.request < 0 || !live ? g.own_keys : min(g.own_keys, visible(g.seen, g.row0 + row, a.group));
             const uint32_t all_see = g.request < 0 ? g.own_keys : visible(g.seen, g.row0, a.group);  // own keys every row sees
             float ref = -INFINITY, sum = 0.0f, seen_most = -INFINITY;
@@ -672,55 +706,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 const uint32_t in_piece = p.both ? row : t * (walk.cta == cta0 ? g.rows : kTileRows) + row;
                 const uint64_t pr = tile_part_row(g, p.h, cta0, walk.cta, a.L.extra_row) + in_piece;
                 const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
+                // to the output only from a request's own tiles, whose tokens follow one another
+                const uint32_t packed_row = g.row0 + row, tok = packed_row / a.group;
+                const uint64_t token = g.token0 + tok, qh = p.h * a.group + (packed_row - tok * a.group);
                 T* out = static_cast<T*>(a.out) + token * a.out_token + qh * a.out_head;
-                // 32 columns at a time through this warp's 4 KB of the tile's queries (no product reads them any
-                // more, and the warp's next queries go there too), so that rows go out in runs of 128 (64) bytes;
-                // 16-byte chunks swizzled against bank conflicts
-                uint8_t* stage = smem + t * Sh::kSlot + (warp & 3) * 4096;
-                auto chunk = [&](uint32_t r, uint32_t k) { return reinterpret_cast<uint4*>(stage + r * 128 + ((k ^ (r & 7)) * 16)); };
 #pragma unroll 1
-                for (uint32_t c = 0; done > 0 && c < D / 32; ++c) {
+                for (uint32_t c = 0; done > 0 && c < D; c += 32) {
                     uint32_t o[32];
-                    tmem_load32(o_col + c * 32, o);
-                    tmem_wait_load();
                     __syncwarp();
-                    if (final) {
-                        uint32_t w[16];
+                    tmem_load32(o_col + c, o);
+                    tmem_wait_load();
+                    if (!live) continue;
+                    if (!final) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            w[j] = ref == -INFINITY ? 0u : Elem<T>::pack(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        for (int j = 0; j < 32; j += 8) store_sector(part_o + pr * D + c + j, o + j);
+                        continue;
+                    }
+                    uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *chunk(lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                        __syncwarp();
+                    for (int j = 0; j < 16; ++j)
+                        w[j] = ref == -INFINITY ? 0u : Elem<T>::pack(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                    if (reinterpret_cast<uintptr_t>(out) & 31u) {
 #pragma unroll
-                        for (uint32_t i = 0; i < 4; ++i) {
-                            const uint32_t r = i * 8 + lane / 4;
-                            T* to = reinterpret_cast<T*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(out), r)) + c * 32 + (lane % 4) * 8;
-                            const uint4 v = *chunk(r, lane % 4);
-                            if ((p.both ? t * kTileRows : 0) + (warp & 3) * 32 + r < g.rows) {
-                                if (reinterpret_cast<uintptr_t>(to) & 15u) {
-                                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k) reinterpret_cast<uint16_t*>(to)[k] = static_cast<uint16_t>(x[k / 2] >> (16 * (k & 1)));
-                                } else {
-                                    *reinterpret_cast<uint4*>(to) = v;
-                                }
-                            }
-                        }
+                        for (int j = 0; j < 32; ++j)
+                            reinterpret_cast<uint16_t*>(out)[c + j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *chunk(lane, j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                        __syncwarp();
-                        const uint64_t pr0 = __shfl_sync(0xFFFFFFFFu, pr, 0);  // the warp's rows follow one another
-#pragma unroll
-                        for (uint32_t i = 0; i < 8; ++i) {
-                            const uint32_t r = i * 4 + lane / 8;
-                            const uint4 v = *chunk(r, lane % 8);
-                            if ((p.both ? t * kTileRows : 0) + (warp & 3) * 32 + r < g.rows)
-                                *reinterpret_cast<uint4*>(part_o + (pr0 + r) * D + c * 32 + (lane % 8) * 4) = v;
-                        }
+                        store_sector(out + c, w);
+                        store_sector(out + c + 16, w + 8);
                     }
                 }
                 if (live) {
