@@ -36,14 +36,26 @@ namespace {
 constexpr uint32_t kPlanThreads = 1024;
 constexpr uint32_t kMaxRequests = AFX_KV_MAX_REQUESTS;
 constexpr uint32_t kKeyAlign = 64;     // 16-row items' key ranges start at multiples of this
-constexpr uint32_t kMinKeys = 256;     // keys of a 16-row item, at least, where a range is cut
-constexpr uint32_t kTargetUnits = 1216;  // 16-row items x heads that the cuts aim at
+constexpr uint32_t kMinKeys = 64;     // keys of a 16-row item, at least, where a range is cut
+// 16-row items x heads that the cuts aim at: a unit a warp of the GPU, or two
+// where there are many groups, of uneven lengths (64 requests of 200 to 1000
+// tokens: 74 us against 78; two requests on 131000 keys, whose join has more
+// pieces then: 121 against 115).
+constexpr uint32_t kTargetUnits = 2432, kFewUnits = 1216;
 constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's tiles take the prefix along
-constexpr uint32_t kMinShare = 4 * kStepBoth;  // cost of a tile CTA, at least
+// Cost of a tile CTA, at least: a CTA's start costs as much as four steps.
+// Where 16-row items keep the other SMs busy, more (64 requests with 8192
+// keys in common: 67 us against 78).
+constexpr uint32_t kMinShare = 4 * kStepBoth, kMinShareBeside = 12 * kStepBoth;
 // What a tile group costs besides its steps (filling and emptying the pipe,
 // masked steps, the output), where CTAs take several whole groups each; where a
 // group is cut over several CTAs, all have that cost alike.
 constexpr uint32_t kGroupCost = 18;
+// Up to this many rows in the batch the 16-row kernel takes all of them, two
+// groups reading the same keys, and the tile kernel is not launched: with 20
+// to 30 rows on a prefix of 500 to 8000 keys 27-33 us against 31-41, on 64000
+// keys 74-76 against 76-78; with 45 rows on 64000 keys 84 against 76.
+constexpr uint32_t kFewRows = 32;
 constexpr uint32_t kFewTokens = 8, kManyMax = 512;
 
 __host__ __device__ inline uint64_t up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
@@ -133,10 +145,13 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     let_next_start();
     __shared__ uint32_t n_many;
     __shared__ Many many[kManyMax];  // requests of more than a few tokens
-    if (threadIdx.x == 0) n_many = 0;
+    if (threadIdx.x == 0) {
+        n_many = 0;
+        *a.at<uint32_t>(a.L.counter) = 0;
+    }
     // the lengths have to make sense before anything is addressed by them
     bool bad = false;
-    Counts<2> first{};  // keys of the 16-row groups, tokens that share tiles on the prefix
+    Counts<3> first{};  // keys of the 16-row groups, tokens that share the prefix's groups, 16-row groups
     if (threadIdx.x == 0 && a.starts[0] != 0) bad = true;
     for (uint32_t r = r0; r < r1; ++r) {
         const int32_t s = a.starts[r], e = a.starts[r + 1], len = a.lens[r];
@@ -147,7 +162,10 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         const uint32_t rows = static_cast<uint32_t>(e - s) * G;
         const Kind k = kind_of(a, rows);
         if (k.own == kRow16)
-            for (uint32_t row = 0; row < rows; row += kRows) first.v[0] += visible(len - (e - s), min(rows, row + kRows) - 1, G);
+            for (uint32_t row = 0; row < rows; row += kRows) {
+                first.v[0] += visible(len - (e - s), min(rows, row + kRows) - 1, G);
+                first.v[2] += 1;
+            }
         if (!k.fused) first.v[1] += e - s;
     }
     const bool refused = __syncthreads_or(bad) != 0;
@@ -158,14 +176,15 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         }
         return;
     }
-    Counts<2> all;
+    Counts<3> all;
     uint32_t packed = static_cast<uint32_t>(block_exclusive(first, &all).v[1]);
     const uint32_t prefix_rows = static_cast<uint32_t>(all.v[1]) * G;
     const uint32_t prefix_kind = prefix_rows == 0 ? kNone : a.tile_ctas && prefix_rows > kRows ? kTile : kRow16;
     const uint32_t groups_p = prefix_kind == kRow16 ? ceil_div(prefix_rows, kRows) : 0;
     const uint32_t tiles_p = prefix_kind == kTile ? ceil_div(prefix_rows, kGroupRows) : 0;
     const uint64_t keys = all.v[0] + static_cast<uint64_t>(groups_p) * a.prefix_len;
-    const uint64_t units = kTargetUnits / a.kv_heads ? kTargetUnits / a.kv_heads : 1;
+    const uint32_t target = (all.v[2] + groups_p) * a.kv_heads * 4 >= kFewUnits ? kTargetUnits : kFewUnits;
+    const uint64_t units = target / a.kv_heads ? target / a.kv_heads : 1;
     const uint64_t want = up((keys + units - 1) / units, kKeyAlign);
     const uint32_t piece = static_cast<uint32_t>(want < kMinKeys ? kMinKeys : want < (1u << 31) ? want : 1u << 31);
 
@@ -285,8 +304,9 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     if (threadIdx.x == 0) {
         const uint64_t c = total.v[4] + total.v[3] * leads + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
         const uint64_t share = (c + ctas - 1) / ctas;
-        *head = PlanHead{a.plan_key, c, share < kMinShare ? kMinShare : share, static_cast<uint32_t>(a.starts[R]),
-                         groups_p * pieces_p + static_cast<uint32_t>(total.v[1]), n_tiles, prefix_kind, static_cast<uint32_t>(total.v[6]), static_cast<uint32_t>(total.v[7])};
+        const uint32_t n_items = groups_p * pieces_p + static_cast<uint32_t>(total.v[1]);
+        const uint64_t least = static_cast<uint64_t>(n_items) * a.kv_heads >= ctas ? kMinShareBeside : kMinShare;
+        *head = PlanHead{a.plan_key, c, share < least ? least : share, static_cast<uint32_t>(a.starts[R]), n_items, n_tiles, prefix_kind, static_cast<uint32_t>(total.v[6]), static_cast<uint32_t>(total.v[7])};
     }
 }
 
@@ -315,7 +335,10 @@ constexpr size_t rows16_smem() {
 }
 
 // A unit is an item's rows and keys of one key/value head; every warp takes
-// units on its own, steps of 16 keys, with no barrier anywhere.  Its copies
+// units on its own, steps of 16 keys, with no barrier anywhere: the next one
+// from a counter, for many CTAs start only when one of the tile kernel's ends
+// (64 requests of 200 to 1000 tokens: 23 us after its last one's end with
+// every warp's units fixed).  Its copies
 // run kStages - 1 steps ahead, over the ends of units, so that memory stays
 // busy while a unit's results are written and the next one's queries loaded.
 // Two CTAs an SM: 8 warps with 16 KB each in flight.
@@ -332,7 +355,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
     let_next_start();
     const PlanHead head = *a.at<PlanHead>(0);
     if (head.key != a.plan_key && threadIdx.x == 0) raise(a.status, AFX_DEV_BAD_PLAN);
-    const uint32_t n_units = head.key == a.plan_key ? head.n_items * a.kv_heads : 0, step = gridDim.x * kWarps;
+    const uint32_t n_units = head.key == a.plan_key ? head.n_items * a.kv_heads : 0;
+    uint32_t* counter = a.at<uint32_t>(a.L.counter);
+    __shared__ uint32_t rings[kWarps][4];  // units whose copies have begun: the copies are at most four units ahead
+    uint32_t* ring = rings[warp];
+    uint32_t opened = 0;
     const Row16Item* items = a.at<Row16Item>(a.L.items16);
     const int32_t* packed = a.at<int32_t>(a.L.packed_token);
     float* part_o = a.at<float>(a.L.part_o);
@@ -344,11 +371,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
     const uint32_t page_mask = (1u << a.shift) - 1;
 
     // the copies: unit c_unit's step c_block goes into stage c_stage
-    uint32_t c_unit = blockIdx.x * kWarps + warp, c_block = 0, c_blocks = 0, c_key0 = 0, c_key1 = 0, c_stage = 0;
+    uint32_t c_unit = 0, c_block = 0, c_blocks = 0, c_key0 = 0, c_key1 = 0, c_stage = 0;
     uint64_t c_head = 0;
     const int32_t* c_pages = nullptr;
     uint32_t c_page = 0;  // lane l: the page of step c_block / 32 * 32 + l
     auto open = [&]() {
+        if (lane == 0) {
+            c_unit = atomicAdd(counter, 1u);
+            ring[opened & 3] = c_unit;
+        }
+        c_unit = __shfl_sync(0xFFFFFFFFu, c_unit, 0);
+        ++opened;
         if (c_unit >= n_units) return;
         const Row16Item& it = items[c_unit / a.kv_heads];
         c_key0 = it.key0;
@@ -388,20 +421,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
                 k_from += hop;
                 v_from += hop;
             }
-            if (++c_block == c_blocks) {
-                c_unit += step;
-                open();
-            }
+            if (++c_block == c_blocks) open();
             c_stage = c_stage + 1 == kStages ? 0 : c_stage + 1;
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
-    open();
+    if (n_units) open();
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) copy_next();
 
     uint32_t stage = 0;
-    for (uint32_t unit = blockIdx.x * kWarps + warp; unit < n_units; unit += step) {
+    for (uint32_t done = 0; done < opened; ++done) {
+        __syncwarp();
+        const uint32_t unit = ring[done & 3];
+        if (unit >= n_units) break;
         const Row16Item it = items[unit / a.kv_heads];
         const uint32_t h = unit % a.kv_heads;
         // the queries as A fragments: rows lane / 4 and lane / 4 + 8
@@ -584,6 +617,18 @@ __device__ __forceinline__ void store_row(T* out, const float (&v)[N]) {
     }
 }
 
+// A lane's elements of a piece's row.
+template <int N>
+__device__ __forceinline__ void load_part(const float* from, float (&v)[N]) {
+    if constexpr (N == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(from);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2*>(from);
+        v[0] = x.x, v[1] = x.y;
+    }
+}
+
 // Eight rows of a tile group's head, put together from its pieces by a warp.
 template <typename T, int D>
 __device__ void join_group_rows(const AttnArgs& a, const TileGroup& g, uint32_t h, uint32_t row0, uint32_t c0, uint32_t c1) {
@@ -592,48 +637,36 @@ __device__ void join_group_rows(const AttnArgs& a, const TileGroup& g, uint32_t 
     const uint32_t q_heads = a.kv_heads * a.group, rows = g.rows;
     const float* part_o = a.at<float>(a.L.part_o);
     const float2* part_ml = a.at<float2>(a.L.part_ml);
-    constexpr uint32_t kAtOnce = 4;  // pieces taken at a time: lane = 8 piece + row
+    constexpr uint32_t kAtOnce = 2;  // pieces taken at a time (mostly there are two): lane = 8 piece + row, twice
     const uint32_t lanes = rows <= kTileRows ? 2 : 1, n = g.cost > g.lead ? (c1 - c0 + 1) * lanes : 0;
-    const uint32_t slot = lane / kJoinRows, mine = min(row0 + lane % kJoinRows, rows - 1);
+    const uint32_t slot = lane / kJoinRows % kAtOnce, mine = min(row0 + lane % kJoinRows, rows - 1);
     float top = -INFINITY, sum = 0.0f, acc[kJoinRows][kPer] = {};
+#pragma unroll 1
     for (uint32_t base = 0; base < n; base += kAtOnce) {
         const uint32_t p = min(base + slot, n - 1), c = c0 + p / lanes;
         const uint64_t row = tile_part_row(g, h, c0, c, a.L.extra_row) + (p % lanes) * (c == c0 ? rows : kTileRows) + mine;
+        float v[kJoinRows][kAtOnce][kPer];  // all loads, then all sums
+#pragma unroll
+        for (uint32_t r = 0; r < kJoinRows; ++r)
+#pragma unroll
+            for (uint32_t q = 0; q < kAtOnce; ++q) load_part(part_o + __shfl_sync(0xFFFFFFFFu, row, q * kJoinRows + r) * D + lane * kPer, v[r][q]);
         const float2 ml = base + slot < n ? part_ml[row] : make_float2(-INFINITY, 0.0f);
-        float most = fmaxf(top, ml.x);
-        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
-        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
+        const float most = fmaxf(top, fmaxf(ml.x, __shfl_xor_sync(0xFFFFFFFFu, ml.x, 8)));
         const float ref = most == -INFINITY ? 0.0f : most, keep = exp2_approx(top - ref), f = exp2_approx(ml.x - ref);
         top = most;
-        float part = f * ml.y;
-        part += __shfl_xor_sync(0xFFFFFFFFu, part, 8);
-        part += __shfl_xor_sync(0xFFFFFFFFu, part, 16);
-        sum = sum * keep + part;
+        const float part = f * ml.y;
+        sum = sum * keep + (part + __shfl_xor_sync(0xFFFFFFFFu, part, 8));
         const uint32_t real = __ballot_sync(0xFFFFFFFFu, ml.x != -INFINITY);  // of the others the sums may never have been written
 #pragma unroll
         for (uint32_t r = 0; r < kJoinRows; ++r) {
             const float k = __shfl_sync(0xFFFFFFFFu, keep, r);
-            float v[kAtOnce][kPer] = {};
-#pragma unroll
-            for (uint32_t q = 0; q < kAtOnce; ++q) {
-                const uint64_t at = __shfl_sync(0xFFFFFFFFu, row, q * kJoinRows + r);
-                if (real >> (q * kJoinRows + r) & 1) {
-                    if constexpr (kPer == 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(part_o + at * D + lane * 4);
-                        v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
-                    } else {
-                        const float2 x = *reinterpret_cast<const float2*>(part_o + at * D + lane * 2);
-                        v[q][0] = x.x, v[q][1] = x.y;
-                    }
-                }
-            }
 #pragma unroll
             for (int j = 0; j < kPer; ++j) acc[r][j] *= k;
 #pragma unroll
             for (uint32_t q = 0; q < kAtOnce; ++q) {
                 const float fr = __shfl_sync(0xFFFFFFFFu, f, q * kJoinRows + r);
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) acc[r][j] += fr * v[q][j];
+                for (int j = 0; j < kPer; ++j) acc[r][j] += real >> (q * kJoinRows + r) & 1 ? fr * v[r][q][j] : 0.0f;
             }
         }
     }
@@ -695,6 +728,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t q_heads = a.kv_heads * a.group;
     wait_for_earlier();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.at<uint32_t>(a.L.counter) = 0;  // for the next layer
     const PlanHead head = *a.at<PlanHead>(0);
     if (head.key != a.plan_key) return;
     const uint32_t tile_blocks = gridDim.x - row_blocks;
@@ -749,22 +783,17 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
             for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
             sum += part;
             const uint32_t live = __ballot_sync(0xFFFFFFFFu, real);
-#pragma unroll 8
-            for (uint32_t j = 0; j < m; ++j) {
-                const float fj = __shfl_sync(0xFFFFFFFFu, f, j);
-                const uint64_t rj = __shfl_sync(0xFFFFFFFFu, row, j);
-                float v[kPer] = {};
-                if (live >> j & 1) {
-                    if constexpr (kPer == 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(part_o + rj * D + lane * 4);
-                        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-                    } else {
-                        const float2 x = *reinterpret_cast<const float2*>(part_o + rj * D + lane * 2);
-                        v[0] = x.x, v[1] = x.y;
-                    }
-                }
+            constexpr uint32_t kAtOnce = kSplit ? 8 : 4;  // loads in flight; past the last piece: row 0
+            for (uint32_t j = 0; j < m; j += kAtOnce) {
+                float v[kAtOnce][kPer];
 #pragma unroll
-                for (int k = 0; k < kPer; ++k) acc[k] += fj * v[k];
+                for (uint32_t i = 0; i < kAtOnce; ++i) load_part(part_o + __shfl_sync(0xFFFFFFFFu, row, j + i) * D + lane * kPer, v[i]);
+#pragma unroll
+                for (uint32_t i = 0; i < kAtOnce; ++i) {
+                    const float fj = __shfl_sync(0xFFFFFFFFu, f, j + i);
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k) acc[k] += live >> (j + i) & 1 ? fj * v[i][k] : 0.0f;
+                }
             }
         }
         if constexpr (kSplit) {
@@ -849,7 +878,8 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
     a->scale_log2 = static_cast<float>(static_cast<double>(d->scale) * 1.4426950408889634074);
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
-    a->tile_ctas = tiles_fit(c) ? static_cast<uint32_t>(sms) : 0u;
+    const bool few = static_cast<uint64_t>(d->n_tokens) * a->group <= kFewRows;
+    a->tile_ctas = !few && tiles_fit(c) ? static_cast<uint32_t>(sms) : 0u;
     // bounds on what the plan writes.  16-row groups: where tiles serve the
     // larger ones, one a request and one on the prefix; every group has one
     // piece, and the cuts add at most kTargetUnits / kv_heads.  Tile groups:
@@ -873,6 +903,7 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
         off = up(off + bytes, 256);
         return at;
     };
+    L.counter = take(4);
     L.tokens = take(sizeof(TokenInfo) * static_cast<uint64_t>(d->n_tokens));
     L.packed_token = take(4ull * d->n_tokens);
     L.groups16 = take(sizeof(Row16Group) * groups);

@@ -81,6 +81,7 @@ struct alignas(16) TileGroup {
 };
 
 struct AttnLayout {
+    uint64_t counter;       // 16-row units taken so far, by this layer
     uint64_t tokens, packed_token, groups16, items16, tiles, tile_first, rest, part_ml, part_o, total;
     uint64_t extra_row;     // rows of the tile kernel's further pieces: 256 a CTA
     uint64_t max_rows;
