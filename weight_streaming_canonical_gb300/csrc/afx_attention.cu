@@ -221,11 +221,13 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
                 tile(row, m, k.fused ? a.prefix_len : 0u, visible(seen, row + m - 1, G), s, seen, k.fused);
             }
     };
-    Counts<8> mine{};
+    // groups | tile groups << 32, pieces, their rows, cost, rows of tile pieces, rest | tokens by row << 32
+    constexpr uint64_t kHigh = 1ull << 32;
+    Counts<6> mine{};
     for (uint32_t r = r0; r < r1; ++r) {
         const uint32_t n = a.starts[r + 1] - a.starts[r];
         const Kind k = kind_of(a, n * G);
-        if (!(k.fused && k.own == kTile)) mine.v[7] += n;
+        if (!(k.fused && k.own == kTile)) mine.v[5] += kHigh * n;
         walk(
             r,
             [&](uint32_t, uint32_t m, uint32_t end, uint32_t, int32_t) {
@@ -235,15 +237,15 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
                 mine.v[2] += static_cast<uint64_t>(pieces) * m;
             },
             [&](uint32_t, uint32_t m, uint32_t prefix, uint32_t own, uint32_t, int32_t, bool single) {
-                mine.v[3] += 1;
-                mine.v[4] += static_cast<uint64_t>(tile_cost(m, prefix, own)) * a.kv_heads;
-                mine.v[5] += static_cast<uint64_t>(m > kTileRows ? m : 2 * m) * a.kv_heads;
-                mine.v[6] += rests(m, prefix + own, single);
+                mine.v[0] += kHigh;
+                mine.v[3] += static_cast<uint64_t>(tile_cost(m, prefix, own)) * a.kv_heads;
+                mine.v[4] += static_cast<uint64_t>(m > kTileRows ? m : 2 * m) * a.kv_heads;
+                mine.v[5] += rests(m, prefix + own, single);
             });
     }
-    Counts<8> total;
-    const Counts<8> at = block_exclusive(mine, &total);
-    const uint32_t n_tiles = tiles_p + static_cast<uint32_t>(total.v[3]);
+    Counts<6> total;
+    const Counts<6> at = block_exclusive(mine, &total);
+    const uint32_t own_tiles = static_cast<uint32_t>(total.v[0] >> 32), n_tiles = tiles_p + own_tiles, tiles_before = static_cast<uint32_t>(at.v[0] >> 32);
     const uint32_t lead = static_cast<uint64_t>(n_tiles) * a.kv_heads >= a.tile_ctas ? kGroupCost : 0;
     const uint32_t cost_full = lead + tile_cost(kGroupRows, a.prefix_len, 0);
     const uint64_t tile_row0 = a.L.max_rows;  // rows of the tile kernel's first pieces start here
@@ -260,9 +262,9 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     }
     const uint64_t leads = static_cast<uint64_t>(lead) * a.kv_heads;
     uint32_t g = static_cast<uint32_t>(at.v[0]) + groups_p, it = static_cast<uint32_t>(at.v[1]) + groups_p * pieces_p,
-             pr = static_cast<uint32_t>(at.v[2]) + (groups_p ? prefix_rows * pieces_p : 0), tg = static_cast<uint32_t>(at.v[3]) + tiles_p;
-    uint32_t* rest = a.at<uint32_t>(a.L.rest) + at.v[6];
-    uint64_t cost = at.v[4] + at.v[3] * leads + cost_p, trow = tile_row0 + at.v[5] + rows_p;
+             pr = static_cast<uint32_t>(at.v[2]) + (groups_p ? prefix_rows * pieces_p : 0), tg = tiles_before + tiles_p;
+    uint32_t* rest = a.at<uint32_t>(a.L.rest) + static_cast<uint32_t>(at.v[5]);
+    uint64_t cost = at.v[3] + tiles_before * leads + cost_p, trow = tile_row0 + at.v[4] + rows_p;
     for (uint32_t r = r0; r < r1; ++r) {
         const uint32_t s = a.starts[r], e = a.starts[r + 1];
         const Kind k = kind_of(a, (e - s) * G);
@@ -302,11 +304,11 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         for (uint32_t t = s + threadIdx.x % 32; t < e; t += 32) write_token(m.request, t, m.mark, t - s, m.own);
     }
     if (threadIdx.x == 0) {
-        const uint64_t c = total.v[4] + total.v[3] * leads + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
+        const uint64_t c = total.v[3] + own_tiles * leads + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
         const uint64_t share = (c + ctas - 1) / ctas;
         const uint32_t n_items = groups_p * pieces_p + static_cast<uint32_t>(total.v[1]);
         const uint64_t least = static_cast<uint64_t>(n_items) * a.kv_heads >= ctas ? kMinShareBeside : kMinShare;
-        *head = PlanHead{a.plan_key, c, share < least ? least : share, static_cast<uint32_t>(a.starts[R]), n_items, n_tiles, prefix_kind, static_cast<uint32_t>(total.v[6]), static_cast<uint32_t>(total.v[7])};
+        *head = PlanHead{a.plan_key, c, share < least ? least : share, static_cast<uint32_t>(a.starts[R]), n_items, n_tiles, prefix_kind, static_cast<uint32_t>(total.v[5]), static_cast<uint32_t>(total.v[5] >> 32)};
     }
 }
 
@@ -702,7 +704,7 @@ __device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t blo
         const uint32_t b = u / kUnits + 1, row0 = u % kUnits * kJoinRows;
         const TileGroup& g = tiles[a.at<uint32_t>(a.L.tile_first)[b]];
         if (!g.single || g.rows <= kTileRows || row0 >= g.rows || g.cost <= g.lead) continue;
-        const uint32_t h = static_cast<uint32_t>((b * head.share - g.cost_begin) / g.cost);
+        const uint32_t h = divide(b * head.share - g.cost_begin, g.cost);
         uint32_t c0, c1;
         tile_ctas(g, h, head.share, &c0, &c1);
         if (c0 + 1 == b && c1 >= b) join_group_rows<T, D>(a, g, h, row0, c0, c1);
@@ -717,11 +719,11 @@ __device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t blo
     }
 }
 
-// The last row_blocks CTAs: rows base .. base + span - 1 of the output a warp;
-// kSplit: one row a CTA, whose warps share its pieces (few rows, each of many
-// pieces).  The others: join_tiles.  Pieces are added in a fixed order.
+// Rows outside tiles of their request's own, span at a time a warp (kSplit: one
+// row a CTA, whose warps share its pieces: few rows, each of many pieces), then
+// join_tiles.  Pieces are added in a fixed order.
 template <typename T, int D, bool kSplit>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, uint32_t span, uint32_t row_blocks) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, uint32_t span) {
     constexpr int kPer = D / 32;
     __shared__ float sh_acc[kSplit ? kJoinWarps : 1][D];
     __shared__ float2 sh_ml[kJoinWarps];
@@ -731,15 +733,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.at<uint32_t>(a.L.counter) = 0;  // for the next layer
     const PlanHead head = *a.at<PlanHead>(0);
     if (head.key != a.plan_key) return;
-    const uint32_t tile_blocks = gridDim.x - row_blocks;
-    if (blockIdx.x < tile_blocks) {
-        join_tiles<T, D>(a, head, blockIdx.x, tile_blocks);
-        return;
-    }
-    if (head.n_by_row == 0) return;
-    const uint32_t block = blockIdx.x - tile_blocks, base = kSplit ? block : (block * kJoinWarps + warp) * span;  // n_tokens * q_heads is below 2^31
-    const uint32_t n_rows = head.n_tokens * q_heads;
-    if (base >= n_rows) return;
+    const uint32_t n_rows = head.n_tokens * q_heads;  // below 2^31
 
     struct Sources {
         Pieces pre, own;
@@ -801,7 +795,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 #pragma unroll
             for (int j = 0; j < kPer; ++j) sh_acc[warp][lane * kPer + j] = acc[j];
             __syncthreads();
-            if (warp) return;
+            if (warp) return;  // the first warp goes on
             top = -INFINITY;
             sum = 0.0f;
 #pragma unroll
@@ -826,15 +820,17 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
             a.lse[static_cast<uint64_t>(s.t) * q_heads + s.qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
     };
     const TokenInfo* tokens = a.at<TokenInfo>(a.L.tokens);
-    if (kSplit || span == 1) {
-        if (tokens[base / q_heads].packed == kInTiles) return;
-        join(sources(base));
-        return;
+    if constexpr (kSplit) {
+        if (blockIdx.x < n_rows && tokens[blockIdx.x / q_heads].packed != kInTiles) join(sources(blockIdx.x));
+    } else if (head.n_by_row) {
+        for (uint64_t at = static_cast<uint64_t>(blockIdx.x * kJoinWarps + warp) * span; at < n_rows; at += static_cast<uint64_t>(gridDim.x) * kJoinWarps * span) {
+            const uint32_t base = static_cast<uint32_t>(at);
+            bool todo = false;
+            if (static_cast<uint32_t>(lane) < span && base + lane < n_rows) todo = tokens[(base + lane) / q_heads].packed != kInTiles;
+            for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, todo); rest; rest &= rest - 1) join(sources(base + __ffs(rest) - 1));
+        }
     }
-    // which of the warp's rows are this kernel's: of a batch of prompts, none
-    bool todo = false;
-    if (static_cast<uint32_t>(lane) < span && base + lane < n_rows) todo = tokens[(base + lane) / q_heads].packed != kInTiles;
-    for (uint32_t rest = __ballot_sync(0xFFFFFFFFu, todo); rest; rest &= rest - 1) join(sources(base + __ffs(rest) - 1));
+    if (head.n_by_row < head.n_tokens) join_tiles<T, D>(a, head, blockIdx.x, gridDim.x);
 }
 
 // ---- host side -----------------------------------------------------------------------
@@ -956,14 +952,14 @@ afx_status launch(const AttnArgs& a, const afx_kv_cache& cache, cudaStream_t s) 
     const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.kv_heads * a.group;
     // a request can have tiles of its own from kFuseRows rows on, without a prefix from kRows + 1
     const bool own_tiles = a.tile_ctas && static_cast<uint64_t>(a.n_tokens) * a.group > (a.prefix_len ? kFuseRows - 1 : kRows);
-    const uint32_t tile_blocks = own_tiles ? sms * 8 : 0;
-    if (rows <= static_cast<uint64_t>(sms) * 8) {  // a CTA a row while they all run at once
+    const uint32_t most = sms * 8, least = own_tiles ? most : 0;
+    if (rows <= most) {  // a CTA a row
         const uint32_t n = static_cast<uint32_t>(rows);
-        AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, true>, n + tile_blocks, kJoinThreads, 0, s, a, 1u, n), "attention_join_kernel launch");
+        AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, true>, n < least ? least : n, kJoinThreads, 0, s, a, 1u), "attention_join_kernel launch");
     } else {
-        const uint64_t span = rows <= static_cast<uint64_t>(sms) * 256 ? 1 : 32, per = span * kJoinWarps;
-        const uint32_t n = static_cast<uint32_t>((rows + per - 1) / per);
-        AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, false>, n + tile_blocks, kJoinThreads, 0, s, a, static_cast<uint32_t>(span), n),
+        const uint64_t span = rows <= static_cast<uint64_t>(sms) * 256 ? 1 : 32, per = span * kJoinWarps, need = (rows + per - 1) / per;
+        const uint32_t n = need > most ? most : static_cast<uint32_t>(need);
+        AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, false>, n < least ? least : n, kJoinThreads, 0, s, a, static_cast<uint32_t>(span)),
                       "attention_join_kernel launch");
     }
     return AFX_OK;

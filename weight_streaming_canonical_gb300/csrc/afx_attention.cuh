@@ -120,12 +120,17 @@ __device__ __forceinline__ uint32_t visible(int32_t seen, uint32_t row, uint32_t
 constexpr uint32_t kStepBoth = 8, kStepOne = 5;
 __host__ __device__ __forceinline__ uint32_t step_cost(uint32_t rows) { return rows > kTileRows ? kStepBoth : kStepOne; }
 
+// Costs mostly fit 32 bits, where a division takes a fraction of the time.
+__device__ __forceinline__ uint32_t divide(uint64_t a, uint64_t b) {
+    return (a | b) >> 32 ? static_cast<uint32_t>(a / b) : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 // The CTAs [first, last] of the tile kernel that hold pieces of a group's
 // head; for a group with keys.
 __device__ __forceinline__ void tile_ctas(const TileGroup& g, uint32_t h, uint64_t share, uint32_t* first, uint32_t* last) {
     const uint64_t begin = g.cost_begin + static_cast<uint64_t>(h) * g.cost;
-    *first = static_cast<uint32_t>((begin + g.lead + step_cost(g.rows) - 1) / share);
-    *last = static_cast<uint32_t>((begin + g.cost - 1) / share);
+    *first = divide(begin + g.lead + step_cost(g.rows) - 1, share);
+    *last = divide(begin + g.cost - 1, share);
 }
 
 // The result row of a tile-kernel piece: the first piece of a group's head

@@ -273,8 +273,8 @@ struct Walk {
             while (at >= groups[g].cost_begin + static_cast<uint64_t>(groups[g].cost) * heads) ++g;
             p->g = groups[g];
             const uint64_t in = at - p->g.cost_begin;
-            p->h = static_cast<uint32_t>(in / p->g.cost);
-            const uint32_t off = static_cast<uint32_t>(in % p->g.cost);
+            p->h = divide(in, p->g.cost);
+            const uint32_t off = static_cast<uint32_t>(in - static_cast<uint64_t>(p->h) * p->g.cost);
             const uint64_t stop = min(end, p->g.cost_begin + (static_cast<uint64_t>(p->h) + 1) * p->g.cost);
             const uint32_t off1 = off + static_cast<uint32_t>(stop - at), lead = p->g.lead, each = step_cost(p->g.rows);
             p->both = p->g.rows > kTileRows;
