@@ -47,10 +47,6 @@ constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's til
 // Where 16-row items keep the other SMs busy, more (64 requests with 8192
 // keys in common: 67 us against 78).
 constexpr uint32_t kMinShare = 4 * kStepBoth, kMinShareBeside = 12 * kStepBoth;
-// What a tile group costs besides its steps (filling and emptying the pipe,
-// masked steps, the output), where CTAs take several whole groups each; where a
-// group is cut over several CTAs, all have that cost alike.
-constexpr uint32_t kGroupCost = 18;
 // Up to this many rows in the batch the 16-row kernel takes all of them, two
 // groups reading the same keys, and the tile kernel is not launched: with 20
 // to 30 rows on a prefix of 500 to 8000 keys 27-33 us against 31-41, on 64000
@@ -245,26 +241,24 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     }
     Counts<6> total;
     const Counts<6> at = block_exclusive(mine, &total);
-    const uint32_t own_tiles = static_cast<uint32_t>(total.v[0] >> 32), n_tiles = tiles_p + own_tiles, tiles_before = static_cast<uint32_t>(at.v[0] >> 32);
-    const uint32_t lead = static_cast<uint64_t>(n_tiles) * a.kv_heads >= a.tile_ctas ? kGroupCost : 0;
-    const uint32_t cost_full = lead + tile_cost(kGroupRows, a.prefix_len, 0);
+    const uint32_t n_tiles = tiles_p + static_cast<uint32_t>(total.v[0] >> 32);
+    const uint32_t cost_full = tile_cost(kGroupRows, a.prefix_len, 0);
     const uint64_t tile_row0 = a.L.max_rows;  // rows of the tile kernel's first pieces start here
     uint64_t cost_p = 0, rows_p = 0;
     if (tiles_p) {
         for (uint32_t g = threadIdx.x; g < tiles_p; g += threads) {
             const uint32_t row0 = g * kGroupRows, rows = min(kGroupRows, prefix_rows - row0);
             tiles[g] = TileGroup{static_cast<uint64_t>(g) * cost_full * a.kv_heads, tile_row0 + static_cast<uint64_t>(row0) * a.kv_heads,
-                                 lead + tile_cost(rows, a.prefix_len, 0), -1, row0, rows, a.prefix_len, 0, 0, 0, 0, lead, {}};
+                                 tile_cost(rows, a.prefix_len, 0), -1, row0, rows, a.prefix_len, 0, 0, 0, 0, {}};
         }
         const uint32_t last = prefix_rows - (tiles_p - 1) * kGroupRows;
-        cost_p = (static_cast<uint64_t>(tiles_p - 1) * cost_full + lead + tile_cost(last, a.prefix_len, 0)) * a.kv_heads;
+        cost_p = (static_cast<uint64_t>(tiles_p - 1) * cost_full + tile_cost(last, a.prefix_len, 0)) * a.kv_heads;
         rows_p = (static_cast<uint64_t>(tiles_p - 1) * kGroupRows + (last > kTileRows ? last : 2 * last)) * a.kv_heads;
     }
-    const uint64_t leads = static_cast<uint64_t>(lead) * a.kv_heads;
     uint32_t g = static_cast<uint32_t>(at.v[0]) + groups_p, it = static_cast<uint32_t>(at.v[1]) + groups_p * pieces_p,
-             pr = static_cast<uint32_t>(at.v[2]) + (groups_p ? prefix_rows * pieces_p : 0), tg = tiles_before + tiles_p;
+             pr = static_cast<uint32_t>(at.v[2]) + (groups_p ? prefix_rows * pieces_p : 0), tg = static_cast<uint32_t>(at.v[0] >> 32) + tiles_p;
     uint32_t* rest = a.at<uint32_t>(a.L.rest) + static_cast<uint32_t>(at.v[5]);
-    uint64_t cost = at.v[3] + tiles_before * leads + cost_p, trow = tile_row0 + at.v[4] + rows_p;
+    uint64_t cost = at.v[3] + cost_p, trow = tile_row0 + at.v[4] + rows_p;
     for (uint32_t r = r0; r < r1; ++r) {
         const uint32_t s = a.starts[r], e = a.starts[r + 1];
         const Kind k = kind_of(a, (e - s) * G);
@@ -278,9 +272,9 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
                     items[it++] = Row16Item{static_cast<int32_t>(r), row, m, p * piece, min(end, (p + 1) * piece), pr, token0, seen};
             },
             [&](uint32_t row, uint32_t m, uint32_t prefix, uint32_t own, uint32_t token0, int32_t seen, bool single) {
-                const uint32_t c = lead + tile_cost(m, prefix, own);
+                const uint32_t c = tile_cost(m, prefix, own);
                 if (rests(m, prefix + own, single)) *rest++ = tg;
-                tiles[tg++] = TileGroup{cost, trow, c, static_cast<int32_t>(r), row, m, prefix, own, token0, seen, single, lead, {}};
+                tiles[tg++] = TileGroup{cost, trow, c, static_cast<int32_t>(r), row, m, prefix, own, token0, seen, single, {}};
                 cost += static_cast<uint64_t>(c) * a.kv_heads;
                 trow += static_cast<uint64_t>(m > kTileRows ? m : 2 * m) * a.kv_heads;
             });
@@ -304,7 +298,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         for (uint32_t t = s + threadIdx.x % 32; t < e; t += 32) write_token(m.request, t, m.mark, t - s, m.own);
     }
     if (threadIdx.x == 0) {
-        const uint64_t c = total.v[3] + own_tiles * leads + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
+        const uint64_t c = total.v[3] + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
         const uint64_t share = (c + ctas - 1) / ctas;
         const uint32_t n_items = groups_p * pieces_p + static_cast<uint32_t>(total.v[1]);
         const uint64_t least = static_cast<uint64_t>(n_items) * a.kv_heads >= ctas ? kMinShareBeside : kMinShare;
@@ -589,7 +583,7 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& h
         p.step16 = static_cast<uint64_t>(g.rows) * a.kv_heads;
     } else if (kind == kTile) {
         const TileGroup g = a.at<TileGroup>(a.L.tiles)[first_group + row / kGroupRows];
-        if (g.cost > g.lead) {
+        if (g.cost) {
             uint32_t c0, c1;
             tile_ctas(g, h, head.share, &c0, &c1);
             p.two = g.rows <= kTileRows;
@@ -640,7 +634,7 @@ __device__ void join_group_rows(const AttnArgs& a, const TileGroup& g, uint32_t 
     const float* part_o = a.at<float>(a.L.part_o);
     const float2* part_ml = a.at<float2>(a.L.part_ml);
     constexpr uint32_t kAtOnce = 2;  // pieces taken at a time (mostly there are two): lane = 8 piece + row, twice
-    const uint32_t lanes = rows <= kTileRows ? 2 : 1, n = g.cost > g.lead ? (c1 - c0 + 1) * lanes : 0;
+    const uint32_t lanes = rows <= kTileRows ? 2 : 1, n = g.cost ? (c1 - c0 + 1) * lanes : 0;
     const uint32_t slot = lane / kJoinRows % kAtOnce, mine = min(row0 + lane % kJoinRows, rows - 1);
     float top = -INFINITY, sum = 0.0f, acc[kJoinRows][kPer] = {};
 #pragma unroll 1
@@ -703,7 +697,7 @@ __device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t blo
     for (uint32_t u = me; u < borders * kUnits; u += warps) {
         const uint32_t b = u / kUnits + 1, row0 = u % kUnits * kJoinRows;
         const TileGroup& g = tiles[a.at<uint32_t>(a.L.tile_first)[b]];
-        if (!g.single || g.rows <= kTileRows || row0 >= g.rows || g.cost <= g.lead) continue;
+        if (!g.single || g.rows <= kTileRows || row0 >= g.rows || !g.cost) continue;
         const uint32_t h = divide(b * head.share - g.cost_begin, g.cost);
         uint32_t c0, c1;
         tile_ctas(g, h, head.share, &c0, &c1);
@@ -714,7 +708,7 @@ __device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t blo
         const TileGroup& g = tiles[a.at<uint32_t>(a.L.rest)[gh / a.kv_heads]];
         if (row0 >= g.rows) continue;
         uint32_t c0 = 0, c1 = 0;
-        if (g.cost > g.lead) tile_ctas(g, h, head.share, &c0, &c1);
+        if (g.cost) tile_ctas(g, h, head.share, &c0, &c1);
         join_group_rows<T, D>(a, g, h, row0, c0, c1);
     }
 }

@@ -64,8 +64,7 @@ struct alignas(16) Row16Item {
 };
 
 // Up to 256 packed rows and the keys they see: `prefix_keys` of the prefix,
-// then `own_keys` of the request.  cost: step_cost a step of 128 keys, after
-// `lead` for what a group costs besides.
+// then `own_keys` of the request.  cost: step_cost a step of 128 keys.
 struct alignas(16) TileGroup {
     uint64_t cost_begin;    // of head 0; head h begins h * cost later
     uint64_t part_row;      // where the results of the first piece of head 0 go
@@ -76,8 +75,7 @@ struct alignas(16) TileGroup {
     uint32_t token0;
     int32_t seen;
     uint32_t single;        // nothing else contributes to these rows
-    uint32_t lead;
-    uint32_t pad[2];
+    uint32_t pad[3];
 };
 
 struct AttnLayout {
@@ -129,7 +127,7 @@ __device__ __forceinline__ uint32_t divide(uint64_t a, uint64_t b) {
 // head; for a group with keys.
 __device__ __forceinline__ void tile_ctas(const TileGroup& g, uint32_t h, uint64_t share, uint32_t* first, uint32_t* last) {
     const uint64_t begin = g.cost_begin + static_cast<uint64_t>(h) * g.cost;
-    *first = divide(begin + g.lead + step_cost(g.rows) - 1, share);
+    *first = divide(begin + step_cost(g.rows) - 1, share);
     *last = divide(begin + g.cost - 1, share);
 }
 

@@ -276,12 +276,12 @@ struct Walk {
             p->h = divide(in, p->g.cost);
             const uint32_t off = static_cast<uint32_t>(in - static_cast<uint64_t>(p->h) * p->g.cost);
             const uint64_t stop = min(end, p->g.cost_begin + (static_cast<uint64_t>(p->h) + 1) * p->g.cost);
-            const uint32_t off1 = off + static_cast<uint32_t>(stop - at), lead = p->g.lead, each = step_cost(p->g.rows);
+            const uint32_t off1 = off + static_cast<uint32_t>(stop - at), each = step_cost(p->g.rows);
             p->both = p->g.rows > kTileRows;
             p->prefix_steps = ceil_div(p->g.prefix_keys, kTileKeys);
             const uint32_t steps = p->prefix_steps + ceil_div(p->g.own_keys, kTileKeys);
-            p->step0 = off > lead ? (off - lead) / each : 0;
-            p->step1 = off1 > lead ? min(steps, (off1 - lead) / each) : 0;
+            p->step0 = off / each;
+            p->step1 = min(steps, off1 / each);
             at = stop;
             if (p->step0 < p->step1) return true;  // else the share ends before the group's first step
         }
