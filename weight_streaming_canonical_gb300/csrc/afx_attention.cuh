@@ -30,10 +30,10 @@ struct PlanHead {
 
 enum Source : uint32_t { kNone = 0, kRow16 = 1, kTile = 2 };
 
-// A request's own keys (with the prefix before them where fused): its rows'
+// A request's own keys (its tiles may have the prefix before them): its rows'
 // first group, of kRows or kGroupRows rows each.
 struct alignas(16) RequestInfo {
-    uint32_t kind, first, fused, pad;
+    uint32_t kind, first, pad[2];
 };
 
 // A token of the queries: its request, its first packed row among the
@@ -82,7 +82,7 @@ struct AttnLayout {
     uint64_t counter;       // 16-row units taken so far, by this layer
     uint64_t tokens, packed_token, groups16, items16, tiles, tile_first, rest, part_ml, part_o, total;
     uint64_t extra_row;     // rows of the tile kernel's further pieces: 256 a CTA
-    uint64_t max_rows;
+    uint64_t max_rows;      // rows of the 16-row kernel's pieces
 };
 
 struct AttnArgs {
