@@ -50,10 +50,12 @@ constexpr uint32_t kMinKeys = 64;     // keys of a 16-row item, at least, where 
 // pieces then: 121 against 115).
 constexpr uint32_t kTargetUnits = 2432, kFewUnits = 1216;
 constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's tiles take the prefix along
-// Cost of a tile CTA, at least: a CTA's start costs as much as four steps.
-// Where 16-row items keep the other SMs busy, more (64 requests with 8192
-// keys in common: 67 us against 78).
-constexpr uint32_t kMinShare = 4 * kStepBoth, kMinShareBeside = 12 * kStepBoth;
+// Cost of a tile CTA, at least: one step where the other SMs would be idle (two
+// prompts of 43 tokens: 32 us, 52 with four steps).  Where the 16-row kernel
+// has as much to do (a key of a head there takes an SM as long as a 16th of a
+// unit of cost here), more, for a CTA's start costs as much as four steps:
+// 64 requests with 8192 keys in common, 67 us against 78.
+constexpr uint32_t kMinShare = kStepBoth, kMinShareBeside = 12 * kStepBoth, kKeysOfCost = 16;
 // Up to this many rows in the batch the 16-row kernel takes all of them, two
 // groups reading the same keys, and the tile kernel is not launched: with 20
 // to 30 rows on a prefix of 500 to 8000 keys 27-33 us against 31-41, on 64000
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
         const uint64_t c = total.v[3] + cost_p, ctas = a.tile_ctas ? a.tile_ctas : 1;
         const uint64_t share = (c + ctas - 1) / ctas;
         const uint32_t n_items = groups_p * pieces_p + static_cast<uint32_t>(total.v[1]);
-        const uint64_t least = static_cast<uint64_t>(n_items) * a.kv_heads >= ctas ? kMinShareBeside : kMinShare;
+        const uint64_t least = keys * a.kv_heads >= kKeysOfCost * c ? kMinShareBeside : kMinShare;
         *head = PlanHead{a.plan_key, c, share < least ? least : share, static_cast<uint32_t>(a.starts[R]), n_items, n_tiles, prefix_kind, static_cast<uint32_t>(total.v[5]), static_cast<uint32_t>(total.v[5] >> 32)};
     }
 }
