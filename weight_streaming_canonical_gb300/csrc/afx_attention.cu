@@ -126,7 +126,8 @@ __device__ __forceinline__ Kind kind_of(const AttnArgs& a, uint32_t rows) {
 }
 
 __device__ __forceinline__ uint32_t tile_cost(uint32_t rows, uint32_t prefix_keys, uint32_t own_keys) {
-    return step_cost(rows) * (ceil_div(prefix_keys, kTileKeys) + ceil_div(own_keys, kTileKeys));
+    const uint32_t steps = ceil_div(prefix_keys, kTileKeys) + ceil_div(own_keys, kTileKeys);
+    return steps ? kGroupCost + step_cost(rows) * steps : 0;
 }
 
 // One CTA.  Requests' rows are cut into groups of 16 (or 256 for the tile

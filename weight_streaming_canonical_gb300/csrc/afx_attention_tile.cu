@@ -290,8 +290,8 @@ struct Walk {
             p->both = p->g.rows > kTileRows;
             p->prefix_steps = ceil_div(p->g.prefix_keys, kTileKeys);
             const uint32_t steps = p->prefix_steps + ceil_div(p->g.own_keys, kTileKeys);
-            p->step0 = off / each;
-            p->step1 = min(steps, off1 / each);
+            p->step0 = off > kGroupCost ? (off - kGroupCost) / each : 0;
+            p->step1 = off1 > kGroupCost ? min(steps, (off1 - kGroupCost) / each) : 0;
             at = stop;
             if (p->step0 < p->step1) return true;  // else the share ends before the group's first step
         }
