@@ -18,20 +18,25 @@
 // what the row asks for:
 //   - temperature 0: the lowest index of the maximum;
 //   - top-k up to 1024 (with or without top-p and min-p): the k-th largest of
-//     the warps' (for larger k the threads') maxima bounds the k-th largest logit from below, so the
-//     tokens from that bound on, a few more than k, go to one CTA, which
-//     orders them and does the rest.  Only the threads whose maximum reaches
-//     the bound look at their tokens again;
+//     the warps' (for larger k the threads') maxima bounds the k-th largest
+//     logit from below, so the tokens from that bound on, a few more than k,
+//     go to one CTA, which orders them and does the rest.  Only the threads
+//     whose maximum reaches the bound look at their tokens again;
 //   - no top-k, top-p 1: one pass of weights (min-p is a condition on each),
 //     then the run of tokens in which the aim falls, walked to the token;
-//   - top-p alone: the row's mass and the mass above a few cuts in y; a histogram of masses over equal steps of
-//     z between two cuts, whose masses say which step the boundary is in; the
-//     tokens of that step, ordered in one CTA, give the last token kept (where
-//     few tokens lie above the cut, they go to one CTA at once);
+//   - top-p alone: the row's mass and the weight above two cuts in y, e^-4 and
+//     e^-8, say how far down the boundary lies.  Where few tokens lie above a
+//     cut, they go to one CTA at once; else a histogram of masses over equal
+//     steps of z says which step the boundary is in, and the tokens of that
+//     step, ordered in one CTA, give the last token kept;
 //   - anything else, and rows where a list above is too long (thousands of
 //     ties): a histogram of counts and masses refined until a list fits.
-// Bound: the read of the logits for many rows; for few rows the chain of
-// cluster barriers.
+//
+// Bound: for few rows the chain of cluster barriers and passes over shared
+// memory (151,936 tokens, one row: greedy 3.4 us, top-k 50 8 us, top-p 0.9 at
+// temperature 1 on logits with a flat tail 23 us); for many rows those passes'
+// instructions: 512 rows of float32, 311 MB, greedy 99 us (3.1 TB/s), top-k 50
+// 170, without cuts 195, top-p 0.9 630.
 #include <cooperative_groups.h>
 
 #include <utility>
