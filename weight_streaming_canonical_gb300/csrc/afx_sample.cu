@@ -387,19 +387,29 @@ __device__ void reach(Shared& sh, const uint64_t (&key)[kPer], const uint64_t (&
 
 __device__ __forceinline__ float place_value(uint64_t p) { return key_value(static_cast<uint32_t>(p >> 32)); }
 
-// Steps of z that cover the list's n tokens, as a Row's are.
-__device__ void list_steps(Shared& sh, Row& row, const uint64_t (&p)[kPer], uint32_t n) {
-    uint64_t least = ~uint64_t{0};
+// Steps of z that just cover the list's n tokens (which may lie far below the
+// row's maximum, and close together), as a Row whose bin() alone counts.
+__device__ Row list_steps(Shared& sh, Row row, const uint64_t (&p)[kPer], uint32_t n) {
+    uint64_t least = ~uint64_t{0}, most = 0;
 #pragma unroll
     for (uint32_t j = 0; j < kPer; ++j)
-        if (threadIdx.x + j * kThreads < n) least = p[j] < least ? p[j] : least;
+        if (threadIdx.x + j * kThreads < n) {
+            least = p[j] < least ? p[j] : least;
+            most = p[j] > most ? p[j] : most;
+        }
     least = ~warp_max(~least);
+    most = warp_max(most);
     __syncthreads();
-    if (threadIdx.x % 32 == 0) sh.scan[threadIdx.x / 32] = ~least;
+    if (threadIdx.x % 32 == 0) {
+        sh.scan[threadIdx.x / 32] = ~least;
+        sh.short_key[threadIdx.x / 32] = most;
+    }
     __syncthreads();
     least = ~warp_max(threadIdx.x % 32 < kWarps ? sh.scan[threadIdx.x % 32] : 0);
+    row.top = place_value(warp_max(threadIdx.x % 32 < kWarps ? sh.short_key[threadIdx.x % 32] : 0));
     const float span = row.top - place_value(least);
     if (span > 0.0f && span < INFINITY) row.step = static_cast<float>(kBins) / span;
+    return row;
 }
 
 // Rank 0: list[0 .. n) holds the tokens around a boundary, before_count and
@@ -415,8 +425,8 @@ __device__ void last_kept(cg::cluster_group& cluster, Shared& sh, Row row, uint3
         w[j] = i < n ? row.mass(row.weight(place_value(p[j]))) : 0;
         mass[j] = by_mass ? w[j] : i < n ? 1 : 0;
     }
-    list_steps(sh, row, p, n);
-    reach(sh, p, mass, by_mass ? before_mass : before_count, aim, [&](uint64_t q) { return row.bin(place_value(q)); });
+    const Row steps = list_steps(sh, row, p, n);
+    reach(sh, p, mass, by_mass ? before_mass : before_count, aim, [&](uint64_t q) { return steps.bin(place_value(q)); });
     const uint64_t last = sh.found_key;
     uint64_t kept = 0, total;
 #pragma unroll
@@ -584,8 +594,8 @@ __device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row 
         p[j] = i < n ? sh.list[i] : 0;
         mass[j] = i < n ? 1 : 0;
     }
-    list_steps(sh, row, p, n);
-    auto step_of = [&](uint64_t q) { return row.bin(place_value(q)); };
+    const Row steps = list_steps(sh, row, p, n);
+    auto step_of = [&](uint64_t q) { return steps.bin(place_value(q)); };
     if (n > k) {
         reach(sh, p, mass, 0, k, step_of);
         threshold = sh.found_key;
