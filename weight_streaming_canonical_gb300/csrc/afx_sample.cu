@@ -340,31 +340,56 @@ __device__ void reach(Shared& sh, const uint64_t (&key)[kPer], const uint64_t (&
         sh.found_before = from;
     }
     __syncthreads();
-    const uint32_t bin = sh.found_bin, n = sh.count[bin];
-    if (n > kShort) {
-        // (ties) bit by bit: the largest key from which on the mass reaches the aim
-        uint64_t t = 0;
-        for (uint64_t bit = uint64_t{1} << 63; bit; bit >>= 1) {
-            uint64_t sum = 0, total;
+    const uint32_t bin = sh.found_bin;
+    uint32_t n = sh.count[bin];
+    uint64_t lo = 0, hi = ~uint64_t{0};  // the step's keys that are meant
+    auto meant = [&](uint32_t j) { return mass[j] && key[j] >= lo && key[j] <= hi && bin_of(key[j]) == bin; };
+    while (n > kShort) {  // ties, mostly (16-bit logits have hundreds): steps of the keys themselves, from the first to the last
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        uint64_t least = ~uint64_t{0}, most = 0;
 #pragma unroll
-            for (uint32_t j = 0; j < kPer; ++j) sum += key[j] >= (t | bit) ? mass[j] : 0;
-            block_exclusive(sh, sum, &total);
-            if (before + total >= aim) t |= bit;
+        for (uint32_t j = 0; j < kPer; ++j)
+            if (meant(j)) {
+                least = key[j] < least ? key[j] : least;
+                most = key[j] > most ? key[j] : most;
+            }
+        least = ~warp_max(~least);
+        most = warp_max(most);
+        const uint64_t start = sh.found_before;
+        __syncthreads();
+        if (lane == 0) {
+            sh.scan[warp] = ~least;
+            sh.short_key[warp] = most;
         }
-        uint64_t sum = 0, total;
+        sh.bins[threadIdx.x] = 0;
+        sh.count[threadIdx.x] = 0;
+        __syncthreads();
+        least = ~warp_max(lane < kWarps ? sh.scan[lane] : 0);
+        most = warp_max(lane < kWarps ? sh.short_key[lane] : 0);
+        const uint64_t span = (most - least) >> kBinBits;
+        const int shift = span ? 64 - __clzll(static_cast<long long>(span)) : 0;
 #pragma unroll
-        for (uint32_t j = 0; j < kPer; ++j) sum += key[j] > t ? mass[j] : 0;
-        block_exclusive(sh, sum, &total);
-        if (threadIdx.x == 0) {
-            sh.found_key = t;
-            sh.found_before = before + total;
+        for (uint32_t j = 0; j < kPer; ++j)
+            if (meant(j)) {
+                const uint32_t b = static_cast<uint32_t>((most - key[j]) >> shift);
+                atomicAdd(reinterpret_cast<unsigned long long*>(&sh.bins[b]), static_cast<unsigned long long>(mass[j]));
+                atomicAdd(&sh.count[b], 1u);
+            }
+        __syncthreads();
+        const uint64_t in_step = sh.bins[threadIdx.x], before_step = start + block_exclusive(sh, in_step, &all);
+        if (before_step < aim && aim <= before_step + in_step) {
+            sh.found_bin = threadIdx.x;
+            sh.found_before = before_step;
         }
         __syncthreads();
-        return;
+        const uint64_t step = sh.found_bin;
+        n = sh.count[step];  // fewer: the first and the last key are in two steps
+        hi = most - (step << shift);
+        lo = hi - least < (uint64_t{1} << shift) ? least : hi - ((uint64_t{1} << shift) - 1);
     }
 #pragma unroll
     for (uint32_t j = 0; j < kPer; ++j)
-        if (mass[j] && bin_of(key[j]) == bin) {
+        if (meant(j)) {
             const uint32_t at = atomicAdd(&sh.short_n, 1u);
             sh.short_key[at] = key[j];
             sh.short_mass[at] = mass[j];
@@ -387,9 +412,17 @@ __device__ void reach(Shared& sh, const uint64_t (&key)[kPer], const uint64_t (&
 
 __device__ __forceinline__ float place_value(uint64_t p) { return key_value(static_cast<uint32_t>(p >> 32)); }
 
-// Steps of z that just cover the list's n tokens (which may lie far below the
-// row's maximum, and close together), as a Row whose bin() alone counts.
-__device__ Row list_steps(Shared& sh, Row row, const uint64_t (&p)[kPer], uint32_t n) {
+// Steps that just cover the list's n tokens, which may lie far below the row's
+// maximum and close together: of z, or of the index where all have one z (in
+// 16-bit logits hundreds do, and additions to one step take their turns).
+struct ListSteps {
+    Row row;
+    bool ties;
+    __device__ uint32_t of(uint64_t p) const {
+        return row.bin(ties ? -static_cast<float>(0xFFFFFFFFu - static_cast<uint32_t>(p)) : place_value(p));
+    }
+};
+__device__ ListSteps list_steps(Shared& sh, const uint64_t (&p)[kPer], uint32_t n) {
     uint64_t least = ~uint64_t{0}, most = 0;
 #pragma unroll
     for (uint32_t j = 0; j < kPer; ++j)
@@ -406,10 +439,14 @@ __device__ Row list_steps(Shared& sh, Row row, const uint64_t (&p)[kPer], uint32
     }
     __syncthreads();
     least = ~warp_max(threadIdx.x % 32 < kWarps ? sh.scan[threadIdx.x % 32] : 0);
-    row.top = place_value(warp_max(threadIdx.x % 32 < kWarps ? sh.short_key[threadIdx.x % 32] : 0));
-    const float span = row.top - place_value(least);
-    if (span > 0.0f && span < INFINITY) row.step = static_cast<float>(kBins) / span;
-    return row;
+    most = warp_max(threadIdx.x % 32 < kWarps ? sh.short_key[threadIdx.x % 32] : 0);
+    ListSteps s;
+    s.ties = least >> 32 == most >> 32;
+    s.row.top = s.ties ? -static_cast<float>(0xFFFFFFFFu - static_cast<uint32_t>(most)) : place_value(most);
+    s.row.inv_t = 1.0f;
+    const float span = s.row.top - (s.ties ? -static_cast<float>(0xFFFFFFFFu - static_cast<uint32_t>(least)) : place_value(least));
+    s.row.step = span > 0.0f && span < INFINITY ? static_cast<float>(kBins) / span : 1.0f;
+    return s;
 }
 
 // Rank 0: list[0 .. n) holds the tokens around a boundary, before_count and
@@ -425,8 +462,8 @@ __device__ void last_kept(cg::cluster_group& cluster, Shared& sh, Row row, uint3
         w[j] = i < n ? row.mass(row.weight(place_value(p[j]))) : 0;
         mass[j] = by_mass ? w[j] : i < n ? 1 : 0;
     }
-    const Row steps = list_steps(sh, row, p, n);
-    reach(sh, p, mass, by_mass ? before_mass : before_count, aim, [&](uint64_t q) { return steps.bin(place_value(q)); });
+    const ListSteps steps = list_steps(sh, p, n);
+    reach(sh, p, mass, by_mass ? before_mass : before_count, aim, [&](uint64_t q) { return steps.of(q); });
     const uint64_t last = sh.found_key;
     uint64_t kept = 0, total;
 #pragma unroll
@@ -594,8 +631,8 @@ __device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row 
         p[j] = i < n ? sh.list[i] : 0;
         mass[j] = i < n ? 1 : 0;
     }
-    const Row steps = list_steps(sh, row, p, n);
-    auto step_of = [&](uint64_t q) { return steps.bin(place_value(q)); };
+    const ListSteps steps = list_steps(sh, p, n);
+    auto step_of = [&](uint64_t q) { return steps.of(q); };
     if (n > k) {
         reach(sh, p, mass, 0, k, step_of);
         threshold = sh.found_key;
