@@ -34,9 +34,10 @@
 //
 // Bound: for few rows the chain of cluster barriers and passes over shared
 // memory (151,936 tokens, one row: greedy 3.4 us, top-k 50 8 us, top-p 0.9 at
-// temperature 1 on logits with a flat tail 23 us); for many rows those passes'
+// temperature 1 on logits with a flat tail 21 us); for many rows those passes'
 // instructions: 512 rows of float32, 311 MB, greedy 99 us (3.1 TB/s), top-k 50
-// 170, without cuts 195, top-p 0.9 630.
+// 170, without cuts 195, top-p 0.9 600; 64 rows of BF16 with mixed parameters
+// 46 us.
 #include <cooperative_groups.h>
 
 #include <utility>
@@ -668,7 +669,7 @@ __device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row 
 __device__ __forceinline__ uint32_t run_index(uint32_t run0, uint32_t i) { return run0 + i * 128 + (threadIdx.x & 31) * 4; }
 
 // The row a cluster takes where not all run at once: of every kThreads rows
-// the ones that take longest first (top-p over the whole row: up to 33 us
+// the ones that take longest first (top-p over the whole row: up to 27 us
 // alone, less at low temperatures, top-k 8, greedy 3), so that no long one starts when the others end:
 // 512 rows of mixed parameters 274 us against 300, 64 rows 56 against 64.
 // The same in all CTAs of a cluster.  It costs a cluster 1 us, so only where
