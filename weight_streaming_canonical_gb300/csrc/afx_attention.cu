@@ -49,6 +49,12 @@ constexpr uint32_t kMinKeys = 64;     // keys of a 16-row item, at least, where 
 // tokens: 74 us against 78; two requests on 131000 keys, whose join has more
 // pieces then: 121 against 115).
 constexpr uint32_t kTargetUnits = 2432, kFewUnits = 1216;
+// Up to this many rows of a source go to the 16-row kernel, two groups reading
+// the same keys, and a batch of no more rows goes without the tile kernel: with
+// 20 to 30 rows on a prefix of 500 to 8000 keys 27-33 us against 31-41, on
+// 64000 keys 74-76 against 76-78; with 45 rows on 64000 keys 84 against 76.
+// Two requests of 24 and 16 rows on 1284 keys: 24 us against 42.
+constexpr uint32_t kTileFrom = 32;
 constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's tiles take the prefix along
 // Cost of a tile CTA, at least: one step where the other SMs would be idle (two
 // prompts of 43 tokens: 32 us, 52 with four steps).  Where the 16-row kernel
@@ -56,12 +62,8 @@ constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's til
 // unit of cost here), more, for a CTA's start costs as much as four steps:
 // 64 requests with 8192 keys in common, 67 us against 78.
 constexpr uint32_t kMinShare = kStepBoth, kMinShareBeside = 12 * kStepBoth, kKeysOfCost = 16;
-// Up to this many rows in the batch the 16-row kernel takes all of them, two
-// groups reading the same keys, and the tile kernel is not launched: with 20
-// to 30 rows on a prefix of 500 to 8000 keys 27-33 us against 31-41, on 64000
-// keys 74-76 against 76-78; with 45 rows on 64000 keys 84 against 76.
-constexpr uint32_t kFewRows = 32;
 constexpr uint32_t kFewTokens = 8, kManyMax = 512;
+constexpr uint32_t kManyPieces = 128;  // of a row, from which its join takes 16 warps
 
 __host__ __device__ inline uint64_t up(uint64_t v, uint64_t a) { return (v + a - 1) / a * a; }
 
@@ -121,7 +123,7 @@ struct Kind {
 };
 
 __device__ __forceinline__ Kind kind_of(const AttnArgs& a, uint32_t rows) {
-    const bool tile = a.tile_ctas && rows > kRows;
+    const bool tile = a.tile_ctas && rows > kTileFrom;
     return Kind{rows == 0 ? kNone : tile ? kTile : kRow16, a.prefix_len == 0 || (tile && rows >= kFuseRows)};
 }
 
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     Counts<3> all;
     uint32_t packed = static_cast<uint32_t>(block_exclusive(first, &all).v[1]);
     const uint32_t prefix_rows = static_cast<uint32_t>(all.v[1]) * G;
-    const uint32_t prefix_kind = prefix_rows == 0 ? kNone : a.tile_ctas && prefix_rows > kRows ? kTile : kRow16;
+    const uint32_t prefix_kind = prefix_rows == 0 ? kNone : a.tile_ctas && prefix_rows > kTileFrom ? kTile : kRow16;
     const uint32_t groups_p = prefix_kind == kRow16 ? ceil_div(prefix_rows, kRows) : 0;
     const uint32_t tiles_p = prefix_kind == kTile ? ceil_div(prefix_rows, kGroupRows) : 0;
     const uint64_t keys = all.v[0] + static_cast<uint64_t>(groups_p) * a.prefix_len;
@@ -607,7 +609,7 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, const PlanHead& h
     return p;
 }
 
-constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kSplitThreads = 512;
 constexpr uint32_t kJoinRows = 8;  // rows of a tile group that a warp puts together at a time
 
 // A lane's elements of an output row, in one store where its address allows.
@@ -701,7 +703,7 @@ __device__ void join_group_rows(const AttnArgs& a, const TileGroup& g, uint32_t 
 template <typename T, int D>
 __device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t block, uint32_t blocks) {
     const TileGroup* tiles = a.at<TileGroup>(a.L.tiles);
-    const uint32_t warps = blocks * kJoinWarps, me = block * kJoinWarps + (threadIdx.x >> 5);
+    const uint32_t per = blockDim.x / 32, warps = blocks * per, me = block * per + (threadIdx.x >> 5);
     const uint32_t borders = head.cost ? static_cast<uint32_t>((head.cost - 1) / head.share) : 0;
     constexpr uint32_t kUnits = kGroupRows / kJoinRows;
     for (uint32_t u = me; u < borders * kUnits; u += warps) {
@@ -724,13 +726,14 @@ __device__ void join_tiles(const AttnArgs& a, const PlanHead& head, uint32_t blo
 }
 
 // Rows outside tiles of their request's own, span at a time a warp (kSplit: one
-// row a CTA, whose warps share its pieces: few rows, each of many pieces), then
+// row a CTA, whose warps, 4 or 16, share its pieces: few rows, each of many), then
 // join_tiles.  Pieces are added in a fixed order.
 template <typename T, int D, bool kSplit>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a, uint32_t span) {
+__global__ void __launch_bounds__(kSplit ? kSplitThreads : kJoinThreads) attention_join_kernel(const AttnArgs a, uint32_t span) {
     constexpr int kPer = D / 32;
-    __shared__ float sh_acc[kSplit ? kJoinWarps : 1][D];
-    __shared__ float2 sh_ml[kJoinWarps];
+    constexpr int kMostWarps = kSplit ? kSplitThreads / 32 : 1;
+    __shared__ float sh_acc[kMostWarps][D];
+    __shared__ float2 sh_ml[kMostWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t q_heads = a.kv_heads * a.group;
     wait_for_earlier();
@@ -758,10 +761,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         const float2* part_ml = a.at<float2>(a.L.part_ml);
         float top = -INFINITY, sum = 0.0f, acc[kPer] = {};
         const uint32_t n = s.pre.count() + s.own.count();
-        constexpr uint32_t kStep = kSplit ? kJoinWarps : 1;
-        const uint32_t off = kSplit ? warp : 0;  // this warp's pieces: off, off + kStep, ...
-        for (uint32_t b = off; b < n; b += 32 * kStep) {
-            const uint32_t p = b + lane * kStep;
+        const uint32_t step = kSplit ? blockDim.x / 32 : 1;
+        const uint32_t off = kSplit ? warp : 0;  // this warp's pieces: off, off + step, ...
+        for (uint32_t b = off; b < n; b += 32 * step) {
+            const uint32_t p = b + lane * step;
             const uint64_t row = p >= n ? 0 : p < s.pre.count() ? s.pre.row(p) : s.own.row(p - s.pre.count());
             const float2 ml = p < n ? part_ml[row] : make_float2(-INFINITY, 0.0f);
             float most = fmaxf(top, ml.x);
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
             const bool real = ml.x != -INFINITY;  // else its sums may never have been written
             const float f = real ? exp2_approx(ml.x - top) : 0.0f;
             float part = f * ml.y;
-            const uint32_t m = min(32u, ceil_div(n - b, kStep));
+            const uint32_t m = min(32u, ceil_div(n - b, step));
 #pragma unroll
             for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
             sum += part;
@@ -802,12 +805,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
             if (warp) return;  // the first warp goes on
             top = -INFINITY;
             sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, sh_ml[w].x);
+            for (uint32_t w = 0; w < step; ++w) top = fmaxf(top, sh_ml[w].x);
 #pragma unroll
             for (int j = 0; j < kPer; ++j) acc[j] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) {
+            for (uint32_t w = 0; w < step; ++w) {
                 const float f = sh_ml[w].x == -INFINITY ? 0.0f : exp2_approx(sh_ml[w].x - top);
                 sum += f * sh_ml[w].y;
 #pragma unroll
@@ -878,10 +879,10 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
     a->scale_log2 = static_cast<float>(static_cast<double>(d->scale) * 1.4426950408889634074);
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
-    const bool few = static_cast<uint64_t>(d->n_tokens) * a->group <= kFewRows;
+    const bool few = static_cast<uint64_t>(d->n_tokens) * a->group <= kTileFrom;
     a->tile_ctas = !few && tiles_fit(c) ? static_cast<uint32_t>(sms) : 0u;
     // bounds on what the plan writes.  16-row groups: where tiles serve the
-    // larger ones, one a request and one on the prefix; every group has one
+    // larger ones, kTileFrom rows a request and on the prefix; every group has one
     // piece, and the cuts add at most kTargetUnits / kv_heads.  Tile groups:
     // full ones, and a last one a request; a group of 128 rows or fewer has
     // its first piece's results twice.  Rows that share the prefix are in
@@ -889,8 +890,8 @@ afx_status prepare(const afx_attention_args* d, AttnArgs* a) {
     const uint64_t rows = static_cast<uint64_t>(d->n_tokens) * a->group, R = d->n_requests;
     const uint64_t extra = kTargetUnits / c.kv_heads + 1;
     const bool tiles = a->tile_ctas != 0;
-    const uint64_t small = tiles ? (rows < kRows * R ? rows : kRows * R) + kRows : 2 * rows;
-    const uint64_t groups = tiles ? R + 1 : 2 * (rows / kRows + 1) + R;
+    const uint64_t small = tiles ? (rows < kTileFrom * R ? rows : kTileFrom * R) + kTileFrom : 2 * rows;
+    const uint64_t groups = tiles ? (R + 1) * (kTileFrom / kRows) : 2 * (rows / kRows + 1) + R;
     const uint64_t shared = rows < kFuseRows * R ? rows : kFuseRows * R;
     const uint64_t tile_rows = tiles ? rows + 2 * shared + 2 * kTileRows : 0;
     AttnLayout& L = a->L;
@@ -954,12 +955,16 @@ afx_status launch(const AttnArgs& a, const afx_kv_cache& cache, cudaStream_t s) 
                   "cudaFuncSetAttribute");
     AFX_SERVE_TRY(launch_early(attention_rows16_kernel<T, D>, sms * 2, kWarps * 32, smem, s, a), "attention_rows16_kernel launch");
     const uint64_t rows = static_cast<uint64_t>(a.n_tokens) * a.kv_heads * a.group;
-    // a request can have tiles of its own from kFuseRows rows on, without a prefix from kRows + 1
-    const bool own_tiles = a.tile_ctas && static_cast<uint64_t>(a.n_tokens) * a.group > (a.prefix_len ? kFuseRows - 1 : kRows);
+    // a request can have tiles of its own from kFuseRows rows on, without a prefix from kTileFrom + 1
+    const bool own_tiles = a.tile_ctas && static_cast<uint64_t>(a.n_tokens) * a.group > (a.prefix_len ? kFuseRows - 1 : kTileFrom);
     const uint32_t most = sms * 8, least = own_tiles ? most : 0;
     if (rows <= most) {  // a CTA a row
         const uint32_t n = static_cast<uint32_t>(rows);
-        AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, true>, n < least ? least : n, kJoinThreads, 0, s, a, 1u), "attention_join_kernel launch");
+        // more warps where rows are few and cut into many pieces (12 rows of one head on 35,737 keys: 38 us against 69;
+        // two requests on 131,000: 118 against 126; caches cold)
+        const bool many = kFewUnits / a.kv_heads >= kManyPieces && a.prefix_len / kMinKeys >= kManyPieces;
+        const uint32_t threads = many && !least && rows <= static_cast<uint64_t>(sms) ? kSplitThreads : kJoinThreads;
+        AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, true>, n < least ? least : n, threads, 0, s, a, 1u), "attention_join_kernel launch");
     } else {
         const uint64_t span = rows <= static_cast<uint64_t>(sms) * 256 ? 1 : 32, per = span * kJoinWarps, need = (rows + per - 1) / per;
         const uint32_t n = need > most ? most : static_cast<uint32_t>(need);
