@@ -52,7 +52,7 @@ namespace {
 
 constexpr int kThreads = 512;      // two CTAs an SM
 constexpr int kWarps = kThreads / 32;
-constexpr uint32_t kBinBits = kThreads == 512 ? 9 : 8, kBins = 1u << kBinBits;  // one a thread
+constexpr uint32_t kBinBits = 9, kBins = 1u << kBinBits;  // one a thread
 static_assert(kBins == kThreads, "a bin a thread");
 constexpr uint32_t kListMax = 2048;    // tokens that one CTA sorts
 constexpr uint32_t kPer = kListMax / kThreads;
