@@ -663,7 +663,8 @@ afx_status afx_attention(const afx_attention_args* args, const void* q_dev, uint
  * infinity (masked).  With m the row's largest logit, y = (z - m) * (1 / T)
  * in float32 and weights e^y, tokens ordered by z, descending, equal ones by
  * index:
- *   temperature  T; a row whose T is not above 0 gets the first token;
+ *   temperature  T; a row whose T is not above 0 gets the first token, and
+ *                T between 0 and 3e-39 counts as 3e-39 (1 / T stays finite);
  *   top_k        keeps the first top_k tokens (<= 0: all);
  *   top_p        of those, keeps the ones before which less than top_p of
  *                their weight lies (>= 1: all; the first always stays);

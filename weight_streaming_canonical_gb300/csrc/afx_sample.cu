@@ -1,8 +1,8 @@
 // sm_103a sampling of one token a row of logits (afx_sample).
 //
 // With z the logits (NaN counts as masked), m their maximum, T the
-// temperature: y = (z - m) * (1 / T), w = e^y.  Tokens are ordered by z,
-// descending, ties by index.  top-k keeps the first k; top-p keeps those
+// temperature (where above 0, at least 3e-39): y = (z - m) * (1 / T),
+// w = e^y.  Tokens are ordered by z, descending, ties by index.  top-k keeps the first k; top-p keeps those
 // whose preceding mass is below p times the mass top-k kept; min-p keeps
 // w >= min_p; the drawn token is the first, by index, at which the running
 // sum of the kept w exceeds u times their sum.
@@ -64,6 +64,8 @@ constexpr int kCuts = 2;               // weights above e^-4 and e^-8 tell how f
 constexpr uint32_t kQueue = 160;       // tokens a warp has found and not yet dealt with: 31 and 128 more
 constexpr float kRange = 30.5f;        // e^-30.5 < 2^-44: no mass below m - 30.5 T
 constexpr float kMassOne = 17592186044416.0f;  // 2^44
+constexpr float kMostF = 3.40282347e38f;       // the largest float32
+constexpr float kLeastT = 3e-39f;              // 1 / T is finite from here on (the maximum's weight is e^(0 / T))
 
 struct SampleArgs {
     const void* logits;
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const T* src = static_cast<const T*>(a.logits) + r * a.row_stride + base;
 
     // the row's parameters, under way with the logits
-    const float temp = a.temperature ? __ldg(a.temperature + r) : 1.0f;
+    float temp = a.temperature ? __ldg(a.temperature + r) : 1.0f;
     const int32_t top_k = a.top_k ? __ldg(a.top_k + r) : 0;
     const float top_p = a.top_p ? __ldg(a.top_p + r) : 1.0f, min_p = a.min_p ? __ldg(a.min_p + r) : 0.0f, u = __ldg(a.u + r);
 
@@ -853,6 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         return;
     }
+    temp = fmaxf(temp, kLeastT);
     row.inv_t = temp == INFINITY ? 1.17549435e-38f : 1.0f / temp;  // not 0: masked logits stay minus infinity
     const bool infinite = row.top == INFINITY;
     if (infinite) {  // infinite logits share everything: as zeros among masked ones
@@ -861,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         row.top = 0.0f;
         __syncthreads();
     }
-    row.step = static_cast<float>(kBins) / (kRange * temp);
+    row.step = fminf(static_cast<float>(kBins) / (kRange * temp), kMostF);  // the steps reach past kRange below T = 5e-38
     Want want;
     want.k = top_k > 0 && static_cast<uint32_t>(top_k) < a.vocab ? top_k : 0;
     want.p = top_p < 1.0f ? top_p : 1.0f;
