@@ -643,8 +643,9 @@ afx_status afx_attention_plan(const afx_attention_args* args, void* workspace_de
  * the end.  Cache contents past a request's length (or the prefix's) are
  * never used, whatever they hold; the values of tokens that a row of the
  * same request does see must be finite for the rows that do not see them
- * yet.  A page outside the pool sets AFX_DEV_BAD_PAGE, a workspace without
- * this description's plan AFX_DEV_BAD_PLAN.  Pieces are joined in a fixed
+ * yet.  A page outside the pool sets AFX_DEV_BAD_PAGE and its tokens are
+ * left out, as if no row saw them; a workspace without this description's
+ * plan sets AFX_DEV_BAD_PLAN.  Pieces are joined in a fixed
  * order: the same call gives the same bits.  Calls that overlap on the GPU
  * need their own workspaces.  Asynchronous on stream.  Errors: AFX_E_ARG,
  * AFX_E_NOSPACE, AFX_E_CUDA. */

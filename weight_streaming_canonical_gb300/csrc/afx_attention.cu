@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
     uint64_t c_head = 0;
     const int32_t* c_pages = nullptr;
     uint32_t c_page = 0;  // lane l: the page of step c_block / 32 * 32 + l
+    uint32_t c_gone = 0;  // a bit each of these 32 steps: the page lies outside the pool, the keys are left out
+    uint32_t absent = 0;  // the same, a bit a stage
     auto open = [&]() {
         if (lane == 0) {
             c_unit = atomicAdd(counter, 1u);
@@ -404,13 +406,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
             if (c_block % 32 == 0) {  // 32 steps' pages at a time
                 const uint32_t i = c_block + lane;
                 const int32_t id = i < c_blocks ? __ldg(c_pages + ((c_key0 + i * kBlockKeys) >> a.shift)) : 0;
-                c_page = id;
-                if (id < 0 || static_cast<uint32_t>(id) >= a.n_pages) {
-                    raise(a.status, AFX_DEV_BAD_PAGE);
-                    c_page = 0;
-                }
+                const bool gone = id < 0 || static_cast<uint32_t>(id) >= a.n_pages;
+                if (gone) raise(a.status, AFX_DEV_BAD_PAGE);
+                c_page = gone ? 0 : id;
+                c_gone = __ballot_sync(0xFFFFFFFFu, gone);
             }
             const uint32_t key = c_key0 + c_block * kBlockKeys;
+            uint32_t end = c_key1;
+            if (c_gone | absent) {
+                const uint32_t gone = c_gone >> (c_block % 32) & 1;
+                absent = (absent & ~(1u << c_stage)) | gone << c_stage;
+                if (gone) end = 0;
+            }
             const uint64_t page = __shfl_sync(0xFFFFFFFFu, c_page, c_block % 32);
             // a lane copies every (32 / kChunks)-th key from its own on, the same 16 bytes of each
             const uint32_t row0 = lane / kChunks, chunk = lane % kChunks;
@@ -422,7 +429,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
 #pragma unroll
             for (int c = 0; c < kBlockKeys * kChunks / 32; ++c) {
                 const uint32_t row = c * (32 / kChunks) + row0;
-                const bool real = key + row < c_key1;  // past the range: zeros, whatever the page holds there
+                const bool real = key + row < end;  // past the range: zeros, whatever the page holds there
                 const uint32_t dst = buf + row * (D * 2) + ((chunk ^ (row & 7)) * 16);
                 copy16(dst, k_from, real);
                 copy16(dst + kTile, v_from, real);
@@ -485,6 +492,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
             asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 1) : "memory");
             __syncwarp();
             const uint32_t buf = mine + stage * 2 * kTile;
+            const uint32_t at_stage = 1u << stage;
             stage = stage + 1 == kStages ? 0 : stage + 1;
             float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
                 Elem<T>::mma(s[0], qf[ks], b[0], b[1]);
                 Elem<T>::mma(s[1], qf[ks], b[2], b[3]);
             }
-            const bool whole = key + kBlockKeys <= it.key1 && key + kBlockKeys <= min_limit;
+            const bool whole = key + kBlockKeys <= it.key1 && key + kBlockKeys <= min_limit && absent == 0;
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
                 for (int j = 0; j < 4; ++j) {
                     float x = s[n][j] * a.scale_log2;
                     const uint32_t kk = key + n * 8 + (lane % 4) * 2 + (j & 1);
-                    if (!whole && (kk >= it.key1 || kk >= limit[j >> 1])) x = -INFINITY;
+                    if (!whole && (absent & at_stage || kk >= it.key1 || kk >= limit[j >> 1])) x = -INFINITY;
                     s[n][j] = x;
                     top[j >> 1] = fmaxf(top[j >> 1], x);
                 }

@@ -79,6 +79,10 @@ struct Ctl {
     uint64_t q_full[2], q_empty[2];    // a tile's queries
     uint64_t s_full[2], p_full[2][2], pv_done[2];
     uint64_t drain;
+    // a tile's last 8 steps: a bit for 16 keys whose page lies outside the pool; read, and written at every step, from
+    // the first such page on.  A step's word is written when the slot of its keys is free: the rows have weighed the
+    // step 3 (heads of 128) or 6 (of 64) before it by then
+    uint32_t any_absent, absent[2][8];
     uint32_t tmem;
     int32_t abort_flag;
 };
@@ -333,6 +337,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         }
         bar_init(&ctl.drain, 1);
         ctl.abort_flag = 0;
+        ctl.any_absent = 0;
+        for (int i = 0; i < 16; ++i) ctl.absent[i / 8][i % 8] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -364,6 +370,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         const uint32_t box = min(1u << a.shift, kTileKeys), page_mask = (1u << a.shift) - 1;
         const bool leader = elect();
         uint32_t slot = kv, phase = 0, seq = kv, tails = 0;
+        uint32_t any_gone = 0, of_tile[2] = {0, 0};  // boxes outside the pool; a tile's steps so far
         bool ok = true;
         while (ok && walk.next(&p)) {
             for (uint32_t s = p.step0; s < p.step1 && ok; ++s) {
@@ -372,14 +379,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 step_keys(p, s, &prefix, &first, &n);
                 const uint32_t used = ceil_div(n, box);  // boxes that hold keys of this step
                 uint32_t page = 0;
+                bool missing = false;
                 if (static_cast<uint32_t>(lane) < used) {
                     const uint32_t col = (first + lane * box) >> a.shift;
                     const int32_t id = prefix ? __ldg(a.prefix_table + col) : __ldg(a.table + static_cast<uint64_t>(p.g.request) * a.table_cols + col);
-                    if (id < 0 || static_cast<uint32_t>(id) >= a.n_pages)
-                        raise(a.status, AFX_DEV_BAD_PAGE);
-                    else
-                        page = id;
+                    missing = id < 0 || static_cast<uint32_t>(id) >= a.n_pages;
+                    if (missing) raise(a.status, AFX_DEV_BAD_PAGE);
+                    page = missing ? a.n_pages : id;  // past the map's end a box is zeros
                 }
+                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, missing);
                 if (seq >= Sh::kSlots) {
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.empty[slot], phase ^ 1u, ctl, a.status));
                     if (!ok) break;
@@ -388,6 +396,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 const bool patch = kv == 1 && n < kTileKeys;
                 uint64_t* bar = patch ? &ctl.tail : &ctl.full[slot];
                 const uint32_t dst = smem_addr(smem + Sh::kQ) + slot * Sh::kSlot;
+                if (kv == 0) {
+                    any_gone |= gone;
+                    if (any_gone) {  // the rows leave these keys out
+                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, lane < 8 && (gone >> (lane * 16 / box) & 1));
+                        for (uint32_t t = 0; t < 2; ++t)
+                            if (leader && (p.both || ((s - p.step0) & 1) == t)) ctl.absent[t][of_tile[t] % 8] = bits;
+                        if (leader) ctl.any_absent = 1;
+                    }
+                    of_tile[0] += p.both || !((s - p.step0) & 1);
+                    of_tile[1] += p.both || ((s - p.step0) & 1);
+                }
                 if (leader) bar_expect(bar, used * box * 128 * Sh::kHalves);
 #pragma unroll 1
                 for (uint32_t b = 0; b < used; ++b) {
@@ -623,13 +642,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     uint32_t key, n;
                     step_keys(p, s, &prefix, &key, &n);
                     const uint32_t sees = prefix ? n : (limit > key ? min(n, limit - key) : 0u);
-                    const bool whole = n == kTileKeys && (prefix || key + kTileKeys <= all_see);
+                    uint32_t absent = 0;
+                    if (__builtin_expect(*reinterpret_cast<volatile uint32_t*>(&ctl.any_absent), 0))
+                        absent = *reinterpret_cast<volatile uint32_t*>(&ctl.absent[t][(s_count - 1) % 8]);
+                    const bool whole = n == kTileKeys && (prefix || key + kTileKeys <= all_see) && absent == 0;
                     uint32_t x[kTileKeys];
                     auto mask = [&](uint32_t half) {
                         if (__builtin_expect(whole, 1)) return;
 #pragma unroll
-                        for (uint32_t j = 0; j < 64; ++j)
-                            if (half * 64 + j >= sees) x[half * 64 + j] = 0xFF800000u;  // -inf
+                        for (uint32_t w = half * 2; w < half * 2 + 2; ++w) {
+                            const uint32_t in = sees > w * 32 ? min(32u, sees - w * 32) : 0;  // keys of these 32 that are seen
+                            const uint32_t real = (in ? 0xFFFFFFFFu >> (32 - in) : 0) &
+                                                  ~((absent >> (2 * w) & 1 ? 0xFFFFu : 0u) | (absent >> (2 * w + 1) & 1 ? 0xFFFF0000u : 0u));
+#pragma unroll
+                            for (uint32_t j = 0; j < 32; ++j)
+                                if (!(real >> j & 1)) x[w * 32 + j] = 0xFF800000u;  // -inf
+                        }
                     };
                     auto half_most = [&](uint32_t half) {
                         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
