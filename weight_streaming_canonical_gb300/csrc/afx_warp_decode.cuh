@@ -97,6 +97,7 @@ struct LaunchArgs {
     uint32_t kind;             // restore: element kind, kKindBF16 / kKindFP16 / kKindE4M3
     uint32_t partial;          // BF16 tensors whose state tables keep only their shallowest nodes
     uint32_t pair_stage;       // restore: 0, or two chunks a lane with a stage of this many bytes a warp
+    uint32_t follows;          // restore: launched so that it may start before the launch before it ends
     int32_t* status;
     TensorArgs t[kMaxTensors];
 };
