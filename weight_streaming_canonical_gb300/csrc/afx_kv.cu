@@ -179,7 +179,12 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TablesArgs
         if (page < 0 || static_cast<uint32_t>(page) >= a.n_pages) raise(a.status, AFX_DEV_BAD_PAGE);
         a.table[static_cast<uint64_t>(r) * a.cols + mv.pages(a.old_len[r]) + (j - g0[r])] = page;
     }
-    for (uint32_t f = gid; f + n_grow < n_drop; f += stride) a.stack[have + f] = mv.freed(f);
+    bool wrong = false;  // an id outside the pool comes back; told at the end, where nothing waits for it
+    for (uint32_t f = gid; f + n_grow < n_drop; f += stride) {
+        const int32_t page = mv.freed(f);
+        wrong |= static_cast<uint32_t>(page) >= a.n_pages;
+        a.stack[have + f] = page;
+    }
     // four tokens a thread: their request is looked up once, their page where it changes
     for (uint32_t t = 4 * gid; t < a.max_tokens; t += 4 * stride) {
         int32_t slot[4], pos[4];
@@ -224,6 +229,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TablesArgs
                 }
         }
     }
+    if (wrong) raise(a.status, AFX_DEV_BAD_PAGE);
 }
 
 struct WriteArgs {
