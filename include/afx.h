@@ -636,16 +636,17 @@ afx_status afx_attention_plan(const afx_attention_args* args, void* workspace_de
 /* out[t][h] = sum over the visible j of softmax_j(scale * q[t][h].k_j) v_j,
  * and, where lse_dev is not NULL, lse_dev[t * q_heads + h] = log sum_j
  * exp(scale * q.k_j).  q_dev and out_dev hold elements of the cache's format
- * at t * token stride + h * head stride (out's rows must not overlap).  A row that
- * sees nothing gets zeros and minus infinity.  Scores, maxima, sums and
- * outputs are held in float32; the softmax weights are rounded to the
- * cache's format for their product with the values, and the output once at
- * the end.  Cache contents past a request's length (or the prefix's) are
- * never used, whatever they hold; the values of tokens that a row of the
- * same request does see must be finite for the rows that do not see them
- * yet.  A page outside the pool sets AFX_DEV_BAD_PAGE and its tokens are
- * left out, as if no row saw them; a workspace without this description's
- * plan sets AFX_DEV_BAD_PLAN.  Pieces are joined in a fixed
+ * at t * token stride + h * head stride (out's rows must not overlap).  A
+ * row that sees nothing, or minus infinity alone, gets zeros and minus
+ * infinity; one that sees NaN (in its query, a key or a value) gets NaN.
+ * Scores, maxima, sums and outputs are held in float32; the softmax weights
+ * are rounded to the cache's format for their product with the values, and
+ * the output once at the end.  Cache contents past a request's length (or
+ * the prefix's) are never used, whatever they hold; the values of tokens
+ * that a row of the same request does see must be finite for the rows that
+ * do not see them yet.  A page outside the pool sets AFX_DEV_BAD_PAGE and
+ * its tokens are left out, as if no row saw them; a workspace without this
+ * description's plan sets AFX_DEV_BAD_PLAN.  Pieces are joined in a fixed
  * order: the same call gives the same bits.  Calls that overlap on the GPU
  * need their own workspaces.  Asynchronous on stream.  Errors: AFX_E_ARG,
  * AFX_E_NOSPACE, AFX_E_CUDA. */

@@ -645,6 +645,10 @@ __device__ __forceinline__ void load_part(const float* from, float (&v)[N]) {
     }
 }
 
+// Whether a piece has a key that the row sees: its maximum is minus infinity
+// also where all scores are NaN (a maximum passes over them), but not its sum 0.
+__device__ __forceinline__ bool has_keys(float2 ml) { return ml.x != -INFINITY || ml.y != 0.0f; }
+
 // Eight rows of a tile group's head, put together from its pieces by a warp.
 template <typename T, int D>
 __device__ void join_group_rows(const AttnArgs& a, const TileGroup& g, uint32_t h, uint32_t row0, uint32_t c0, uint32_t c1) {
@@ -672,7 +676,7 @@ __device__ void join_group_rows(const AttnArgs& a, const TileGroup& g, uint32_t 
         top = most;
         const float part = f * ml.y;
         sum = sum * keep + (part + __shfl_xor_sync(0xFFFFFFFFu, part, 8));
-        const uint32_t real = __ballot_sync(0xFFFFFFFFu, ml.x != -INFINITY);  // of the others the sums may never have been written
+        const uint32_t real = __ballot_sync(0xFFFFFFFFu, has_keys(ml));  // of the others the sums may never have been written
 #pragma unroll
         for (uint32_t r = 0; r < kJoinRows; ++r) {
             const float k = __shfl_sync(0xFFFFFFFFu, keep, r);
@@ -686,10 +690,10 @@ __device__ void join_group_rows(const AttnArgs& a, const TileGroup& g, uint32_t 
             }
         }
     }
-    const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const uint32_t pr = g.row0 + mine, tok = pr / a.group, token = g.token0 + tok, qh = h * a.group + (pr - tok * a.group);
     if (a.lse && lane < static_cast<int>(kJoinRows) && row0 + lane < rows)
-        a.lse[static_cast<uint64_t>(token) * q_heads + qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+        a.lse[static_cast<uint64_t>(token) * q_heads + qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     const uint64_t dst = token * a.out_token + qh * a.out_head;
 #pragma unroll
     for (uint32_t r = 0; r < kJoinRows; ++r) {
@@ -778,20 +782,20 @@ __global__ void __launch_bounds__(kSplit ? kSplitThreads : kJoinThreads) attenti
             float most = fmaxf(top, ml.x);
 #pragma unroll
             for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-            if (most == -INFINITY) continue;  // none of these pieces has a key that the row sees
-            const float keep = exp2_approx(top - most);
+            const bool real = has_keys(ml);  // else its sums may never have been written
+            const uint32_t live = __ballot_sync(0xFFFFFFFFu, real);
+            if (!live) continue;  // none of these pieces has a key that the row sees
+            const float ref = most == -INFINITY ? 0.0f : most, keep = exp2_approx(top - ref);
             top = most;
             sum *= keep;
 #pragma unroll
             for (int j = 0; j < kPer; ++j) acc[j] *= keep;
-            const bool real = ml.x != -INFINITY;  // else its sums may never have been written
-            const float f = real ? exp2_approx(ml.x - top) : 0.0f;
+            const float f = real ? exp2_approx(ml.x - ref) : 0.0f;
             float part = f * ml.y;
             const uint32_t m = min(32u, ceil_div(n - b, step));
 #pragma unroll
             for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
             sum += part;
-            const uint32_t live = __ballot_sync(0xFFFFFFFFu, real);
             constexpr uint32_t kAtOnce = kSplit ? 8 : 4;  // loads in flight; past the last piece: row 0
             for (uint32_t j = 0; j < m; j += kAtOnce) {
                 float v[kAtOnce][kPer];
@@ -816,21 +820,22 @@ __global__ void __launch_bounds__(kSplit ? kSplitThreads : kJoinThreads) attenti
             for (uint32_t w = 0; w < step; ++w) top = fmaxf(top, sh_ml[w].x);
 #pragma unroll
             for (int j = 0; j < kPer; ++j) acc[j] = 0.0f;
+            const float ref = top == -INFINITY ? 0.0f : top;
             for (uint32_t w = 0; w < step; ++w) {
-                const float f = sh_ml[w].x == -INFINITY ? 0.0f : exp2_approx(sh_ml[w].x - top);
+                const float f = exp2_approx(sh_ml[w].x - ref);
                 sum += f * sh_ml[w].y;
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) acc[j] += f * sh_acc[w][lane * kPer + j];
             }
         }
         // a row that sees no key: zeros, and the logarithm of an empty sum
-        const float inv = top == -INFINITY ? 0.0f : 1.0f / sum;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         T* out = static_cast<T*>(a.out) + s.t * a.out_token + s.qh * a.out_head + lane * kPer;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) acc[j] *= inv;
         store_row<T, kPer>(out, acc);
         if (a.lse && lane == 0)
-            a.lse[static_cast<uint64_t>(s.t) * q_heads + s.qh] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+            a.lse[static_cast<uint64_t>(s.t) * q_heads + s.qh] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     };
     const TokenInfo* tokens = a.at<TokenInfo>(a.L.tokens);
     if constexpr (kSplit) {

@@ -743,7 +743,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                 const bool final = g.single && cta0 == cta1 && p.both;
                 const uint32_t in_piece = p.both ? row : t * (walk.cta == cta0 ? g.rows : kTileRows) + row;
                 const uint64_t pr = tile_part_row(g, p.h, cta0, walk.cta, a.L.extra_row) + in_piece;
-                const float inv = ref == -INFINITY ? 0.0f : 1.0f / sum;
+                const bool empty = done == 0 || sum == 0.0f;  // nothing seen: zeros (with NaN among the scores the sum is NaN)
+                const float inv = empty ? 0.0f : 1.0f / sum;
                 // to the output only from a request's own tiles, whose tokens follow one another
                 const uint32_t packed_row = g.row0 + row, tok = packed_row / a.group;
                 const uint64_t token = g.token0 + tok, qh = p.h * a.group + (packed_row - tok * a.group);
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        w[j] = ref == -INFINITY ? 0u : Elem<T>::pack(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        w[j] = empty ? 0u : Elem<T>::pack(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
                     if (reinterpret_cast<uintptr_t>(out) & 31u) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -778,7 +779,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                         part_ml[pr] = make_float2(ref, sum);
                     else if (a.lse)
                         a.lse[token * (static_cast<uint64_t>(a.kv_heads) * a.group) + qh] =
-                            ref == -INFINITY ? -INFINITY : (ref + log2f(sum)) * kLn2;
+                            empty ? -INFINITY : (ref + log2f(sum)) * kLn2;
                 }
             }
             fence_before();  // O has been read before the next piece's products, which wait for this tile's weights
