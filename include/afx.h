@@ -640,7 +640,8 @@ afx_status afx_attention_plan(const afx_attention_args* args, void* workspace_de
  * row that sees nothing, or minus infinity alone, gets zeros and minus
  * infinity; one that sees NaN (in its query, a key or a value) gets NaN.
  * Scores, maxima, sums and outputs are held in float32; the softmax weights
- * are rounded to the cache's format for their product with the values, and
+ * are rounded to the cache's format for their product with the values
+ * (FP16: those below 2^-21 of the row's largest to within 2^-32 of it), and
  * the output once at the end.  Cache contents past a request's length (or
  * the prefix's) are never used, whatever they hold; the values of tokens
  * that a row of the same request does see must be finite for the rows that

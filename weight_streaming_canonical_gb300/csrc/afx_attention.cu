@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
         for (int n = 0; n < D / 8; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[n][j] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        constexpr float kRise = kLag + Elem<T>::kUp;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // references and sums
 
         for (uint32_t key = it.key0; key < it.key1; key += kBlockKeys) {
             copy_next();
@@ -520,10 +521,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows16_kernel(const 
                 top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
                 top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 2));
             }
-            if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kLag || top[1] > m[1] + kLag)) {
+            if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kRise || top[1] > m[1] + kRise)) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const float next = fmaxf(m[half], top[half]);
+                    const float next = fmaxf(m[half], top[half] - Elem<T>::kUp);
                     const float f = next == -INFINITY ? 1.0f : exp2_approx(m[half] - next);
                     m[half] = next;
                     l[half] *= f;

@@ -154,6 +154,8 @@ struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
     static constexpr uint32_t kMmaType = 1;  // in the tcgen05 instruction descriptor
+    static constexpr float kUp = 0.0f;
+    static constexpr float kHigh = 14.0f;
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -169,6 +171,8 @@ struct Elem<__nv_bfloat16> {
 template <>
 struct Elem<__half> {
     static constexpr uint32_t kMmaType = 0;
+    static constexpr float kUp = 7.0f;
+    static constexpr float kHigh = 15.0f;
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -188,10 +192,15 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// A row's reference maximum lags behind by up to this many powers of two:
-// exact all the same (numerator and denominator use the same reference), it
-// saves scaling the sums on every small rise; weights stay below 2^8, which both
-// 16-bit types hold.
+// Weights are 2^(score - reference), the reference kUp below a maximum of the
+// row's scores that lags behind by up to kLag powers of two (in the tile
+// kernel, until the next step, by more: to where weights reach 2^kHigh): exact
+// all the same (numerator and denominator use the same reference), and it
+// saves scaling the sums on every small rise.  FP16 holds weights from 2^-25
+// to 2^16 (the ones below 2^-14 to 2^-25 each): 7 powers of two up, 131,000
+// keys that are each below 2^-26 of the largest one are still in the product
+// with V as they are in the float32 sum; without, they were in the sum alone,
+// up to 0.4 % of it.
 constexpr float kLag = 8.0f;
 
 constexpr float kLn2 = 0.693147180559945309f;

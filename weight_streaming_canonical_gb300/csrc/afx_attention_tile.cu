@@ -57,7 +57,6 @@ constexpr int kTileThreads = 384;
 constexpr int kRegsLaunch = 168, kRegsRows = 208, kRegsOther = 88;
 static_assert(256 * kRegsRows + 128 * kRegsOther <= kTileThreads * kRegsLaunch, "register shares");
 constexpr uint32_t kWaitPolls = 1u << 22;
-constexpr float kHigh = 14.0f;  // weights stay below 2^14: FP16 holds them, and their sums are far from float32's end
 
 template <int D>
 struct Shape {
@@ -612,6 +611,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
         float* part_o = a.at<float>(a.L.part_o);
         float2* part_ml = a.at<float2>(a.L.part_ml);
         const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);  // not 0: masked scores stay minus infinity
+        constexpr float kRise = kLag + Elem<T>::kUp;
         uint32_t s_count = 0, pv_count = 0;
         bool ok = true;
         while (ok && walk.next(&p)) {
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
             // a new reference: the sums so far are scaled to it (the scores' barrier of this step says that the
             // product with the last step's weights is done too)
             auto rebase = [&](float most) {
-                const float next = most > ref + kLag ? most : ref;
+                const float next = most > ref + kRise ? most - Elem<T>::kUp : ref;
                 const float f = next == -INFINITY ? 1.0f : exp2_approx(ref - next);
                 ref = next;
                 sum *= f;
@@ -699,12 +699,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                     tmem_load32(s_col, x);
                     tmem_load32(s_col + 32, x + 32);
                     tmem_wait_load();
-                    if (__builtin_expect(done > 0 && __any_sync(0xFFFFFFFFu, seen_most > ref + kLag), 0)) rebase(seen_most);
+                    if (__builtin_expect(done > 0 && __any_sync(0xFFFFFFFFu, seen_most > ref + kRise), 0)) rebase(seen_most);
                     tmem_load32(s_col + 64, x + 64);
                     tmem_load32(s_col + 96, x + 96);
                     mask(0);
                     float most = half_most(0);
-                    if (done == 0) ref = most;
+                    if (done == 0) ref = most - Elem<T>::kUp;
 #pragma unroll 1
                     for (bool again = false;; again = true) {
                         weigh(x);
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attention_tile_kernel(const _
                         tmem_wait_load();
                         mask(1);
                         most = fmaxf(most, half_most(1));
-                        if (__builtin_expect(!__any_sync(0xFFFFFFFFu, most > ref + kHigh), 1)) break;
+                        if (__builtin_expect(!__any_sync(0xFFFFFFFFu, most > ref + Elem<T>::kHigh), 1)) break;
                         rebase(most);
                     }
                     seen_most = most;
