@@ -25,10 +25,12 @@
 // the output themselves; the others share tiles on the prefix.
 //
 // Bound: few rows, the read of the cache (two requests on 131,000 common keys,
-// 537 MB: 89 us, 6.1 TB/s, in the 16-row kernel, 99 with plan and join); many
-// rows, the products (see the tile kernel); small batches, the chain of plan,
-// attention and join (4 requests on 1003 keys: 18 us, 6 of them the plan's, 4
-// the join's).
+// 537 MB: 88 us, 6.1 TB/s, in the 16-row kernel); many rows, the products
+// (see the tile kernel); small batches, the chain of plan, attention and join
+// (4 requests on 1003 keys: each alone 6, 10 and 8 us).
+//
+// Times beside the constants below: one call of plan and attention between
+// two events, caches flushed; both sides in one run.
 #include <initializer_list>
 
 #include "afx_attention.cuh"
@@ -44,23 +46,26 @@ constexpr uint32_t kPlanThreads = 1024;
 constexpr uint32_t kMaxRequests = AFX_KV_MAX_REQUESTS;
 constexpr uint32_t kKeyAlign = 64;     // 16-row items' key ranges start at multiples of this
 constexpr uint32_t kMinKeys = 64;     // keys of a 16-row item, at least, where a range is cut
-// 16-row items x heads that the cuts aim at: a unit a warp of the GPU, or two
-// where there are many groups, of uneven lengths (64 requests of 200 to 1000
-// tokens: 74 us against 78; two requests on 131000 keys, whose join has more
-// pieces then: 121 against 115).
+// 16-row items x heads that the cuts aim at: a unit a warp of the GPU (152 SMs
+// of 8 warps), or two where there are many groups, of uneven lengths (64
+// requests of 200 to 1000 tokens on 8192 in common: 78 us with two, 80 with
+// one; two requests on 131,000 keys, whose join has more pieces with two: 117
+// with one, 122 with two; 5 on 8000: 32 and 40).
 constexpr uint32_t kTargetUnits = 2432, kFewUnits = 1216;
 // Up to this many rows of a source go to the 16-row kernel, two groups reading
-// the same keys, and a batch of no more rows goes without the tile kernel: with
-// 20 to 30 rows on a prefix of 500 to 8000 keys 27-33 us against 31-41, on
-// 64000 keys 74-76 against 76-78; with 45 rows on 64000 keys 84 against 76.
-// Two requests of 24 and 16 rows on 1284 keys: 24 us against 42.
+// the same keys, and a batch of no more rows goes without the tile kernel.  25
+// rows on 500, 8000 and 64,000 keys: 24, 32 and 77 us, with the limit at 16
+// rows 31-34, 43 and 88; two requests of 24 and 16 rows on 1284 keys each: 26
+// and 47.  A limit of 48 costs 45 rows on 8000 and 64,000 keys 36 and 85 us
+// where they take 43 and 88 now.
 constexpr uint32_t kTileFrom = 32;
 constexpr uint32_t kFuseRows = 128;    // packed rows from which a request's tiles take the prefix along
 // Cost of a tile CTA, at least: one step where the other SMs would be idle (two
-// prompts of 43 tokens: 32 us, 52 with four steps).  Where the 16-row kernel
-// has as much to do (a key of a head there takes an SM as long as a 16th of a
-// unit of cost here), more, for a CTA's start costs as much as four steps:
-// 64 requests with 8192 keys in common, 67 us against 78.
+// prompts of 43 tokens, 24 heads on 2, on 600 keys 42 us, on 500 of their own
+// 40; with twelve steps 57 and 59, with four 46 and 41).  Where the 16-row
+// kernel has as much to do (a key of a head there takes an SM as long as a
+// 16th of a unit of cost here), twelve, for a CTA's start costs as much as
+// four steps: 64 requests with 8192 keys in common, 78 us, with one step 91.
 constexpr uint32_t kMinShare = kStepBoth, kMinShareBeside = 12 * kStepBoth, kKeysOfCost = 16;
 constexpr uint32_t kFewTokens = 8, kManyMax = 512;
 constexpr uint32_t kManyPieces = 128;  // of a row, from which its join takes 16 warps
@@ -974,8 +979,9 @@ afx_status launch(const AttnArgs& a, const afx_kv_cache& cache, cudaStream_t s) 
     const uint32_t most = sms * 8, least = own_tiles ? most : 0;
     if (rows <= most) {  // a CTA a row
         const uint32_t n = static_cast<uint32_t>(rows);
-        // more warps where rows are few and cut into many pieces (12 rows of one head on 35,737 keys: 38 us against 69;
-        // two requests on 131,000: 118 against 126; caches cold)
+        // more warps where rows are few and cut into many pieces (12 rows a head of two on 35,737 keys: 39 us, 67 with
+        // 4 warps; two requests on 131,000: 117 and 126).  By the prefix alone, whose length the host has: requests
+        // whose own tokens are as many take the 4 warps (one of 100,000 tokens: 108 us)
         const bool many = kFewUnits / a.kv_heads >= kManyPieces && a.prefix_len / kMinKeys >= kManyPieces;
         const uint32_t threads = many && !least && rows <= static_cast<uint64_t>(sms) ? kSplitThreads : kJoinThreads;
         AFX_SERVE_TRY(launch_early(attention_join_kernel<T, D, true>, n < least ? least : n, threads, 0, s, a, 1u), "attention_join_kernel launch");

@@ -115,11 +115,11 @@ __device__ __forceinline__ uint32_t visible(int32_t seen, uint32_t row, uint32_t
 
 // More than 128 rows: both tiles work on every step's keys.  Fewer: the tiles
 // take the steps in turn, and half the products need as many keys (measured:
-// 3330 cycles a step for both, 2010 for one).
+// some 3200 cycles a step for both, 2000 for one).
 constexpr uint32_t kStepBoth = 8, kStepOne = 5;
 // What a group costs besides: filling and emptying the pipe, masked steps, the
-// output (24 requests of 5 to 11 tokens on 5722 keys in common: 69 us, 101
-// without; 78 of 5 to 12 tokens on 16,025: 278 against 366).
+// output (24 requests of 5 to 11 tokens on 5722 keys in common: 77 us a call,
+// caches flushed, 121 without; 78 of 5 to 12 tokens on 16,025: 311 and 516).
 constexpr uint32_t kGroupCost = 20;
 __host__ __device__ __forceinline__ uint32_t step_cost(uint32_t rows) { return rows > kTileRows ? kStepBoth : kStepOne; }
 

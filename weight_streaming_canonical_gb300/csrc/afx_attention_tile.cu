@@ -33,7 +33,7 @@
 // Bound: the products' chain (scores, weights, values, scores ...) of two
 // tiles; 3200 cycles a step of both tiles, of which the products take 2048.
 // 16 prompts of 200 to 500 tokens on 4100 keys in common, 40 heads of 128 on
-// 8, BF16: 400 us, 1.14 PFLOP/s of what the masks leave, 60 % of a large library
+// 8, BF16: 394 us, 1.16 PFLOP/s of what the masks leave, 61 % of a large library
 // product's rate on this GPU.
 //
 // Every wait is bounded: one that runs out raises AFX_DEV_TIMEOUT and a
@@ -90,8 +90,8 @@ static_assert(sizeof(Ctl) <= 1024, "control block");
 struct TileArgs {
     CUtensorMap k, v;
     AttnArgs a;
-    // where token, head and page stand among the map's outer dimensions (by stride, smallest first)
-    uint32_t token_at, head_at, page_at;
+    // where token and head stand among the map's outer dimensions (by stride, smallest first); page has the place that is left
+    uint32_t token_at, head_at;
 };
 
 // ---- barriers, TMA, tensor memory ------------------------------------------------
@@ -254,13 +254,13 @@ __device__ __noinline__ void scale_columns(uint32_t addr, int n, float f) {
 // same ones.
 struct Walk {
     const TileGroup* groups;
-    uint64_t at, end, share;
+    uint64_t at, end;
     uint32_t n, heads, cta, g;
 
     __device__ Walk(const AttnArgs& a, const PlanHead& head)
-        : groups(a.at<TileGroup>(a.L.tiles)), share(head.share), n(head.n_tiles), heads(a.kv_heads), cta(blockIdx.x), g(0) {
-        at = static_cast<uint64_t>(cta) * share;
-        end = at + share < head.cost ? at + share : head.cost;
+        : groups(a.at<TileGroup>(a.L.tiles)), n(head.n_tiles), heads(a.kv_heads), cta(blockIdx.x), g(0) {
+        at = static_cast<uint64_t>(cta) * head.share;
+        end = at + head.share < head.cost ? at + head.share : head.cost;
         if (at >= end) return;
         uint32_t lo = 0, hi = n;  // the group that holds `at`
 #pragma unroll 1
@@ -891,7 +891,10 @@ afx_status launch_tiles(const AttnArgs& a, const afx_kv_cache& cache, cudaStream
     args.a = a;
     PoolDim d[3];
     pool_dims(cache, d);
-    for (uint32_t i = 0; i < 3; ++i) (d[i].which == 0 ? args.token_at : d[i].which == 1 ? args.head_at : args.page_at) = i;
+    for (uint32_t i = 0; i < 3; ++i) {
+        if (d[i].which == 0) args.token_at = i;
+        if (d[i].which == 1) args.head_at = i;
+    }
     afx_status st = pool_map(&args.k, cache.k_dev, cache, d);
     if (st == AFX_OK) st = pool_map(&args.v, cache.v_dev, cache, d);
     if (st != AFX_OK) return st;

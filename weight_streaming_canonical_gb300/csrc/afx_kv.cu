@@ -15,13 +15,13 @@
 // pages, finding a token's request by bisection of the sums.
 // Bound: latency (a launch, the lengths, the sums, a bisection, the table, the
 // store); the 8 bytes a new token written come to less.  4096 requests with a
-// new prompt for one in ten (300,000 new tokens): 13 us; one step of 8
-// requests: 5 us, less than a call takes the host.
+// new prompt for one in ten (300,000 new tokens): 16 us alone with cold caches;
+// one step of 8 requests: 7 us, less than a call takes the host.
 //
 // kv_write_kernel copies each new token's keys and values into its slot:
 // 2 * heads * dim elements read and written once, 16 bytes a lane and four
 // loads in flight a lane.  Bound: HBM bandwidth: 32,701 tokens of 8 heads of
-// 128, 268 MB moved, in 42 us, 6.3 TB/s; one step of 64 tokens 1.8 us.
+// 128, 268 MB moved, in 42 us a call, 6.3 TB/s; one step of 64 tokens 3 us alone.
 #include "afx_serving.cuh"
 
 namespace afx {

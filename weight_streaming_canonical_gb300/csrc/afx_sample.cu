@@ -33,11 +33,10 @@
 //     ties): a histogram of counts and masses refined until a list fits.
 //
 // Bound: for few rows the chain of cluster barriers and passes over shared
-// memory (151,936 tokens, one row: greedy 3.4 us, top-k 50 8 us, top-p 0.9 at
-// temperature 1 on logits with a flat tail 21 us); for many rows those passes'
-// instructions: 512 rows of float32, 311 MB, greedy 99 us (3.1 TB/s), top-k 50
-// 170, without cuts 195, top-p 0.9 600; 64 rows of BF16 with mixed parameters
-// 46 us.
+// memory; for many rows those passes' instructions.  151,936 tokens of
+// float32, the kernel alone, caches cold: one row greedy 6 us, top-k 50 13,
+// without cuts 17, top-p 0.9 at temperature 1 on logits with a flat tail 45;
+// 512 rows, 311 MB, 118 (2.6 TB/s), 192, 221 and 615.
 #include <cooperative_groups.h>
 
 #include <utility>
@@ -50,7 +49,7 @@ namespace afx {
 namespace serve {
 namespace {
 
-constexpr int kThreads = 512;      // two CTAs an SM
+constexpr int kThreads = 512;      // two CTAs an SM, where their tokens fit
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kBinBits = 9, kBins = 1u << kBinBits;  // one a thread
 static_assert(kBins == kThreads, "a bin a thread");
@@ -671,9 +670,10 @@ __device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row 
 __device__ __forceinline__ uint32_t run_index(uint32_t run0, uint32_t i) { return run0 + i * 128 + (threadIdx.x & 31) * 4; }
 
 // The row a cluster takes where not all run at once: of every kThreads rows
-// the ones that take longest first (top-p over the whole row: up to 27 us
-// alone, less at low temperatures, top-k 8, greedy 3), so that no long one starts when the others end:
-// 512 rows of mixed parameters 274 us against 300, 64 rows 56 against 64.
+// the ones that take longest first (top-p over the whole row: more than three
+// times as long as top-k, less at low temperatures), so that no long one
+// starts when the others end: 512 rows of mixed parameters 273 us, 281
+// without; 64 rows of BF16 54 and 62 (a call, caches flushed).
 // The same in all CTAs of a cluster.  It costs a cluster 1 us, so only where
 // there is a top-p.
 __device__ uint32_t row_in_order(const SampleArgs& a, Shared& sh, uint32_t place) {
@@ -1164,8 +1164,9 @@ extern "C" afx_status afx_sample(const void* logits_dev, uint32_t type, uint32_t
     a.tokens = tokens_dev;
     a.logprobs = logprobs_dev;
     a.vocab = vocab;
-    // CTAs a row: as few as hold it in 32,768 tokens each (the barriers cost
-    // less), more while the GPU has two CTAs an SM to give and 4096 tokens are left for each
+    // CTAs a row: as few as hold it in 32,640 tokens each (the barriers cost
+    // less), more while the GPU has two CTAs an SM to give and 4096 tokens are left for each.  Two CTAs fit an SM up
+    // to some 20,200 tokens each; with many rows, vocabularies that leave a CTA more have one
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
     uint32_t ranks = 1;
