@@ -517,6 +517,63 @@ afx_status afx_prefill_fused_batch(const afx_desc* descs, const void* const* con
                                    float* const* ys_dev, uint32_t count, void* workspace_dev, uint64_t workspace_bytes,
                                    afx_stream_t stream, int32_t* status_dev);
 
+/* ---- products of E4M3 weights -----------------------------------------------
+ *
+ * What follows the restore of an E4M3 container: the product of a step's
+ * activations with weights of 8 bits, a float32 scale for each block of 128
+ * rows and 128 columns of the weights and, of the activations, for each token
+ * and 128 columns.  "Memory requirements of language model inference on a
+ * consumer GPU", section "Number formats for weights", names 8-bit formats;
+ * the pages give no product for them, and the layouts are the library's own.
+ * Inference only: no gradients. */
+
+#define AFX_FP8_BLOCK 128
+
+/* Element types of activations, logits and results. */
+#define AFX_TYPE_BF16 0u
+#define AFX_TYPE_FP16 1u
+#define AFX_TYPE_F32 2u
+
+/* Rounds activations to E4M3.  Block b of token t is x_dev[t * x_stride + c],
+ * 128 b <= c < min(128 b + 128, cols); with a the largest magnitude in it,
+ * scales_dev[b * scale_stride + t] = max(a / 448, 2^-126), rounded to float32
+ * once, and q_dev[t * q_stride + c] = E4M3(x / scale), the quotient rounded to
+ * float32 and then to the nearest E4M3 value, ties to even.  A block that
+ * holds NaN or infinity gets NaN for its scale and all its values.  Strides
+ * in elements, q_stride and x_stride at least cols, scale_stride at least
+ * n_tokens; bytes of a row past cols are left as they are.  Any alignment (16
+ * bytes, with rows that keep it, is fastest); the arrays must not overlap.
+ * n_tokens and cols below 2^24.  One launch, asynchronous on stream.
+ * Errors: AFX_E_ARG, AFX_E_CUDA. */
+afx_status afx_fp8_quantize(const void* x_dev, uint32_t type, uint64_t x_stride, uint32_t n_tokens, uint32_t cols,
+                            uint8_t* q_dev, uint64_t q_stride, float* scales_dev, uint64_t scale_stride,
+                            afx_stream_t stream);
+
+/* y[t][r] = sum over blocks b of x_scales[b][t] * w_scales[r / 128][b] *
+ * sum over the block's c of x[t][c] * w[r][c], with
+ *   w          w_dev[r * w_stride + c], E4M3 bytes, rows x cols: what
+ *              afx_decode restores (w_stride = cols), or any rows;
+ *   w_scales   w_scales_dev[(r / 128) * ceil(cols / 128) + b];
+ *   x          x_dev[t * x_stride + c] and x_scales_dev[b * x_scale_stride + t],
+ *              as afx_fp8_quantize writes them;
+ *   y          y_dev[t * y_stride + r] of y_type (AFX_TYPE_*), overwritten;
+ *              y_stride at least rows.
+ * Products are exact and each block's sum is held in float32 by the tensor
+ * cores; the scaled sums are added in float32, in a fixed order (the same
+ * call gives the same bits), and rounded once to y_type.  NaN in x, w or a
+ * scale reaches every y that it belongs to.  w_dev and x_dev 16-byte aligned
+ * with w_stride and x_stride multiples of 16; cols itself may be any number;
+ * y of any alignment (32 bytes, with rows that keep it, is fastest).  cols from
+ * 1 on; n_tokens, rows and cols below 2^24; w_stride and x_stride below 2^32.
+ * One launch, no workspace, asynchronous on stream.  A wait past its
+ * limit sets AFX_DEV_TIMEOUT in *status_dev (nullable; the result is then
+ * unspecified).  y must not overlap the inputs.  Errors: AFX_E_ARG,
+ * AFX_E_CUDA. */
+afx_status afx_fp8_product(const uint8_t* w_dev, uint64_t w_stride, const float* w_scales_dev, uint32_t rows,
+                           uint32_t cols, const uint8_t* x_dev, uint64_t x_stride, const float* x_scales_dev,
+                           uint64_t x_scale_stride, uint32_t n_tokens, void* y_dev, uint32_t y_type,
+                           uint64_t y_stride, afx_stream_t stream, int32_t* status_dev);
+
 /* ---- serving: cache, attention, sampling ----------------------------------
  *
  * What a decode step does between its weight products: the pages of the
@@ -596,6 +653,82 @@ afx_status afx_kv_tables(uint32_t page_tokens, uint32_t n_pages, const int32_t* 
 afx_status afx_kv_write(const afx_kv_cache* cache, const void* k_dev, const void* v_dev, uint64_t token_stride,
                         uint64_t head_stride, const int32_t* slots_dev, uint32_t n_tokens, afx_stream_t stream,
                         int32_t* status_dev);
+
+/* ---- rotary positions ---------------------------------------------------
+ *
+ * What turns a step's queries and keys by their tokens' positions, of one
+ * axis (text) or several (time, height and width of images and video), on
+ * their way from the product to the attention and the cache. */
+
+#define AFX_ROTARY_MAX_PAIRS 128
+#define AFX_ROTARY_MAX_AXES 8
+#define AFX_ROTARY_HALVES 0u
+#define AFX_ROTARY_NEIGHBOURS 1u
+
+/* How a head is turned: filled by afx_rotary_plan, host memory. */
+typedef struct afx_rotary {
+    uint64_t step[AFX_ROTARY_MAX_PAIRS]; /* pair i's turns a position, times 2^64, whole turns left out */
+    uint8_t axis[AFX_ROTARY_MAX_PAIRS];  /* the axis whose position turns pair i */
+    uint32_t head_dim, rotary_dim, n_axes;
+    uint32_t pairs;                      /* AFX_ROTARY_HALVES or AFX_ROTARY_NEIGHBOURS */
+    float amplitude;
+    uint32_t reserved;
+} afx_rotary;
+
+/* Plans a rotation of the first rotary_dim of a head's head_dim elements (both
+ * even, rotary_dim at most head_dim, head_dim at most 256).  Pair i <
+ * rotary_dim / 2 is elements i and i + rotary_dim / 2 (AFX_ROTARY_HALVES) or
+ * 2 i and 2 i + 1 (AFX_ROTARY_NEIGHBOURS); with (a, b) its elements and
+ * angle = position[axis_of_pair[i]] * frequencies[i], it becomes
+ * amplitude * (a cos - b sin, a sin + b cos).  frequencies: radians a
+ * position, finite, or NULL for base^(-2 i / rotary_dim), base above 0;
+ * axis_of_pair: below n_axes, or NULL for axis 0 throughout.  Elements past
+ * rotary_dim stay as they are.  Host only.  Errors: AFX_E_ARG. */
+afx_status afx_rotary_plan(uint32_t head_dim, uint32_t rotary_dim, uint32_t pairs, double base,
+                           const double* frequencies, uint32_t n_axes, const uint8_t* axis_of_pair, float amplitude,
+                           afx_rotary* out);
+
+/* y[t][h] = x[t][h] turned to positions_dev[axis * axis_stride + t], for
+ * n_tokens tokens of heads heads: element i of head h of token t at
+ * t * token stride + h * head stride + i of x_dev (x_type) and y_dev (y_type).
+ * Angles are held as 64-bit fractions of a turn, so that a position of any
+ * size, negative ones too, loses no accuracy but that of its frequency in 53
+ * bits; sines and cosines are those of a 32-bit angle; the pair's products
+ * and sums are float32, rounded once to y_type.  y may be x itself (the same address,
+ * type and strides); otherwise they must not overlap.  Any strides and
+ * alignment (16-byte aligned rows are fastest); y's rows must not overlap.
+ * One launch, asynchronous on stream.  Errors: AFX_E_ARG, AFX_E_CUDA. */
+afx_status afx_rotate(const afx_rotary* rotary, const int32_t* positions_dev, uint64_t axis_stride, uint32_t n_tokens,
+                      const void* x_dev, uint32_t x_type, uint64_t x_token_stride, uint64_t x_head_stride,
+                      uint32_t heads, void* y_dev, uint32_t y_type, uint64_t y_token_stride, uint64_t y_head_stride,
+                      afx_stream_t stream);
+
+/* A step's queries, keys and values as a product leaves them: heads of the
+ * cache's head_dim elements of type, views of one tensor or of several. */
+typedef struct afx_qkv {
+    const void *q_dev, *k_dev, *v_dev;
+    uint64_t q_token_stride, q_head_stride; /* elements */
+    uint64_t k_token_stride, k_head_stride;
+    uint64_t v_token_stride, v_head_stride;
+    uint32_t type;    /* AFX_TYPE_* */
+    uint32_t q_heads; /* 0: keys and values alone */
+    uint32_t n_tokens;
+    uint32_t reserved;
+} afx_qkv;
+
+/* afx_rotate of the queries into q_out_dev (of the cache's format) and of the
+ * keys into the cache, with the values, at slots_dev[t], all in one launch: what
+ * two rotations and afx_kv_write leave, without the keys' and values' way
+ * through memory.  A token with a negative slot is padding: nothing of it is
+ * read or written, its row of q_out_dev included.  A slot past the pool sets
+ * AFX_DEV_BAD_PAGE, and its keys and values are left out.  Two tokens must not
+ * have the same slot.  q_out_dev may be the queries themselves (address, type
+ * and strides); nothing else may overlap.  Asynchronous on stream.
+ * Errors: AFX_E_ARG, AFX_E_CUDA. */
+afx_status afx_rotate_write(const afx_rotary* rotary, const int32_t* positions_dev, uint64_t axis_stride,
+                            const afx_qkv* in, void* q_out_dev, uint64_t q_out_token_stride,
+                            uint64_t q_out_head_stride, const afx_kv_cache* cache, const int32_t* slots_dev,
+                            afx_stream_t stream, int32_t* status_dev);
 
 /* Attention of a batch's new tokens over a prefix that all its requests
  * share and each request's own cached tokens.  The new tokens of request r
@@ -685,6 +818,70 @@ afx_status afx_sample(const void* logits_dev, uint32_t type, uint32_t rows, uint
                       const float* temperature_dev, const int32_t* top_k_dev, const float* top_p_dev,
                       const float* min_p_dev, const float* u_dev, int32_t* tokens_dev, float* logprobs_dev,
                       afx_stream_t stream);
+
+/* ---- verification of drafts -------------------------------------------------
+ *
+ * A step that feeds a request its last token and drafted ones behind it
+ * (afx_kv_tables and afx_attention take them as any new tokens) gives logits
+ * for every row; this call says how many of the drafts stand, and draws the
+ * token behind them, so that the tokens are distributed as afx_sample's. */
+
+/* What afx_sample takes, one value a request; each may be NULL. */
+typedef struct afx_sampling {
+    const float* temperature_dev;
+    const int32_t* top_k_dev;
+    const float* top_p_dev;
+    const float* min_p_dev;
+} afx_sampling;
+
+/* Request r's rows are starts_dev[r] .. starts_dev[r + 1] - 1, those of its new tokens in the step.
+ * Row t was fed tokens_dev[t]; the draft that row t decides on is
+ * tokens_dev[t + 1], and the last row has none.  A negative token, or one
+ * past the vocabulary, ends the request's drafts before it. */
+typedef struct afx_verify_args {
+    const void* logits_dev;       /* the target's: row t at logits_dev + t * row_stride elements */
+    const void* draft_logits_dev; /* the logits that row t's draft was drawn from, at row t; NULL: the drafts
+                                     were not drawn (looked up, say): their probability counts as 1 */
+    uint64_t row_stride, draft_row_stride;
+    uint32_t type, draft_type;    /* AFX_TYPE_* */
+    uint32_t vocab;               /* at most AFX_SAMPLE_MAX_VOCAB */
+    uint32_t n_requests;          /* 1 .. AFX_KV_MAX_REQUESTS */
+    uint32_t n_tokens;            /* rows; starts_dev[n_requests] may be lower: the rest is left alone */
+    uint32_t reserved;
+    const int32_t* starts_dev;    /* [n_requests + 1] */
+    const int32_t* tokens_dev;    /* [n_tokens] */
+    afx_sampling sampling, draft_sampling;
+    const float* u_dev;           /* [n_tokens], in [0, 1): row t's draft */
+    const float* draw_u_dev;      /* [n_requests], in [0, 1): the token behind the drafts that stand */
+} afx_verify_args;
+
+/* Bytes of device workspace for n_tokens rows of n_requests requests. */
+afx_status afx_verify_workspace(uint32_t n_tokens, uint32_t n_requests, uint64_t* bytes);
+
+/* With p_t(x) token x's share of the weights that afx_sample keeps of row t
+ * under the request's parameters (temperature 0: 1 for its first token), and
+ * q_t(x) the same of the draft's row under draft_sampling (without draft
+ * logits: 1 for the draft, 0 otherwise), row by row: row t's draft d stands
+ * where u_dev[t] * q_t(d) < p_t(d).  At the first row whose draft does not,
+ * a token is drawn from max(p_t - q_t, 0); where the drafts end, from p_t. The
+ * token drawn is the first, by index, at which the running sum exceeds
+ * draw_u_dev[r] times the whole; weights are summed as integers of 2^-44.
+ * Where nothing is left of max(p_t - q_t, 0) (the draft was none that q_t
+ * allows), the draw is from p_t.
+ * Written for request r: out_tokens_dev[t], its row by row new tokens: the
+ * drafts that stand, the token drawn, then -1; counts_dev[r], how many these
+ * are; logprobs_dev[t] (nullable), log p_t of each (0 behind the last).  A
+ * row to draw from without anything above minus infinity gives token -1 and minus infinity and
+ * is not counted.  A request without rows has count 0.  Rows from
+ * starts_dev[n_requests] on are left as they are.  Starts that do not begin
+ * at 0, fall or pass n_tokens set AFX_DEV_BAD_LENGTH: counts are 0 and
+ * nothing else is written.
+ * workspace_dev: 256-byte aligned, of at least afx_verify_workspace bytes,
+ * contents ignored; calls that overlap on the GPU need their own.  The
+ * outputs must not overlap the inputs.  The same call gives the same bits.  Asynchronous on stream.
+ * Errors: AFX_E_ARG, AFX_E_NOSPACE, AFX_E_CUDA. */
+afx_status afx_verify(const afx_verify_args* args, int32_t* out_tokens_dev, int32_t* counts_dev, float* logprobs_dev,
+                      void* workspace_dev, uint64_t workspace_bytes, afx_stream_t stream, int32_t* status_dev);
 
 /* ---- residency planning ------------------------------------------------
  *

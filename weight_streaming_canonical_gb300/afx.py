@@ -172,6 +172,29 @@ class afx_attention_args(ctypes.Structure):
     ]
 
 
+AFX_ROTARY_MAX_PAIRS, AFX_ROTARY_MAX_AXES = 128, 8
+AFX_ROTARY_HALVES, AFX_ROTARY_NEIGHBOURS = 0, 1
+
+
+class afx_rotary(ctypes.Structure):
+    _fields_ = [
+        ("step", ctypes.c_uint64 * AFX_ROTARY_MAX_PAIRS), ("axis", ctypes.c_uint8 * AFX_ROTARY_MAX_PAIRS),
+        ("head_dim", ctypes.c_uint32), ("rotary_dim", ctypes.c_uint32), ("n_axes", ctypes.c_uint32),
+        ("pairs", ctypes.c_uint32), ("amplitude", ctypes.c_float), ("reserved", ctypes.c_uint32),
+    ]
+
+
+class afx_qkv(ctypes.Structure):
+    _fields_ = [
+        ("q_dev", ctypes.c_void_p), ("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_uint64), ("q_head_stride", ctypes.c_uint64), ("k_token_stride", ctypes.c_uint64),
+        ("k_head_stride", ctypes.c_uint64), ("v_token_stride", ctypes.c_uint64), ("v_head_stride", ctypes.c_uint64),
+        ("type", ctypes.c_uint32), ("q_heads", ctypes.c_uint32), ("n_tokens", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+    ]
+
+
+AFX_FP8_BLOCK = 128
+AFX_TYPE_BF16, AFX_TYPE_FP16, AFX_TYPE_F32 = 0, 1, 2
 AFX_KV_MAX_REQUESTS = 16384
 AFX_SAMPLE_MAX_VOCAB = 524288
 AFX_LOGITS_BF16, AFX_LOGITS_FP16, AFX_LOGITS_F32 = 0, 1, 2
@@ -182,6 +205,13 @@ _lib.afx_attention_plan.argtypes = [ctypes.POINTER(afx_attention_args), _vp, _u6
 _lib.afx_attention.argtypes = [ctypes.POINTER(afx_attention_args), _vp, _u64, _u64, _vp, _u64, _u64, _vp, _vp, _u64, _vp,
                                _i32p]
 _lib.afx_sample.argtypes = [_vp, _u32, _u32, _u32, _u64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.afx_fp8_quantize.argtypes = [_vp, _u32, _u64, _u32, _u32, _vp, _u64, _vp, _u64, _vp]
+_lib.afx_fp8_product.argtypes = [_vp, _u64, _vp, _u32, _u32, _vp, _u64, _vp, _u64, _u32, _vp, _u32, _u64, _vp, _i32p]
+_lib.afx_rotary_plan.argtypes = [_u32, _u32, _u32, ctypes.c_double, ctypes.POINTER(ctypes.c_double), _u32,
+                                 ctypes.POINTER(ctypes.c_uint8), ctypes.c_float, ctypes.POINTER(afx_rotary)]
+_lib.afx_rotate.argtypes = [ctypes.POINTER(afx_rotary), _vp, _u64, _u32, _vp, _u32, _u64, _u64, _u32, _vp, _u32, _u64, _u64, _vp]
+_lib.afx_rotate_write.argtypes = [ctypes.POINTER(afx_rotary), _vp, _u64, ctypes.POINTER(afx_qkv), _vp, _u64, _u64,
+                                  ctypes.POINTER(afx_kv_cache), _vp, _vp, _i32p]
 _lib.afx_last_error.argtypes = []
 _lib.afx_last_error.restype = ctypes.c_char_p
 _lib.afx_status_string.argtypes = [ctypes.c_int]
@@ -192,7 +222,8 @@ for _f in (_lib.afx_build_code, _lib.afx_build_code_fmt, _lib.afx_encode_bound, 
            _lib.afx_plan_residency, _lib.afx_debug_bounds_report, _lib.afx_prefill, _lib.afx_prefill_batch,
            _lib.afx_tile_order, _lib.afx_prefill_fused, _lib.afx_prefill_fused_batch,
            _lib.afx_prefill_fused_workspace, _lib.afx_kv_tables, _lib.afx_kv_write, _lib.afx_attention_workspace,
-           _lib.afx_attention_plan, _lib.afx_attention, _lib.afx_sample):
+           _lib.afx_attention_plan, _lib.afx_attention, _lib.afx_sample, _lib.afx_fp8_quantize, _lib.afx_fp8_product,
+           _lib.afx_rotary_plan, _lib.afx_rotate, _lib.afx_rotate_write):
     _f.restype = ctypes.c_int
 
 
@@ -508,6 +539,53 @@ def afx_prefill_fused_batch(descs, containers_dev, shapes, xs_dev, ys_dev, works
                                                                     _stream_handle(stream), _dev_ptr(status_dev)))
 
 
+_E4M3 = ("torch.uint8", "torch.float8_e4m3fn")
+
+
+def _rows(x, name: str, types) -> tuple:
+    """(address, row stride) of a CUDA matrix with contiguous rows."""
+    if not x.is_cuda or x.dim() != 2 or str(x.dtype) not in types or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA matrix with contiguous rows, of {', '.join(t.split('.')[1] for t in types)}")
+    return x.data_ptr(), x.stride(0)
+
+
+def _block_scales(scales, blocks: int, n: int, name: str) -> tuple:
+    if not scales.is_cuda or scales.dim() != 2 or str(scales.dtype) != "torch.float32" or tuple(scales.shape) != (blocks, n) or \
+            (n > 1 and scales.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA float32 matrix [{blocks}][{n}] with contiguous rows")
+    return scales.data_ptr(), scales.stride(0)
+
+
+def afx_fp8_quantize(x, q, scales, stream=None) -> None:
+    """Rounds x [tokens][cols] (bfloat16, float16 or float32, rows may be strided) to E4M3 in blocks of 128 columns: q
+    uint8 or float8_e4m3fn [tokens][cols or more] (the columns past cols are left as they are), scales float32
+    [ceil(cols / 128)][tokens]."""
+    px, pq = _rows(x, "x", tuple(_TYPES)), _rows(q, "q", _E4M3)
+    n, cols = x.shape
+    if q.shape[0] != n or q.shape[1] < cols:
+        raise ValueError("q must have a row of cols elements or more for each of x")
+    ps = _block_scales(scales, -(-cols // AFX_FP8_BLOCK), n, "scales")
+    _check("afx_fp8_quantize", _lib.afx_fp8_quantize(px[0], _TYPES[str(x.dtype)], px[1], n, cols, *pq, *ps, _stream_handle(stream)))
+
+
+def afx_fp8_product(w, w_scales, x, x_scales, y, stream=None, status_dev=None) -> None:
+    """y = x W^T: w [rows][cols] E4M3 (uint8 or float8_e4m3fn; what afx_decode restores of an E4M3 container) with
+    w_scales float32 [ceil(rows / 128)][ceil(cols / 128)], contiguous; x [tokens][cols or more] and x_scales
+    [ceil(cols / 128)][tokens] as afx_fp8_quantize writes them; y [tokens][rows] bfloat16, float16 or float32.  Rows of
+    w and x start on 16 bytes."""
+    pw, px, py = _rows(w, "w", _E4M3), _rows(x, "x", _E4M3), _rows(y, "y", tuple(_TYPES))
+    rows, cols = w.shape
+    n = x.shape[0]
+    if x.shape[1] < cols or tuple(y.shape) != (n, rows):
+        raise ValueError("x must have cols columns or more, and y must be [tokens][rows]")
+    blocks = -(-cols // AFX_FP8_BLOCK)
+    if str(w_scales.dtype) != "torch.float32" or tuple(w_scales.shape) != (-(-rows // AFX_FP8_BLOCK), blocks):
+        raise ValueError(f"w_scales must be a float32 matrix [{-(-rows // AFX_FP8_BLOCK)}][{blocks}]")
+    ps = _block_scales(x_scales, blocks, n, "x_scales")
+    _check("afx_fp8_product", _lib.afx_fp8_product(*pw, _dev_ptr(w_scales), rows, cols, *px, *ps, n, py[0], _TYPES[str(y.dtype)], py[1],
+                                                   _stream_handle(stream), _dev_ptr(status_dev)))
+
+
 def afx_plan_residency(tensors, device_budget_bytes: int, link_gbs: float, restore_gbs: float,
                        overlapped: bool = True) -> tuple[list[int], float, int]:
     """tensors: [(decoded_bytes, compressed_bytes)].  Returns (placements, step_ms, resident_bytes)."""
@@ -649,6 +727,91 @@ def afx_attention(args: afx_attention_args, q, out, workspace_dev, lse=None, str
     _check("afx_attention", _lib.afx_attention(
         ctypes.byref(args), *pq, *po, _float_ptr(lse, args.n_tokens * args.q_heads, "lse"), _dev_ptr(workspace_dev),
         workspace_dev.numel() * workspace_dev.element_size(), _stream_handle(stream), _dev_ptr(status_dev)))
+
+
+_TYPES = {"torch.bfloat16": AFX_TYPE_BF16, "torch.float16": AFX_TYPE_FP16, "torch.float32": AFX_TYPE_F32}
+
+
+def rotary(head_dim: int, rotary_dim: int | None = None, base: float = 10_000.0, sections=None, order: str = "blocks",
+           pairs: str = "halves", frequencies=None, amplitude: float = 1.0) -> afx_rotary:
+    """The plan of a rotation of heads' first rotary_dim elements (all by default), for afx_rotate and
+    afx_rotate_write.  pairs: "halves" (i and i + rotary_dim / 2) or "neighbours" (2 i and 2 i + 1).  sections: how
+    many pairs each axis turns, in the axes' order, together rotary_dim / 2 (one axis by default); order: "blocks" of
+    pairs, or "interleaved", an axis after the other while it has pairs left.  frequencies: radians a position for each
+    pair, instead of base ** (-2 i / rotary_dim)."""
+    rotary_dim = head_dim if rotary_dim is None else rotary_dim
+    n = rotary_dim // 2
+    sections = [n] if sections is None else [int(v) for v in sections]
+    if sum(sections) != n or min(sections, default=0) < 0:
+        raise ValueError(f"the sections' pairs must add up to {n}")
+    if order == "blocks":
+        axes = [a for a, count in enumerate(sections) for _ in range(count)]
+    elif order == "interleaved":
+        axes = [a for i in range(max(sections)) for a, count in enumerate(sections) if i < count]
+    else:
+        raise ValueError('order is "blocks" or "interleaved"')
+    if pairs not in ("halves", "neighbours"):
+        raise ValueError('pairs is "halves" or "neighbours"')
+    if frequencies is not None and len(frequencies) != n:
+        raise ValueError(f"there must be {n} frequencies")
+    plan = afx_rotary()
+    _check("afx_rotary_plan", _lib.afx_rotary_plan(
+        head_dim, rotary_dim, AFX_ROTARY_HALVES if pairs == "halves" else AFX_ROTARY_NEIGHBOURS, base,
+        (ctypes.c_double * n)(*[float(f) for f in frequencies]) if frequencies is not None else None, len(sections),
+        (ctypes.c_uint8 * n)(*axes), amplitude, ctypes.byref(plan)))
+    return plan
+
+
+def _positions(positions, plan: afx_rotary, n_tokens: int) -> tuple:
+    """(address, axis stride) of int32 positions: [n_tokens], or [axes][n_tokens]."""
+    rows = positions if positions.dim() == 2 else positions[None]
+    if not positions.is_cuda or str(positions.dtype) != "torch.int32" or rows.dim() != 2 or rows.shape[0] != plan.n_axes or \
+            rows.shape[1] != n_tokens or (n_tokens > 1 and rows.stride(1) != 1):
+        raise ValueError(f"positions must be a CUDA int32 tensor [{plan.n_axes}][{n_tokens}]")
+    return positions.data_ptr(), rows.stride(0) if plan.n_axes > 1 else n_tokens
+
+
+def _heads(x, dim: int, name: str, tokens: int | None = None) -> tuple:
+    """(address, token stride, head stride) of a CUDA tensor [tokens][heads][dim]."""
+    if not x.is_cuda or x.dim() != 3 or x.shape[2] != dim or str(x.dtype) not in _TYPES or (tokens is not None and x.shape[0] != tokens):
+        raise ValueError(f"{name} must be a CUDA tensor [tokens][heads][{dim}] of bfloat16, float16 or float32")
+    if x.stride(2) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return x.data_ptr(), x.stride(0), x.stride(1)
+
+
+def afx_rotate(plan: afx_rotary, positions, x, y, stream=None) -> None:
+    """y = x turned by the tokens' positions: x, y [tokens][heads][head_dim] (views allowed; y may be x), positions
+    int32 [tokens] or [axes][tokens]."""
+    px = _heads(x, plan.head_dim, "x")
+    py = _heads(y, plan.head_dim, "y", x.shape[0])
+    if x.shape != y.shape:
+        raise ValueError("x and y must have the same shape")
+    n = x.shape[0]
+    _check("afx_rotate", _lib.afx_rotate(ctypes.byref(plan), *_positions(positions, plan, n), n, px[0], _TYPES[str(x.dtype)], *px[1:],
+                                         x.shape[1], py[0], _TYPES[str(y.dtype)], *py[1:], _stream_handle(stream)))
+
+
+def afx_rotate_write(plan: afx_rotary, positions, q, k, v, q_out, cache: afx_kv_cache, slots, stream=None, status_dev=None) -> None:
+    """Turns q [tokens][q_heads][head_dim] into q_out (of the cache's type; may be q itself) and k
+    [tokens][kv_heads][head_dim] into the cache, with v, at slots (int32 [tokens]).  q, k and v have one type, bfloat16,
+    float16 or float32; q and q_out may both be None."""
+    dim, n = cache.head_dim, k.shape[0]
+    pk, pv = _heads(k, dim, "k"), _heads(v, dim, "v", n)
+    if k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads or v.dtype != k.dtype:
+        raise ValueError(f"k and v must have {cache.kv_heads} heads and one type")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out are both given, or both None")
+    pq = po = (0, 0, 0)
+    heads = 0
+    if q is not None:
+        pq, po, heads = _heads(q, dim, "q", n), _heads(q_out, dim, "q_out", n), q.shape[1]
+        if q.dtype != k.dtype or q_out.shape != q.shape or _KV_FORMATS.get(str(q_out.dtype)) != cache.format:
+            raise ValueError("q must have the type of k and v, and q_out the shape of q and the cache's type")
+    qkv = afx_qkv(pq[0], pk[0], pv[0], *pq[1:], *pk[1:], *pv[1:], _TYPES[str(k.dtype)], heads, n, 0)
+    _check("afx_rotate_write", _lib.afx_rotate_write(
+        ctypes.byref(plan), *_positions(positions, plan, n), ctypes.byref(qkv), *po, ctypes.byref(cache),
+        _int32_ptr(slots, n, "slots"), _stream_handle(stream), _dev_ptr(status_dev)))
 
 
 _LOGITS = {"torch.bfloat16": AFX_LOGITS_BF16, "torch.float16": AFX_LOGITS_FP16, "torch.float32": AFX_LOGITS_F32}
