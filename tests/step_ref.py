@@ -91,3 +91,76 @@ def rotate(x, positions, frequencies, axis_of_pair, rotary_dim, pairs, amplitude
         both = abs(amplitude) * (src[..., a].abs() + src[..., b].abs())
         reach[..., a] = reach[..., b] = both
     return y, reach
+
+
+def shares(z, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, near=0.0):
+    """(p, sure, doubtful, amount): every token's share of what the parameters keep of logits z, in 64 bits; sure: no min-p boundary
+    came within `near`, relative, of the other side; doubtful: the tokens around the top-p boundary that float32 weights may
+    keep or not, amount their share together.  A
+    weight e^y is off by 3 |y| 2^-24 (the difference, the reciprocal of T and their product are rounded) and 2^-22
+    (the exponential), relative, so a running sum's share of the whole by at most twice the weights' mean of that, and
+    2^-44 a token; half as much again is allowed for."""
+    z = np.where(np.isnan(z), -np.inf, z.astype(np.float64))
+    p = np.zeros(len(z))
+    m = z.max()
+    if m == -np.inf:
+        return p, True, set(), 0.0
+    if not temperature > 0:
+        p[int(np.argmax(z))] = 1.0
+        return p, True, set(), 0.0
+    with np.errstate(invalid="ignore"):
+        y = np.where(z == m, 0.0, np.where(z == -np.inf, -np.inf, (z - m) / temperature))
+    w = np.exp(y)
+    order = np.lexsort((np.arange(len(z)), -z))
+    if top_k > 0:
+        order = order[:top_k]
+    sure, doubtful, amount = True, set(), 0.0
+    keep = np.ones(len(order), bool)
+    if top_p < 1:
+        before = (np.cumsum(w[order]) - w[order]) / w[order].sum()
+        keep &= before < top_p
+        share = w[order] / w[order].sum()
+        off = 2 * (share * (3 * np.where(share > 0, np.abs(y[order]), 0.0) * 2.0 ** -24 + 2.0 ** -22)).sum() + len(order) * 2.0 ** -44
+        close = np.abs(before - top_p) <= 1.5 * off
+        doubtful, amount = set(order[close].tolist()), float(share[close].sum()) / top_p
+    if min_p > 0:
+        keep &= w[order] >= min(min_p, 1.0)
+        sure &= np.abs(w[order] / min(min_p, 1.0) - 1).min() > near
+    keep[0] = True
+    p[order[keep]] = w[order[keep]] / w[order[keep]].sum()
+    return p, bool(sure), doubtful, amount
+
+
+def verify(p_rows, q_rows, drafts, u, draw_u, nears, doubtful):
+    """(drafts that stand, the tokens that may be drawn behind them, sure) of one request: p_rows and q_rows the target's
+    and the drafts' shares row by row (q_rows None: drafts that were not drawn); sure: no draft's test came within the
+    row's `near` of the other result or was about one of a row's doubtful tokens.  A token may be drawn if draw_u is within `near` of
+    its part of the running sum, of what is left over where that is a part.  -1: nothing to draw from."""
+    sure, out = True, []
+    rest, near = p_rows[len(drafts)], nears[len(drafts)]
+    for i, d in enumerate(drafts):
+        p, near = p_rows[i], nears[i]
+        if d < 0 or d >= len(p):
+            rest = p
+            break
+        sure &= d not in doubtful[i]
+        q = q_rows[i] if q_rows is not None else (np.arange(len(p)) == d) * 1.0
+        sure &= abs(u[i] * q[d] - p[d]) > near * max(p[d], u[i] * q[d]) or p[d] == q[d] == 0
+        if u[i] * q[d] < p[d]:
+            out.append(d)
+            near = nears[len(drafts)]
+            continue
+        rest = np.maximum(p - q, 0.0)
+        left = rest.sum()
+        if left == 0:
+            rest = p
+        else:  # the differences' errors against their sum
+            near = near / min(left, 1.0)
+        break
+    if rest.sum() == 0:
+        return out, {-1}, sure
+    run = np.cumsum(rest) / rest.sum()
+    before = np.concatenate([[0.0], run[:-1]])
+    may = (before <= draw_u + near) & (draw_u < run + near) & (rest > 0)
+    may[np.nonzero(rest)[0][-1]] |= draw_u >= 1 - near
+    return out, set(np.nonzero(may)[0].tolist()) | doubtful[len(out)], bool(sure)

@@ -71,6 +71,25 @@ def test_rotation_arguments(afx):
         afx.afx_rotate(plan, torch.zeros(2, dtype=torch.int32), torch.zeros((2, 1, 64)), torch.zeros((2, 1, 64)))
 
 
+def test_verify_arguments(afx):
+    lib, E = afx._lib, afx.AFX_E_ARG
+    size = ctypes.c_uint64(7)
+    for n, r in ((0, 0), (4, 16_385), ((1 << 24) + 1, 1)):
+        assert lib.afx_verify_workspace(n, r, ctypes.byref(size)) == E and size.value == 7
+    assert lib.afx_verify_workspace(10, 2, None) == E
+    assert afx.afx_verify_workspace(1000, 3) >= 64_000
+    none = afx.afx_sampling(None, None, None, None)
+
+    def verify(logits=P, draft=P, stride=8, kind=2, draft_kind=2, vocab=8, requests=1, n=2, starts=P, workspace=P):
+        a = afx.afx_verify_args(logits, draft, stride, stride, kind, draft_kind, vocab, requests, n, 0, starts, P, none, none, P, P)
+        return lib.afx_verify(ctypes.byref(a), P, P, None, workspace, 1 << 20, None, None)
+
+    assert lib.afx_verify(None, P, P, None, P, 1 << 20, None, None) == E
+    for bad in ({"kind": 3}, {"draft_kind": 3}, {"vocab": 0}, {"vocab": 524_289}, {"requests": 0}, {"requests": 16_385}, {"n": (1 << 24) + 1}, {"stride": 7},
+                {"starts": None}, {"logits": None}, {"workspace": None}, {}):  # the last: host memory
+        assert verify(**bad) == E
+
+
 def test_rounding_s_reference():
     """The tests' own rounding to E4M3 against torch's conversion."""
     x = torch.cat([torch.linspace(-448, 448, 4001), torch.exp2(torch.linspace(-14, 8.8, 999)), torch.tensor(ref.e4m3_values()[:127]).float()])
@@ -85,7 +104,7 @@ def test_structures_have_the_header_s_layout(afx, tmp_path):
     gcc = shutil.which("gcc")
     if not gcc:
         pytest.skip("gcc not available")
-    names = ["afx_rotary", "afx_qkv"]
+    names = ["afx_rotary", "afx_qkv", "afx_sampling", "afx_verify_args"]
     fields = [(s, f) for s in names for f, _ in getattr(afx, s)._fields_]
     lines = ['#include "afx.h"', "#include <stddef.h>", "#include <stdio.h>", "int main(void) {"]
     lines += [f'printf("%zu\\n", sizeof({s}));' for s in names] + [f'printf("%zu\\n", offsetof({s}, {f}));' for s, f in fields]

@@ -193,6 +193,23 @@ class afx_qkv(ctypes.Structure):
     ]
 
 
+class afx_sampling(ctypes.Structure):
+    _fields_ = [
+        ("temperature_dev", ctypes.c_void_p), ("top_k_dev", ctypes.c_void_p), ("top_p_dev", ctypes.c_void_p),
+        ("min_p_dev", ctypes.c_void_p),
+    ]
+
+
+class afx_verify_args(ctypes.Structure):
+    _fields_ = [
+        ("logits_dev", ctypes.c_void_p), ("draft_logits_dev", ctypes.c_void_p), ("row_stride", ctypes.c_uint64),
+        ("draft_row_stride", ctypes.c_uint64), ("type", ctypes.c_uint32), ("draft_type", ctypes.c_uint32),
+        ("vocab", ctypes.c_uint32), ("n_requests", ctypes.c_uint32), ("n_tokens", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+        ("starts_dev", ctypes.c_void_p), ("tokens_dev", ctypes.c_void_p), ("sampling", afx_sampling),
+        ("draft_sampling", afx_sampling), ("u_dev", ctypes.c_void_p), ("draw_u_dev", ctypes.c_void_p),
+    ]
+
+
 AFX_FP8_BLOCK = 128
 AFX_TYPE_BF16, AFX_TYPE_FP16, AFX_TYPE_F32 = 0, 1, 2
 AFX_KV_MAX_REQUESTS = 16384
@@ -212,6 +229,8 @@ _lib.afx_rotary_plan.argtypes = [_u32, _u32, _u32, ctypes.c_double, ctypes.POINT
 _lib.afx_rotate.argtypes = [ctypes.POINTER(afx_rotary), _vp, _u64, _u32, _vp, _u32, _u64, _u64, _u32, _vp, _u32, _u64, _u64, _vp]
 _lib.afx_rotate_write.argtypes = [ctypes.POINTER(afx_rotary), _vp, _u64, ctypes.POINTER(afx_qkv), _vp, _u64, _u64,
                                   ctypes.POINTER(afx_kv_cache), _vp, _vp, _i32p]
+_lib.afx_verify_workspace.argtypes = [_u32, _u32, ctypes.POINTER(ctypes.c_uint64)]
+_lib.afx_verify.argtypes = [ctypes.POINTER(afx_verify_args), _vp, _vp, _vp, _vp, _u64, _vp, _i32p]
 _lib.afx_last_error.argtypes = []
 _lib.afx_last_error.restype = ctypes.c_char_p
 _lib.afx_status_string.argtypes = [ctypes.c_int]
@@ -223,7 +242,7 @@ for _f in (_lib.afx_build_code, _lib.afx_build_code_fmt, _lib.afx_encode_bound, 
            _lib.afx_tile_order, _lib.afx_prefill_fused, _lib.afx_prefill_fused_batch,
            _lib.afx_prefill_fused_workspace, _lib.afx_kv_tables, _lib.afx_kv_write, _lib.afx_attention_workspace,
            _lib.afx_attention_plan, _lib.afx_attention, _lib.afx_sample, _lib.afx_fp8_quantize, _lib.afx_fp8_product,
-           _lib.afx_rotary_plan, _lib.afx_rotate, _lib.afx_rotate_write):
+           _lib.afx_rotary_plan, _lib.afx_rotate, _lib.afx_rotate_write, _lib.afx_verify_workspace, _lib.afx_verify):
     _f.restype = ctypes.c_int
 
 
@@ -539,12 +558,27 @@ def afx_prefill_fused_batch(descs, containers_dev, shapes, xs_dev, ys_dev, works
                                                                     _stream_handle(stream), _dev_ptr(status_dev)))
 
 
-_E4M3 = ("torch.uint8", "torch.float8_e4m3fn")
+_TYPES = {"torch.bfloat16": AFX_TYPE_BF16, "torch.float16": AFX_TYPE_FP16, "torch.float32": AFX_TYPE_F32}
+_E4M3 = {"torch.uint8": 0, "torch.float8_e4m3fn": 0}
+_names: dict = {}  # of torch's types: a lookup where str() would make the name anew each time
+
+
+def _name_of(x) -> str:
+    kind = x.dtype
+    name = _names.get(kind)
+    if name is None:
+        name = _names[kind] = str(kind)
+    return name
+
+
+def _type_of(x) -> int:
+    """AFX_TYPE_* of a tensor that has been checked to be of one of them."""
+    return _TYPES[_name_of(x)]
 
 
 def _rows(x, name: str, types) -> tuple:
     """(address, row stride) of a CUDA matrix with contiguous rows."""
-    if not x.is_cuda or x.dim() != 2 or str(x.dtype) not in types or (x.shape[1] > 1 and x.stride(1) != 1):
+    if not x.is_cuda or x.dim() != 2 or _name_of(x) not in types or (x.stride(1) != 1 and x.shape[1] > 1):
         raise ValueError(f"{name} must be a CUDA matrix with contiguous rows, of {', '.join(t.split('.')[1] for t in types)}")
     return x.data_ptr(), x.stride(0)
 
@@ -560,12 +594,12 @@ def afx_fp8_quantize(x, q, scales, stream=None) -> None:
     """Rounds x [tokens][cols] (bfloat16, float16 or float32, rows may be strided) to E4M3 in blocks of 128 columns: q
     uint8 or float8_e4m3fn [tokens][cols or more] (the columns past cols are left as they are), scales float32
     [ceil(cols / 128)][tokens]."""
-    px, pq = _rows(x, "x", tuple(_TYPES)), _rows(q, "q", _E4M3)
+    px, pq = _rows(x, "x", _TYPES), _rows(q, "q", _E4M3)
     n, cols = x.shape
     if q.shape[0] != n or q.shape[1] < cols:
         raise ValueError("q must have a row of cols elements or more for each of x")
     ps = _block_scales(scales, -(-cols // AFX_FP8_BLOCK), n, "scales")
-    _check("afx_fp8_quantize", _lib.afx_fp8_quantize(px[0], _TYPES[str(x.dtype)], px[1], n, cols, *pq, *ps, _stream_handle(stream)))
+    _check("afx_fp8_quantize", _lib.afx_fp8_quantize(px[0], _type_of(x), px[1], n, cols, *pq, *ps, _stream_handle(stream)))
 
 
 def afx_fp8_product(w, w_scales, x, x_scales, y, stream=None, status_dev=None) -> None:
@@ -573,16 +607,16 @@ def afx_fp8_product(w, w_scales, x, x_scales, y, stream=None, status_dev=None) -
     w_scales float32 [ceil(rows / 128)][ceil(cols / 128)], contiguous; x [tokens][cols or more] and x_scales
     [ceil(cols / 128)][tokens] as afx_fp8_quantize writes them; y [tokens][rows] bfloat16, float16 or float32.  Rows of
     w and x start on 16 bytes."""
-    pw, px, py = _rows(w, "w", _E4M3), _rows(x, "x", _E4M3), _rows(y, "y", tuple(_TYPES))
+    pw, px, py = _rows(w, "w", _E4M3), _rows(x, "x", _E4M3), _rows(y, "y", _TYPES)
     rows, cols = w.shape
     n = x.shape[0]
     if x.shape[1] < cols or tuple(y.shape) != (n, rows):
         raise ValueError("x must have cols columns or more, and y must be [tokens][rows]")
     blocks = -(-cols // AFX_FP8_BLOCK)
-    if str(w_scales.dtype) != "torch.float32" or tuple(w_scales.shape) != (-(-rows // AFX_FP8_BLOCK), blocks):
+    if _name_of(w_scales) != "torch.float32" or tuple(w_scales.shape) != (-(-rows // AFX_FP8_BLOCK), blocks):
         raise ValueError(f"w_scales must be a float32 matrix [{-(-rows // AFX_FP8_BLOCK)}][{blocks}]")
     ps = _block_scales(x_scales, blocks, n, "x_scales")
-    _check("afx_fp8_product", _lib.afx_fp8_product(*pw, _dev_ptr(w_scales), rows, cols, *px, *ps, n, py[0], _TYPES[str(y.dtype)], py[1],
+    _check("afx_fp8_product", _lib.afx_fp8_product(*pw, _dev_ptr(w_scales), rows, cols, *px, *ps, n, py[0], _type_of(y), py[1],
                                                    _stream_handle(stream), _dev_ptr(status_dev)))
 
 
@@ -729,8 +763,6 @@ def afx_attention(args: afx_attention_args, q, out, workspace_dev, lse=None, str
         workspace_dev.numel() * workspace_dev.element_size(), _stream_handle(stream), _dev_ptr(status_dev)))
 
 
-_TYPES = {"torch.bfloat16": AFX_TYPE_BF16, "torch.float16": AFX_TYPE_FP16, "torch.float32": AFX_TYPE_F32}
-
 
 def rotary(head_dim: int, rotary_dim: int | None = None, base: float = 10_000.0, sections=None, order: str = "blocks",
            pairs: str = "halves", frequencies=None, amplitude: float = 1.0) -> afx_rotary:
@@ -773,7 +805,7 @@ def _positions(positions, plan: afx_rotary, n_tokens: int) -> tuple:
 
 def _heads(x, dim: int, name: str, tokens: int | None = None) -> tuple:
     """(address, token stride, head stride) of a CUDA tensor [tokens][heads][dim]."""
-    if not x.is_cuda or x.dim() != 3 or x.shape[2] != dim or str(x.dtype) not in _TYPES or (tokens is not None and x.shape[0] != tokens):
+    if not x.is_cuda or x.dim() != 3 or x.shape[2] != dim or _name_of(x) not in _TYPES or (tokens is not None and x.shape[0] != tokens):
         raise ValueError(f"{name} must be a CUDA tensor [tokens][heads][{dim}] of bfloat16, float16 or float32")
     if x.stride(2) != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
@@ -788,8 +820,8 @@ def afx_rotate(plan: afx_rotary, positions, x, y, stream=None) -> None:
     if x.shape != y.shape:
         raise ValueError("x and y must have the same shape")
     n = x.shape[0]
-    _check("afx_rotate", _lib.afx_rotate(ctypes.byref(plan), *_positions(positions, plan, n), n, px[0], _TYPES[str(x.dtype)], *px[1:],
-                                         x.shape[1], py[0], _TYPES[str(y.dtype)], *py[1:], _stream_handle(stream)))
+    _check("afx_rotate", _lib.afx_rotate(ctypes.byref(plan), *_positions(positions, plan, n), n, px[0], _type_of(x), *px[1:],
+                                         x.shape[1], py[0], _type_of(y), *py[1:], _stream_handle(stream)))
 
 
 def afx_rotate_write(plan: afx_rotary, positions, q, k, v, q_out, cache: afx_kv_cache, slots, stream=None, status_dev=None) -> None:
@@ -808,7 +840,7 @@ def afx_rotate_write(plan: afx_rotary, positions, q, k, v, q_out, cache: afx_kv_
         pq, po, heads = _heads(q, dim, "q", n), _heads(q_out, dim, "q_out", n), q.shape[1]
         if q.dtype != k.dtype or q_out.shape != q.shape or _KV_FORMATS.get(str(q_out.dtype)) != cache.format:
             raise ValueError("q must have the type of k and v, and q_out the shape of q and the cache's type")
-    qkv = afx_qkv(pq[0], pk[0], pv[0], *pq[1:], *pk[1:], *pv[1:], _TYPES[str(k.dtype)], heads, n, 0)
+    qkv = afx_qkv(pq[0], pk[0], pv[0], *pq[1:], *pk[1:], *pv[1:], _type_of(k), heads, n, 0)
     _check("afx_rotate_write", _lib.afx_rotate_write(
         ctypes.byref(plan), *_positions(positions, plan, n), ctypes.byref(qkv), *po, ctypes.byref(cache),
         _int32_ptr(slots, n, "slots"), _stream_handle(stream), _dev_ptr(status_dev)))
@@ -832,6 +864,51 @@ def afx_sample(logits, u, tokens, logprobs=None, temperature=None, top_k=None, t
         _float_ptr(temperature, rows, "temperature"), _int32_ptr(top_k, rows, "top_k") if top_k is not None else 0,
         _float_ptr(top_p, rows, "top_p"), _float_ptr(min_p, rows, "min_p"), _float_ptr(u, rows, "u"),
         _int32_ptr(tokens, rows, "tokens"), _float_ptr(logprobs, rows, "logprobs"), _stream_handle(stream)))
+
+
+def afx_verify_workspace(n_tokens: int, n_requests: int) -> int:
+    """Bytes of device workspace that afx_verify needs for so many rows and requests."""
+    v = ctypes.c_uint64(0)
+    _check("afx_verify_workspace", _lib.afx_verify_workspace(n_tokens, n_requests, ctypes.byref(v)))
+    return int(v.value)
+
+
+def _sampling(params, requests: int) -> afx_sampling:
+    p = params or {}
+    if not p.keys() <= {"temperature", "top_k", "top_p", "min_p"}:
+        raise ValueError("parameters are temperature, top_k, top_p and min_p")
+    top_k = p.get("top_k")
+    return afx_sampling(_float_ptr(p.get("temperature"), requests, "temperature"),
+                        _int32_ptr(top_k, requests, "top_k") if top_k is not None else 0,
+                        _float_ptr(p.get("top_p"), requests, "top_p"), _float_ptr(p.get("min_p"), requests, "min_p"))
+
+
+def afx_verify(logits, tokens, starts, u, draw_u, out_tokens, counts, workspace_dev, params=None, draft_logits=None,
+               draft_params=None, logprobs=None, stream=None, status_dev=None) -> None:
+    """How many of each request's drafts stand, and the token behind them: logits CUDA [rows][vocab] and tokens int32
+    [rows] of a step's rows (row t was fed tokens[t] and decides on tokens[t + 1]), starts int32 [requests + 1],
+    draft_logits [rows][vocab] the ones the drafts were drawn from (None: they were not drawn), u float32 [rows] and
+    draw_u [requests] in [0, 1).  params, draft_params: dicts of temperature, top_p, min_p (float32 [requests]) and
+    top_k (int32 [requests]), each optional, as for afx_sample.  Written: out_tokens int32 [rows], counts int32
+    [requests], logprobs float32 [rows] (optional)."""
+    requests = starts.numel() - 1
+    pl = _rows(logits, "logits", _TYPES)
+    rows, vocab = logits.shape
+    pd, draft_type = (0, 0), 0
+    if draft_logits is not None:
+        pd, draft_type = _rows(draft_logits, "draft_logits", _TYPES), _type_of(draft_logits)
+        if draft_logits.shape != logits.shape:
+            raise ValueError("draft_logits must have the shape of logits")
+    if u is None or draw_u is None:
+        raise ValueError("u and draw_u must hold one number in [0, 1) a row and a request")
+    args = afx_verify_args(pl[0], pd[0], pl[1], pd[1], _type_of(logits), draft_type, vocab, requests, rows, 0,
+                           _int32_ptr(starts, requests + 1, "starts"), _int32_ptr(tokens, rows, "tokens"),
+                           _sampling(params, requests), _sampling(draft_params, requests), _float_ptr(u, rows, "u"),
+                           _float_ptr(draw_u, requests, "draw_u"))
+    _check("afx_verify", _lib.afx_verify(
+        ctypes.byref(args), _int32_ptr(out_tokens, rows, "out_tokens"), _int32_ptr(counts, requests, "counts"),
+        _float_ptr(logprobs, rows, "logprobs"), _dev_ptr(workspace_dev), workspace_dev.numel() * workspace_dev.element_size(),
+        _stream_handle(stream), _dev_ptr(status_dev)))
 
 
 def afx_debug_bounds_report() -> tuple[int, bool]:

@@ -39,9 +39,10 @@
 // 512 rows, 311 MB, 118 (2.6 TB/s), 192, 221 and 615.
 #include <cooperative_groups.h>
 
+#include <type_traits>
 #include <utility>
 
-#include "afx_serving.cuh"
+#include "afx_sample.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -56,13 +57,11 @@ static_assert(kBins == kThreads, "a bin a thread");
 constexpr uint32_t kListMax = 2048;    // tokens that one CTA sorts
 constexpr uint32_t kPer = kListMax / kThreads;
 constexpr uint32_t kTopMax = 1024;     // top-k that goes by the threads' maxima
-constexpr uint32_t kMaxCluster = 16;
 constexpr uint32_t kTooMany = 1u << 26;
 constexpr uint32_t kShort = 256;       // tokens that are ordered pair by pair
 constexpr int kCuts = 2;               // weights above e^-4 and e^-8 tell how far down top-p reaches
 constexpr uint32_t kQueue = 160;       // tokens a warp has found and not yet dealt with: 31 and 128 more
 constexpr float kRange = 30.5f;        // e^-30.5 < 2^-44: no mass below m - 30.5 T
-constexpr float kMassOne = 17592186044416.0f;  // 2^44
 constexpr float kMostF = 3.40282347e38f;       // the largest float32
 constexpr float kLeastT = 3e-39f;              // 1 / T is finite from here on (the maximum's weight is e^(0 / T))
 
@@ -75,6 +74,14 @@ struct SampleArgs {
     float* logprobs;
     uint32_t vocab, slice, run, wide;  // run: tokens of a warp
     uint32_t rows, ordered;
+};
+
+// A verification's rows: r < rows of the first side, then of the second.
+struct RecordArgs {
+    Side side[2];
+    const int32_t *starts, *tokens;
+    uint32_t n_requests, rows, skip, vocab, slice, run;  // skip: rows before the launch's first
+    uint32_t wide[2];
 };
 
 struct alignas(16) Shared {
@@ -111,19 +118,6 @@ struct alignas(16) Shared {
 
 static_assert(2 * (sizeof(Shared) + 19008 * sizeof(float) + 1024) <= 228 * 1024, "two CTAs an SM at 152,064 tokens over eight");
 
-// The order of float32 as unsigned integers.
-__device__ __forceinline__ uint32_t order_key(float z) {
-    const uint32_t b = __float_as_uint(z);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-}
-// A token's place in the order: larger comes first; ties by lower index.
-__device__ __forceinline__ uint64_t place(float z, uint32_t index) {
-    return static_cast<uint64_t>(order_key(z)) << 32 | (0xFFFFFFFFu - index);
-}
-
 struct Row {
     float top, inv_t, step;  // m, 1 / T, bins a unit of z
     // y and w of a logit (top is finite, inv_t above 0); w as an integer of 2^-44
@@ -135,27 +129,6 @@ struct Row {
         if (z == top) return 0;
         const float b = (top - z) * step;
         return b < static_cast<float>(kBins - 1) ? static_cast<uint32_t>(b) : kBins - 1;
-    }
-};
-
-// A sum of weights as integers of 2^-44, without a conversion a weight: adding
-// 2 leaves the weight's multiple of 2^-22 in the sum's last bits; what is
-// left, at most 2^-23, added to 1.5 * 2^-21 and rounded down, leaves its
-// multiple of 2^-44 there.  The bits are added up as they are and the
-// constants taken off at the end (up to 1023 weights).
-struct MassSum {
-    uint32_t hi = 0, lo = 0, n = 0;
-    static constexpr float kHi = 2.0f, kLo = 1.5f / 2097152.0f;
-    __device__ __forceinline__ void add(float w) {
-        const float t = __fadd_rn(w, kHi);
-        hi += __float_as_uint(t);
-        lo += __float_as_uint(__fadd_rd(__fsub_rn(w, __fsub_rn(t, kHi)), kLo));
-        ++n;
-    }
-    __device__ __forceinline__ uint64_t total() const {
-        const uint32_t h = hi - n * __float_as_uint(kHi);
-        const int32_t l = static_cast<int32_t>(lo - n * __float_as_uint(kLo));
-        return (static_cast<uint64_t>(h) << 22) + static_cast<uint64_t>(static_cast<int64_t>(l));
     }
 };
 
@@ -172,43 +145,6 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
     return v;
 }
-__device__ __forceinline__ uint64_t warp_inclusive(uint64_t v) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
-}
-
-template <typename T>
-__device__ __forceinline__ float load_logit(const T* p);
-template <>
-__device__ __forceinline__ float load_logit<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-template <>
-__device__ __forceinline__ float load_logit<__half>(const __half* p) { return __half2float(*p); }
-
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void load4(const __half* p, float (&x)[4]) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-    x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
-}
-
-// NaN counts as masked (a maximum passes over it); -0 and +0 are one value.
-__device__ __forceinline__ float clean(float z) { return fmaxf(z, -INFINITY) + 0.0f; }
-
 // Sums the CTAs' histograms into every CTA's all_count (all_mass, or bins from
 // coarse and fine), which
 // nobody may be reading; before it, a cluster barrier behind the counting.
@@ -570,11 +506,6 @@ struct Want {  // a row's parameters
     double u;
 };
 
-// floor(u * total), below total.
-__device__ __forceinline__ uint64_t aim_of(double u, uint64_t total) {
-    const double scaled = u > 0.0 ? u * static_cast<double>(total) : 0.0;
-    return scaled < static_cast<double>(total) ? min(static_cast<uint64_t>(scaled), total - 1) : total - 1;
-}
 // ceil(p * mass), from 1 to mass: what has to be reached.
 __device__ __forceinline__ uint64_t limit_of(float p, uint64_t mass) {
     const double aim = ceil(static_cast<double>(p) * static_cast<double>(mass));
@@ -587,11 +518,33 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, uint32_t r, con
     if (a.logprobs) a.logprobs[r] = row.scaled(z) - logf(static_cast<float>(total) * (1.0f / kMassOne));
 }
 
+__device__ __forceinline__ void write_record(Kept* to, const Row& row, float least, bool infinite, uint64_t threshold, uint64_t total) {
+    Kept k;
+    k.top = row.top;
+    k.inv_t = row.inv_t;
+    k.least = least;
+    k.infinite = infinite;
+    k.threshold = threshold;
+    k.total = total;
+    *to = k;
+}
+// The record of a list's kept tokens, from the least of the threads' places; all of the CTA.  sh.threshold holds ~0.
+__device__ void write_least_place(Shared& sh, uint64_t mine, Kept* to, const Row& row, const Want& want, uint64_t total, bool infinite) {
+    const uint64_t least = ~warp_max(~mine);
+    if (threadIdx.x % 32 == 0) atomicMin(reinterpret_cast<unsigned long long*>(&sh.threshold), static_cast<unsigned long long>(least));
+    __syncthreads();
+    if (threadIdx.x == 0) write_record(to, row, want.least, infinite, sh.threshold, total);
+}
+
 // list[0 .. n) holds all tokens that can be kept: the rest of the row's
 // choice, by one CTA.  row_mass: what top-p is a share of, 0 for the mass of
 // what top-k keeps.
-__device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row row, const Want& want, uint32_t n, uint64_t row_mass) {
+// kRecord: nothing is drawn; the record of what is kept is written to *record.
+template <bool kRecord>
+__device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row row, const Want& want, uint32_t n, uint64_t row_mass, Kept* record,
+                               bool infinite) {
     const uint32_t k = want.k ? want.k : n;
+    if (kRecord && threadIdx.x == 0) sh.threshold = ~uint64_t{0};  // barriers follow
     if (n <= kShort) {
         const Element el(n);
         const bool real = el.e < n, one = real && el.part == 0;
@@ -615,6 +568,10 @@ __device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row 
         const uint64_t kept = by_k && before < limit && weight >= want.least ? w : 0;
         if (one) sh.bins[el.e] = kept;
         block_exclusive(sh, one ? kept : 0, &total);  // a barrier as well
+        if constexpr (kRecord) {
+            write_least_place(sh, one && kept ? mine : ~uint64_t{0}, record, row, want, total, infinite);
+            return;
+        }
         before = 0;
 #pragma unroll 4
         for (uint32_t j = el.part; j < n; j += el.parts)  // lower indexes have larger low halves
@@ -650,14 +607,20 @@ __device__ void draw_from_list(const SampleArgs& a, uint32_t r, Shared& sh, Row 
         threshold = sh.found_key > threshold ? sh.found_key : threshold;
     }
     sum = 0;
+    uint64_t least_place = ~uint64_t{0};
 #pragma unroll
     for (uint32_t j = 0; j < kPer; ++j) {
         mass[j] = p[j] >= threshold && mass[j] && weight(j) >= want.least ? mass[j] : 0;
         sum += mass[j];
+        if (kRecord && mass[j] && p[j] < least_place) least_place = p[j];
         p[j] = (p[j] & 0xFFFFFFFFu) << 32 | (p[j] >> 32);  // by index, the lowest first
     }
     uint64_t total;
     block_exclusive(sh, sum, &total);
+    if constexpr (kRecord) {
+        write_least_place(sh, least_place, record, row, want, total, infinite);
+        return;
+    }
     const uint32_t share = ceil_div(a.vocab, kBins);
     reach(sh, p, mass, 0, aim_of(want.u, total) + 1, [&](uint64_t q) { return (0xFFFFFFFFu - static_cast<uint32_t>(q >> 32)) / share; });
 #pragma unroll
@@ -709,14 +672,26 @@ __device__ uint32_t row_in_order(const SampleArgs& a, Shared& sh, uint32_t place
     return sh.short_n;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+// Args: SampleArgs, or RecordArgs for a verification's rows, whose logits and
+// parameters are found by the row's side and request, and of which the record
+// is kept instead of a token drawn.
+template <typename T, typename Args>
+__device__ __forceinline__ void row_choice(const Args& args) {
+    constexpr bool kRecord = std::is_same<Args, RecordArgs>::value;
     extern __shared__ __align__(16) uint8_t raw[];
     Shared& sh = *reinterpret_cast<Shared*>(raw);
     float* z = reinterpret_cast<float*>(raw + sizeof(Shared));
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    SampleArgs a;
+    Kept* record = nullptr;
+    if constexpr (kRecord) {
+        a.vocab = args.vocab, a.slice = args.slice, a.run = args.run;
+        a.u = nullptr, a.tokens = nullptr, a.logprobs = nullptr;
+    } else {
+        a = args;
+    }
     const uint32_t base = min(a.vocab, rank * a.slice), n = min(a.vocab - base, a.slice);
     // this warp's run: a multiple of 128 tokens long, so that a lane's four are aligned
     const uint32_t run0 = min(n, warp * a.run), run1 = min(n, run0 + a.run);
@@ -724,13 +699,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     wait_for_earlier();
     let_next_start();
     uint32_t r = blockIdx.x / ranks;
-    if (a.ordered) r = row_in_order(a, sh, r);
+    uint32_t of_params = r;  // where the row's parameters stand
+    if constexpr (kRecord) {
+        r += args.skip;
+        const bool second = r >= args.rows;
+        const Side& side = args.side[second];
+        if (second) r -= args.rows;
+        // the request whose rows r is among: as many before it as end by r
+        of_params = 0;
+        for (uint32_t i = 0; i < args.n_requests; i += kThreads)
+            of_params += __syncthreads_count(i + threadIdx.x < args.n_requests && __ldg(args.starts + 1 + i + threadIdx.x) <= static_cast<int32_t>(r));
+        const bool used = of_params < args.n_requests &&
+                          (!second || draft_of(args.tokens, static_cast<int32_t>(r), min(__ldg(args.starts + 1 + of_params), static_cast<int32_t>(args.rows)), args.vocab) >= 0);
+        if (!used) {  // the whole cluster
+            cluster.barrier_wait(std::move(started));
+            return;
+        }
+        a.logits = side.logits, a.row_stride = side.row_stride, a.wide = args.wide[second];
+        a.temperature = side.temperature, a.top_k = side.top_k, a.top_p = side.top_p, a.min_p = side.min_p;
+        record = side.kept + r;
+    } else {
+        if (a.ordered) of_params = r = row_in_order(a, sh, r);
+    }
     const T* src = static_cast<const T*>(a.logits) + r * a.row_stride + base;
 
     // the row's parameters, under way with the logits
-    float temp = a.temperature ? __ldg(a.temperature + r) : 1.0f;
-    const int32_t top_k = a.top_k ? __ldg(a.top_k + r) : 0;
-    const float top_p = a.top_p ? __ldg(a.top_p + r) : 1.0f, min_p = a.min_p ? __ldg(a.min_p + r) : 0.0f, u = __ldg(a.u + r);
+    float temp = a.temperature ? __ldg(a.temperature + of_params) : 1.0f;
+    const int32_t top_k = a.top_k ? __ldg(a.top_k + of_params) : 0;
+    const float top_p = a.top_p ? __ldg(a.top_p + of_params) : 1.0f, min_p = a.min_p ? __ldg(a.min_p + of_params) : 0.0f,
+                u = kRecord ? 0.0f : __ldg(a.u + r);
 
     // pass 1: the slice into shared memory, NaN as minus infinity and -0 as 0; the thread's maximum
     float mine = -INFINITY;
@@ -797,8 +794,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     for (int d = 16; d; d >>= 1) row.top = fmaxf(row.top, __shfl_xor_sync(0xFFFFFFFFu, row.top, d));
     if (row.top == -INFINITY) {  // nothing to draw from
         if (rank == 0 && threadIdx.x == 0) {
-            a.tokens[r] = -1;
-            if (a.logprobs) a.logprobs[r] = -INFINITY;
+            if constexpr (kRecord) {
+                row.inv_t = 1.0f;
+                write_record(record, row, 0.0f, false, ~uint64_t{0}, 0);
+            } else {
+                a.tokens[r] = -1;
+                if (a.logprobs) a.logprobs[r] = -INFINITY;
+            }
         }
         return;  // the whole cluster: no rank reads another's memory any more
     }
@@ -850,8 +852,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             });
         cluster.sync();
         if (rank == 0 && threadIdx.x == 0) {
-            a.tokens[r] = static_cast<int32_t>(sh.first);
-            if (a.logprobs) a.logprobs[r] = 0.0f;
+            if constexpr (kRecord) {
+                const bool top_infinite = row.top == INFINITY;
+                if (top_infinite) row.top = 0.0f;
+                row.inv_t = 1.0f;
+                write_record(record, row, 0.0f, top_infinite, place(row.top, sh.first), static_cast<uint64_t>(kMassOne));
+            } else {
+                a.tokens[r] = static_cast<int32_t>(sh.first);
+                if (a.logprobs) a.logprobs[r] = 0.0f;
+            }
         }
         return;
     }
@@ -898,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const uint32_t listed = zero->list_n;
         auto read = cluster.barrier_arrive();  // every rank has read it once this barrier is through
         if (listed <= kListMax && rank) return true;
-        if (listed <= kListMax) draw_from_list(a, r, sh, row, want, listed, row_mass);
+        if (listed <= kListMax) draw_from_list<kRecord>(a, r, sh, row, want, listed, row_mass, record, infinite);
         cluster.barrier_wait(std::move(read));
         return listed <= kListMax;
     };
@@ -1093,6 +1102,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (i < rank) before += sh.total[i];
         total += sh.total[i];
     }
+    if constexpr (kRecord) {
+        if (rank == 0 && threadIdx.x == 0) write_record(record, row, want.least, infinite, threshold, total);
+        return;
+    }
     const uint64_t aim = aim_of(want.u, total);
     if (before <= aim && aim < before + mass) {  // the aim falls into this warp's run
         for (uint32_t i = run0; i < run1; i += 32) {
@@ -1106,13 +1119,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 }
 
 template <typename T>
-afx_status launch(const SampleArgs& a, uint32_t rows, uint32_t ranks, cudaStream_t s) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+    row_choice<T>(a);
+}
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) verify_record_kernel(const __grid_constant__ RecordArgs a) {
+    row_choice<T>(a);
+}
+
+template <typename Args>
+afx_status launch(void (*kernel)(const Args), const Args& a, uint32_t rows, uint32_t ranks, cudaStream_t s) {
     const size_t smem = sizeof(Shared) + static_cast<size_t>(a.slice) * sizeof(float);
     // the same for every call: calls on other threads set it too
     constexpr size_t most = sizeof(Shared) + AFX_SAMPLE_MAX_VOCAB / kMaxCluster * sizeof(float);
-    AFX_SERVE_TRY(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most)),
+    AFX_SERVE_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most)),
                   "cudaFuncSetAttribute");
-    AFX_SERVE_TRY(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
+    AFX_SERVE_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
                   "cudaFuncSetAttribute");
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(rows * ranks);
@@ -1127,11 +1149,55 @@ afx_status launch(const SampleArgs& a, uint32_t rows, uint32_t ranks, cudaStream
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    AFX_SERVE_TRY(cudaLaunchKernelEx(&cfg, sample_kernel<T>, a), "sample_kernel launch");
+    AFX_SERVE_TRY(cudaLaunchKernelEx(&cfg, kernel, a), "sampling kernel launch");
     return AFX_OK;
 }
 
+// CTAs a row: as few as hold it in 32,640 tokens each (the barriers cost
+// less), more while the GPU has two CTAs an SM to give and 4096 tokens are left for each.  Two CTAs fit an SM up
+// to some 20,200 tokens each; with many rows, vocabularies that leave a CTA more have one
+uint32_t ctas_a_row(uint64_t rows, uint32_t vocab, int sms) {
+    uint32_t ranks = 1;
+    while (ranks < kMaxCluster &&
+           (vocab / ranks > 32768 - 128 || (vocab / ranks > 4096 && rows * ranks * 2 <= static_cast<uint64_t>(sms) * 2)))
+        ranks *= 2;
+    return ranks;
+}
+
 }  // namespace
+
+afx_status launch_records(const Side& target, const Side& draft, uint32_t rows, uint32_t vocab, const int32_t* starts, const int32_t* tokens,
+                          uint32_t n_requests, cudaStream_t s) {
+    const int sms = current_sms();
+    if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
+    RecordArgs a{};
+    a.side[0] = target;
+    a.side[1] = draft;
+    a.starts = starts;
+    a.tokens = tokens;
+    a.n_requests = n_requests;
+    a.rows = rows;
+    a.vocab = vocab;
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t size = a.side[i].type == AFX_LOGITS_F32 ? 4 : 2;
+        a.wide[i] = !((reinterpret_cast<uintptr_t>(a.side[i].logits) | (rows > 1 ? a.side[i].row_stride * size : 0)) & 15u);
+    }
+    // `count` rows from row `skip` on, all of one type
+    auto go = [&](uint32_t type, uint32_t skip, uint32_t count) {
+        const uint32_t ranks = ctas_a_row(count, vocab, sms);
+        a.skip = skip;
+        a.slice = ceil_div(ceil_div(vocab, ranks), 128) * 128;
+        a.run = ceil_div(a.slice, kWarps * 128) * 128;
+        if (type == AFX_LOGITS_F32) return launch(verify_record_kernel<float>, a, count, ranks, s);
+        if (type == AFX_LOGITS_BF16) return launch(verify_record_kernel<__nv_bfloat16>, a, count, ranks, s);
+        return launch(verify_record_kernel<__half>, a, count, ranks, s);
+    };
+    if (!draft.logits) return go(target.type, 0, rows);
+    if (draft.type == target.type) return go(target.type, 0, 2 * rows);
+    const afx_status st = go(target.type, 0, rows);
+    return st == AFX_OK ? go(draft.type, rows, rows) : st;
+}
+
 }  // namespace serve
 }  // namespace afx
 
@@ -1164,22 +1230,16 @@ extern "C" afx_status afx_sample(const void* logits_dev, uint32_t type, uint32_t
     a.tokens = tokens_dev;
     a.logprobs = logprobs_dev;
     a.vocab = vocab;
-    // CTAs a row: as few as hold it in 32,640 tokens each (the barriers cost
-    // less), more while the GPU has two CTAs an SM to give and 4096 tokens are left for each.  Two CTAs fit an SM up
-    // to some 20,200 tokens each; with many rows, vocabularies that leave a CTA more have one
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
-    uint32_t ranks = 1;
-    while (ranks < kMaxCluster &&
-           (vocab / ranks > 32768 - 128 || (vocab / ranks > 4096 && static_cast<uint64_t>(rows) * ranks * 2 <= static_cast<uint64_t>(sms) * 2)))
-        ranks *= 2;
+    const uint32_t ranks = ctas_a_row(rows, vocab, sms);
     a.rows = rows;
     a.ordered = top_p_dev && rows > 1 && static_cast<uint64_t>(rows) * ranks > static_cast<uint64_t>(sms) * 2;
     a.slice = ceil_div(ceil_div(vocab, ranks), 128) * 128;
     a.run = ceil_div(a.slice, kWarps * 128) * 128;
     a.wide = !((reinterpret_cast<uintptr_t>(logits_dev) | (rows > 1 ? row_stride * size : 0)) & 15u);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (type == AFX_LOGITS_F32) return launch<float>(a, rows, ranks, s);
-    if (type == AFX_LOGITS_BF16) return launch<__nv_bfloat16>(a, rows, ranks, s);
-    return launch<__half>(a, rows, ranks, s);
+    if (type == AFX_LOGITS_F32) return launch(sample_kernel<float>, a, rows, ranks, s);
+    if (type == AFX_LOGITS_BF16) return launch(sample_kernel<__nv_bfloat16>, a, rows, ranks, s);
+    return launch(sample_kernel<__half>, a, rows, ranks, s);
 }
