@@ -709,7 +709,7 @@ __device__ __forceinline__ void row_choice(const Args& args) {
         of_params = 0;
         for (uint32_t i = 0; i < args.n_requests; i += kThreads)
             of_params += __syncthreads_count(i + threadIdx.x < args.n_requests && __ldg(args.starts + 1 + i + threadIdx.x) <= static_cast<int32_t>(r));
-        const bool used = of_params < args.n_requests &&
+        const bool used = of_params < args.n_requests && temperature_of(side, of_params) > 0.0f && !keeps_all(side, of_params, args.vocab) &&
                           (!second || draft_of(args.tokens, static_cast<int32_t>(r), min(__ldg(args.starts + 1 + of_params), static_cast<int32_t>(args.rows)), args.vocab) >= 0);
         if (!used) {  // the whole cluster
             cluster.barrier_wait(std::move(started));
@@ -845,22 +845,15 @@ __device__ __forceinline__ void row_choice(const Args& args) {
         if (lane < static_cast<int>(n_q)) f(q[lane], z[q[lane]]);
         __syncwarp();
     };
-    if (!(temp > 0.0f)) {  // the maximum itself
+    if (!kRecord && !(temp > 0.0f)) {  // the maximum itself
         if (mine == row.top)
             each([&](uint32_t i, float x) {
                 if (x == row.top) atomicMin(&zero->first, base + i);
             });
         cluster.sync();
         if (rank == 0 && threadIdx.x == 0) {
-            if constexpr (kRecord) {
-                const bool top_infinite = row.top == INFINITY;
-                if (top_infinite) row.top = 0.0f;
-                row.inv_t = 1.0f;
-                write_record(record, row, 0.0f, top_infinite, place(row.top, sh.first), static_cast<uint64_t>(kMassOne));
-            } else {
-                a.tokens[r] = static_cast<int32_t>(sh.first);
-                if (a.logprobs) a.logprobs[r] = 0.0f;
-            }
+            a.tokens[r] = static_cast<int32_t>(sh.first);
+            if (a.logprobs) a.logprobs[r] = 0.0f;
         }
         return;
     }

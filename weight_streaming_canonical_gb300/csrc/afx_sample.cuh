@@ -115,8 +115,24 @@ struct Side {
     uint32_t type;
 };
 
-// Records what every row that a request's starts name keeps: of the target's
-// rows, and of the drafts' those that a draft comes from.
+// A row that keeps all its tokens, or (temperature 0) the first one alone, is
+// not recorded: one pass over it says what there is to know.
+__device__ __forceinline__ bool keeps_all(const Side& side, uint32_t request, uint32_t vocab) {
+    const int32_t k = side.top_k ? __ldg(side.top_k + request) : 0;
+    return !(k > 0 && static_cast<uint32_t>(k) < vocab) && !(side.top_p && __ldg(side.top_p + request) < 1.0f) &&
+           !(side.min_p && __ldg(side.min_p + request) > 0.0f);
+}
+__device__ __forceinline__ float temperature_of(const Side& side, uint32_t request) {
+    return side.temperature ? __ldg(side.temperature + request) : 1.0f;
+}
+// 1 / T as afx_sample takes it
+__device__ __forceinline__ float inverse_temperature(float t) {
+    constexpr float kLeast = 3e-39f;  // 1 / T is finite from here on
+    return t == INFINITY ? 1.17549435e-38f : 1.0f / fmaxf(t, kLeast);
+}
+
+// Records what the rows that a request's starts name keep, where they keep
+// less than all: of the target's rows, and of the drafts' those that a draft comes from.
 afx_status launch_records(const Side& target, const Side& draft, uint32_t rows, uint32_t vocab, const int32_t* starts, const int32_t* tokens,
                           uint32_t n_requests, cudaStream_t s);
 
