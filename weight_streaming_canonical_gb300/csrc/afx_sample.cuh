@@ -118,9 +118,10 @@ struct Side {
 // A row that keeps all its tokens, or (temperature 0) the first one alone, is
 // not recorded: one pass over it says what there is to know.
 __device__ __forceinline__ bool keeps_all(const Side& side, uint32_t request, uint32_t vocab) {
+    // three loads at once
     const int32_t k = side.top_k ? __ldg(side.top_k + request) : 0;
-    return !(k > 0 && static_cast<uint32_t>(k) < vocab) && !(side.top_p && __ldg(side.top_p + request) < 1.0f) &&
-           !(side.min_p && __ldg(side.min_p + request) > 0.0f);
+    const float top_p = side.top_p ? __ldg(side.top_p + request) : 1.0f, min_p = side.min_p ? __ldg(side.min_p + request) : 0.0f;
+    return !((k > 0) & (static_cast<uint32_t>(k) < vocab)) & !(top_p < 1.0f) & !(min_p > 0.0f);
 }
 __device__ __forceinline__ float temperature_of(const Side& side, uint32_t request) {
     return side.temperature ? __ldg(side.temperature + request) : 1.0f;

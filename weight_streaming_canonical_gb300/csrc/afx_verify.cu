@@ -45,6 +45,12 @@ constexpr uint32_t kChunk = 512;        // tokens of a warp at a time
 constexpr uint32_t kGroups = kChunk / 128;
 constexpr uint32_t kMostChunks = AFX_SAMPLE_MAX_VOCAB / kWarps / kChunk;  // of a warp, one CTA a row
 
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    return v;
+}
+
 struct Part {  // of a row: its maximum, sum of e^((z - m) / T), lowest index of the maximum, infinite logits
     float top, sum;
     uint32_t first, infinite;
@@ -84,7 +90,7 @@ __device__ __forceinline__ void join(Part& a, const Part& b, float inv_t) {
 
 template <typename T>
 __global__ void __launch_bounds__(kScanThreads) verify_scan_kernel(const __grid_constant__ VerifyArgs a, const uint32_t row0) {
-    constexpr uint32_t kRuns = 8;  // of four tokens a thread, in flight
+    constexpr uint32_t kRuns = 4;  // of four tokens a thread, in flight
     __shared__ Part warps[kScanThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier();
@@ -173,21 +179,30 @@ __global__ void __launch_bounds__(kScanThreads) verify_scan_kernel(const __grid_
 }
 
 // What row r of a side keeps, recorded or from its parts.
-__device__ Kept kept_of(const VerifyArgs& a, int which, uint32_t request, uint32_t r) {
+struct Kind {  // of a request's rows of a side
+    bool recorded, greedy;
+    float inv_t;
+    __device__ Kind(const Side& side, uint32_t request, uint32_t vocab) {
+        const float t = temperature_of(side, request);
+        const bool all = keeps_all(side, request, vocab);
+        greedy = !(t > 0.0f);
+        recorded = !greedy & !all;
+        inv_t = greedy ? 1.0f : inverse_temperature(t);
+    }
+};
+__device__ Kept kept_of(const VerifyArgs& a, int which, const Kind& kind, uint32_t r) {
     const Side& side = a.side[which];
-    const float t = temperature_of(side, request);
-    if (t > 0.0f && !keeps_all(side, request, a.vocab)) return side.kept[r];
+    if (kind.recorded) return side.kept[r];
     const Part* parts = a.parts + (static_cast<uint64_t>(which) * a.n_tokens + r) * a.n_parts;
-    const float inv_t = t > 0.0f ? inverse_temperature(t) : 1.0f;
     Part all = parts[0];
-    for (uint32_t i = 1; i < a.n_parts; ++i) join(all, parts[i], inv_t);
+    for (uint32_t i = 1; i < a.n_parts; ++i) join(all, parts[i], kind.inv_t);
     Kept k;
     k.infinite = all.top == INFINITY;
     k.top = k.infinite ? 0.0f : all.top;
-    k.inv_t = inv_t;
+    k.inv_t = kind.inv_t;
     k.least = 0.0f;
-    k.threshold = t > 0.0f ? 0 : place(k.top, all.first);
-    const float sum = !(t > 0.0f) ? 1.0f : k.infinite ? static_cast<float>(all.infinite) : all.sum;
+    k.threshold = kind.greedy ? place(k.top, all.first) : 0;
+    const float sum = kind.greedy ? 1.0f : k.infinite ? static_cast<float>(all.infinite) : all.sum;
     k.total = all.top == -INFINITY ? 0 : static_cast<uint64_t>(static_cast<double>(sum) * kMassOne);
     return k;
 }
@@ -205,81 +220,52 @@ __device__ __forceinline__ float log_share(const Kept& p, float z, uint64_t tota
     return p.scaled(z) - logf(static_cast<float>(total) * (1.0f / kMassOne));
 }
 
-// x times a number held as the sum of two float32: the quotient by its inverse, rounded nearly always as the exact one is
-struct Inverse {
-    float hi, lo;
-    __device__ explicit Inverse(uint64_t total) {
-        const double inv = total ? static_cast<double>(kMassOne) / static_cast<double>(total) : 0.0;
-        hi = static_cast<float>(inv);
-        lo = static_cast<float>(inv - static_cast<double>(hi));
+// What a side keeps of the row to draw from, with its order's last place as a
+// logit and an index, and its weights' sum as the inverse to multiply with,
+// held as the sum of two float32: rounded nearly always as the exact quotient.
+struct Shares {
+    float top, inv_t, least, low, inv_hi, inv_lo;
+    uint32_t last, infinite;
+    __device__ void set(const Kept& k) {
+        top = k.top, inv_t = k.inv_t, least = k.least, infinite = k.infinite;
+        low = k.threshold ? key_value(static_cast<uint32_t>(k.threshold >> 32)) : -INFINITY;
+        last = k.threshold ? 0xFFFFFFFFu - static_cast<uint32_t>(k.threshold) : 0xFFFFFFFFu;
+        inv_hi = 1.0f, inv_lo = 0.0f;
     }
-    __device__ float times(float x) const { return fmaf(x, hi, x * lo); }
+    __device__ void divide_by(uint64_t total) {
+        if (total == 0) return;
+        // total / 2^44 as two float32; a step of Newton's method from the inverse of the first
+        const float hi = static_cast<float>(total), lo = static_cast<float>(static_cast<int64_t>(total - static_cast<uint64_t>(hi)));
+        const float t_hi = hi * (1.0f / kMassOne), t_lo = lo * (1.0f / kMassOne);
+        inv_hi = __frcp_rn(t_hi);
+        inv_lo = inv_hi * (fmaf(-inv_hi, t_hi, 1.0f) - inv_hi * t_lo);
+    }
+    __device__ __forceinline__ float value(float z) const {
+        z = clean(z);
+        return infinite ? (z == INFINITY ? 0.0f : -INFINITY) : z;
+    }
+    __device__ __forceinline__ bool keeps(float x, uint32_t i) const { return x > low || (x == low && i <= last); }
+    // x as value() gives it; e^minus infinity is 0
+    __device__ __forceinline__ float weight(float x, uint32_t i) const {
+        const float w = expf((x - top) * inv_t);
+        return keeps(x, i) && w >= least ? w : 0.0f;
+    }
+    __device__ __forceinline__ float share(float w) const { return fmaf(w, inv_hi, w * inv_lo); }
 };
 
-enum Weights { kOfTarget, kWithoutDraft, kLeftOver, kSums };  // kSums: those of p and of q, apart
+// four logits from i on, of tokens below end
+template <typename T>
+__device__ __forceinline__ void load_four(const T* row, bool wide, uint32_t i, uint32_t end, float (&x)[4]) {
+    if (wide && i + 4 <= end) {
+        load4(row + i, x);
+    } else {
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) x[c] = i + c < end ? load_logit(row + i + c) : -INFINITY;
+    }
+}
 
 template <typename P, typename Q>
-struct Draw {
-    const P* z_row;
-    const Q* q_row;
-    Kept p, q;
-    float low;        // of p's tokens; minus infinity where all are kept
-    bool p_all, q_all, z_wide, q_wide;
-    int32_t refused;
-    Inverse p_inv{0}, q_inv{0};
-
-    // four logits from i on (of tokens below end)
-    template <typename T>
-    __device__ static void load(const T* row, bool wide, uint32_t i, uint32_t end, float (&x)[4]) {
-        if (wide && i + 4 <= end) {
-            load4(row + i, x);
-        } else {
-#pragma unroll
-            for (uint32_t c = 0; c < 4; ++c) x[c] = i + c < end ? load_logit(row + i + c) : -INFINITY;
-        }
-    }
-    __device__ static float weight(const Kept& k, bool all, float x, uint32_t i) {
-        return all ? expf(k.scaled(x)) : k.weight(x, i);  // e^minus infinity is 0
-    }
-    // token i's mass, x and y its logits as value() gives them
-    __device__ uint64_t mass(Weights w, uint32_t i, float x, float y) const {
-        const float px = weight(p, p_all, x, i);
-        if (w == kLeftOver) return static_cast<uint64_t>(fmaxf(p_inv.times(px) - q_inv.times(weight(q, q_all, y, i)), 0.0f) * kMassOne);
-        if (w == kWithoutDraft && i == static_cast<uint32_t>(refused)) return 0;
-        return static_cast<uint64_t>(px * kMassOne);
-    }
-    // this lane's logits of a chunk; false: no lane's can have mass
-    __device__ bool chunk(Weights w, uint32_t i0, uint32_t end, float (&x)[kGroups][4], float (&y)[kGroups][4]) const {
-        const uint32_t lane = threadIdx.x & 31;
-        float most = -INFINITY;
-#pragma unroll
-        for (uint32_t j = 0; j < kGroups; ++j) load(z_row, z_wide, i0 + j * 128 + lane * 4, end, x[j]);
-        if (w >= kLeftOver && p_all)  // most of q's are needed
-#pragma unroll
-            for (uint32_t j = 0; j < kGroups; ++j) load(q_row, q_wide, i0 + j * 128 + lane * 4, end, y[j]);
-#pragma unroll
-        for (uint32_t j = 0; j < kGroups; ++j)
-#pragma unroll
-            for (uint32_t c = 0; c < 4; ++c) {
-                x[j][c] = p.value(clean(x[j][c]));
-                most = fmaxf(most, x[j][c]);
-            }
-        if (w != kSums && !__any_sync(0xFFFFFFFFu, most > -INFINITY && most >= low)) return false;
-        if (w >= kLeftOver) {
-            if (!p_all)
-#pragma unroll
-                for (uint32_t j = 0; j < kGroups; ++j) load(q_row, q_wide, i0 + j * 128 + lane * 4, end, y[j]);
-#pragma unroll
-            for (uint32_t j = 0; j < kGroups; ++j)
-#pragma unroll
-                for (uint32_t c = 0; c < 4; ++c) y[j][c] = q.value(clean(y[j][c]));
-        }
-        return true;
-    }
-};
-
-template <typename P, typename Q>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -289,6 +275,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     auto started = cluster.barrier_arrive();  // a rank's memory may be written once its CTA runs
     wait_for_earlier();
     let_next_start();
+    const int32_t row0 = __ldg(a.starts + r), row1 = __ldg(a.starts + r + 1);
+    const Kind p_kind(target, r, a.vocab), q_kind(draft, r, a.vocab);
     // all of the call or nothing: every CTA looks at all starts
     int bad = 0;
     for (uint32_t i = threadIdx.x; i <= a.n_requests; i += kThreads) {
@@ -296,7 +284,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         bad |= s < before || s > static_cast<int32_t>(a.n_tokens) || (i == 0 && s != 0);
     }
     bad = __syncthreads_or(bad);
-    const int32_t row0 = __ldg(a.starts + r), row1 = __ldg(a.starts + r + 1);
     cluster.barrier_wait(std::move(started));
     if (bad || row0 == row1) {
         if (rank == 0 && threadIdx.x == 0) {
@@ -319,14 +306,17 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             const int32_t d = draft_of(a.tokens, t, row1, a.vocab);
             bool stands = d >= 0;
             if (stands) {
-                const Kept p = kept_of(a, 0, r, t);
-                const double share = static_cast<double>(p.weight(p.value(z_of(t, d)), d)) * kMassOne / static_cast<double>(p.total);
-                double other = 1.0;
+                const Kept p = kept_of(a, 0, p_kind, t);
+                // u q < p, as products with the sums: of 64-bit numbers there are few units
+                const double w = p.weight(p.value(z_of(t, d)), d);
+                const double u = __ldg(a.u + t);
                 if (draft.logits) {
-                    const Kept q = kept_of(a, 1, r, t);
-                    other = q.total ? static_cast<double>(q.weight(q.value(q_of(t, d)), d)) * kMassOne / static_cast<double>(q.total) : 0.0;
+                    const Kept q = kept_of(a, 1, q_kind, t);
+                    const double other = q.total ? q.weight(q.value(q_of(t, d)), d) : 0.0f;
+                    stands = u * other * static_cast<double>(p.total) < w * static_cast<double>(q.total ? q.total : 1);
+                } else {
+                    stands = u * static_cast<double>(p.total) < w * kMassOne;
                 }
-                stands = p.total && static_cast<double>(__ldg(a.u + t)) * other < share;
             }
             if (!stands) atomicMin(&sh.first, i);
         }
@@ -336,9 +326,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         if (stood < last) break;
     }
     const int32_t t = row0 + stood;
-    Draw<P, Q> draw;
-    draw.p = kept_of(a, 0, r, t);
-    const bool nothing = draw.p.top == -INFINITY, greedy = !(temperature_of(target, r) > 0.0f);
+    const Kept kept = kept_of(a, 0, p_kind, t);
+    const bool nothing = kept.top == -INFINITY, greedy = p_kind.greedy;
     if (rank == 0) {
         for (int32_t i = threadIdx.x; i <= last; i += kThreads) {
             if (i == stood && !nothing) continue;
@@ -347,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             if (a.logprobs) {
                 float l = i == stood ? -INFINITY : 0.0f;
                 if (i < stood) {
-                    const Kept k = kept_of(a, 0, r, row0 + i);
+                    const Kept k = kept_of(a, 0, p_kind, row0 + i);
                     l = log_share(k, k.value(z_of(row0 + i, d)), k.total);
                 }
                 a.logprobs[row0 + i] = l;
@@ -356,115 +345,159 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         if (threadIdx.x == 0) {
             a.counts[r] = nothing ? stood : stood + 1;
             if (greedy && !nothing) {  // the one token that p keeps, whatever q is
-                a.out_tokens[t] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(draw.p.threshold));
+                a.out_tokens[t] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(kept.threshold));
                 if (a.logprobs) a.logprobs[t] = 0.0f;
             }
         }
     }
     if (nothing || greedy) return;  // the whole cluster
 
-    // the draw
-    draw.refused = draft_of(a.tokens, t, row1, a.vocab);
-    Weights weights = draw.refused < 0 ? kOfTarget : kWithoutDraft;
-    draw.q = Kept{};
-    if (draw.refused >= 0 && draft.logits) {
-        draw.q = kept_of(a, 1, r, t);
-        weights = draw.q.total ? kLeftOver : kOfTarget;
+    // the draw: from the weights of p, those of all but the draft, or the shares of p above those of q
+    const int32_t refused = draft_of(a.tokens, t, row1, a.vocab);
+    Shares p, q;
+    p.set(kept);
+    uint64_t p_total = kept.total, q_total = 0;
+    bool both = false;
+    uint32_t without = 0xFFFFFFFFu;
+    if (refused >= 0 && draft.logits) {
+        const Kept k = kept_of(a, 1, q_kind, t);
+        q.set(k);
+        q_total = k.total;
+        both = q_total != 0;
+    } else if (refused >= 0) {
+        without = refused;
     }
     const uint32_t base = min(a.vocab, rank * a.slice), n = min(a.vocab - base, a.slice);
     const uint32_t run0 = base + min(n, warp * a.run), run1 = min(base + n, run0 + a.run);
-    draw.z_row = static_cast<const P*>(target.logits) + t * target.row_stride;
-    draw.q_row = static_cast<const Q*>(draft.logits) + t * draft.row_stride;
-    draw.z_wide = a.wide[0], draw.q_wide = a.wide[1];
-    draw.p_all = draw.p.threshold == 0 && draw.p.least == 0.0f, draw.q_all = draw.q.threshold == 0 && draw.q.least == 0.0f;
-    draw.low = draw.p.threshold ? key_value(static_cast<uint32_t>(draw.p.threshold >> 32)) : -INFINITY;
-    uint64_t before = 0, mine = 0, total = 0;
+    const P* z_row = static_cast<const P*>(target.logits) + t * target.row_stride;
+    const Q* q_row = static_cast<const Q*>(draft.logits) + t * draft.row_stride;
+    uint64_t before = 0, mine = 0, total = 0, q_sum = 0;
     uint32_t turn = 0;
-    // the masses of every chunk of this warp's run, of its run (mine), of the runs before it and of the row
-    auto sum_up = [&](Weights w) {
-        uint64_t of_run[2] = {0, 0};
-        uint32_t k = 0;
-        for (uint32_t i0 = run0; i0 < run1; i0 += kChunk, ++k) {
-            float x[kGroups][4], y[kGroups][4];
-            uint64_t sum[2] = {0, 0};
-            if (draw.chunk(w, i0, run1, x, y)) {
-                if (w == kSums) {
-                    MassSum s[2];
-#pragma unroll
-                    for (uint32_t j = 0; j < kGroups; ++j)
-#pragma unroll
-                        for (uint32_t c = 0; c < 4; ++c) {
-                            const uint32_t i = i0 + j * 128 + lane * 4 + c;
-                            s[0].add(draw.weight(draw.p, draw.p_all, x[j][c], i));
-                            s[1].add(draw.weight(draw.q, draw.q_all, y[j][c], i));
-                        }
-                    sum[0] = s[0].total(), sum[1] = s[1].total();
-                } else if (w != kLeftOver && draw.p_all) {
-                    MassSum s;
-#pragma unroll
-                    for (uint32_t j = 0; j < kGroups; ++j)
-#pragma unroll
-                        for (uint32_t c = 0; c < 4; ++c) {
-                            const float px = expf(draw.p.scaled(x[j][c]));
-                            s.add(w == kWithoutDraft && i0 + j * 128 + lane * 4 + c == static_cast<uint32_t>(draw.refused) ? 0.0f : px);
-                        }
-                    sum[0] = s.total();
-                } else {
-#pragma unroll
-                    for (uint32_t j = 0; j < kGroups; ++j)
-#pragma unroll
-                        for (uint32_t c = 0; c < 4; ++c)
-                            if (x[j][c] > -INFINITY && x[j][c] >= draw.low) sum[0] += draw.mass(w, i0 + j * 128 + lane * 4 + c, x[j][c], y[j][c]);
-                }
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) {
-                sum[0] += __shfl_xor_sync(0xFFFFFFFFu, sum[0], d);
-                if (w == kSums) sum[1] += __shfl_xor_sync(0xFFFFFFFFu, sum[1], d);
-            }
-            if (lane == 0) sh.chunks[warp][k] = sum[0];
-            of_run[0] += sum[0], of_run[1] += sum[1];
-        }
+    // From the masses of each chunk of this warp's run: of its run (mine), of the runs before it and of the row
+    auto join_runs = [&](uint64_t of_run, uint64_t q_of_run) {
         __syncthreads();
-        if (lane == 0) sh.warps[0][warp] = of_run[0], sh.warps[1][warp] = of_run[1];
+        if (lane == 0) sh.warps[0][warp] = of_run, sh.warps[1][warp] = q_of_run;
         __syncthreads();
-        uint64_t of_slice[2] = {0, 0};
+        uint64_t of_slice = 0, q_of_slice = 0;
         before = 0;
         for (uint32_t i = 0; i < kWarps; ++i) {
             if (i < warp) before += sh.warps[0][i];
-            of_slice[0] += sh.warps[0][i], of_slice[1] += sh.warps[1][i];
+            of_slice += sh.warps[0][i], q_of_slice += sh.warps[1][i];
         }
         if (threadIdx.x < ranks) {
             Shared* other = cluster.map_shared_rank(&sh, threadIdx.x);
-            other->total[turn][0][rank] = of_slice[0], other->total[turn][1][rank] = of_slice[1];
+            other->total[turn][0][rank] = of_slice, other->total[turn][1][rank] = q_of_slice;
         }
         cluster.sync();
-        total = 0;
-        uint64_t second = 0;
+        total = q_sum = 0;
         for (uint32_t i = 0; i < ranks; ++i) {
             if (i < rank) before += sh.total[turn][0][i];
             total += sh.total[turn][0][i];
-            second += sh.total[turn][1][i];
+            q_sum += sh.total[turn][1][i];
         }
-        mine = of_run[0];
+        mine = of_run;
         ++turn;
-        return second;
     };
-    if (weights == kLeftOver) {
-        uint64_t p_total = draw.p.total, q_total = draw.q.total;
-        const bool q_summed = !(temperature_of(draft, r) > 0.0f) || !keeps_all(draft, r, a.vocab);
-        const bool p_summed = !keeps_all(target, r, a.vocab);
-        if (!p_summed || !q_summed) {
-            const uint64_t second = sum_up(kSums);
-            if (!p_summed) p_total = total;
-            if (!q_summed) q_total = second;
+    auto sum_of_p = [&] {
+        uint64_t of_run = 0;
+        uint32_t k = 0;
+        float x[kGroups][4];
+        auto load = [&](uint32_t i0) {
+#pragma unroll
+            for (uint32_t j = 0; j < kGroups; ++j) load_four(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1, x[j]);
+        };
+        for (uint32_t i0 = run0; i0 < run1; i0 += kChunk, ++k) {
+            load(i0);
+            bool any = false;
+#pragma unroll
+            for (uint32_t j = 0; j < kGroups; ++j)
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c) {
+                    x[j][c] = p.value(x[j][c]);
+                    any |= x[j][c] >= p.low;
+                }
+            uint64_t sum = 0;
+            if (__any_sync(0xFFFFFFFFu, any)) {
+                MassSum s;
+#pragma unroll
+                for (uint32_t j = 0; j < kGroups; ++j)
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c) {
+                        const uint32_t i = i0 + j * 128 + lane * 4 + c;
+                        s.add(i == without ? 0.0f : p.weight(x[j][c], i));
+                    }
+                sum = warp_sum(s.total());
+            }
+            if (lane == 0) sh.chunks[warp][k] = sum;
+            of_run += sum;
         }
-        draw.p_inv = Inverse(p_total), draw.q_inv = Inverse(q_total);
+        join_runs(of_run, 0);
+    };
+    // sums: the weights of p and of q, apart; otherwise the shares of p above those of q
+    auto sum_of_both = [&](bool sums) {
+        uint64_t of_run = 0, q_of_run = 0;
+        uint32_t k = 0;
+        for (uint32_t i0 = run0; i0 < run1; i0 += kChunk, ++k) {
+            float x[kGroups][4], y[kGroups][4];
+            bool any = sums || p.low == -INFINITY;  // all are meant, so both rows' loads go out together
+#pragma unroll
+            for (uint32_t j = 0; j < kGroups; ++j) load_four(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1, x[j]);
+            if (any)
+#pragma unroll
+                for (uint32_t j = 0; j < kGroups; ++j) load_four(q_row, a.wide[1], i0 + j * 128 + lane * 4, run1, y[j]);
+            bool late = !any;
+#pragma unroll
+            for (uint32_t j = 0; j < kGroups; ++j)
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c) {
+                    x[j][c] = p.value(x[j][c]);
+                    any |= x[j][c] >= p.low;
+                }
+            uint64_t sum = 0, q_of_chunk = 0;
+            if (__any_sync(0xFFFFFFFFu, any)) {
+                if (late)
+#pragma unroll
+                    for (uint32_t j = 0; j < kGroups; ++j) load_four(q_row, a.wide[1], i0 + j * 128 + lane * 4, run1, y[j]);
+                MassSum s, q_s;
+#pragma unroll
+                for (uint32_t j = 0; j < kGroups; ++j)
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c) {
+                        const uint32_t i = i0 + j * 128 + lane * 4 + c;
+                        const float wp = p.weight(x[j][c], i), wq = q.weight(q.value(y[j][c]), i);
+                        s.add(sums ? wp : fmaxf(p.share(wp) - q.share(wq), 0.0f));
+                        q_s.add(wq);
+                    }
+                sum = warp_sum(s.total());
+                if (sums) q_of_chunk = warp_sum(q_s.total());
+            }
+            if (lane == 0) sh.chunks[warp][k] = sum;
+            of_run += sum, q_of_run += q_of_chunk;
+        }
+        join_runs(of_run, q_of_run);
+    };
+    if (both) {
+        // sums of the scan, of float32, are summed anew
+        const bool p_summed = p_kind.recorded, q_summed = q_kind.recorded || q_kind.greedy;
+        if (!p_summed || !q_summed) {
+            sum_of_both(true);
+            if (!p_summed) p_total = total;
+            if (!q_summed) q_total = q_sum;
+        }
+        p.divide_by(p_total), q.divide_by(q_total);
+        sum_of_both(false);
+        if (total == 0) {  // nothing is left over
+            both = false;
+            p.inv_hi = 1.0f, p.inv_lo = 0.0f;
+        }
     }
-    sum_up(weights);
-    if (total == 0 && weights != kOfTarget) {  // nothing is left over
-        weights = kOfTarget;
-        sum_up(weights);
+    if (!both) {
+        sum_of_p();
+        if (total == 0 && without != 0xFFFFFFFFu) {
+            without = 0xFFFFFFFFu;
+            sum_of_p();
+        }
+        if (without == 0xFFFFFFFFu) p_total = total;
     }
     const uint64_t aim = aim_of(static_cast<double>(__ldg(a.draw_u + r)), total);
     if (!(before <= aim && aim < before + mine)) return;
@@ -482,15 +515,19 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         }
         before += __shfl_sync(0xFFFFFFFFu, inc, 31);
     }
-    float x[kGroups][4], y[kGroups][4];
-    const uint32_t i0 = run0 + chunk * kChunk;
-    draw.chunk(weights, i0, run1, x, y);
-#pragma unroll
+#pragma unroll 1
     for (uint32_t j = 0; j < kGroups; ++j) {
+        const uint32_t i = run0 + chunk * kChunk + j * 128 + lane * 4;
+        float x[4], y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        load_four(z_row, a.wide[0], i, run1, x);
+        if (both) load_four(q_row, a.wide[1], i, run1, y);
         uint64_t m[4], sum = 0;
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
-            m[c] = x[j][c] > -INFINITY && x[j][c] >= draw.low ? draw.mass(weights, i0 + j * 128 + lane * 4 + c, x[j][c], y[j][c]) : 0;
+            x[c] = p.value(x[c]);
+            float w = i + c == without ? 0.0f : p.weight(x[c], i + c);
+            if (both) w = fmaxf(p.share(w) - q.share(q.weight(q.value(y[c]), i + c)), 0.0f);
+            m[c] = static_cast<uint64_t>(w * kMassOne);
             sum += m[c];
         }
         const uint64_t inc = warp_inclusive(sum);
@@ -498,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
             if (at <= aim && aim < at + m[c]) {
-                a.out_tokens[t] = static_cast<int32_t>(i0 + j * 128 + lane * 4 + c);
-                if (a.logprobs) a.logprobs[t] = log_share(draw.p, x[j][c], weights == kOfTarget ? total : draw.p.total);
+                a.out_tokens[t] = static_cast<int32_t>(i + c);
+                if (a.logprobs) a.logprobs[t] = log_share(kept, x[c], p_total);
             }
             at += m[c];
         }
@@ -632,7 +669,7 @@ extern "C" afx_status afx_verify(const afx_verify_args* args, int32_t* out_token
     a.vocab = v.vocab;
     // a request's row over as many CTAs as there is room for two an SM, with 2048 tokens or more each
     uint32_t ranks = 1;
-    while (ranks < kMaxCluster && v.vocab / ranks > 4096 && static_cast<uint64_t>(v.n_requests) * ranks <= static_cast<uint64_t>(sms)) ranks *= 2;
+    while (ranks < kMaxCluster && v.vocab / ranks > 4096 && static_cast<uint64_t>(v.n_requests) * ranks <= static_cast<uint64_t>(sms) * 3) ranks *= 2;
     a.slice = ceil_div(ceil_div(v.vocab, ranks), 128) * 128;
     a.run = ceil_div(a.slice, kWarps * kChunk) * kChunk;
     auto aligned = [&](const void* p, uint64_t stride, uint32_t bytes) {
@@ -643,7 +680,7 @@ extern "C" afx_status afx_verify(const afx_verify_args* args, int32_t* out_token
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (v.n_tokens) {
         // parts of rows: enough CTAs to fill the GPU several times over, with 1024 tokens or more each
-        const uint64_t all = static_cast<uint64_t>(v.n_tokens) * (v.draft_logits_dev ? 2 : 1), want = (8ull * sms + all - 1) / all;
+        const uint64_t all = static_cast<uint64_t>(v.n_tokens) * (v.draft_logits_dev ? 2 : 1), want = (16ull * sms + all - 1) / all;
         a.n_parts = static_cast<uint32_t>(want > kMostParts ? kMostParts : want);
         a.part = ceil_div(ceil_div(v.vocab, a.n_parts), 1024) * 1024;
         a.n_parts = ceil_div(v.vocab, a.part);
