@@ -7,23 +7,32 @@
 // CTA take eight tokens, whose scales share a sector.
 // Bound: HBM bandwidth; x is read once.
 //
-// fp8_product_kernel: y = x W^T, a tile of 128 tokens by BN rows of W a CTA, in
-// steps of 128 columns, the block of the scales.  A step is
+// fp8_product_kernel: y = x W^T in steps of 128 columns, the block of the
+// scales.  A step of a tile is
 //     D  = X_b W_b^T                    (tcgen05, E4M3, float32 in tensor memory)
 //     y += D * (x_scale[token] * w_scale[row block])
 // where y stays in registers: lane = token, so that a thread has one token's
-// scale and, with all its columns within one or two row blocks, a factor a
-// run of 32 columns.  The tensor cores cannot apply these factors themselves
-// (their scaled form takes powers of two for every 32 elements), so a step's
-// sums are read back; two buffers of them in tensor memory let the products of
-// one step run while the other's sums are read.
+// factors.  The tensor cores cannot apply these themselves (their scaled form
+// takes powers of two for every 32 elements), so a step's sums are read back.
+// Four buffers of them in tensor memory keep the products going while the sums
+// of others are read: from a product's end to the next one into its buffer it
+// takes some 1000 cycles, the products of a step 256 or 512.
+//
+// Two shapes.  For up to 128 tokens, and where tiles are few, a tile is 128
+// tokens by BN rows of W, a CTA; W goes through once, which bounds it.  For more, a pair of
+// CTAs has a tile of 256 tokens by 2 NH rows (cta_group::2): each loads its
+// own 128 tokens and half of the rows, 32 KB a step where a CTA alone would
+// load 48 KB at the 60 bytes a cycle that an SM gets from L2.  A pair's step is two
+// products of NH rows each, with buffers of their own.
 //
 // Roles of a CTA's 12 warps: 0-7 the sums (a quarter of the lanes and half of
-// the columns each; they take registers from the others), 8 issues the products, 9 loads by TMA (128-byte rows with the
-// 128-byte swizzle; columns past the matrix are zeros) into a ring of steps.
-// Where tiles are fewer than SMs, a cluster of CTAs shares a tile: each takes a run
-// of steps, and their sums are added through distributed shared memory in the
-// order of the CTAs.
+// the columns each; they take registers from the others), 8 issues the products
+// (of a pair, the first CTA's), 9 loads by TMA (128-byte rows with the 128-byte
+// swizzle; columns past the matrix are zeros) into a ring of steps, 10 multiplies the
+// tokens' scales with the row blocks' into shared memory.
+// Where tiles are fewer than SMs, a cluster of CTAs shares a tile: each (each pair)
+// takes a run of steps, and their sums are added through distributed shared memory in
+// the order of the CTAs.
 //
 // Every wait is bounded: one that runs out raises AFX_DEV_TIMEOUT and a flag
 // that all roles poll; copies and products in flight are waited for and the
@@ -31,6 +40,7 @@
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <cstdio>
 
 #include "afx_tensor.cuh"
@@ -116,8 +126,8 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const Quant
 
 // ---- the product -------------------------------------------------------------------
 
-constexpr uint32_t kTokens = 128;   // of a tile
-constexpr int kSumWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
+constexpr uint32_t kTokens = 128;   // of a CTA's tile
+constexpr uint32_t kSumWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kFactorWarp = 10;
 constexpr int kProductThreads = 384;
 // registers a thread: as launched, then of the warps with the sums and of the
 // others (what the ones add is what the others gave up)
@@ -125,16 +135,19 @@ constexpr int kRegsLaunch = 168, kRegsSums = 208, kRegsOther = 88;
 static_assert(256 * kRegsSums + 128 * kRegsOther <= kProductThreads * kRegsLaunch, "register shares");
 constexpr uint32_t kMostStages = 16;
 constexpr uint32_t kSmemMost = 232448;  // 227 KB, what a CTA can have
-constexpr uint32_t kMostSplit = 8;
+constexpr uint32_t kMostSplit = 8;      // CTAs, or pairs up to half of it, that share a tile
+constexpr uint32_t kBufs = 4;           // buffers of sums in tensor memory
 
 struct Ctl {
     uint64_t full[kMostStages], empty[kMostStages];
-    uint64_t sums_full[2], sums_empty[2], drain;
+    uint64_t sums_full[kBufs], sums_empty[kBufs], factors_empty[kBufs], drain;
     uint32_t tmem;
     int32_t abort_flag;
+    alignas(16) float factors[kBufs][2][kTokens];  // of a buffer's one or two row blocks
 };
-constexpr uint32_t kCtlBytes = 512;
+constexpr uint32_t kCtlBytes = 5120;
 static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
+constexpr uint32_t kStageFloats = 32 * 33;  // of a warp, where y's rows are not whole sectors
 
 struct ProductArgs {
     CUtensorMap x, w;
@@ -158,32 +171,72 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Ctl& ctl,
     return false;
 }
 
-__device__ __forceinline__ void load_box(uint32_t lane, uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t y, uint64_t* bar) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.u32 q, %5, 0;\n"
-        " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "r"(lane)
-        : "memory");
+// A box of rows of bytes; of a pair, the bytes count at the first CTA's barrier.
+template <bool kPair>
+__device__ __forceinline__ void load_box(uint32_t lane, uint32_t dst, const CUtensorMap* map, uint32_t x, uint32_t y, uint32_t bar) {
+    if constexpr (kPair)
+        asm volatile(
+            "{\n .reg .pred q;\n setp.ne.u32 q, %5, 0;\n"
+            " @q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(lane)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred q;\n setp.ne.u32 q, %5, 0;\n"
+            " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(lane)
+            : "memory");
+}
+// The same box into L2, which later writes of it reach.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, uint32_t x, uint32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
 }
 
+template <bool kPair>
 __device__ __forceinline__ void mma_e4m3(uint32_t lane, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lane)
-        : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+            " @q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lane)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+            " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lane)
+            : "memory");
+}
+// An arrival at this barrier (of a pair: of both CTAs, `mask`) once the products so far are done.
+template <bool kPair>
+__device__ __forceinline__ void commit_products(uint32_t lane, uint64_t* bar, uint16_t mask) {
+    if constexpr (kPair)
+        asm volatile(
+            "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+            " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}\n" ::"r"(smem_addr(bar)),
+            "r"(lane), "h"(mask)
+            : "memory");
+    else
+        commit(lane, bar);
 }
 
-// The columns loaded by tmem_load32 may be used behind this: they are its
-// operands, so that no use of them is moved before it.
-__device__ __forceinline__ void wait_columns(uint32_t (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]),
-                   "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
-                   "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
-                   "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
-                 :
-                 : "memory");
+// 32 columns of this thread's lane, as pairs, behind the wait for them: one
+// statement, so that no use of them can be moved before the wait.
+__device__ __forceinline__ void load_pairs(uint32_t addr, uint64_t (&v)[16]) {
+    asm volatile(
+        "{\n .reg .b32 t<32>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, t16, t17, t18, t19, t20, "
+        "t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
+        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
+        " mov.b64 %8, {t16, t17}; mov.b64 %9, {t18, t19}; mov.b64 %10, {t20, t21}; mov.b64 %11, {t22, t23};\n"
+        " mov.b64 %12, {t24, t25}; mov.b64 %13, {t26, t27}; mov.b64 %14, {t28, t29}; mov.b64 %15, {t30, t31};\n"
+        "}\n"
+        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]),
+          "=l"(v[11]), "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15])
+        : "r"(addr)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t two_16(uint32_t type, float lo, float hi) {
@@ -201,53 +254,80 @@ __device__ __forceinline__ void store_one(const ProductArgs& a, uint64_t at, flo
         reinterpret_cast<uint16_t*>(a.y)[at] = static_cast<uint16_t>(two_16(a.y_type, v, 0.0f));
 }
 
-template <int BN>
+// N: rows of W of one product: of a CTA's tile, or of half a pair's.
+template <uint32_t N, bool kPair>
 struct Tile {
-    static constexpr uint32_t kRuns = BN / 64;       // runs of 32 columns a warp
-    static constexpr uint32_t kWBytes = BN * kBlock;
-    static constexpr uint32_t kColumns = BN == 64 ? 128 : BN == 128 ? 256 : 512;  // of tensor memory, a power of two
-    static constexpr uint32_t kPartRow = BN + 4;     // floats between tokens' sums in shared memory
+    static constexpr uint32_t kRows = kPair ? 2 * N : N;         // of W
+    static constexpr uint32_t kProducts = kPair ? 2 : 1;         // a step
+    static constexpr uint32_t kColumns = kPair ? N : N / 2;      // of a sum warp
+    static constexpr uint32_t kRuns = kColumns / 32;             // of them, in runs of 32
+    static constexpr uint32_t kWBytes = N * kBlock;              // a CTA's part of a step's W
+    static constexpr uint32_t kTmem = N * kBufs <= 256 ? 256 : 512;  // columns of tensor memory, a power of two
+    static constexpr uint32_t kRowBlocks = N % kBlock && kBlock % N ? 2 : 1;  // that a product's rows are among
+    static constexpr uint32_t kPartRow = kRows + 4;              // floats between tokens' sums in shared memory
+    static constexpr uint32_t kArrivals = kPair ? kSumWarps / 2 : kSumWarps;  // that read a buffer, in one CTA
 };
 
-template <int BN>
+template <uint32_t N, bool kPair>
 __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const __grid_constant__ ProductArgs a) {
-    using T = Tile<BN>;
+    using T = Tile<N, kPair>;
     extern __shared__ uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Ctl& ctl = *reinterpret_cast<Ctl*>(smem);
-    uint8_t* w_ring = smem + 1024;
+    uint8_t* w_ring = smem + kCtlBytes;
     uint8_t* x_ring = w_ring + a.stages * T::kWBytes;
     float* staging = reinterpret_cast<float*>(x_ring + a.stages * a.box * kBlock + (kTokens - a.box) * kBlock);  // where !sectors
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // CTAs of a cluster: `split` of them, or pairs
+    const uint32_t group = kPair ? 2 * a.split : a.split, rank = blockIdx.x % group;
+    const uint32_t side = kPair ? rank & 1 : 0, part = kPair ? rank >> 1 : rank, head = rank - side;  // head: the pair's first CTA
+    const uint16_t both = static_cast<uint16_t>(3u << head);
+    // a group's tiles: one where several share it, else every gridDim.x / group-th; its steps of a tile
+    const uint32_t step0 = static_cast<uint32_t>(static_cast<uint64_t>(a.blocks) * part / a.split),
+                   step1 = static_cast<uint32_t>(static_cast<uint64_t>(a.blocks) * (part + 1) / a.split);
+    const uint32_t first = blockIdx.x / group, stride = gridDim.x / group;
+    auto tokens_of = [&](uint32_t tile) { return tile % a.tiles_m * (kPair ? 2 * kTokens : kTokens) + side * kTokens; };
+    auto rows_of = [&](uint32_t tile) { return tile / a.tiles_m * T::kRows; };
+    // this CTA's rows of a tile's product h
+    auto w_row = [&](uint32_t r0, uint32_t h) { return r0 + h * N + side * (N / 2); };
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < a.stages; ++i) {
             bar_init(&ctl.full[i], 1);
             bar_init(&ctl.empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(&ctl.sums_full[i], 1);
-            bar_init(&ctl.sums_empty[i], kSumWarps);
+        for (uint32_t i = 0; i < kBufs; ++i) {
+            bar_init(&ctl.sums_full[i], 2);  // the products and the factors
+            bar_init(&ctl.sums_empty[i], kPair ? 2 * T::kArrivals : T::kArrivals);
+            bar_init(&ctl.factors_empty[i], T::kArrivals);
         }
         bar_init(&ctl.drain, 1);
         ctl.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&ctl.tmem)), "r"(T::kColumns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&ctl.tmem)), "r"(T::kTmem) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(&ctl.tmem)), "r"(T::kTmem) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+        }
+    }
+    if (warp == kLoadWarp && first < a.tiles) {
+        // the first steps' weights are on their way to L2 while the kernel before this one ends: where it writes
+        // them, the copies below find what it wrote
+        for (uint32_t i = lane; i < a.stages * T::kProducts; i += 32) {
+            const uint32_t s = step0 + i / T::kProducts;
+            if (s < step1) prefetch_box(&a.w, s * kBlock, w_row(rows_of(first), i % T::kProducts));
+        }
     }
     fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync();  // the barriers that the other CTA arrives at are there
     fence_after();
     const uint32_t tmem = ctl.tmem;
     wait_for_earlier();
     let_next_start();
-
-    // a CTA's tiles: one a cluster, or every gridDim.x-th; its steps of a tile
-    const uint32_t rank = blockIdx.x % a.split;
-    const uint32_t step0 = static_cast<uint32_t>(static_cast<uint64_t>(a.blocks) * rank / a.split),
-                   step1 = static_cast<uint32_t>(static_cast<uint64_t>(a.blocks) * (rank + 1) / a.split);
-    const uint32_t first = blockIdx.x / a.split, stride = gridDim.x / a.split;
 
     if (warp >= kSumWarps) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsOther));
@@ -256,110 +336,180 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
         uint32_t it = 0, slot = 0, phase = 0;
         bool ok = true;
         for (uint32_t tile = first; ok && tile < a.tiles; tile += stride) {
-            const uint32_t t0 = tile % a.tiles_m * kTokens, r0 = tile / a.tiles_m * BN;
+            const uint32_t t0 = tokens_of(tile), r0 = rows_of(tile);
             for (uint32_t s = step0; s < step1; ++s, ++it) {
                 if (it >= a.stages) {
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.empty[slot], phase ^ 1u, ctl, a.status));
                     if (!ok) break;
                 }
-                if (leader) bar_expect(&ctl.full[slot], T::kWBytes + a.box * kBlock);
+                const uint32_t bar = kPair ? peer_addr(smem_addr(&ctl.full[slot]), head) : smem_addr(&ctl.full[slot]);
+                if (leader && side == 0) bar_expect(&ctl.full[slot], (kPair ? 2 : 1) * (T::kWBytes + a.box * kBlock));
                 __syncwarp();
-                load_box(leader, smem_addr(w_ring + slot * T::kWBytes), &a.w, s * kBlock, r0, &ctl.full[slot]);
-                load_box(leader, smem_addr(x_ring + slot * a.box * kBlock), &a.x, s * kBlock, t0, &ctl.full[slot]);
+                const uint32_t w = smem_addr(w_ring + slot * T::kWBytes);
+                if constexpr (kPair) {
+                    load_box<true>(leader, w, &a.w, s * kBlock, w_row(r0, 0), bar);
+                    load_box<true>(leader, w + T::kWBytes / 2, &a.w, s * kBlock, w_row(r0, 1), bar);
+                } else {
+                    load_box<false>(leader, w, &a.w, s * kBlock, r0, bar);
+                }
+                load_box<kPair>(leader, smem_addr(x_ring + slot * a.box * kBlock), &a.x, s * kBlock, t0, bar);
                 if (++slot == a.stages) {
                     slot = 0;
                     phase ^= 1u;
                 }
             }
         }
-        if (!ok)  // copies in flight write this CTA's shared memory
+        if (!ok && side == 0)  // copies in flight write shared memory
             for (uint32_t q = it > a.stages ? it - a.stages : 0; q < it; ++q)
                 if (!bar_drain(&ctl.full[q % a.stages], q / a.stages & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
       } else if (warp == kMmaWarp) {
-        // float32 sums of E4M3 by E4M3, both with their columns contiguous
-        constexpr uint32_t kInstruction = 1u << 4 | (BN >> 3) << 17 | (kTokens >> 4) << 24;
-        const bool leader = elect();
-        const uint64_t x_desc = operand(smem_addr(x_ring), 16), w_desc = operand(smem_addr(w_ring), 16);
-        uint32_t it = 0, slot = 0, phase = 0;
-        bool ok = true;
-        for (uint32_t tile = first; ok && tile < a.tiles; tile += stride) {
-            for (uint32_t s = step0; s < step1; ++s, ++it) {
-                const uint32_t buf = it & 1u;
-                ok = __all_sync(0xFFFFFFFFu, (it < 2 || bar_wait(&ctl.sums_empty[buf], ((it >> 1) - 1) & 1u, ctl, a.status)) &&
-                                                 bar_wait(&ctl.full[slot], phase, ctl, a.status));
-                if (!ok) break;
-                fence_after();
-                const uint64_t xd = x_desc + slot * (a.box * kBlock >> 4), wd = w_desc + slot * (T::kWBytes >> 4);
+        if (side == 0) {
+            // float32 sums of E4M3 by E4M3, both with their columns contiguous
+            constexpr uint32_t kInstruction = 1u << 4 | (N >> 3) << 17 | ((kPair ? 2 : 1) * kTokens >> 4) << 24;
+            const bool leader = elect();
+            const uint64_t x_desc = operand(smem_addr(x_ring), 16), w_desc = operand(smem_addr(w_ring), 16);
+            uint32_t it = 0, slot = 0, phase = 0;
+            bool ok = true;
+            for (uint32_t tile = first; ok && tile < a.tiles; tile += stride) {
+                for (uint32_t s = step0; s < step1; ++s) {
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.full[slot], phase, ctl, a.status));
+                    const uint64_t xd = x_desc + slot * (a.box * kBlock >> 4), wd = w_desc + slot * (T::kWBytes >> 4);
 #pragma unroll
-                for (uint32_t k = 0; k < kBlock / 32; ++k) mma_e4m3(leader, tmem + buf * BN, xd + k * 2, wd + k * 2, kInstruction, k != 0);
-                commit(leader, &ctl.empty[slot]);
-                commit(leader, &ctl.sums_full[buf]);
-                if (++slot == a.stages) {
-                    slot = 0;
-                    phase ^= 1u;
+                    for (uint32_t h = 0; h < T::kProducts; ++h, ++it) {
+                        const uint32_t buf = it % kBufs;
+                        ok = ok && __all_sync(0xFFFFFFFFu, it < kBufs || bar_wait(&ctl.sums_empty[buf], (it / kBufs - 1) & 1u, ctl, a.status));
+                        if (!ok) break;
+                        fence_after();
+#pragma unroll
+                        for (uint32_t k = 0; k < kBlock / 32; ++k)
+                            mma_e4m3<kPair>(leader, tmem + buf * N, xd + k * 2, wd + h * (T::kWBytes / 2 >> 4) + k * 2, kInstruction, k != 0);
+                        if (h + 1 == T::kProducts) commit_products<kPair>(leader, &ctl.empty[slot], both);
+                        commit_products<kPair>(leader, &ctl.sums_full[buf], both);
+                    }
+                    if (!ok) break;
+                    if (++slot == a.stages) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
+            commit_products<kPair>(leader, &ctl.drain, both);  // arrivals above land before a CTA ends
         }
-        commit(leader, &ctl.drain);  // arrivals above land before this CTA ends
         if (!bar_drain(&ctl.drain, 0)) raise(a.status, AFX_DEV_UNDRAINED);
-      }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsSums));
-        const uint32_t quarter = warp % 4, half = warp / 4;
-        const uint32_t column0 = half * (BN / 2), lanes = quarter * 32;
+      } else if (warp == kFactorWarp) {
+        // four tokens a lane, their scales loaded four steps at a time while the four before are used (a register that
+        // is handed on each step waits for its load each step); the row blocks' for 32 steps, a lane a step
+        constexpr uint32_t kScales = T::kProducts * T::kRowBlocks, kAhead = 4;
         uint32_t it = 0;
         bool ok = true;
         for (uint32_t tile = first; ok && tile < a.tiles; tile += stride) {
-            const uint32_t t0 = tile % a.tiles_m * kTokens, r0 = tile / a.tiles_m * BN + column0;
+            const uint32_t t0 = tokens_of(tile), r0 = rows_of(tile);
+            float x[kAhead][4], x_next[kAhead][4], w[kScales], w_next[kScales];
+            auto x_scales = [&](uint32_t s) {
+#pragma unroll
+                for (uint32_t j = 0; j < kAhead; ++j)
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        const uint32_t t = t0 + lane + 32 * i;
+                        x_next[j][i] = t < a.n_tokens && s + j < step1 ? __ldg(a.x_scales + (s + j) * a.x_scale_stride + t) : 0.0f;
+                    }
+            };
+            auto w_scales = [&](uint32_t s) {
+#pragma unroll
+                for (uint32_t i = 0; i < kScales; ++i) {
+                    const uint32_t rb = min((r0 + i / T::kRowBlocks * N) / kBlock + i % T::kRowBlocks, a.row_blocks - 1);
+                    w_next[i] = s + lane < step1 ? __ldg(a.w_scales + static_cast<uint64_t>(rb) * a.blocks + s + lane) : 0.0f;
+                }
+            };
+            x_scales(step0);
+            w_scales(step0);
+            for (uint32_t s0 = step0; ok && s0 < step1; s0 += kAhead) {
+                const uint32_t in32 = (s0 - step0) & 31u;
+                if (in32 == 0) {
+#pragma unroll
+                    for (uint32_t i = 0; i < kScales; ++i) w[i] = w_next[i];
+                    w_scales(s0 + 32);
+                }
+#pragma unroll
+                for (uint32_t j = 0; j < kAhead; ++j)
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) x[j][i] = x_next[j][i];
+                x_scales(s0 + kAhead);
+#pragma unroll
+                for (uint32_t j = 0; j < kAhead; ++j) {
+                    if (s0 + j >= step1) break;
+#pragma unroll
+                    for (uint32_t h = 0; h < T::kProducts; ++h, ++it) {
+                        const uint32_t buf = it % kBufs;
+                        ok = ok && __all_sync(0xFFFFFFFFu, it < kBufs || bar_wait(&ctl.factors_empty[buf], (it / kBufs - 1) & 1u, ctl, a.status));
+                        if (!ok) break;
+#pragma unroll
+                        for (uint32_t i = 0; i < T::kRowBlocks; ++i) {
+                            const float f = __shfl_sync(0xFFFFFFFFu, w[h * T::kRowBlocks + i], in32 + j);
+#pragma unroll
+                            for (uint32_t c = 0; c < 4; ++c) ctl.factors[buf][i][lane + 32 * c] = x[j][c] * f;
+                        }
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&ctl.sums_full[buf]);
+                    }
+                    if (!ok) break;
+                }
+            }
+        }
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsSums));
+        // a CTA alone: half of the columns; a pair: one of a step's two products
+        const uint32_t lanes = warp % 4 * 32, half = warp / 4;
+        const uint32_t column0 = kPair ? 0 : half * T::kColumns;  // in a buffer
+        const uint32_t row_in_tile = half * T::kColumns;          // the same of W, in a pair's tile too
+        uint32_t it = 0;
+        bool ok = true;
+        for (uint32_t tile = first; ok && tile < a.tiles; tile += stride) {
+            const uint32_t t0 = tokens_of(tile), r0 = rows_of(tile) + row_in_tile;
             const uint32_t token = t0 + lanes + lane;
             const bool any = t0 + lanes < a.n_tokens, real = token < a.n_tokens;
+            const uint32_t rb0 = kPair ? r0 / kBlock : 0;
             uint64_t sum[T::kRuns][16];
 #pragma unroll
             for (uint32_t r = 0; r < T::kRuns; ++r)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sum[r][i] = 0;
-            // a token's scales two steps ahead; the row blocks' for 32 steps, a lane a step
-            const float* xs = a.x_scales + (real ? token : 0);
-            auto x_scale = [&](uint32_t s) { return real && s < step1 ? __ldg(xs + s * a.x_scale_stride) : 0.0f; };
-            float now = x_scale(step0), next = x_scale(step0 + 1);
-            const uint32_t rb0 = min(r0 / kBlock, a.row_blocks - 1), rb1 = min((r0 + BN / 2 - 1) / kBlock, a.row_blocks - 1);
-            auto w_scale = [&](uint32_t rb, uint32_t s) { return s + lane < step1 ? __ldg(a.w_scales + static_cast<uint64_t>(rb) * a.blocks + s + lane) : 0.0f; };
-            float w0 = w_scale(rb0, step0), w1 = w_scale(rb1, step0), w0_next = w_scale(rb0, step0 + 32), w1_next = w_scale(rb1, step0 + 32);
             for (uint32_t s = step0; s < step1; ++s, ++it) {
-                const uint32_t buf = it & 1u, in32 = (s - step0) & 31u;
-                if (in32 == 0 && s != step0) {
-                    w0 = w0_next, w1 = w1_next;
-                    w0_next = w_scale(rb0, s + 32), w1_next = w_scale(rb1, s + 32);
-                }
-                const float later = x_scale(s + 2);
-                const float f0 = now * __shfl_sync(0xFFFFFFFFu, w0, in32), f1 = now * __shfl_sync(0xFFFFFFFFu, w1, in32);
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.sums_full[buf], it >> 1 & 1u, ctl, a.status));
+                const uint32_t unit = kPair ? 2 * it + half : it, buf = unit % kBufs;
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.sums_full[buf], unit / kBufs & 1u, ctl, a.status));
                 if (!ok) break;
                 fence_after();
+                const uint32_t empty = kPair ? peer_addr(smem_addr(&ctl.sums_empty[buf]), head) : smem_addr(&ctl.sums_empty[buf]);
+                auto release = [&] {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive_cluster(empty);
+                        bar_arrive(&ctl.factors_empty[buf]);
+                    }
+                };
                 if (any) {
-                    const uint32_t from = tmem + (lanes << 16) + buf * BN + column0;
-                    uint32_t v[2][32];
-                    tmem_load32(from, v[0]);
+                    const uint32_t from = tmem + (lanes << 16) + buf * N + column0;
+                    const float f0 = ctl.factors[buf][0][lanes + lane], f1 = T::kRowBlocks > 1 ? ctl.factors[buf][1][lanes + lane] : f0;
 #pragma unroll
                     for (uint32_t r = 0; r < T::kRuns; ++r) {
-                        wait_columns(v[r & 1]);
-                        if (r + 1 < T::kRuns) tmem_load32(from + (r + 1) * 32, v[(r + 1) & 1]);
-                        const float f = (r0 + r * 32) / kBlock == rb0 ? f0 : f1;
+                        uint64_t v[16];
+                        load_pairs(from + r * 32, v);
+                        if (r + 1 == T::kRuns) release();  // all have been read
+                        const float f = T::kRowBlocks == 1 || (r0 + r * 32) / kBlock == rb0 ? f0 : f1;
                         const uint64_t ff = pack2(f, f);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            sum[r][i] = fma2(pack2(__uint_as_float(v[r & 1][2 * i]), __uint_as_float(v[r & 1][2 * i + 1])), ff, sum[r][i]);
+                        for (int i = 0; i < 16; ++i) sum[r][i] = fma2(v[i], ff, sum[r][i]);
                     }
+                } else {
+                    release();
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&ctl.sums_empty[buf]);
-                now = next, next = later;
             }
             if (!ok) break;
             if (a.split > 1) {  // into shared memory, whose copies and products are all done with
                 if (real) {
-                    float* part = reinterpret_cast<float*>(w_ring) + (lanes + lane) * T::kPartRow + column0;
+                    float* to = reinterpret_cast<float*>(w_ring) + (lanes + lane) * T::kPartRow + row_in_tile;
 #pragma unroll
                     for (uint32_t r = 0; r < T::kRuns; ++r)
 #pragma unroll
@@ -367,7 +517,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
                             float4 f;
                             unpack2(sum[r][i], &f.x, &f.y);
                             unpack2(sum[r][i + 1], &f.z, &f.w);
-                            *reinterpret_cast<float4*>(part + r * 32 + i * 2) = f;
+                            *reinterpret_cast<float4*>(to + r * 32 + i * 2) = f;
                         }
                 }
             } else if (any) {
@@ -399,7 +549,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
                         continue;
                     }
                     // a token's 32 rows by 32 lanes, through shared memory
-                    float* stage = staging + warp * (32 * 33);
+                    float* stage = staging + warp * kStageFloats;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) unpack2(sum[r][i], &stage[lane * 33 + 2 * i], &stage[lane * 33 + 2 * i + 1]);
                     __syncwarp();
@@ -417,22 +567,42 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
     __syncthreads();
     if (warp == kMmaWarp) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(T::kColumns) : "memory");
+        if constexpr (kPair)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(T::kTmem) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(T::kTmem) : "memory");
     }
+    if (kPair || a.split > 1) cluster_sync();  // every CTA's sums are there, and no arrival is to come
     if (a.split > 1) {
         cg::cluster_group cluster = cg::this_cluster();
-        cluster.sync();  // every CTA's sums are there
-        const uint32_t t0 = first % a.tiles_m * kTokens, r0 = first / a.tiles_m * BN;
-        const uint32_t tokens = min(kTokens, a.n_tokens - t0);
-        const float* part = reinterpret_cast<const float*>(w_ring);
-        for (uint32_t e = rank * kProductThreads + threadIdx.x; e < tokens * BN; e += a.split * kProductThreads) {
-            const uint32_t t = e / BN, c = e % BN;
+        const uint32_t t0 = tokens_of(first), r0 = rows_of(first);
+        const uint32_t tokens = t0 < a.n_tokens ? min(kTokens, a.n_tokens - t0) : 0;
+        const float* sums = reinterpret_cast<const float*>(w_ring);
+        for (uint32_t e = (part * kProductThreads + threadIdx.x) * 4; e < tokens * T::kRows; e += a.split * kProductThreads * 4) {
+            const uint32_t t = e / T::kRows, c = e % T::kRows;
             if (r0 + c >= a.rows) continue;
-            float sum = 0.0f;
-            for (uint32_t i = 0; i < a.split; ++i) sum += *cluster.map_shared_rank(part + t * T::kPartRow + c, i);
-            store_one(a, static_cast<uint64_t>(t0 + t) * a.y_stride + r0 + c, sum);
+            float4 v[kMostSplit];
+#pragma unroll
+            for (uint32_t i = 0; i < kMostSplit; ++i)
+                if (i < a.split) v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums + t * T::kPartRow + c, kPair ? 2 * i + side : i));
+            float4 sum = v[0];
+#pragma unroll
+            for (uint32_t i = 1; i < kMostSplit; ++i)
+                if (i < a.split) sum.x += v[i].x, sum.y += v[i].y, sum.z += v[i].z, sum.w += v[i].w;
+            const uint64_t at = static_cast<uint64_t>(t0 + t) * a.y_stride + r0 + c;
+            const float of[4] = {sum.x, sum.y, sum.z, sum.w};
+            if (a.sectors) {  // rows are a multiple of 32
+                if (a.y_type == AFX_TYPE_F32)
+                    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.y) + at) = sum;
+                else
+                    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + at) = make_uint2(two_16(a.y_type, of[0], of[1]), two_16(a.y_type, of[2], of[3]));
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i)
+                    if (r0 + c + i < a.rows) store_one(a, at + i, of[i]);
+            }
         }
-        cluster.sync();  // no CTA ends while its sums are read
+        cluster_sync();  // no CTA ends while its sums are read
     }
 }
 
@@ -454,46 +624,119 @@ afx_status byte_map(CUtensorMap* map, const uint8_t* p, uint32_t rows, uint32_t 
     return AFX_OK;
 }
 
-constexpr uint32_t kStagingBytes = kSumWarps * 32 * 33 * sizeof(float);
+constexpr uint32_t kStagingBytes = kSumWarps * kStageFloats * sizeof(float);
 
-template <int BN>
-afx_status launch_product(ProductArgs& a, uint32_t grid, cudaStream_t s) {
-    using T = Tile<BN>;
-    const uint32_t fixed = 1024 + 1024 + (kTokens - a.box) * kBlock + (a.sectors || a.split > 1 ? 0 : kStagingBytes);
-    const uint32_t step = T::kWBytes + a.box * kBlock;
-    a.stages = (kSmemMost - fixed) / step;
-    if (a.stages > kMostStages) a.stages = kMostStages;
-    // the sums of a CTA of several lie over the ring
-    static_assert(kTokens * T::kPartRow * sizeof(float) <= 3 * (T::kWBytes + kTokens * kBlock), "sums fit the ring");
-    // the warps with the sums wait for the registers that they ask for: they must be there
-    static std::once_flag once;
-    static int regs = 0;
-    std::call_once(once, [] {
-        cudaFuncAttributes f{};
-        if (cudaFuncGetAttributes(&f, fp8_product_kernel<BN>) == cudaSuccess)
-            regs = f.numRegs;
-        else
-            cudaGetLastError();
-    });
-    if (regs < kRegsLaunch) return afx_fail(AFX_E_CUDA, "fp8_product_kernel was built with too few registers", 0);
-    AFX_SERVE_TRY(cudaFuncSetAttribute(fp8_product_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMost)),
-                  "cudaFuncSetAttribute");
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kProductThreads);
-    cfg.dynamicSmemBytes = kSmemMost;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2] = {};
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = a.split;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    AFX_SERVE_TRY(cudaLaunchKernelEx(&cfg, fp8_product_kernel<BN>, a), "fp8_product_kernel launch");
-    return AFX_OK;
-}
+// How a product is cut: by tiles of `rows` rows of W (a pair's: of 256 tokens), `split` CTAs or pairs to each.
+struct Cut {
+    uint32_t n;  // rows of one product
+    bool pair;
+    uint32_t split;
+};
+
+template <uint32_t N, bool kPair>
+struct Launch {
+    using T = Tile<N, kPair>;
+
+    // Clusters of this kernel that run at once on the current device; asked once a device.
+    static uint32_t at_once(uint32_t split, int sms) {
+        constexpr int kDevices = 16;
+        static std::atomic<uint32_t> known[kDevices][kMostSplit + 1];
+        const uint32_t size = split * (kPair ? 2 : 1);
+        if (size == 1) return sms;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+        std::atomic<uint32_t>* k = dev < kDevices ? &known[dev][split] : nullptr;
+        if (k)
+            if (const uint32_t v = k->load(std::memory_order_relaxed)) return v - 1;
+        int n = 0;
+        if (prepare() == AFX_OK) {
+            cudaLaunchAttribute at[2];
+            cudaLaunchConfig_t cfg = config(size, size, nullptr, at);
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, fp8_product_kernel<N, kPair>, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+        }
+        if (k) k->store(static_cast<uint32_t>(n) + 1, std::memory_order_relaxed);
+        return static_cast<uint32_t>(n);
+    }
+    static cudaLaunchConfig_t config(uint32_t grid, uint32_t cluster, cudaStream_t s, cudaLaunchAttribute (&at)[2]) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(kProductThreads);
+        cfg.dynamicSmemBytes = kSmemMost;
+        cfg.stream = s;
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = cluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 2;
+        return cfg;
+    }
+    static afx_status prepare() {
+        // the warps with the sums wait for the registers that they ask for: they must be there
+        static std::once_flag once;
+        static int regs = 0;
+        std::call_once(once, [] {
+            cudaFuncAttributes f{};
+            if (cudaFuncGetAttributes(&f, fp8_product_kernel<N, kPair>) == cudaSuccess)
+                regs = f.numRegs;
+            else
+                cudaGetLastError();
+        });
+        if (regs < kRegsLaunch) return afx_fail(AFX_E_CUDA, "fp8_product_kernel was built with too few registers", 0);
+        AFX_SERVE_TRY(cudaFuncSetAttribute(fp8_product_kernel<N, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMost)),
+                      "cudaFuncSetAttribute");
+        return AFX_OK;
+    }
+    // cycles, roughly: a step's products take 2 N a CTA each, its loads arrive at 60 bytes a cycle; and what a wave
+    // and a join take besides
+    static void consider(const ProductArgs& a, int sms, Cut* best, double* least) {
+        const uint32_t tokens = (kPair ? 2 : 1) * kTokens, tiles_m = ceil_div(a.n_tokens, tokens);
+        const uint64_t tiles = static_cast<uint64_t>(tiles_m) * ceil_div(a.rows, T::kRows);
+        const uint32_t box = kPair || a.n_tokens >= kTokens ? kTokens : ceil_div(a.n_tokens, 8) * 8;
+        const double products = 2.2 * T::kRows, loads = (T::kWBytes + box * kBlock) / 60.0, step = products > loads ? products : loads;
+        for (uint32_t split = 1; split <= kMostSplit / (kPair ? 2 : 1) && split <= a.blocks; ++split) {
+            const uint32_t slots = at_once(split, sms);
+            if (slots == 0 || (split > 1 && tiles > slots)) continue;
+            const double waves = static_cast<double>((tiles + slots - 1) / slots);
+            double cost = waves * (ceil_div(a.blocks, split) * step + 1000.0) + (split > 1 ? 2500.0 : 0.0);
+            // W from memory, at what all SMs get of it
+            const double memory = static_cast<double>(a.rows) * a.blocks * kBlock / 3400.0 + 3000.0;
+            if (cost < memory) cost = memory + 0.05 * cost;
+            if (cost < *least) *least = cost, *best = Cut{N, kPair, split};
+        }
+    }
+    static afx_status go(ProductArgs& a, uint32_t split, const uint8_t* w, uint32_t cols, uint64_t w_stride, const uint8_t* x, uint64_t x_stride, int sms,
+                         cudaStream_t s) {
+        a.split = split;
+        const uint32_t group = split * (kPair ? 2 : 1);
+        a.tiles_m = ceil_div(a.n_tokens, (kPair ? 2 : 1) * kTokens);
+        const uint64_t tiles = static_cast<uint64_t>(a.tiles_m) * ceil_div(a.rows, T::kRows);
+        if (tiles > INT32_MAX / 16) return afx_fail(AFX_E_ARG, "the result has too many tiles", 0);
+        a.tiles = static_cast<uint32_t>(tiles);
+        a.box = kPair || a.n_tokens >= kTokens ? kTokens : ceil_div(a.n_tokens, 8) * 8;
+        const uint32_t fixed = 1024 + kCtlBytes + (kTokens - a.box) * kBlock + (a.sectors || split > 1 ? 0 : kStagingBytes);
+        a.stages = (kSmemMost - fixed) / (T::kWBytes + a.box * kBlock);
+        if (a.stages > kMostStages) a.stages = kMostStages;
+        // the sums of a CTA of several lie over the ring, which holds as many steps with fewer tokens
+        static_assert(kTokens * T::kPartRow * sizeof(float) <= (kSmemMost - 1024 - kCtlBytes) / (T::kWBytes + kTokens * kBlock) * (T::kWBytes + kTokens * kBlock),
+                      "sums fit the ring");
+        afx_status st = prepare();
+        if (st == AFX_OK) st = byte_map(&a.x, x, a.n_tokens, cols, x_stride, a.box);
+        if (st == AFX_OK) st = byte_map(&a.w, w, a.rows, cols, w_stride, kPair ? N / 2 : N);
+        if (st != AFX_OK) return st;
+        const uint32_t slots = split > 1 ? a.tiles : at_once(1, sms);
+        if (slots == 0) return afx_fail(AFX_E_CUDA, "no cluster of fp8_product_kernel fits this device", 0);
+        cudaLaunchAttribute at[2] = {};
+        const cudaLaunchConfig_t cfg = config((a.tiles < slots ? a.tiles : slots) * group, group, s, at);
+        AFX_SERVE_TRY(cudaLaunchKernelEx(&cfg, fp8_product_kernel<N, kPair>, a), "fp8_product_kernel launch");
+        return AFX_OK;
+    }
+};
 
 }  // namespace
 }  // namespace serve
@@ -577,34 +820,23 @@ extern "C" afx_status afx_fp8_product(const uint8_t* w_dev, uint64_t w_stride, c
     a.rows = rows;
     a.blocks = ceil_div(cols, kBlock);
     a.row_blocks = ceil_div(rows, kBlock);
-    a.tiles_m = ceil_div(n_tokens, kTokens);
-    a.box = n_tokens >= kTokens ? kTokens : ceil_div(n_tokens, 8) * 8;
     a.y_type = y_type;
     a.sectors = rows % 32 == 0 && !((reinterpret_cast<uintptr_t>(y_dev) | (n_tokens > 1 ? y_stride * size : 0)) & 31u);
-    // The tile's rows and the CTAs a tile, by what a wave of CTAs takes in cycles: a step's products take 2 BN, its
-    // loads arrive at 64 bytes a cycle; and what a CTA takes besides
-    uint32_t best_bn = 128, best_split = 1;
-    double best = 1e300;
-    for (uint32_t bn = 64; bn <= 256; bn += 64)
-        for (uint32_t split = 1; split <= kMostSplit && split <= a.blocks; ++split) {
-            const uint64_t ctas = static_cast<uint64_t>(a.tiles_m) * ceil_div(rows, bn) * split;
-            if (split > 1 && ctas > static_cast<uint64_t>(sms)) continue;
-            const double waves = static_cast<double>((ctas + sms - 1) / sms);
-            const double step = 2.0 * bn > (bn + a.box) * 2.0 ? 2.0 * bn : (bn + a.box) * 2.0;
-            const double cost = waves * (ceil_div(a.blocks, split) * step + 500.0 + 2.0 * bn) + (split > 1 ? 1500.0 + 200.0 * split : 0.0);
-            if (cost < best) best = cost, best_bn = bn, best_split = split;
-        }
-    a.split = best_split;
-    const uint64_t tiles = static_cast<uint64_t>(a.tiles_m) * ceil_div(rows, best_bn);
-    if (tiles > INT32_MAX) return afx_fail(AFX_E_ARG, "the result has too many tiles", 0);
-    a.tiles = static_cast<uint32_t>(tiles);
-    const uint32_t grid = a.split > 1 || tiles < static_cast<uint64_t>(sms) ? a.tiles * a.split : static_cast<uint32_t>(sms);
-    afx_status st = byte_map(&a.x, x_dev, n_tokens, cols, x_stride, a.box);
-    if (st == AFX_OK) st = byte_map(&a.w, w_dev, rows, cols, w_stride, best_bn);
-    if (st != AFX_OK) return st;
+    Cut cut{128, false, 1};
+    double least = 1e300;
+    Launch<64, false>::consider(a, sms, &cut, &least);
+    Launch<128, false>::consider(a, sms, &cut, &least);
+    if (n_tokens > kTokens) {
+        Launch<64, true>::consider(a, sms, &cut, &least);
+        Launch<96, true>::consider(a, sms, &cut, &least);
+        Launch<128, true>::consider(a, sms, &cut, &least);
+    }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (best_bn == 64) return launch_product<64>(a, grid, s);
-    if (best_bn == 128) return launch_product<128>(a, grid, s);
-    if (best_bn == 192) return launch_product<192>(a, grid, s);
-    return launch_product<256>(a, grid, s);
+    if (cut.pair) {
+        if (cut.n == 64) return Launch<64, true>::go(a, cut.split, w_dev, cols, w_stride, x_dev, x_stride, sms, s);
+        if (cut.n == 96) return Launch<96, true>::go(a, cut.split, w_dev, cols, w_stride, x_dev, x_stride, sms, s);
+        return Launch<128, true>::go(a, cut.split, w_dev, cols, w_stride, x_dev, x_stride, sms, s);
+    }
+    if (cut.n == 64) return Launch<64, false>::go(a, cut.split, w_dev, cols, w_stride, x_dev, x_stride, sms, s);
+    return Launch<128, false>::go(a, cut.split, w_dev, cols, w_stride, x_dev, x_stride, sms, s);
 }

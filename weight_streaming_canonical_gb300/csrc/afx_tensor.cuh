@@ -33,6 +33,19 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
                  : "memory");
     return done != 0;
 }
+// addr: of this CTA or, by peer_addr, of another one of the cluster.  Not for handing on what lies in memory: a release
+// to the whole cluster takes hundreds of cycles, and tensor memory has fences of its own
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
 // Bounded, without giving up early: for what is in flight.
 __device__ __forceinline__ bool bar_drain(uint64_t* b, uint32_t parity) {
 #pragma unroll 1
