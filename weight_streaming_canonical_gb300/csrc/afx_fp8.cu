@@ -26,9 +26,9 @@
 // products of NH rows each, with buffers of their own.
 //
 // Roles of a CTA's 12 warps: 0-7 the sums (a quarter of the lanes and half of
-// the columns each; they take registers from the others), 8 issues the products
-// (of a pair, the first CTA's), 9 loads by TMA (128-byte rows with the 128-byte
-// swizzle; columns past the matrix are zeros) into a ring of steps, 10 multiplies the
+// the columns each; they take registers from the others), 8 and 9 issue the products
+// (of a pair, the first CTA's), 10 loads by TMA (128-byte rows with the 128-byte
+// swizzle; columns past the matrix are zeros) into a ring of steps, 11 multiplies the
 // tokens' scales with the row blocks' into shared memory.
 // Where tiles are fewer than SMs, a cluster of CTAs shares a tile: each (each pair)
 // takes a run of steps, and their sums are added through distributed shared memory in
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const Quant
 // ---- the product -------------------------------------------------------------------
 
 constexpr uint32_t kTokens = 128;   // of a CTA's tile
-constexpr uint32_t kSumWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kFactorWarp = 10;
+constexpr uint32_t kSumWarps = 8, kMmaWarp = 8, kLoadWarp = 10, kFactorWarp = 11;  // products: two warps
 constexpr int kProductThreads = 384;
 // registers a thread: as launched, then of the warps with the sums and of the
 // others (what the ones add is what the others gave up)
@@ -169,6 +169,14 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Ctl& ctl,
     *reinterpret_cast<volatile int32_t*>(&ctl.abort_flag) = 1;
     raise(status, AFX_DEV_TIMEOUT);
     return false;
+}
+
+// Two barriers at once, tested side by side: a test takes some 180 cycles, also of a barrier that has been through for
+// long.  All of the warp; once: the second one is not meant.
+__device__ __forceinline__ bool bar_wait_both(uint64_t* b, uint32_t parity, uint64_t* c, uint32_t c_parity, bool once, Ctl& ctl, int32_t* status) {
+    const bool first = bar_try(b, parity), second = once || bar_try(c, c_parity);
+    if (__all_sync(0xFFFFFFFFu, first && second)) return true;
+    return __all_sync(0xFFFFFFFFu, bar_wait(b, parity, ctl, status) && (once || bar_wait(c, c_parity, ctl, status)));
 }
 
 // A box of rows of bytes; of a pair, the bytes count at the first CTA's barrier.
@@ -220,23 +228,30 @@ __device__ __forceinline__ void commit_products(uint32_t lane, uint64_t* bar, ui
         commit(lane, bar);
 }
 
-// 32 columns of this thread's lane, as pairs, behind the wait for them: one
-// statement, so that no use of them can be moved before the wait.
-__device__ __forceinline__ void load_pairs(uint32_t addr, uint64_t (&v)[16]) {
-    asm volatile(
-        "{\n .reg .b32 t<32>;\n"
-        " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15, t16, t17, t18, t19, t20, "
-        "t21, t22, t23, t24, t25, t26, t27, t28, t29, t30, t31}, [%16];\n"
-        " tcgen05.wait::ld.sync.aligned;\n"
-        " mov.b64 %0, {t0, t1}; mov.b64 %1, {t2, t3}; mov.b64 %2, {t4, t5}; mov.b64 %3, {t6, t7};\n"
-        " mov.b64 %4, {t8, t9}; mov.b64 %5, {t10, t11}; mov.b64 %6, {t12, t13}; mov.b64 %7, {t14, t15};\n"
-        " mov.b64 %8, {t16, t17}; mov.b64 %9, {t18, t19}; mov.b64 %10, {t20, t21}; mov.b64 %11, {t22, t23};\n"
-        " mov.b64 %12, {t24, t25}; mov.b64 %13, {t26, t27}; mov.b64 %14, {t28, t29}; mov.b64 %15, {t30, t31};\n"
-        "}\n"
-        : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]), "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]),
-          "=l"(v[11]), "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15])
-        : "r"(addr)
-        : "memory");
+// Columns loaded from tensor memory may be used behind wait_columns: they are
+// its operands, so that no use of them is moved before it.
+__device__ __forceinline__ void load_columns(uint32_t addr, uint32_t (&v)[32]) { tmem_load32(addr, v); }
+__device__ __forceinline__ void wait_columns(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void load_columns(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+                 : AFX_R8(v, 0), AFX_R8(v, 8)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void wait_columns(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t two_16(uint32_t type, float lo, float hi) {
@@ -261,6 +276,8 @@ struct Tile {
     static constexpr uint32_t kProducts = kPair ? 2 : 1;         // a step
     static constexpr uint32_t kColumns = kPair ? N : N / 2;      // of a sum warp
     static constexpr uint32_t kRuns = kColumns / 32;             // of them, in runs of 32
+    static constexpr uint32_t kWidth = kRuns < 4 ? 32 : 16;      // of them, loaded at once; and how many loads the
+    static constexpr uint32_t kLoads = kRuns < 4 ? 2 : 1;        // registers hold beside the sums
     static constexpr uint32_t kWBytes = N * kBlock;              // a CTA's part of a step's W
     static constexpr uint32_t kTmem = N * kBufs <= 256 ? 256 : 512;  // columns of tensor memory, a power of two
     static constexpr uint32_t kRowBlocks = N % kBlock && kBlock % N ? 2 : 1;  // that a product's rows are among
@@ -293,14 +310,14 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < a.stages; ++i) {
             bar_init(&ctl.full[i], 1);
-            bar_init(&ctl.empty[i], 1);
+            bar_init(&ctl.empty[i], T::kProducts);
         }
         for (uint32_t i = 0; i < kBufs; ++i) {
             bar_init(&ctl.sums_full[i], 2);  // the products and the factors
             bar_init(&ctl.sums_empty[i], kPair ? 2 * T::kArrivals : T::kArrivals);
             bar_init(&ctl.factors_empty[i], T::kArrivals);
         }
-        bar_init(&ctl.drain, 1);
+        bar_init(&ctl.drain, 2);
         ctl.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -362,35 +379,32 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
         if (!ok && side == 0)  // copies in flight write shared memory
             for (uint32_t q = it > a.stages ? it - a.stages : 0; q < it; ++q)
                 if (!bar_drain(&ctl.full[q % a.stages], q / a.stages & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
-      } else if (warp == kMmaWarp) {
+      } else if (warp < kLoadWarp) {
+        // of a pair's step a product each, else every second step: waiting and issuing take one warp longer than the
+        // products
+        const uint32_t m = warp - kMmaWarp;
         if (side == 0) {
             // float32 sums of E4M3 by E4M3, both with their columns contiguous
             constexpr uint32_t kInstruction = 1u << 4 | (N >> 3) << 17 | ((kPair ? 2 : 1) * kTokens >> 4) << 24;
+            constexpr uint32_t kStride = kPair ? 1 : 2;  // steps
             const bool leader = elect();
-            const uint64_t x_desc = operand(smem_addr(x_ring), 16), w_desc = operand(smem_addr(w_ring), 16);
-            uint32_t it = 0, slot = 0, phase = 0;
-            bool ok = true;
-            for (uint32_t tile = first; ok && tile < a.tiles; tile += stride) {
-                for (uint32_t s = step0; s < step1; ++s) {
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.full[slot], phase, ctl, a.status));
-                    const uint64_t xd = x_desc + slot * (a.box * kBlock >> 4), wd = w_desc + slot * (T::kWBytes >> 4);
+            const uint64_t x_desc = operand(smem_addr(x_ring), 16), w_desc = operand(smem_addr(w_ring) + (kPair ? m * (T::kWBytes / 2) : 0), 16);
+            const uint32_t own = (step1 - step0) * ((a.tiles - first + stride - 1) / stride);  // steps of this CTA's tiles
+            uint32_t slot = kPair ? 0 : m % a.stages, phase = kPair ? 0 : m / a.stages & 1u;
+            for (uint32_t it = kPair ? 0 : m; it < own; it += kStride) {
+                const uint32_t unit = kPair ? 2 * it + m : it, buf = unit % kBufs;
+                if (!bar_wait_both(&ctl.full[slot], phase, &ctl.sums_empty[buf], (unit / kBufs - 1) & 1u, unit < kBufs, ctl, a.status)) break;
+                fence_after();
+                const uint64_t xd = x_desc + slot * (a.box * kBlock >> 4), wd = w_desc + slot * (T::kWBytes >> 4);
 #pragma unroll
-                    for (uint32_t h = 0; h < T::kProducts; ++h, ++it) {
-                        const uint32_t buf = it % kBufs;
-                        ok = ok && __all_sync(0xFFFFFFFFu, it < kBufs || bar_wait(&ctl.sums_empty[buf], (it / kBufs - 1) & 1u, ctl, a.status));
-                        if (!ok) break;
-                        fence_after();
-#pragma unroll
-                        for (uint32_t k = 0; k < kBlock / 32; ++k)
-                            mma_e4m3<kPair>(leader, tmem + buf * N, xd + k * 2, wd + h * (T::kWBytes / 2 >> 4) + k * 2, kInstruction, k != 0);
-                        if (h + 1 == T::kProducts) commit_products<kPair>(leader, &ctl.empty[slot], both);
-                        commit_products<kPair>(leader, &ctl.sums_full[buf], both);
-                    }
-                    if (!ok) break;
-                    if (++slot == a.stages) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
+                for (uint32_t k = 0; k < kBlock / 32; ++k)
+                    mma_e4m3<kPair>(leader, tmem + buf * N, xd + k * 2, wd + k * 2, kInstruction, k != 0);
+                commit_products<kPair>(leader, &ctl.empty[slot], both);
+                commit_products<kPair>(leader, &ctl.sums_full[buf], both);
+                slot += kStride;
+                if (slot >= a.stages) {
+                    slot -= a.stages;
+                    phase ^= 1u;
                 }
             }
             commit_products<kPair>(leader, &ctl.drain, both);  // arrivals above land before a CTA ends
@@ -441,8 +455,11 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
 #pragma unroll
                     for (uint32_t h = 0; h < T::kProducts; ++h, ++it) {
                         const uint32_t buf = it % kBufs;
-                        ok = ok && __all_sync(0xFFFFFFFFu, it < kBufs || bar_wait(&ctl.factors_empty[buf], (it / kBufs - 1) & 1u, ctl, a.status));
-                        if (!ok) break;
+                        if (h == 0 && it >= kBufs) {
+                            const uint32_t parity = (it / kBufs - 1) & 1u;
+                            ok = bar_wait_both(&ctl.factors_empty[buf], parity, &ctl.factors_empty[(buf + 1) % kBufs], parity, !kPair, ctl, a.status);
+                            if (!ok) break;
+                        }
 #pragma unroll
                         for (uint32_t i = 0; i < T::kRowBlocks; ++i) {
                             const float f = __shfl_sync(0xFFFFFFFFu, w[h * T::kRowBlocks + i], in32 + j);
@@ -464,7 +481,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
         const uint32_t column0 = kPair ? 0 : half * T::kColumns;  // in a buffer
         const uint32_t row_in_tile = half * T::kColumns;          // the same of W, in a pair's tile too
         uint32_t it = 0;
-        bool ok = true;
+        bool ok = true, ready = false;
         for (uint32_t tile = first; ok && tile < a.tiles; tile += stride) {
             const uint32_t t0 = tokens_of(tile), r0 = rows_of(tile) + row_in_tile;
             const uint32_t token = t0 + lanes + lane;
@@ -477,9 +494,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
                 for (int i = 0; i < 16; ++i) sum[r][i] = 0;
             for (uint32_t s = step0; s < step1; ++s, ++it) {
                 const uint32_t unit = kPair ? 2 * it + half : it, buf = unit % kBufs;
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.sums_full[buf], unit / kBufs & 1u, ctl, a.status));
+                if (!__all_sync(0xFFFFFFFFu, ready)) ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.sums_full[buf], unit / kBufs & 1u, ctl, a.status));
                 if (!ok) break;
                 fence_after();
+                // the next one's barrier, tested while this one is worked on
+                const uint32_t next_unit = unit + (kPair ? 2 : 1);
+                ready = bar_try_now(&ctl.sums_full[next_unit % kBufs], next_unit / kBufs & 1u);
                 const uint32_t empty = kPair ? peer_addr(smem_addr(&ctl.sums_empty[buf]), head) : smem_addr(&ctl.sums_empty[buf]);
                 auto release = [&] {
                     fence_before();
@@ -492,15 +512,29 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
                 if (any) {
                     const uint32_t from = tmem + (lanes << 16) + buf * N + column0;
                     const float f0 = ctl.factors[buf][0][lanes + lane], f1 = T::kRowBlocks > 1 ? ctl.factors[buf][1][lanes + lane] : f0;
+                    // loads are under way while the columns before are added, where the registers hold both
+                    constexpr uint32_t kWidth = T::kWidth, kPieces = T::kColumns / kWidth;
+                    uint32_t v[T::kLoads][kWidth];
+                    if (T::kLoads > 1) {
+                        load_columns(from, v[0]);
+                        wait_columns(v[0]);
+                    }
 #pragma unroll
-                    for (uint32_t r = 0; r < T::kRuns; ++r) {
-                        uint64_t v[16];
-                        load_pairs(from + r * 32, v);
-                        if (r + 1 == T::kRuns) release();  // all have been read
-                        const float f = T::kRowBlocks == 1 || (r0 + r * 32) / kBlock == rb0 ? f0 : f1;
+                    for (uint32_t q = 0; q < kPieces; ++q) {
+                        const uint32_t next = q + T::kLoads - 1;
+                        if (next < kPieces) {
+                            load_columns(from + next * kWidth, v[next % T::kLoads]);
+                            if (T::kLoads == 1) wait_columns(v[0]);
+                        }
+                        if (q + 1 == kPieces) release();  // all have been read
+                        const float f = T::kRowBlocks == 1 || (r0 + q * kWidth) / kBlock == rb0 ? f0 : f1;
                         const uint64_t ff = pack2(f, f);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) sum[r][i] = fma2(v[i], ff, sum[r][i]);
+                        for (uint32_t i = 0; i < kWidth / 2; ++i) {
+                            uint64_t& to = sum[q * kWidth / 32][q * kWidth % 32 / 2 + i];
+                            to = fma2(pack2(__uint_as_float(v[q % T::kLoads][2 * i]), __uint_as_float(v[q % T::kLoads][2 * i + 1])), ff, to);
+                        }
+                        if (T::kLoads > 1 && next < kPieces) wait_columns(v[next % T::kLoads]);
                     }
                 } else {
                     release();
