@@ -30,7 +30,7 @@
 // (of a pair, the first CTA's), 10 loads by TMA (128-byte rows with the 128-byte
 // swizzle; columns past the matrix are zeros) into a ring of steps, 11 multiplies the
 // tokens' scales with the row blocks' into shared memory.
-// Where tiles are fewer than SMs, a cluster of CTAs shares a tile: each (each pair)
+// Where tiles are fewer than SMs, a cluster of CTAs shares a tile: each
 // takes a run of steps, and their sums are added through distributed shared memory in
 // the order of the CTAs.
 //
@@ -135,7 +135,7 @@ constexpr int kRegsLaunch = 168, kRegsSums = 208, kRegsOther = 88;
 static_assert(256 * kRegsSums + 128 * kRegsOther <= kProductThreads * kRegsLaunch, "register shares");
 constexpr uint32_t kMostStages = 16;
 constexpr uint32_t kSmemMost = 232448;  // 227 KB, what a CTA can have
-constexpr uint32_t kMostSplit = 8;      // CTAs, or pairs up to half of it, that share a tile
+constexpr uint32_t kMostSplit = 8;      // CTAs that share a tile
 constexpr uint32_t kBufs = 4;           // buffers of sums in tensor memory
 
 struct Ctl {
@@ -215,14 +215,14 @@ __device__ __forceinline__ void mma_e4m3(uint32_t lane, uint32_t d, uint64_t a, 
             "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lane)
             : "memory");
 }
-// An arrival at this barrier (of a pair: of both CTAs, `mask`) once the products so far are done.
+// An arrival at this barrier (of a pair: of both CTAs) once the products so far are done.
 template <bool kPair>
-__device__ __forceinline__ void commit_products(uint32_t lane, uint64_t* bar, uint16_t mask) {
+__device__ __forceinline__ void commit_products(uint32_t lane, uint64_t* bar) {
     if constexpr (kPair)
         asm volatile(
             "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
             " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}\n" ::"r"(smem_addr(bar)),
-            "r"(lane), "h"(mask)
+            "r"(lane), "h"(static_cast<uint16_t>(3))
             : "memory");
     else
         commit(lane, bar);
@@ -295,10 +295,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
     uint8_t* x_ring = w_ring + a.stages * T::kWBytes;
     float* staging = reinterpret_cast<float*>(x_ring + a.stages * a.box * kBlock + (kTokens - a.box) * kBlock);  // where !sectors
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // CTAs of a cluster: `split` of them, or pairs
-    const uint32_t group = kPair ? 2 * a.split : a.split, rank = blockIdx.x % group;
-    const uint32_t side = kPair ? rank & 1 : 0, part = kPair ? rank >> 1 : rank, head = rank - side;  // head: the pair's first CTA
-    const uint16_t both = static_cast<uint16_t>(3u << head);
+    // CTAs of a cluster: a pair, or the `split` ones of a tile
+    const uint32_t group = kPair ? 2 : a.split, rank = blockIdx.x % group;
+    const uint32_t side = kPair ? rank : 0, part = kPair ? 0 : rank;
     // a group's tiles: one where several share it, else every gridDim.x / group-th; its steps of a tile
     const uint32_t step0 = static_cast<uint32_t>(static_cast<uint64_t>(a.blocks) * part / a.split),
                    step1 = static_cast<uint32_t>(static_cast<uint64_t>(a.blocks) * (part + 1) / a.split);
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(&ctl.empty[slot], phase ^ 1u, ctl, a.status));
                     if (!ok) break;
                 }
-                const uint32_t bar = kPair ? peer_addr(smem_addr(&ctl.full[slot]), head) : smem_addr(&ctl.full[slot]);
+                const uint32_t bar = kPair ? peer_addr(smem_addr(&ctl.full[slot]), 0) : smem_addr(&ctl.full[slot]);
                 if (leader && side == 0) bar_expect(&ctl.full[slot], (kPair ? 2 : 1) * (T::kWBytes + a.box * kBlock));
                 __syncwarp();
                 const uint32_t w = smem_addr(w_ring + slot * T::kWBytes);
@@ -399,15 +398,15 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
 #pragma unroll
                 for (uint32_t k = 0; k < kBlock / 32; ++k)
                     mma_e4m3<kPair>(leader, tmem + buf * N, xd + k * 2, wd + k * 2, kInstruction, k != 0);
-                commit_products<kPair>(leader, &ctl.empty[slot], both);
-                commit_products<kPair>(leader, &ctl.sums_full[buf], both);
+                commit_products<kPair>(leader, &ctl.empty[slot]);
+                commit_products<kPair>(leader, &ctl.sums_full[buf]);
                 slot += kStride;
                 if (slot >= a.stages) {
                     slot -= a.stages;
                     phase ^= 1u;
                 }
             }
-            commit_products<kPair>(leader, &ctl.drain, both);  // arrivals above land before a CTA ends
+            commit_products<kPair>(leader, &ctl.drain);  // arrivals above land before a CTA ends
         }
         if (!bar_drain(&ctl.drain, 0)) raise(a.status, AFX_DEV_UNDRAINED);
       } else if (warp == kFactorWarp) {
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
                 // the next one's barrier, tested while this one is worked on
                 const uint32_t next_unit = unit + (kPair ? 2 : 1);
                 ready = bar_try_now(&ctl.sums_full[next_unit % kBufs], next_unit / kBufs & 1u);
-                const uint32_t empty = kPair ? peer_addr(smem_addr(&ctl.sums_empty[buf]), head) : smem_addr(&ctl.sums_empty[buf]);
+                const uint32_t empty = kPair ? peer_addr(smem_addr(&ctl.sums_empty[buf]), 0) : smem_addr(&ctl.sums_empty[buf]);
                 auto release = [&] {
                     fence_before();
                     __syncwarp();
@@ -541,7 +540,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
                 }
             }
             if (!ok) break;
-            if (a.split > 1) {  // into shared memory, whose copies and products are all done with
+            if (!kPair && a.split > 1) {  // into shared memory, whose copies and products are all done with
                 if (real) {
                     float* to = reinterpret_cast<float*>(w_ring) + (lanes + lane) * T::kPartRow + row_in_tile;
 #pragma unroll
@@ -607,7 +606,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(T::kTmem) : "memory");
     }
     if (kPair || a.split > 1) cluster_sync();  // every CTA's sums are there, and no arrival is to come
-    if (a.split > 1) {
+    if (!kPair && a.split > 1) {
         cg::cluster_group cluster = cg::this_cluster();
         const uint32_t t0 = tokens_of(first), r0 = rows_of(first);
         const uint32_t tokens = t0 < a.n_tokens ? min(kTokens, a.n_tokens - t0) : 0;
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
             float4 v[kMostSplit];
 #pragma unroll
             for (uint32_t i = 0; i < kMostSplit; ++i)
-                if (i < a.split) v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums + t * T::kPartRow + c, kPair ? 2 * i + side : i));
+                if (i < a.split) v[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums + t * T::kPartRow + c, i));
             float4 sum = v[0];
 #pragma unroll
             for (uint32_t i = 1; i < kMostSplit; ++i)
@@ -660,7 +659,7 @@ afx_status byte_map(CUtensorMap* map, const uint8_t* p, uint32_t rows, uint32_t 
 
 constexpr uint32_t kStagingBytes = kSumWarps * kStageFloats * sizeof(float);
 
-// How a product is cut: by tiles of `rows` rows of W (a pair's: of 256 tokens), `split` CTAs or pairs to each.
+// How a product is cut: tiles for CTAs, `split` to each, or for pairs.
 struct Cut {
     uint32_t n;  // rows of one product
     bool pair;
@@ -726,21 +725,23 @@ struct Launch {
                       "cudaFuncSetAttribute");
         return AFX_OK;
     }
-    // cycles, roughly: a step's products take 2 N a CTA each, its loads arrive at 60 bytes a cycle; and what a wave
-    // and a join take besides
+    // In cycles: a step of a tile (measured with other tiles on all SMs: 400 whatever the rows for up to 64 tokens,
+    // 430 and 500 for 64 and 128 rows by 128 tokens, 900 and 1000 for pairs of 192 and 256), a wave's
+    // start and end and the join of a tile's CTAs.  700 tokens by 5120 rows of 17,408: pairs of 256 rows 70 us, CTAs of 128
+    // 71; 300 by 17,408 of 5120: 46 and 35; 501 by 7168 of 5120: pairs of 192 rows 23.6, of 256 24.9; 1 by 5120 of 5120: three CTAs of 128 rows to a tile
+    // 9.1 us, two 9.9, one 11.7, tiles of 64 rows 11.0.
     static void consider(const ProductArgs& a, int sms, Cut* best, double* least) {
         const uint32_t tokens = (kPair ? 2 : 1) * kTokens, tiles_m = ceil_div(a.n_tokens, tokens);
         const uint64_t tiles = static_cast<uint64_t>(tiles_m) * ceil_div(a.rows, T::kRows);
-        const uint32_t box = kPair || a.n_tokens >= kTokens ? kTokens : ceil_div(a.n_tokens, 8) * 8;
-        const double products = 2.2 * T::kRows, loads = (T::kWBytes + box * kBlock) / 60.0, step = products > loads ? products : loads;
-        for (uint32_t split = 1; split <= kMostSplit / (kPair ? 2 : 1) && split <= a.blocks; ++split) {
+        const double step = kPair ? (N == 96 ? 900.0 : 1000.0) : a.n_tokens <= 64 ? 400.0 : N == 64 ? 430.0 : 500.0;
+        for (uint32_t split = 1; split <= (kPair ? 1 : kMostSplit) && split <= a.blocks; ++split) {
             const uint32_t slots = at_once(split, sms);
             if (slots == 0 || (split > 1 && tiles > slots)) continue;
             const double waves = static_cast<double>((tiles + slots - 1) / slots);
-            double cost = waves * (ceil_div(a.blocks, split) * step + 1000.0) + (split > 1 ? 2500.0 : 0.0);
-            // W from memory, at what all SMs get of it
+            double cost = waves * (ceil_div(a.blocks, split) * step + 600.0) + (split > 1 ? 2000.0 + 100.0 * split : 0.0);
+            // W from memory, at what all SMs get of it; the smaller of the two is hidden in part
             const double memory = static_cast<double>(a.rows) * a.blocks * kBlock / 3400.0 + 3000.0;
-            if (cost < memory) cost = memory + 0.05 * cost;
+            cost = cost > memory ? cost + 0.3 * memory : memory + 0.3 * cost;
             if (cost < *least) *least = cost, *best = Cut{N, kPair, split};
         }
     }
@@ -861,13 +862,11 @@ extern "C" afx_status afx_fp8_product(const uint8_t* w_dev, uint64_t w_stride, c
     Launch<64, false>::consider(a, sms, &cut, &least);
     Launch<128, false>::consider(a, sms, &cut, &least);
     if (n_tokens > kTokens) {
-        Launch<64, true>::consider(a, sms, &cut, &least);
         Launch<96, true>::consider(a, sms, &cut, &least);
         Launch<128, true>::consider(a, sms, &cut, &least);
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (cut.pair) {
-        if (cut.n == 64) return Launch<64, true>::go(a, cut.split, w_dev, cols, w_stride, x_dev, x_stride, sms, s);
         if (cut.n == 96) return Launch<96, true>::go(a, cut.split, w_dev, cols, w_stride, x_dev, x_stride, sms, s);
         return Launch<128, true>::go(a, cut.split, w_dev, cols, w_stride, x_dev, x_stride, sms, s);
     }
