@@ -243,3 +243,19 @@ def test_nothing_to_do(afx):
     afx.afx_fp8_quantize(e((0, 64), device="cuda"), e((0, 64), dtype=torch.uint8, device="cuda"), e((1, 0), device="cuda"))
     w, w_scales = _weights(128, 64, 1)
     afx.afx_fp8_product(w, w_scales, e((0, 64), dtype=torch.uint8, device="cuda"), e((1, 0), device="cuda"), e((0, 128), device="cuda"))
+
+
+def test_rounding_at_borders_of_scales(afx):
+    """Quotients beside the borders between two E4M3 values, for scales from the smallest to the largest and any last bits."""
+    g = torch.Generator().manual_seed(77)
+    rows = 4000
+    scale = torch.exp2(torch.randint(-126, 118, (rows,), generator=g).float()) * (1 + torch.rand(rows, generator=g))
+    top = (scale.double() * 448).clamp(max=3.3e38).float()
+    v = torch.tensor(ref.e4m3_values()[:127])
+    border = ((v[1:] + v[:-1]) / 2)[torch.randint(0, 126, (rows, 127), generator=g)]
+    x = (border * scale.double()[:, None]).float()
+    bits = x.view(torch.int32) + torch.randint(-2, 3, x.shape, generator=g).to(torch.int32)
+    x = torch.minimum(bits.clamp(min=0).view(torch.float32), top[:, None])
+    x = torch.cat([x, top[:, None]], 1).cuda()
+    q, scales = _quantized(afx, x)
+    _check_quantized(x, q, scales)

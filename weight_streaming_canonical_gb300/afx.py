@@ -291,6 +291,17 @@ def _check_out(desc: afx_desc, out) -> None:
         raise ValueError(f"the output must hold n elements of {element_bytes(desc.format)} bytes")
 
 
+_names: dict = {}  # of torch's types: a lookup where str() would make the name anew each time
+
+
+def _name_of(x) -> str:
+    kind = x.dtype
+    name = _names.get(kind)
+    if name is None:
+        name = _names[kind] = str(kind)
+    return name
+
+
 def _dev_ptr(t) -> int:
     if t is None:
         return 0
@@ -310,10 +321,25 @@ def _buf_ptr(t) -> int:
 
 def _stream_handle(stream) -> int:
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone, without a Stream object
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     return getattr(stream, "cuda_stream", stream)
+
+
+_current_stream = None
+
+
+def _find_current_stream():
+    """A function that returns the current stream's handle, of the current device."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle alone, without a Stream object
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    torch.cuda.current_device()  # starts torch's CUDA side, where nothing has yet
+    if raw and device:
+        return lambda: raw(device())
+    return lambda: torch.cuda.current_stream().cuda_stream
 
 
 # ---- C entry points ---------------------------------------------------------
@@ -560,46 +586,30 @@ def afx_prefill_fused_batch(descs, containers_dev, shapes, xs_dev, ys_dev, works
 
 _TYPES = {"torch.bfloat16": AFX_TYPE_BF16, "torch.float16": AFX_TYPE_FP16, "torch.float32": AFX_TYPE_F32}
 _E4M3 = {"torch.uint8": 0, "torch.float8_e4m3fn": 0}
-_names: dict = {}  # of torch's types: a lookup where str() would make the name anew each time
-
-
-def _name_of(x) -> str:
-    kind = x.dtype
-    name = _names.get(kind)
-    if name is None:
-        name = _names[kind] = str(kind)
-    return name
-
-
-def _type_of(x) -> int:
-    """AFX_TYPE_* of a tensor that has been checked to be of one of them."""
-    return _TYPES[_name_of(x)]
-
-
 def _rows(x, name: str, types) -> tuple:
-    """(address, row stride) of a CUDA matrix with contiguous rows."""
-    if not x.is_cuda or x.dim() != 2 or _name_of(x) not in types or (x.stride(1) != 1 and x.shape[1] > 1):
+    """(address, row stride, rows, columns, AFX_TYPE_* or 0) of a CUDA matrix with contiguous rows."""
+    shape, strides = x.shape, x.stride()
+    code = types.get(_name_of(x))
+    if code is None or len(shape) != 2 or not x.is_cuda or (strides[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be a CUDA matrix with contiguous rows, of {', '.join(t.split('.')[1] for t in types)}")
-    return x.data_ptr(), x.stride(0)
+    return x.data_ptr(), strides[0], shape[0], shape[1], code
 
 
-def _block_scales(scales, blocks: int, n: int, name: str) -> tuple:
-    if not scales.is_cuda or scales.dim() != 2 or str(scales.dtype) != "torch.float32" or tuple(scales.shape) != (blocks, n) or \
-            (n > 1 and scales.stride(1) != 1):
-        raise ValueError(f"{name} must be a CUDA float32 matrix [{blocks}][{n}] with contiguous rows")
-    return scales.data_ptr(), scales.stride(0)
+_F32 = {"torch.float32": AFX_TYPE_F32}
 
 
 def afx_fp8_quantize(x, q, scales, stream=None) -> None:
     """Rounds x [tokens][cols] (bfloat16, float16 or float32, rows may be strided) to E4M3 in blocks of 128 columns: q
     uint8 or float8_e4m3fn [tokens][cols or more] (the columns past cols are left as they are), scales float32
     [ceil(cols / 128)][tokens]."""
-    px, pq = _rows(x, "x", _TYPES), _rows(q, "q", _E4M3)
-    n, cols = x.shape
-    if q.shape[0] != n or q.shape[1] < cols:
+    px, x_stride, n, cols, kind = _rows(x, "x", _TYPES)
+    pq, q_stride, q_rows, q_cols, _ = _rows(q, "q", _E4M3)
+    ps, s_stride, s_rows, s_cols, _ = _rows(scales, "scales", _F32)
+    if q_rows != n or q_cols < cols:
         raise ValueError("q must have a row of cols elements or more for each of x")
-    ps = _block_scales(scales, -(-cols // AFX_FP8_BLOCK), n, "scales")
-    _check("afx_fp8_quantize", _lib.afx_fp8_quantize(px[0], _type_of(x), px[1], n, cols, *pq, *ps, _stream_handle(stream)))
+    if s_rows != -(-cols // AFX_FP8_BLOCK) or s_cols != n:
+        raise ValueError(f"scales must be [{-(-cols // AFX_FP8_BLOCK)}][{n}]")
+    _check("afx_fp8_quantize", _lib.afx_fp8_quantize(px, kind, x_stride, n, cols, pq, q_stride, ps, s_stride, _stream_handle(stream)))
 
 
 def afx_fp8_product(w, w_scales, x, x_scales, y, stream=None, status_dev=None) -> None:
@@ -607,16 +617,19 @@ def afx_fp8_product(w, w_scales, x, x_scales, y, stream=None, status_dev=None) -
     w_scales float32 [ceil(rows / 128)][ceil(cols / 128)], contiguous; x [tokens][cols or more] and x_scales
     [ceil(cols / 128)][tokens] as afx_fp8_quantize writes them; y [tokens][rows] bfloat16, float16 or float32.  Rows of
     w and x start on 16 bytes."""
-    pw, px, py = _rows(w, "w", _E4M3), _rows(x, "x", _E4M3), _rows(y, "y", _TYPES)
-    rows, cols = w.shape
-    n = x.shape[0]
-    if x.shape[1] < cols or tuple(y.shape) != (n, rows):
+    pw, w_stride, rows, cols, _ = _rows(w, "w", _E4M3)
+    px, x_stride, n, x_cols, _ = _rows(x, "x", _E4M3)
+    py, y_stride, y_rows, y_cols, kind = _rows(y, "y", _TYPES)
+    ps, s_stride, s_rows, s_cols, _ = _rows(x_scales, "x_scales", _F32)
+    pws, ws_stride, ws_rows, ws_cols, _ = _rows(w_scales, "w_scales", _F32)
+    blocks, row_blocks = -(-cols // AFX_FP8_BLOCK), -(-rows // AFX_FP8_BLOCK)
+    if x_cols < cols or y_rows != n or y_cols != rows:
         raise ValueError("x must have cols columns or more, and y must be [tokens][rows]")
-    blocks = -(-cols // AFX_FP8_BLOCK)
-    if _name_of(w_scales) != "torch.float32" or tuple(w_scales.shape) != (-(-rows // AFX_FP8_BLOCK), blocks):
-        raise ValueError(f"w_scales must be a float32 matrix [{-(-rows // AFX_FP8_BLOCK)}][{blocks}]")
-    ps = _block_scales(x_scales, blocks, n, "x_scales")
-    _check("afx_fp8_product", _lib.afx_fp8_product(*pw, _dev_ptr(w_scales), rows, cols, *px, *ps, n, py[0], _type_of(y), py[1],
+    if s_rows != blocks or s_cols != n:
+        raise ValueError(f"x_scales must be [{blocks}][{n}]")
+    if ws_rows != row_blocks or ws_cols != blocks or (ws_stride != blocks and row_blocks > 1):
+        raise ValueError(f"w_scales must be [{row_blocks}][{blocks}], contiguous")
+    _check("afx_fp8_product", _lib.afx_fp8_product(pw, w_stride, pws, rows, cols, px, x_stride, ps, s_stride, n, py, kind, y_stride,
                                                    _stream_handle(stream), _dev_ptr(status_dev)))
 
 
@@ -648,7 +661,7 @@ def afx_sync(stream=None, timeout_ms: int = 0, status_dev=None) -> tuple[int, in
 
 def _int32_ptr(t, count: int, name: str) -> int:
     """The address of a contiguous CUDA int32 tensor of at least count values."""
-    if str(t.dtype) != "torch.int32" or t.numel() < count:
+    if _name_of(t) != "torch.int32" or t.numel() < count:
         raise ValueError(f"{name} must be an int32 tensor of at least {count} values")
     return _dev_ptr(t)
 
@@ -656,7 +669,7 @@ def _int32_ptr(t, count: int, name: str) -> int:
 def _float_ptr(t, count: int, name: str) -> int:
     if t is None:
         return 0
-    if str(t.dtype) != "torch.float32" or t.numel() != count:
+    if _name_of(t) != "torch.float32" or t.numel() != count:
         raise ValueError(f"{name} must be a float32 tensor of {count} values")
     return _dev_ptr(t)
 
@@ -794,55 +807,57 @@ def rotary(head_dim: int, rotary_dim: int | None = None, base: float = 10_000.0,
     return plan
 
 
-def _positions(positions, plan: afx_rotary, n_tokens: int) -> tuple:
+def _positions(positions, axes: int, n_tokens: int) -> tuple:
     """(address, axis stride) of int32 positions: [n_tokens], or [axes][n_tokens]."""
-    rows = positions if positions.dim() == 2 else positions[None]
-    if not positions.is_cuda or str(positions.dtype) != "torch.int32" or rows.dim() != 2 or rows.shape[0] != plan.n_axes or \
-            rows.shape[1] != n_tokens or (n_tokens > 1 and rows.stride(1) != 1):
-        raise ValueError(f"positions must be a CUDA int32 tensor [{plan.n_axes}][{n_tokens}]")
-    return positions.data_ptr(), rows.stride(0) if plan.n_axes > 1 else n_tokens
+    shape, strides = positions.shape, positions.stride()
+    if len(shape) == 1:
+        shape, strides = (1, *shape), (n_tokens, *strides)
+    if _name_of(positions) != "torch.int32" or not positions.is_cuda or len(shape) != 2 or shape[0] != axes or shape[1] != n_tokens or \
+            (strides[1] != 1 and n_tokens > 1):
+        raise ValueError(f"positions must be a CUDA int32 tensor [{axes}][{n_tokens}]")
+    return positions.data_ptr(), strides[0] if axes > 1 else n_tokens
 
 
-def _heads(x, dim: int, name: str, tokens: int | None = None) -> tuple:
-    """(address, token stride, head stride) of a CUDA tensor [tokens][heads][dim]."""
-    if not x.is_cuda or x.dim() != 3 or x.shape[2] != dim or _name_of(x) not in _TYPES or (tokens is not None and x.shape[0] != tokens):
-        raise ValueError(f"{name} must be a CUDA tensor [tokens][heads][{dim}] of bfloat16, float16 or float32")
-    if x.stride(2) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return x.data_ptr(), x.stride(0), x.stride(1)
+def _heads(x, dim: int, name: str) -> tuple:
+    """(address, token stride, head stride, tokens, heads, AFX_TYPE_*) of a CUDA tensor [tokens][heads][dim]."""
+    shape, strides = x.shape, x.stride()
+    code = _TYPES.get(_name_of(x))
+    if code is None or len(shape) != 3 or not x.is_cuda or shape[2] != dim or strides[2] != 1:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens][heads][{dim}] of bfloat16, float16 or float32, its last dimension contiguous")
+    return x.data_ptr(), strides[0], strides[1], shape[0], shape[1], code
 
 
 def afx_rotate(plan: afx_rotary, positions, x, y, stream=None) -> None:
     """y = x turned by the tokens' positions: x, y [tokens][heads][head_dim] (views allowed; y may be x), positions
     int32 [tokens] or [axes][tokens]."""
-    px = _heads(x, plan.head_dim, "x")
-    py = _heads(y, plan.head_dim, "y", x.shape[0])
-    if x.shape != y.shape:
+    px, xt, xh, n, heads, kind = _heads(x, plan.head_dim, "x")
+    py, yt, yh, y_n, y_heads, y_kind = _heads(y, plan.head_dim, "y")
+    if y_n != n or y_heads != heads:
         raise ValueError("x and y must have the same shape")
-    n = x.shape[0]
-    _check("afx_rotate", _lib.afx_rotate(ctypes.byref(plan), *_positions(positions, plan, n), n, px[0], _type_of(x), *px[1:],
-                                         x.shape[1], py[0], _type_of(y), *py[1:], _stream_handle(stream)))
+    _check("afx_rotate", _lib.afx_rotate(ctypes.byref(plan), *_positions(positions, plan.n_axes, n), n, px, kind, xt, xh, heads, py, y_kind,
+                                         yt, yh, _stream_handle(stream)))
 
 
 def afx_rotate_write(plan: afx_rotary, positions, q, k, v, q_out, cache: afx_kv_cache, slots, stream=None, status_dev=None) -> None:
     """Turns q [tokens][q_heads][head_dim] into q_out (of the cache's type; may be q itself) and k
     [tokens][kv_heads][head_dim] into the cache, with v, at slots (int32 [tokens]).  q, k and v have one type, bfloat16,
     float16 or float32; q and q_out may both be None."""
-    dim, n = cache.head_dim, k.shape[0]
-    pk, pv = _heads(k, dim, "k"), _heads(v, dim, "v", n)
-    if k.shape[1] != cache.kv_heads or v.shape[1] != cache.kv_heads or v.dtype != k.dtype:
-        raise ValueError(f"k and v must have {cache.kv_heads} heads and one type")
+    dim, kv_heads = cache.head_dim, cache.kv_heads
+    pk, kt, kh, n, heads, kind = _heads(k, dim, "k")
+    pv, vt, vh, v_n, v_heads, v_kind = _heads(v, dim, "v")
+    if heads != kv_heads or v_heads != kv_heads or v_n != n or v_kind != kind:
+        raise ValueError(f"k and v must have {kv_heads} heads, the same tokens and one type")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out are both given, or both None")
-    pq = po = (0, 0, 0)
-    heads = 0
+    pq = qt = qh = po = ot = oh = heads = 0
     if q is not None:
-        pq, po, heads = _heads(q, dim, "q", n), _heads(q_out, dim, "q_out", n), q.shape[1]
-        if q.dtype != k.dtype or q_out.shape != q.shape or _KV_FORMATS.get(str(q_out.dtype)) != cache.format:
-            raise ValueError("q must have the type of k and v, and q_out the shape of q and the cache's type")
-    qkv = afx_qkv(pq[0], pk[0], pv[0], *pq[1:], *pk[1:], *pv[1:], _type_of(k), heads, n, 0)
+        pq, qt, qh, q_n, heads, q_kind = _heads(q, dim, "q")
+        po, ot, oh, o_n, o_heads, _ = _heads(q_out, dim, "q_out")
+        if q_kind != kind or q_n != n or o_n != n or o_heads != heads or _KV_FORMATS.get(_name_of(q_out)) != cache.format:
+            raise ValueError("q must have the type and tokens of k and v, and q_out the shape of q and the cache's type")
+    qkv = afx_qkv(pq, pk, pv, qt, qh, kt, kh, vt, vh, kind, heads, n, 0)
     _check("afx_rotate_write", _lib.afx_rotate_write(
-        ctypes.byref(plan), *_positions(positions, plan, n), ctypes.byref(qkv), *po, ctypes.byref(cache),
+        ctypes.byref(plan), *_positions(positions, plan.n_axes, n), ctypes.byref(qkv), po, ot, oh, ctypes.byref(cache),
         _int32_ptr(slots, n, "slots"), _stream_handle(stream), _dev_ptr(status_dev)))
 
 
@@ -873,9 +888,14 @@ def afx_verify_workspace(n_tokens: int, n_requests: int) -> int:
     return int(v.value)
 
 
+_PARAMETERS = {"temperature", "top_k", "top_p", "min_p"}
+
+
 def _sampling(params, requests: int) -> afx_sampling:
-    p = params or {}
-    if not p.keys() <= {"temperature", "top_k", "top_p", "min_p"}:
+    if not params:
+        return afx_sampling()
+    p = params
+    if not p.keys() <= _PARAMETERS:
         raise ValueError("parameters are temperature, top_k, top_p and min_p")
     top_k = p.get("top_k")
     return afx_sampling(_float_ptr(p.get("temperature"), requests, "temperature"),
@@ -892,18 +912,18 @@ def afx_verify(logits, tokens, starts, u, draw_u, out_tokens, counts, workspace_
     top_k (int32 [requests]), each optional, as for afx_sample.  Written: out_tokens int32 [rows], counts int32
     [requests], logprobs float32 [rows] (optional)."""
     requests = starts.numel() - 1
-    pl = _rows(logits, "logits", _TYPES)
-    rows, vocab = logits.shape
-    pd, draft_type = (0, 0), 0
+    pl, stride, rows, vocab, kind = _rows(logits, "logits", _TYPES)
+    pd = draft_stride = draft_kind = 0
     if draft_logits is not None:
-        pd, draft_type = _rows(draft_logits, "draft_logits", _TYPES), _type_of(draft_logits)
-        if draft_logits.shape != logits.shape:
+        pd, draft_stride, draft_rows, draft_vocab, draft_kind = _rows(draft_logits, "draft_logits", _TYPES)
+        if draft_rows != rows or draft_vocab != vocab:
             raise ValueError("draft_logits must have the shape of logits")
     if u is None or draw_u is None:
         raise ValueError("u and draw_u must hold one number in [0, 1) a row and a request")
-    args = afx_verify_args(pl[0], pd[0], pl[1], pd[1], _type_of(logits), draft_type, vocab, requests, rows, 0,
-                           _int32_ptr(starts, requests + 1, "starts"), _int32_ptr(tokens, rows, "tokens"),
-                           _sampling(params, requests), _sampling(draft_params, requests), _float_ptr(u, rows, "u"),
+    sampling = _sampling(params, requests)
+    args = afx_verify_args(pl, pd, stride, draft_stride, kind, draft_kind, vocab, requests, rows, 0,
+                           _int32_ptr(starts, requests + 1, "starts"), _int32_ptr(tokens, rows, "tokens"), sampling,
+                           sampling if draft_params is params else _sampling(draft_params, requests), _float_ptr(u, rows, "u"),
                            _float_ptr(draw_u, requests, "draw_u"))
     _check("afx_verify", _lib.afx_verify(
         ctypes.byref(args), _int32_ptr(out_tokens, rows, "out_tokens"), _int32_ptr(counts, requests, "counts"),

@@ -74,6 +74,23 @@ __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float widen(__half x) { return __half2float(x); }
 
+// x / scale, rounded to float32.  With r the rounded reciprocal and q = x r, q + r (x - q scale) is the rounded quotient
+// (Markstein's theorem) as long as x - q scale is exact, which tiny scales do not allow: those divide.  The scale is the
+// same in all lanes.
+__device__ __forceinline__ void quotients(const float (&x)[4], float scale, float (&q)[4]) {
+    if (scale < 0x1p-90f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = __fdiv_rn(x[i], scale);
+        return;
+    }
+    const float r = __frcp_rn(scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float near = x[i] * r;
+        q[i] = fmaf(r, fmaf(-near, scale, x[i]), near);
+    }
+}
+
 // wide: runs of four elements and bytes are aligned.
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const QuantArgs a, const bool wide) {
@@ -109,8 +126,10 @@ __global__ void __launch_bounds__(kQuantThreads) fp8_quantize_kernel(const Quant
             const float scale = most >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__fdiv_rn(__uint_as_float(most), 448.0f), 0x1p-126f);
             const uint32_t c = (b + j) * kBlock + lane * 4;
             // saturating: a quotient may be 448 and a rounding
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[j][0], scale), __fdiv_rn(v[j][1], scale)), __NV_SATFINITE, __NV_E4M3),
-                           hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[j][2], scale), __fdiv_rn(v[j][3], scale)), __NV_SATFINITE, __NV_E4M3);
+            float q4[4];
+            quotients(v[j], scale, q4);
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q4[0], q4[1]), __NV_SATFINITE, __NV_E4M3),
+                           hi = __nv_cvt_float2_to_fp8x2(make_float2(q4[2], q4[3]), __NV_SATFINITE, __NV_E4M3);
             const uint32_t bytes = lo | hi << 16;
             if (wide && c + 4 <= a.cols) {
                 *reinterpret_cast<uint32_t*>(q + c) = bytes;

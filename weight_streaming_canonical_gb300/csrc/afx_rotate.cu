@@ -16,6 +16,7 @@
 //
 // Bound: HBM bandwidth; each element is read and written once.
 #include <cmath>
+#include <type_traits>
 
 #include "afx_serving.cuh"
 
@@ -27,7 +28,7 @@ afx_status check_cache(const afx_kv_cache* c, uint32_t* shift);  // afx_kv.cu
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kMostTokens = 4;  // of a CTA: a warp works out 8 pairs of 4 tokens at once
+constexpr uint32_t kMostTokens = 4;  // of a CTA
 
 struct Heads {  // one of queries, keys, values
     const uint8_t* src;
@@ -48,10 +49,6 @@ struct RotateArgs {
 };
 
 template <typename T>
-struct alignas(16) Run {  // 8 elements
-    T v[8];
-};
-template <typename T>
 __device__ __forceinline__ float widen(T x);
 template <>
 __device__ __forceinline__ float widen<float>(float x) { return x; }
@@ -68,45 +65,81 @@ __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float x) { return
 template <>
 __device__ __forceinline__ __half narrow<__half>(float x) { return __float2half_rn(x); }
 
-// V elements from byte address p.
+// V elements as they lie in memory: loads of several go out before the first is widened.
 template <typename T, int V>
-__device__ __forceinline__ void load_run(const uint8_t* p, float (&x)[V]) {
-    if constexpr (V == 8) {
-        const Run<T> r = *reinterpret_cast<const Run<T>*>(p);
+struct Raw {
+    uint4 w[V * sizeof(T) / 16];
+    __device__ __forceinline__ void load(const uint8_t* p) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = widen<T>(r.v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = widen<T>(reinterpret_cast<const T*>(p)[i]);
+        for (uint32_t i = 0; i < V * sizeof(T) / 16; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
     }
-}
+    __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+        for (uint32_t i = 0; i < V * sizeof(T) / 16; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    x[i * 4 + j] = __uint_as_float(u[j]);
+                } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                    x[2 * j] = __uint_as_float(u[j] << 16), x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+                    x[2 * j] = f.x, x[2 * j + 1] = f.y;
+                }
+            }
+        }
+    }
+};
+template <typename T>
+struct Raw<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const uint8_t* p) { v = *reinterpret_cast<const T*>(p); }
+    __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = widen<T>(v); }
+};
 template <typename T, int V>
 __device__ __forceinline__ void store_run(uint8_t* p, const float (&x)[V]) {
-    if constexpr (V == 8) {
-        Run<T> r;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r.v[i] = narrow<T>(x[i]);
-        *reinterpret_cast<Run<T>*>(p) = r;
+    if constexpr (V == 1) {
+        *reinterpret_cast<T*>(p) = narrow<T>(x[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
     } else {
+        uint32_t u[4];
 #pragma unroll
-        for (int i = 0; i < V; ++i) reinterpret_cast<T*>(p)[i] = narrow<T>(x[i]);
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                u[j] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+                u[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     }
 }
 
 // V pairs a thread: 8, or 1 where addresses, strides or sizes do not allow 16-byte accesses.
 template <typename In, typename Out, int V>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) rotate_kernel(const __grid_constant__ RotateArgs a) {
     __shared__ __align__(16) float turn[kMostTokens][2][AFX_ROTARY_MAX_PAIRS];  // cosines, sines
+    __shared__ int32_t slot_of[kMostTokens];  // negative: padding
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier();
     let_next_start();
     const uint32_t t0 = blockIdx.x * a.tokens, n = min(a.tokens, a.n_tokens - t0);
     const uint32_t half = a.plan.rotary_dim / 2;
     {
+        if (threadIdx.x < n) {
+            const int32_t slot = a.slots ? __ldg(a.slots + t0 + threadIdx.x) : 0;
+            if (slot >= 0 && a.slots && static_cast<uint32_t>(slot) >= a.n_slots) raise(a.status, AFX_DEV_BAD_PAGE);
+            slot_of[threadIdx.x] = slot;
+        }
         // 8 pairs of 4 tokens a warp: the plan's values are read by all lanes alike (reads of the parameters at
         // addresses of each lane's own take turns) and each lane keeps its pair's
-        const uint32_t t = lane / 8;
-        for (uint32_t c = warp * 8; c < half; c += kThreads / 32 * 8) {
+        for (uint32_t u = warp; u < ceil_div(half, 8) * ceil_div(n, 4); u += kThreads / 32) {
+            const uint32_t c = u % ceil_div(half, 8) * 8, t = u / ceil_div(half, 8) * 4 + lane / 8;
             uint64_t step = 0;
             uint32_t axis = 0;
 #pragma unroll
@@ -134,10 +167,10 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     const bool apart = a.plan.pairs == AFX_ROTARY_HALVES && place < turned;
     const uint32_t e0 = apart ? place * V : 2 * place * V, e1 = apart ? half + place * V : e0 + V;
     const uint32_t heads = a.q.n + a.k.n + a.v.n;
-    constexpr int kAtOnce = 2;
+    constexpr int kAtOnce = V == 8 && sizeof(In) == 4 ? 2 : 4;
     uint32_t t = 0, h = threadIdx.x / places;
     while (t < n) {
-        float x[kAtOnce][2][V];
+        Raw<In, V> raw[kAtOnce][2];
         uint8_t* to[kAtOnce];
         uint32_t of[kAtOnce];  // its token; the highest bit: not turned
 #pragma unroll
@@ -146,26 +179,19 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
             to[j] = nullptr;
             of[j] = t;
             if (t < n) {
-                const bool is_q = h < a.q.n, is_k = !is_q && h < a.q.n + a.k.n;
-                const Heads& s = is_q ? a.q : is_k ? a.k : a.v;
-                const uint32_t in = is_q ? h : is_k ? h - a.q.n : h - a.q.n - a.k.n;
-                const int32_t slot = a.slots ? __ldg(a.slots + t0 + t) : 0;
-                bool real = slot >= 0;  // negative: padding
-                uint64_t dst = static_cast<uint64_t>(t0 + t) * s.dst_token + in * s.dst_head;
-                if (!is_q) {
-                    if (real && static_cast<uint32_t>(slot) >= a.n_slots) {
-                        raise(a.status, AFX_DEV_BAD_PAGE);
-                        real = false;
-                    }
-                    dst = (static_cast<uint32_t>(slot) >> a.shift) * s.dst_page + (static_cast<uint32_t>(slot) & ((1u << a.shift) - 1)) * s.dst_token +
-                          in * s.dst_head;
-                }
-                if (real) {
+                const bool is_q = h < a.q.n, is_v = h >= a.q.n + a.k.n;
+                const Heads& s = is_q ? a.q : is_v ? a.v : a.k;
+                const uint32_t in = is_q ? h : is_v ? h - a.q.n - a.k.n : h - a.q.n;
+                const int32_t slot = slot_of[t];
+                const uint64_t dst = is_q ? static_cast<uint64_t>(t0 + t) * s.dst_token
+                                          : (static_cast<uint32_t>(slot) >> a.shift) * s.dst_page +
+                                                (static_cast<uint32_t>(slot) & ((1u << a.shift) - 1)) * s.dst_token;
+                if (slot >= 0 && (is_q || static_cast<uint32_t>(slot) < a.n_slots)) {
                     const uint8_t* from = s.src + static_cast<uint64_t>(t0 + t) * s.src_token + in * s.src_head;
-                    load_run<In, V>(from + e0 * sizeof(In), x[j][0]);
-                    load_run<In, V>(from + e1 * sizeof(In), x[j][1]);
-                    to[j] = s.dst + dst;
-                    if (place >= turned || (!is_q && !is_k)) of[j] |= 0x80000000u;
+                    raw[j][0].load(from + e0 * sizeof(In));
+                    raw[j][1].load(from + e1 * sizeof(In));
+                    to[j] = s.dst + dst + in * s.dst_head;
+                    if (place >= turned || is_v) of[j] |= 0x80000000u;
                 }
             }
             h += rows;
@@ -173,6 +199,9 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             if (!to[j]) continue;
+            float x[2][V];
+            raw[j][0].get(x[0]);
+            raw[j][1].get(x[1]);
             if (!(of[j] >> 31)) {
                 const float* c = &turn[of[j]][0][place * V];
                 const float* s = &turn[of[j]][1][place * V];
@@ -180,13 +209,13 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
                 if (apart) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        y[0][i] = x[j][0][i] * c[i] - x[j][1][i] * s[i];
-                        y[1][i] = x[j][0][i] * s[i] + x[j][1][i] * c[i];
+                        y[0][i] = x[0][i] * c[i] - x[1][i] * s[i];
+                        y[1][i] = x[0][i] * s[i] + x[1][i] * c[i];
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {  // elements 2 i and 2 i + 1 of the 2 V
-                        const float p = x[j][2 * i / V][2 * i % V], q = x[j][(2 * i + 1) / V][(2 * i + 1) % V];
+                        const float p = x[2 * i / V][2 * i % V], q = x[(2 * i + 1) / V][(2 * i + 1) % V];
                         y[2 * i / V][2 * i % V] = p * c[i] - q * s[i];
                         y[(2 * i + 1) / V][(2 * i + 1) % V] = p * s[i] + q * c[i];
                     }
@@ -194,8 +223,8 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
                 store_run<Out, V>(to[j] + e0 * sizeof(Out), y[0]);
                 store_run<Out, V>(to[j] + e1 * sizeof(Out), y[1]);
             } else {
-                store_run<Out, V>(to[j] + e0 * sizeof(Out), x[j][0]);
-                store_run<Out, V>(to[j] + e1 * sizeof(Out), x[j][1]);
+                store_run<Out, V>(to[j] + e0 * sizeof(Out), x[0]);
+                store_run<Out, V>(to[j] + e1 * sizeof(Out), x[1]);
             }
         }
     }
