@@ -696,7 +696,9 @@ __device__ __forceinline__ void row_choice(const Args& args) {
     // this warp's run: a multiple of 128 tokens long, so that a lane's four are aligned
     const uint32_t run0 = min(n, warp * a.run), run1 = min(n, run0 + a.run);
     auto started = cluster.barrier_arrive();  // a rank's memory may be written once its CTA runs
-    wait_for_earlier();
+    // The records' kernel runs beside the scan that is launched before it: that one's CTAs have all waited for the work
+    // before when this one starts, so there is nothing to wait for but at the end, for the kernel behind
+    if (!kRecord) wait_for_earlier();
     let_next_start();
     uint32_t r = blockIdx.x / ranks;
     uint32_t of_params = r;  // where the row's parameters stand
@@ -1118,6 +1120,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) verify_record_kernel(const __grid_constant__ RecordArgs a) {
     row_choice<T>(a);
+    if (threadIdx.x == 0) wait_for_earlier();
 }
 
 template <typename Args>

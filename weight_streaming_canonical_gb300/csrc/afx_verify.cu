@@ -66,10 +66,28 @@ struct VerifyArgs {
     int32_t* status;
     uint32_t n_requests, n_tokens, vocab, slice, run;
     uint32_t n_parts, part;
-    uint32_t wide[2];
+    uint32_t wide[2], scan_wide[2];  // rows are aligned for four tokens' loads, for 16 bytes'
 };
 
 // ---- one pass over rows that keep all ------------------------------------------------
+
+// 16 bytes of logits
+__device__ __forceinline__ void load_wide(const float* p, float (&x)[4]) { load4(p, x); }
+__device__ __forceinline__ void load_wide(const __nv_bfloat16* p, float (&x)[8]) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load_wide(const __half* p, float (&x)[8]) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {  // two last places off at most
     float y;
@@ -90,7 +108,7 @@ __device__ __forceinline__ void join(Part& a, const Part& b, float inv_t) {
 
 template <typename T>
 __global__ void __launch_bounds__(kScanThreads) verify_scan_kernel(const __grid_constant__ VerifyArgs a, const uint32_t row0) {
-    constexpr uint32_t kRuns = 4;  // of four tokens a thread, in flight
+    constexpr uint32_t kPer = 16 / sizeof(T), kRuns = 4;  // tokens a load, loads in flight
     __shared__ Part warps[kScanThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     wait_for_earlier();
@@ -110,25 +128,25 @@ __global__ void __launch_bounds__(kScanThreads) verify_scan_kernel(const __grid_
     const float inv_t = t > 0.0f ? inverse_temperature(t) : 1.0f;
     const uint32_t at0 = blockIdx.x * a.part, at1 = min(a.vocab, at0 + a.part);
     const T* z = static_cast<const T*>(side.logits) + r * side.row_stride;
-    const bool wide = a.wide[second];
+    const bool wide = a.scan_wide[second];
     Part mine{-INFINITY, 0.0f, 0xFFFFFFFFu, 0};
-    for (uint32_t i0 = at0; i0 < at1; i0 += kScanThreads * 4 * kRuns) {
-        float x[kRuns][4];
+    for (uint32_t i0 = at0; i0 < at1; i0 += kScanThreads * kPer * kRuns) {
+        float x[kRuns][kPer];
 #pragma unroll
         for (uint32_t j = 0; j < kRuns; ++j) {
-            const uint32_t i = i0 + (j * kScanThreads + threadIdx.x) * 4;
-            if (wide && i + 4 <= at1) {
-                load4(z + i, x[j]);
+            const uint32_t i = i0 + (j * kScanThreads + threadIdx.x) * kPer;
+            if (wide && i + kPer <= at1) {
+                load_wide(z + i, x[j]);
             } else {
 #pragma unroll
-                for (uint32_t c = 0; c < 4; ++c) x[j][c] = i + c < at1 ? load_logit(z + i + c) : -INFINITY;
+                for (uint32_t c = 0; c < kPer; ++c) x[j][c] = i + c < at1 ? load_logit(z + i + c) : -INFINITY;
             }
         }
         float top = -INFINITY;
 #pragma unroll
         for (uint32_t j = 0; j < kRuns; ++j)
 #pragma unroll
-            for (uint32_t c = 0; c < 4; ++c) {
+            for (uint32_t c = 0; c < kPer; ++c) {
                 x[j][c] = clean(x[j][c]);
                 top = fmaxf(top, x[j][c]);
             }
@@ -138,8 +156,8 @@ __global__ void __launch_bounds__(kScanThreads) verify_scan_kernel(const __grid_
 #pragma unroll
                 for (uint32_t j = kRuns; j-- > 0;)
 #pragma unroll
-                    for (uint32_t c = 4; c-- > 0;)
-                        if (x[j][c] == top) mine.first = i0 + (j * kScanThreads + threadIdx.x) * 4 + c;
+                    for (uint32_t c = kPer; c-- > 0;)
+                        if (x[j][c] == top) mine.first = i0 + (j * kScanThreads + threadIdx.x) * kPer + c;
             mine.top = fmaxf(mine.top, top);
             continue;
         }
@@ -151,14 +169,14 @@ __global__ void __launch_bounds__(kScanThreads) verify_scan_kernel(const __grid_
 #pragma unroll
             for (uint32_t j = 0; j < kRuns; ++j)
 #pragma unroll
-                for (uint32_t c = 0; c < 4; ++c) mine.infinite += x[j][c] == INFINITY;
+                for (uint32_t c = 0; c < kPer; ++c) mine.infinite += x[j][c] == INFINITY;
             continue;
         }
         float sum[4] = {};
 #pragma unroll
         for (uint32_t j = 0; j < kRuns; ++j)
 #pragma unroll
-            for (uint32_t c = 0; c < 4; ++c) sum[c] += exp2_approx((x[j][c] - mine.top) * inv_t * 1.44269504f);
+            for (uint32_t c = 0; c < kPer; ++c) sum[c % 4] += exp2_approx((x[j][c] - mine.top) * inv_t * 1.44269504f);
         mine.sum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 #pragma unroll
@@ -214,6 +232,7 @@ struct Shared {
     uint64_t warps[2][kWarps];
     uint64_t total[3][2][kMaxCluster];     // every rank's masses, turn by turn
     int32_t first;
+    uint16_t queue[kWarps][kChunk];        // tokens of a chunk that p keeps
 };
 
 __device__ __forceinline__ float log_share(const Kept& p, float z, uint64_t total) {
@@ -438,38 +457,47 @@ __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const __grid_consta
         uint64_t of_run = 0, q_of_run = 0;
         uint32_t k = 0;
         for (uint32_t i0 = run0; i0 < run1; i0 += kChunk, ++k) {
-            float x[kGroups][4], y[kGroups][4];
-            bool any = sums || p.low == -INFINITY;  // all are meant, so both rows' loads go out together
+            uint64_t sum = 0, q_of_chunk = 0;
+            float x[kGroups][4];
 #pragma unroll
             for (uint32_t j = 0; j < kGroups; ++j) load_four(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1, x[j]);
-            if (any)
+            if (sums || p.low == -INFINITY) {  // all are meant, so both rows' loads go out together
+                float y[kGroups][4];
 #pragma unroll
                 for (uint32_t j = 0; j < kGroups; ++j) load_four(q_row, a.wide[1], i0 + j * 128 + lane * 4, run1, y[j]);
-            bool late = !any;
-#pragma unroll
-            for (uint32_t j = 0; j < kGroups; ++j)
-#pragma unroll
-                for (uint32_t c = 0; c < 4; ++c) {
-                    x[j][c] = p.value(x[j][c]);
-                    any |= x[j][c] >= p.low;
-                }
-            uint64_t sum = 0, q_of_chunk = 0;
-            if (__any_sync(0xFFFFFFFFu, any)) {
-                if (late)
-#pragma unroll
-                    for (uint32_t j = 0; j < kGroups; ++j) load_four(q_row, a.wide[1], i0 + j * 128 + lane * 4, run1, y[j]);
                 MassSum s, q_s;
 #pragma unroll
                 for (uint32_t j = 0; j < kGroups; ++j)
 #pragma unroll
                     for (uint32_t c = 0; c < 4; ++c) {
                         const uint32_t i = i0 + j * 128 + lane * 4 + c;
-                        const float wp = p.weight(x[j][c], i), wq = q.weight(q.value(y[j][c]), i);
+                        const float wp = p.weight(p.value(x[j][c]), i), wq = q.weight(q.value(y[j][c]), i);
                         s.add(sums ? wp : fmaxf(p.share(wp) - q.share(wq), 0.0f));
                         q_s.add(wq);
                     }
                 sum = warp_sum(s.total());
                 if (sums) q_of_chunk = warp_sum(q_s.total());
+            } else {  // the tokens that p keeps are few: collected first, so that the lanes work together
+                uint16_t* queue = sh.queue[warp];
+                uint32_t n_q = 0;
+#pragma unroll
+                for (uint32_t j = 0; j < kGroups; ++j)
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c) {
+                        const bool take = p.value(x[j][c]) >= p.low;
+                        const uint32_t taken = __ballot_sync(0xFFFFFFFFu, take);
+                        if (take) queue[n_q + __popc(taken & ((1u << lane) - 1))] = static_cast<uint16_t>(j * 128 + lane * 4 + c);
+                        n_q += __popc(taken);
+                    }
+                __syncwarp();
+                MassSum s;
+                for (uint32_t e = lane; e < n_q; e += 32) {
+                    const uint32_t i = i0 + queue[e];
+                    const float wq = q.weight(q.value(load_logit(q_row + i)), i), wp = p.weight(p.value(load_logit(z_row + i)), i);
+                    s.add(fmaxf(p.share(wp) - q.share(wq), 0.0f));
+                }
+                sum = n_q ? warp_sum(s.total()) : 0;
+                __syncwarp();
             }
             if (lane == 0) sh.chunks[warp][k] = sum;
             of_run += sum, q_of_run += q_of_chunk;
@@ -672,11 +700,13 @@ extern "C" afx_status afx_verify(const afx_verify_args* args, int32_t* out_token
     while (ranks < kMaxCluster && v.vocab / ranks > 4096 && static_cast<uint64_t>(v.n_requests) * ranks <= static_cast<uint64_t>(sms) * 3) ranks *= 2;
     a.slice = ceil_div(ceil_div(v.vocab, ranks), 128) * 128;
     a.run = ceil_div(a.slice, kWarps * kChunk) * kChunk;
-    auto aligned = [&](const void* p, uint64_t stride, uint32_t bytes) {
-        return !((reinterpret_cast<uintptr_t>(p) | (v.n_tokens > 1 ? stride * bytes : 0)) & (4 * bytes - 1));
+    auto aligned = [&](const void* p, uint64_t stride, uint32_t bytes, uint32_t to) {
+        return !((reinterpret_cast<uintptr_t>(p) | (v.n_tokens > 1 ? stride * bytes : 0)) & (to - 1));
     };
-    a.wide[0] = aligned(v.logits_dev, v.row_stride, size);
-    a.wide[1] = v.draft_logits_dev && aligned(v.draft_logits_dev, v.draft_row_stride, draft_size);
+    a.wide[0] = aligned(v.logits_dev, v.row_stride, size, 4 * size);
+    a.scan_wide[0] = aligned(v.logits_dev, v.row_stride, size, 16);
+    a.wide[1] = v.draft_logits_dev && aligned(v.draft_logits_dev, v.draft_row_stride, draft_size, 4 * draft_size);
+    a.scan_wide[1] = v.draft_logits_dev && aligned(v.draft_logits_dev, v.draft_row_stride, draft_size, 16);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (v.n_tokens) {
         // parts of rows: enough CTAs to fill the GPU several times over, with 1024 tokens or more each
