@@ -770,7 +770,8 @@ struct Launch {
         const uint32_t group = split * (kPair ? 2 : 1);
         a.tiles_m = ceil_div(a.n_tokens, (kPair ? 2 : 1) * kTokens);
         const uint64_t tiles = static_cast<uint64_t>(a.tiles_m) * ceil_div(a.rows, T::kRows);
-        if (tiles > INT32_MAX / 16) return afx_fail(AFX_E_ARG, "the result has too many tiles", 0);
+        // a CTA counts its steps in 32 bits
+        if (tiles > INT32_MAX / 16 || (tiles / sms + 1) * 2 * a.blocks > INT32_MAX) return afx_fail(AFX_E_ARG, "the product has too many tiles", 0);
         a.tiles = static_cast<uint32_t>(tiles);
         a.box = kPair || a.n_tokens >= kTokens ? kTokens : ceil_div(a.n_tokens, 8) * 8;
         const uint32_t fixed = 1024 + kCtlBytes + (kTokens - a.box) * kBlock + (a.sectors || split > 1 ? 0 : kStagingBytes);
@@ -807,8 +808,8 @@ extern "C" afx_status afx_fp8_quantize(const void* x_dev, uint32_t type, uint64_
     if (n_tokens > 1 && (x_stride < cols || q_stride < cols)) return afx_fail(AFX_E_ARG, "rows lie at least cols apart", 0);
     if (cols > kBlock && scale_stride < n_tokens) return afx_fail(AFX_E_ARG, "blocks' scales lie at least n_tokens apart", 0);
     const uint32_t size = type == AFX_TYPE_F32 ? 4 : 2;
-    if (!device_ptr(x_dev, size) || !device_ptr(q_dev, 1) || !device_ptr(scales_dev, 4))
-        return afx_fail(AFX_E_ARG, "the arrays must be device memory", 0);
+    if (!device_ptr_here(x_dev, size) || !device_ptr_here(q_dev, 1) || !device_ptr_here(scales_dev, 4))
+        return afx_fail(AFX_E_ARG, "the arrays must be memory of the current device", 0);
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
     QuantArgs a{};
@@ -859,9 +860,9 @@ extern "C" afx_status afx_fp8_product(const uint8_t* w_dev, uint64_t w_stride, c
     if (cols > kBlock && x_scale_stride < n_tokens) return afx_fail(AFX_E_ARG, "blocks' scales lie at least n_tokens apart", 0);
     if (n_tokens > 1 && y_stride < rows) return afx_fail(AFX_E_ARG, "rows of the result lie at least `rows` apart", 0);
     const uint32_t size = y_type == AFX_TYPE_F32 ? 4 : 2;
-    if (!device_ptr(w_dev, 16) || !device_ptr(x_dev, 16)) return afx_fail(AFX_E_ARG, "weights and activations must be 16-byte aligned device memory", 0);
-    if (!device_ptr(w_scales_dev, 4) || !device_ptr(x_scales_dev, 4) || !device_ptr(y_dev, size) || (status_dev && !device_ptr(status_dev, 4)))
-        return afx_fail(AFX_E_ARG, "the arrays must be device memory", 0);
+    if (!device_ptr_here(w_dev, 16) || !device_ptr_here(x_dev, 16)) return afx_fail(AFX_E_ARG, "weights and activations must be 16-byte aligned memory of the current device", 0);
+    if (!device_ptr_here(w_scales_dev, 4) || !device_ptr_here(x_scales_dev, 4) || !device_ptr_here(y_dev, size) || (status_dev && !device_ptr_here(status_dev, 4)))
+        return afx_fail(AFX_E_ARG, "the arrays must be memory of the current device", 0);
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
     ProductArgs a;

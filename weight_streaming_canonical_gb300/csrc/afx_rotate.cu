@@ -330,8 +330,8 @@ extern "C" afx_status afx_rotate(const afx_rotary* rotary, const int32_t* positi
         return afx_fail(AFX_E_ARG, "rows of the result must not overlap", 0);
     if (x_dev == y_dev && (x_type != y_type || (n_tokens > 1 && x_token_stride != y_token_stride) || (heads > 1 && x_head_stride != y_head_stride)))
         return afx_fail(AFX_E_ARG, "in place, types and strides are the same", 0);
-    if (!device_ptr(positions_dev, 4) || !device_ptr(x_dev, type_size(x_type)) || !device_ptr(y_dev, type_size(y_type)))
-        return afx_fail(AFX_E_ARG, "the arrays must be device memory", 0);
+    if (!device_ptr_here(positions_dev, 4) || !device_ptr_here(x_dev, type_size(x_type)) || !device_ptr_here(y_dev, type_size(y_type)))
+        return afx_fail(AFX_E_ARG, "the arrays must be memory of the current device", 0);
     RotateArgs a{};
     a.plan = *rotary;
     a.positions = positions_dev;
@@ -363,11 +363,11 @@ extern "C" afx_status afx_rotate_write(const afx_rotary* rotary, const int32_t* 
         if (in->q_dev == q_out_dev && (in->type != out || (in->n_tokens > 1 && in->q_token_stride != q_out_token_stride) ||
                                        (in->q_heads > 1 && in->q_head_stride != q_out_head_stride)))
             return afx_fail(AFX_E_ARG, "in place, types and strides are the same", 0);
-        if (!device_ptr(in->q_dev, size) || !device_ptr(q_out_dev, 2)) return afx_fail(AFX_E_ARG, "the queries must be device memory", 0);
+        if (!device_ptr_here(in->q_dev, size) || !device_ptr_here(q_out_dev, 2)) return afx_fail(AFX_E_ARG, "the queries must be memory of the current device", 0);
     }
-    if (!device_ptr(positions_dev, 4) || !device_ptr(in->k_dev, size) || !device_ptr(in->v_dev, size) || !device_ptr(slots_dev, 4) ||
-        (status_dev && !device_ptr(status_dev, 4)))
-        return afx_fail(AFX_E_ARG, "positions, keys, values and slots must be device memory", 0);
+    if (!device_ptr_here(positions_dev, 4) || !device_ptr_here(in->k_dev, size) || !device_ptr_here(in->v_dev, size) || !device_ptr_here(slots_dev, 4) ||
+        (status_dev && !device_ptr_here(status_dev, 4)))
+        return afx_fail(AFX_E_ARG, "positions, keys, values and slots must be memory of the current device", 0);
     a.plan = *rotary;
     a.positions = positions_dev;
     a.axis_stride = axis_stride;

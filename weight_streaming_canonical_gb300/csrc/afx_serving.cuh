@@ -32,6 +32,18 @@ inline bool device_ptr(const void* p, uintptr_t align) {
     return at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged;
 }
 
+// The same, and on the current device, where the kernel is going to run.
+inline bool device_ptr_here(const void* p, uintptr_t align) {
+    if (!p || (reinterpret_cast<uintptr_t>(p) & (align - 1))) return false;
+    cudaPointerAttributes at{};
+    int dev = -1;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return at.type == cudaMemoryTypeManaged || (at.type == cudaMemoryTypeDevice && at.device == dev);
+}
+
 inline int current_sms() {
     int dev = -1, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {

@@ -27,6 +27,7 @@
 // first sums their masses.
 #include <cooperative_groups.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "afx_sample.cuh"
@@ -282,9 +283,40 @@ __device__ __forceinline__ void load_four(const T* row, bool wide, uint32_t i, u
         for (uint32_t c = 0; c < 4; ++c) x[c] = i + c < end ? load_logit(row + i + c) : -INFINITY;
     }
 }
+// The same as they lie in memory, so that they can be under way while others are worked on.
+template <typename T>
+struct RawFour {
+    uint32_t w[sizeof(T)];  // 4 sizeof(T) bytes
+    __device__ __forceinline__ void load(const T* row, bool wide, uint32_t i, uint32_t end) {
+        if (wide && i + 4 <= end) {
+            if constexpr (sizeof(T) == 4) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i));
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + i));
+                w[0] = v.x, w[1] = v.y;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) w[c] = i + c < end ? __ldg(reinterpret_cast<const uint32_t*>(row + i + c)) : 0xFF800000u;
+        } else {
+            constexpr uint32_t kNone = std::is_same<T, __half>::value ? 0xFC00u : 0xFF80u;  // minus infinity
+            uint32_t h[4];
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) h[c] = i + c < end ? __ldg(reinterpret_cast<const uint16_t*>(row + i + c)) : kNone;
+            w[0] = h[0] | h[1] << 16, w[1] = h[2] | h[3] << 16;
+        }
+    }
+    __device__ __forceinline__ float get(uint32_t c) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[c]);
+        const uint32_t h = c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xFFFFu;
+        if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+        return __uint_as_float(h << 16);
+    }
+};
 
 template <typename P, typename Q>
-__global__ void __launch_bounds__(kThreads, 3) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(P) + sizeof(Q) > 4 ? 2 : 3) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -420,35 +452,46 @@ __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const __grid_consta
     auto sum_of_p = [&] {
         uint64_t of_run = 0;
         uint32_t k = 0;
-        float x[kGroups][4];
-        auto load = [&](uint32_t i0) {
+        RawFour<P> raw[kGroups], next[kGroups];
+        auto fetch = [&](uint32_t i0, RawFour<P>(&to)[kGroups]) {
 #pragma unroll
-            for (uint32_t j = 0; j < kGroups; ++j) load_four(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1, x[j]);
+            for (uint32_t j = 0; j < kGroups; ++j) to[j].load(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1);
         };
+        fetch(run0, raw);
+        const bool plain = p.low == -INFINITY && p.least == 0.0f && !p.infinite;
+#pragma unroll 1
         for (uint32_t i0 = run0; i0 < run1; i0 += kChunk, ++k) {
-            load(i0);
-            bool any = false;
-#pragma unroll
-            for (uint32_t j = 0; j < kGroups; ++j)
-#pragma unroll
-                for (uint32_t c = 0; c < 4; ++c) {
-                    x[j][c] = p.value(x[j][c]);
-                    any |= x[j][c] >= p.low;
-                }
+            fetch(i0 + kChunk, next);
             uint64_t sum = 0;
-            if (__any_sync(0xFFFFFFFFu, any)) {
+            if (plain && without - i0 >= kChunk) {
                 MassSum s;
 #pragma unroll
                 for (uint32_t j = 0; j < kGroups; ++j)
 #pragma unroll
-                    for (uint32_t c = 0; c < 4; ++c) {
-                        const uint32_t i = i0 + j * 128 + lane * 4 + c;
-                        s.add(i == without ? 0.0f : p.weight(x[j][c], i));
-                    }
+                    for (uint32_t c = 0; c < 4; ++c) s.add(expf((clean(raw[j].get(c)) - p.top) * p.inv_t));
                 sum = warp_sum(s.total());
+            } else {
+                bool any = false;
+#pragma unroll
+                for (uint32_t j = 0; j < kGroups; ++j)
+#pragma unroll
+                    for (uint32_t c = 0; c < 4; ++c) any |= p.value(raw[j].get(c)) >= p.low;
+                if (__any_sync(0xFFFFFFFFu, any)) {
+                    MassSum s;
+#pragma unroll
+                    for (uint32_t j = 0; j < kGroups; ++j)
+#pragma unroll
+                        for (uint32_t c = 0; c < 4; ++c) {
+                            const uint32_t i = i0 + j * 128 + lane * 4 + c;
+                            s.add(i == without ? 0.0f : p.weight(p.value(raw[j].get(c)), i));
+                        }
+                    sum = warp_sum(s.total());
+                }
             }
             if (lane == 0) sh.chunks[warp][k] = sum;
             of_run += sum;
+#pragma unroll
+            for (uint32_t j = 0; j < kGroups; ++j) raw[j] = next[j];
         }
         join_runs(of_run, 0);
     };
@@ -456,22 +499,32 @@ __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const __grid_consta
     auto sum_of_both = [&](bool sums) {
         uint64_t of_run = 0, q_of_run = 0;
         uint32_t k = 0;
+        const bool whole = sums || p.low == -INFINITY;  // all tokens are meant: both rows are read
+        RawFour<P> raw[kGroups], next[kGroups];
+        RawFour<Q> q_raw[kGroups], q_next[kGroups];
+        auto fetch = [&](uint32_t i0, RawFour<P>(&to)[kGroups], RawFour<Q>(&q_to)[kGroups]) {
+#pragma unroll
+            for (uint32_t j = 0; j < kGroups; ++j) to[j].load(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1);
+            if (whole)
+#pragma unroll
+                for (uint32_t j = 0; j < kGroups; ++j) q_to[j].load(q_row, a.wide[1], i0 + j * 128 + lane * 4, run1);
+        };
+        fetch(run0, raw, q_raw);
+#pragma unroll 1
         for (uint32_t i0 = run0; i0 < run1; i0 += kChunk, ++k) {
             uint64_t sum = 0, q_of_chunk = 0;
-            float x[kGroups][4];
+            if (i0 != run0)
 #pragma unroll
-            for (uint32_t j = 0; j < kGroups; ++j) load_four(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1, x[j]);
-            if (sums || p.low == -INFINITY) {  // all are meant, so both rows' loads go out together
-                float y[kGroups][4];
-#pragma unroll
-                for (uint32_t j = 0; j < kGroups; ++j) load_four(q_row, a.wide[1], i0 + j * 128 + lane * 4, run1, y[j]);
+                for (uint32_t j = 0; j < kGroups; ++j) raw[j] = next[j], q_raw[j] = q_next[j];
+            fetch(i0 + kChunk, next, q_next);
+            if (whole) {
                 MassSum s, q_s;
 #pragma unroll
                 for (uint32_t j = 0; j < kGroups; ++j)
 #pragma unroll
                     for (uint32_t c = 0; c < 4; ++c) {
                         const uint32_t i = i0 + j * 128 + lane * 4 + c;
-                        const float wp = p.weight(p.value(x[j][c]), i), wq = q.weight(q.value(y[j][c]), i);
+                        const float wp = p.weight(p.value(raw[j].get(c)), i), wq = q.weight(q.value(q_raw[j].get(c)), i);
                         s.add(sums ? wp : fmaxf(p.share(wp) - q.share(wq), 0.0f));
                         q_s.add(wq);
                     }
@@ -484,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_kernel(const __grid_consta
                 for (uint32_t j = 0; j < kGroups; ++j)
 #pragma unroll
                     for (uint32_t c = 0; c < 4; ++c) {
-                        const bool take = p.value(x[j][c]) >= p.low;
+                        const bool take = p.value(raw[j].get(c)) >= p.low;
                         const uint32_t taken = __ballot_sync(0xFFFFFFFFu, take);
                         if (take) queue[n_q + __popc(taken & ((1u << lane) - 1))] = static_cast<uint16_t>(j * 128 + lane * 4 + c);
                         n_q += __popc(taken);
@@ -625,8 +678,8 @@ uint64_t workspace_bytes_of(uint32_t n_tokens) {
 }
 
 bool sampling_ok(const afx_sampling& s) {
-    return (!s.temperature_dev || device_ptr(s.temperature_dev, 4)) && (!s.top_k_dev || device_ptr(s.top_k_dev, 4)) &&
-           (!s.top_p_dev || device_ptr(s.top_p_dev, 4)) && (!s.min_p_dev || device_ptr(s.min_p_dev, 4));
+    return (!s.temperature_dev || device_ptr_here(s.temperature_dev, 4)) && (!s.top_k_dev || device_ptr_here(s.top_k_dev, 4)) &&
+           (!s.top_p_dev || device_ptr_here(s.top_p_dev, 4)) && (!s.min_p_dev || device_ptr_here(s.min_p_dev, 4));
 }
 
 Side side_of(const void* logits, uint32_t type, uint64_t stride, const afx_sampling& s, Kept* kept) {
@@ -670,12 +723,12 @@ extern "C" afx_status afx_verify(const afx_verify_args* args, int32_t* out_token
         return afx_fail(AFX_E_ARG, "rows of logits lie at least a row apart", 0);
     // no rows: counts of 0 all the same
     const uint32_t size = v.type == AFX_TYPE_F32 ? 4 : 2, draft_size = v.draft_type == AFX_TYPE_F32 ? 4 : 2;
-    if (!device_ptr(v.starts_dev, 4) || !device_ptr(counts_dev, 4) || !device_ptr(v.draw_u_dev, 4) ||
-        (v.n_tokens && (!device_ptr(v.logits_dev, size) || !device_ptr(v.tokens_dev, 4) || !device_ptr(v.u_dev, 4) || !device_ptr(out_tokens_dev, 4) ||
-                        (logprobs_dev && !device_ptr(logprobs_dev, 4)) || (v.draft_logits_dev && !device_ptr(v.draft_logits_dev, draft_size)))) ||
-        !sampling_ok(v.sampling) || (v.draft_logits_dev && !sampling_ok(v.draft_sampling)) || (status_dev && !device_ptr(status_dev, 4)))
-        return afx_fail(AFX_E_ARG, "the arrays must be device memory", 0);
-    if (!device_ptr(workspace_dev, 256)) return afx_fail(AFX_E_ARG, "the workspace must be 256-byte aligned device memory", 0);
+    if (!device_ptr_here(v.starts_dev, 4) || !device_ptr_here(counts_dev, 4) || !device_ptr_here(v.draw_u_dev, 4) ||
+        (v.n_tokens && (!device_ptr_here(v.logits_dev, size) || !device_ptr_here(v.tokens_dev, 4) || !device_ptr_here(v.u_dev, 4) || !device_ptr_here(out_tokens_dev, 4) ||
+                        (logprobs_dev && !device_ptr_here(logprobs_dev, 4)) || (v.draft_logits_dev && !device_ptr_here(v.draft_logits_dev, draft_size)))) ||
+        !sampling_ok(v.sampling) || (v.draft_logits_dev && !sampling_ok(v.draft_sampling)) || (status_dev && !device_ptr_here(status_dev, 4)))
+        return afx_fail(AFX_E_ARG, "the arrays must be memory of the current device", 0);
+    if (!device_ptr_here(workspace_dev, 256)) return afx_fail(AFX_E_ARG, "the workspace must be 256-byte aligned memory of the current device", 0);
     if (workspace_bytes < workspace_bytes_of(v.n_tokens)) return afx_fail(AFX_E_NOSPACE, "the workspace is smaller than afx_verify_workspace", 0);
     const int sms = current_sms();
     if (sms <= 0) return afx_fail(AFX_E_CUDA, "cannot query the SM count", 0);
