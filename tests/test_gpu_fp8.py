@@ -259,3 +259,59 @@ def test_rounding_at_borders_of_scales(afx):
     x = torch.cat([x, top[:, None]], 1).cuda()
     q, scales = _quantized(afx, x)
     _check_quantized(x, q, scales)
+
+
+# shapes whose tiles go to pairs of CTAs: 192 and 256 rows a tile; last tiles of a few tokens or rows, columns that end inside a
+# block, one block, several tiles a pair, long sums
+PAIRS = [(501, 7168, 384), (512, 7296, 1000), (700, 5120, 640), (2000, 9999, 384), (777, 14_000, 1000), (3000, 5000, 128), (700, 5120, 17_408)]
+
+
+@pytest.mark.parametrize("n,rows,cols", PAIRS)
+def test_product_by_pairs(afx, n, rows, cols):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = _activations(n, cols, BF16, n + rows, spread=False)
+    q, x_scales = _quantized(afx, x)
+    w, w_scales = _weights(rows, cols, cols, width=-(-cols // 16) * 16)
+    for kind in (BF16, F32):
+        whole = torch.full((n + 1, rows + 5), 5.0, dtype=kind, device="cuda")
+        for y in (torch.full((n, rows), 77.0, dtype=kind, device="cuda"), whole[:n, 1:rows + 1]):
+            afx.afx_fp8_product(w, w_scales, q, x_scales, y, status_dev=status)
+            _check_product(w, w_scales, q, x_scales, y)
+        assert (whole[n] == 5).all() and (whole[:, 0] == 5).all() and (whole[:, rows + 1:] == 5).all()
+        assert torch.equal(y, _product(afx, w, w_scales, q, x_scales, kind))
+    assert status.item() == 0
+
+
+def test_pairs_with_special_values(afx):
+    x = _activations(700, 384, F32, 1, spread=False)
+    x[300, 7] = float("nan")
+    x[650] = 0
+    q, x_scales = _quantized(afx, x)
+    w, w_scales = _weights(5120, 384, 2)
+    w[3000, 383] = 0x7F
+    w_scales[2, 1] = float("inf")
+    y = _product(afx, w, w_scales, q, x_scales, F32)
+    assert y[300].isnan().all() and y[:, 3000].isnan().all()
+    rest = torch.ones_like(y, dtype=torch.bool)
+    rest[300] = rest[:, 3000] = rest[:, 256:384] = False
+    assert y[rest].isfinite().all() and not y[:300, 256:384].isfinite().any()
+    assert (y[650, :256] == 0).all()
+
+
+def test_products_side_by_side(afx):
+    """Calls on two streams at once, of every shape of tile, have their own results."""
+    sets = []
+    for i, (n, rows, cols) in enumerate([(700, 5120, 640), (501, 7168, 384), (64, 640, 2048), (300, 20_000, 256), (5, 1024, 5120)]):
+        q, x_scales = _quantized(afx, _activations(n, cols, BF16, i, spread=False))
+        sets.append((*_weights(rows, cols, i), q, x_scales))
+    want = [_product(afx, *s, F32) for s in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[torch.empty_like(w) for w in want] for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k, stream in enumerate(streams):
+            for i in range(len(sets)):
+                at = (i + 2 * k) % len(sets)
+                afx.afx_fp8_product(*sets[at], got[k][at], stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for one in got for a, b in zip(one, want))

@@ -284,3 +284,57 @@ def test_a_workspace_too_small_is_refused(afx):
     c = _case([2], 100, F32, F32, 1)
     with pytest.raises(afx.AfxError):
         _run(afx, c, None, extra=-256)
+
+
+def test_more_rows_than_a_grid_has(afx):
+    """16,384 requests of five rows each: the same as in calls of 1024 requests."""
+    n, k, vocab = 16_384, 5, 24
+    c = _case([k - 1] * n, vocab, F32, BF16, 51)
+    params = {"temperature": torch.linspace(0, 2, n, device="cuda"), "top_k": torch.arange(n, dtype=torch.int32, device="cuda") % 9}
+    whole = _run(afx, c, params, params)
+    assert whole["status"].item() == 0 and (whole["counts"] >= 1).all()
+    for r in range(0, n, 1024):
+        part = {key: v[r * k:(r + 1024) * k] if v.shape[0] == n * k else v[r:r + 1024] for key, v in c.items() if key != "starts"}
+        part["starts"] = c["starts"][:1025].clone()
+        p = {key: v[r:r + 1024].clone() for key, v in params.items()}
+        o = _run(afx, part, p, p)
+        assert torch.equal(o["counts"], whole["counts"][r:r + 1024])
+        assert torch.equal(o["tokens"], whole["tokens"][r * k:(r + 1024) * k]) and torch.equal(o["logprobs"], whole["logprobs"][r * k:(r + 1024) * k])
+
+
+def test_two_calls_at_once(afx):
+    cases = [_case([3] * 20, 30_000, kind, kind, 61 + i) for i, kind in enumerate((F32, BF16))]
+    params = _params(20, 7)
+    want = [_run(afx, c, params, params) for c in cases]
+    streams, outs = [torch.cuda.Stream() for _ in cases], []
+    torch.cuda.synchronize()
+    for c, stream in zip(cases, streams):
+        with torch.cuda.stream(stream):
+            outs.append(_run(afx, c, params, params))
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert all(torch.equal(a[k], b[k]) for k in ("tokens", "counts", "logprobs"))
+
+
+def test_min_p_alone_and_flat_rows(afx):
+    """Rows of equal logits, where every boundary lies among ties, and min-p without another cut."""
+    c = _case([2, 3, 1], 3000, F32, F32, 71)
+    for key in ("logits", "draft_logits"):
+        c[key][:4] = 1.25
+    for params in ({"min_p": torch.tensor([0.02, 0.3, 1.0], device="cuda")}, {"top_k": torch.tensor([7, 2999, 3000], dtype=torch.int32, device="cuda")},
+                   {"top_p": torch.tensor([0.3, 0.7, 0.999], device="cuda")}):
+        _check(c, _run(afx, c, params, params), params, params, least_sure=0.3)
+        _check(c, _run(afx, c, params, None), params, None, least_sure=0.3)
+        _check(c, _run(afx, c, None, params), None, params, least_sure=0.3)
+
+
+def test_extreme_temperatures(afx):
+    c = _case([2] * 6, 500, F32, F32, 81)
+    params = {"temperature": torch.tensor([1e-38, 1e-3, 1e30, math.inf, float("nan"), -1.0], device="cuda")}
+    o = _run(afx, c, params, params)
+    assert o["status"].item() == 0 and ((o["tokens"] >= -1) & (o["tokens"] < 500)).all()
+    top = c["logits"].argmax(1).tolist()
+    got = o["tokens"].tolist()
+    for r in (0, 4, 5):  # so cold that the largest logit alone is left, or temperature 0
+        at = 3 * r
+        assert got[at] == top[at]
