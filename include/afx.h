@@ -694,8 +694,8 @@ afx_status afx_rotary_plan(uint32_t head_dim, uint32_t rotary_dim, uint32_t pair
  * Angles are held as 64-bit fractions of a turn, so that a position of any
  * size, negative ones too, loses no accuracy but that of its frequency in 53
  * bits; sines and cosines are those of a 32-bit angle; the pair's products
- * and sums are float32, rounded once to y_type.  y may be x itself (the same address,
- * type and strides); otherwise they must not overlap.  Any strides and
+ * and sums are float32, rounded once to y_type.  y may be x itself (the same
+ * address, type and strides); otherwise they must not overlap.  Any strides and
  * alignment (16-byte aligned rows are fastest); y's rows must not overlap.
  * One launch, asynchronous on stream.  Errors: AFX_E_ARG, AFX_E_CUDA. */
 afx_status afx_rotate(const afx_rotary* rotary, const int32_t* positions_dev, uint64_t axis_stride, uint32_t n_tokens,
@@ -834,8 +834,8 @@ typedef struct afx_sampling {
     const float* min_p_dev;
 } afx_sampling;
 
-/* Request r's rows are starts_dev[r] .. starts_dev[r + 1] - 1, those of its new tokens in the step.
- * Row t was fed tokens_dev[t]; the draft that row t decides on is
+/* Request r's rows are starts_dev[r] .. starts_dev[r + 1] - 1, those of its new
+ * tokens in the step.  Row t was fed tokens_dev[t]; the draft that row t decides on is
  * tokens_dev[t + 1], and the last row has none.  A negative token, or one
  * past the vocabulary, ends the request's drafts before it. */
 typedef struct afx_verify_args {
@@ -868,17 +868,18 @@ afx_status afx_verify_workspace(uint32_t n_tokens, uint32_t n_requests, uint64_t
  * draw_u_dev[r] times the whole; weights are summed as integers of 2^-44.
  * Where nothing is left of max(p_t - q_t, 0) (the draft was none that q_t
  * allows), the draw is from p_t.
- * Written for request r: out_tokens_dev[t], its row by row new tokens: the
+ * Written for request r: out_tokens_dev[t], its new tokens, a row each: the
  * drafts that stand, the token drawn, then -1; counts_dev[r], how many these
- * are; logprobs_dev[t] (nullable), log p_t of each (0 behind the last).  A
- * row to draw from without anything above minus infinity gives token -1 and minus infinity and
- * is not counted.  A request without rows has count 0.  Rows from
+ * are; logprobs_dev[t] (nullable), log p_t of each (0 behind the last).  Where
+ * the row to draw from has nothing above minus infinity, its token is -1, its
+ * log probability minus infinity, and it is not counted.  A request without rows has count 0.  Rows from
  * starts_dev[n_requests] on are left as they are.  Starts that do not begin
  * at 0, fall or pass n_tokens set AFX_DEV_BAD_LENGTH: counts are 0 and
  * nothing else is written.
  * workspace_dev: 256-byte aligned, of at least afx_verify_workspace bytes,
  * contents ignored; calls that overlap on the GPU need their own.  The
- * outputs must not overlap the inputs.  The same call gives the same bits.  Asynchronous on stream.
+ * outputs must not overlap the inputs.  The same call gives the same bits.
+ * Two to four launches, asynchronous on stream.
  * Errors: AFX_E_ARG, AFX_E_NOSPACE, AFX_E_CUDA. */
 afx_status afx_verify(const afx_verify_args* args, int32_t* out_tokens_dev, int32_t* counts_dev, float* logprobs_dev,
                       void* workspace_dev, uint64_t workspace_bytes, afx_stream_t stream, int32_t* status_dev);

@@ -2,10 +2,11 @@
 // (afx_fp8_quantize, afx_fp8_product).
 //
 // fp8_quantize_kernel: for each token and block of 128 columns the largest
-// magnitude a, scale = max(a / 448, 2^-126), values E4M3(x / scale).  A warp a
-// block, four elements a lane, several blocks in flight; the eight warps of a
+// magnitude a, scale = max(a / 448, 2^-126), values E4M3(x / scale).  Half a
+// warp a block, eight elements a lane, four blocks in flight; the eight warps of a
 // CTA take eight tokens, whose scales share a sector.
-// Bound: HBM bandwidth; x is read once.
+// Bound: HBM bandwidth for float32 (8191 tokens of 17,408: 107 us, 6.7 TB/s); for 16 bits the instructions of a block, of
+// which fewer than half depend on its elements (4096 of 17,408, BF16: 46 us, 4.7 TB/s; a warp a block took 65).
 //
 // fp8_product_kernel: y = x W^T in steps of 128 columns, the block of the
 // scales.  A step of a tile is
@@ -42,6 +43,7 @@
 
 #include <atomic>
 #include <cstdio>
+#include <type_traits>
 
 #include "afx_tensor.cuh"
 
@@ -56,7 +58,7 @@ constexpr uint32_t kBlock = AFX_FP8_BLOCK;
 // ---- rounding activations ----------------------------------------------------------
 
 constexpr int kQuantThreads = 256;
-constexpr uint32_t kQuantAtOnce = 4;  // blocks in flight a warp
+constexpr uint32_t kQuantAtOnce = 2;  // pairs of blocks in flight a warp
 
 struct QuantArgs {
     const void* x;
@@ -66,35 +68,73 @@ struct QuantArgs {
     uint32_t n_tokens, cols, blocks, per_cta;  // per_cta: blocks that a CTA does of its eight tokens
 };
 
-template <typename T>
-struct alignas(4 * sizeof(T)) Four {
-    T v[4];
-};
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
-
 // x / scale, rounded to float32.  With r the rounded reciprocal and q = x r, q + r (x - q scale) is the rounded quotient
-// (Markstein's theorem) as long as x - q scale is exact, which tiny scales do not allow: those divide.  The scale is the
-// same in all lanes.
-__device__ __forceinline__ void quotients(const float (&x)[4], float scale, float (&q)[4]) {
+// (Markstein's theorem) as long as x - q scale is exact, which tiny scales do not allow: those divide.
+__device__ __forceinline__ void quotients(const float (&x)[8], float scale, float (&q)[8]) {
     if (scale < 0x1p-90f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = __fdiv_rn(x[i], scale);
+        for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(x[i], scale);
         return;
     }
     const float r = __frcp_rn(scale);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const float near = x[i] * r;
         q[i] = fmaf(r, fmaf(-near, scale, x[i]), near);
     }
 }
 
-// wide: runs of four elements and bytes are aligned.
+// max(a / 448, 2^-126) of a magnitude's bits, the quotient in the same way; NaN for NaN and infinity.
+__device__ __forceinline__ float scale_of(uint32_t bits) {
+    const float a = __uint_as_float(bits);
+    if (bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+    if (a < 0x1p-80f) return fmaxf(__fdiv_rn(a, 448.0f), 0x1p-126f);
+    constexpr float r = 1.0f / 448.0f;
+    const float near = a * r;
+    return fmaf(r, fmaf(-near, 448.0f, a), near);
+}
+
+// Eight elements from i on, of a row's up to end (zeros past it), as they lie in memory.
+template <typename T>
+struct RawEight {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void load(const T* row, bool wide, uint32_t i, uint32_t end) {
+        if (wide && i + 8 <= end) {
+#pragma unroll
+            for (uint32_t k = 0; k < sizeof(T) / 2; ++k) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i) + k);
+                w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (uint32_t c = 0; c < 8; ++c) w[c] = i + c < end ? __ldg(reinterpret_cast<const uint32_t*>(row + i + c)) : 0;
+        } else {
+            const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+            for (uint32_t c = 0; c < 8; c += 2)
+                w[c / 2] = (i + c < end ? __ldg(r + i + c) : 0u) | (i + c + 1 < end ? __ldg(r + i + c + 1) : 0u) << 16;
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (uint32_t c = 0; c < 8; ++c) {
+            if constexpr (sizeof(T) == 4) {
+                x[c] = __uint_as_float(w[c]);
+            } else if constexpr (std::is_same<T, __half>::value) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[c / 2]));
+                x[c] = c % 2 ? f.y : f.x;
+            } else {
+                x[c] = __uint_as_float(c % 2 ? w[c / 2] & 0xFFFF0000u : w[c / 2] << 16);
+            }
+        }
+    }
+};
+
+// Half a warp a block, eight elements a lane.  wide: runs of eight elements are aligned for 16-byte loads, of eight bytes
+// for one store.
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads, 6) fp8_quantize_kernel(const QuantArgs a, const bool wide) {
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in = lane % 16 * 8;
     wait_for_earlier();
     let_next_start();
     const uint32_t t = blockIdx.x * (kQuantThreads / 32) + warp;
@@ -102,43 +142,41 @@ __global__ void __launch_bounds__(kQuantThreads, 6) fp8_quantize_kernel(const Qu
     const T* x = static_cast<const T*>(a.x) + t * a.x_stride;
     uint8_t* q = a.q + t * a.q_stride;
     const uint32_t b0 = blockIdx.y * a.per_cta, b1 = min(a.blocks, b0 + a.per_cta);
-    for (uint32_t b = b0; b < b1; b += kQuantAtOnce) {
-        float v[kQuantAtOnce][4];
+    for (uint32_t first = b0; first < b1; first += 2 * kQuantAtOnce) {
+        RawEight<T> raw[kQuantAtOnce];
 #pragma unroll
         for (uint32_t j = 0; j < kQuantAtOnce; ++j) {
-            const uint32_t c = (b + j) * kBlock + lane * 4;
-            if (wide && b + j < b1 && c + 4 <= a.cols) {
-                const Four<T> f = *reinterpret_cast<const Four<T>*>(x + c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[j][i] = widen(f.v[i]);
-            } else {
-#pragma unroll
-                for (uint32_t i = 0; i < 4; ++i) v[j][i] = b + j < b1 && c + i < a.cols ? widen(x[c + i]) : 0.0f;
-            }
+            if (first + 2 * j >= b1) break;
+            const uint32_t b = min(first + 2 * j + lane / 16, b1 - 1);  // a half without a block reads the other's
+            raw[j].load(x, wide, b * kBlock + in, a.cols);
         }
 #pragma unroll
         for (uint32_t j = 0; j < kQuantAtOnce; ++j) {
-            if (b + j >= b1) break;
+            const uint32_t b = first + 2 * j + lane / 16, c = b * kBlock + in;
+            if (first + 2 * j >= b1) break;
+            float v[8], q8[8];
+            raw[j].get(v);
             uint32_t most = 0;  // of the magnitudes' bits, which NaN and infinity lead
 #pragma unroll
-            for (int i = 0; i < 4; ++i) most = max(most, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
-            most = __reduce_max_sync(0xFFFFFFFFu, most);
-            const float scale = most >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : fmaxf(__fdiv_rn(__uint_as_float(most), 448.0f), 0x1p-126f);
-            const uint32_t c = (b + j) * kBlock + lane * 4;
-            // saturating: a quotient may be 448 and a rounding
-            float q4[4];
-            quotients(v[j], scale, q4);
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q4[0], q4[1]), __NV_SATFINITE, __NV_E4M3),
-                           hi = __nv_cvt_float2_to_fp8x2(make_float2(q4[2], q4[3]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t bytes = lo | hi << 16;
-            if (wide && c + 4 <= a.cols) {
-                *reinterpret_cast<uint32_t*>(q + c) = bytes;
+            for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int d = 8; d; d >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+            const float scale = scale_of(most);
+            quotients(v, scale, q8);
+            uint32_t bytes[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)  // saturating: a quotient may be 448 and a rounding
+                bytes[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q8[4 * i], q8[4 * i + 1]), __NV_SATFINITE, __NV_E4M3)) |
+                           static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q8[4 * i + 2], q8[4 * i + 3]), __NV_SATFINITE, __NV_E4M3)) << 16;
+            if (b >= b1) continue;
+            if (wide && c + 8 <= a.cols) {
+                *reinterpret_cast<uint2*>(q + c) = make_uint2(bytes[0], bytes[1]);
             } else {
 #pragma unroll
-                for (uint32_t i = 0; i < 4; ++i)
-                    if (c + i < a.cols) q[c + i] = static_cast<uint8_t>(bytes >> (8 * i));
+                for (uint32_t i = 0; i < 8; ++i)
+                    if (c + i < a.cols) q[c + i] = static_cast<uint8_t>(bytes[i / 4] >> (8 * (i % 4)));
             }
-            if (lane == 0) a.scales[(b + j) * a.scale_stride + t] = scale;
+            if (in == 0) a.scales[b * a.scale_stride + t] = scale;
         }
     }
 }
@@ -822,14 +860,14 @@ extern "C" afx_status afx_fp8_quantize(const void* x_dev, uint32_t type, uint64_
     a.n_tokens = n_tokens;
     a.cols = cols;
     a.blocks = ceil_div(cols, kBlock);
-    const bool wide = !((reinterpret_cast<uintptr_t>(x_dev) | (n_tokens > 1 ? x_stride * size : 0)) & (4 * size - 1)) &&
-                      !((reinterpret_cast<uintptr_t>(q_dev) | (n_tokens > 1 ? q_stride : 0)) & 3u);
+    const bool wide = !((reinterpret_cast<uintptr_t>(x_dev) | (n_tokens > 1 ? x_stride * size : 0)) & 15u) &&
+                      !((reinterpret_cast<uintptr_t>(q_dev) | (n_tokens > 1 ? q_stride : 0)) & 7u);
     // Eight tokens a CTA; their blocks over as many CTAs as fill the SMs ten times over (8191 tokens of 17,408: 110 us,
     // 132 with CTAs for one filling, 124 with 40), in fours where there are many
     const uint32_t groups = ceil_div(n_tokens, kQuantThreads / 32);
     uint32_t parts = ceil_div(static_cast<uint32_t>(sms) * 64, groups);
     a.per_cta = ceil_div(a.blocks, parts);
-    if (a.per_cta > 1) a.per_cta = ceil_div(a.per_cta, kQuantAtOnce) * kQuantAtOnce;
+    a.per_cta = a.per_cta <= 2 ? 2 : ceil_div(a.per_cta, 2 * kQuantAtOnce) * 2 * kQuantAtOnce;
     parts = ceil_div(a.blocks, a.per_cta);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(groups, parts);

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "afx_internal.h"
 
@@ -83,6 +84,40 @@ __device__ __forceinline__ void raise(int32_t* status, int32_t bits) {
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
+
+// Four elements from i on, of a row's up to end (past it: none), as they lie in
+// memory, so that they can be under way while others are worked on.  wide: the
+// row is aligned for a load of all four.
+template <typename T>
+struct RawFour {
+    uint32_t w[sizeof(T)];  // 4 sizeof(T) bytes
+    __device__ __forceinline__ void load(const T* row, bool wide, uint32_t i, uint32_t end, float none) {
+        if (wide && i + 4 <= end) {
+            if constexpr (sizeof(T) == 4) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i));
+                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            } else {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + i));
+                w[0] = v.x, w[1] = v.y;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) w[c] = i + c < end ? __ldg(reinterpret_cast<const uint32_t*>(row + i + c)) : __float_as_uint(none);
+        } else {
+            const uint32_t other = std::is_same<T, __half>::value ? __half_as_ushort(__float2half_rn(none)) : __float_as_uint(none) >> 16;
+            uint32_t h[4];
+#pragma unroll
+            for (uint32_t c = 0; c < 4; ++c) h[c] = i + c < end ? __ldg(reinterpret_cast<const uint16_t*>(row + i + c)) : other;
+            w[0] = h[0] | h[1] << 16, w[1] = h[2] | h[3] << 16;
+        }
+    }
+    __device__ __forceinline__ float get(uint32_t c) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[c]);
+        const uint32_t h = c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xFFFFu;
+        if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+        return __uint_as_float(h << 16);
+    }
+};
 
 __host__ __device__ inline uint32_t ceil_div(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
 

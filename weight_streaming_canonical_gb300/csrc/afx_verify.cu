@@ -283,38 +283,6 @@ __device__ __forceinline__ void load_four(const T* row, bool wide, uint32_t i, u
         for (uint32_t c = 0; c < 4; ++c) x[c] = i + c < end ? load_logit(row + i + c) : -INFINITY;
     }
 }
-// The same as they lie in memory, so that they can be under way while others are worked on.
-template <typename T>
-struct RawFour {
-    uint32_t w[sizeof(T)];  // 4 sizeof(T) bytes
-    __device__ __forceinline__ void load(const T* row, bool wide, uint32_t i, uint32_t end) {
-        if (wide && i + 4 <= end) {
-            if constexpr (sizeof(T) == 4) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i));
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            } else {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(row + i));
-                w[0] = v.x, w[1] = v.y;
-            }
-        } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (uint32_t c = 0; c < 4; ++c) w[c] = i + c < end ? __ldg(reinterpret_cast<const uint32_t*>(row + i + c)) : 0xFF800000u;
-        } else {
-            constexpr uint32_t kNone = std::is_same<T, __half>::value ? 0xFC00u : 0xFF80u;  // minus infinity
-            uint32_t h[4];
-#pragma unroll
-            for (uint32_t c = 0; c < 4; ++c) h[c] = i + c < end ? __ldg(reinterpret_cast<const uint16_t*>(row + i + c)) : kNone;
-            w[0] = h[0] | h[1] << 16, w[1] = h[2] | h[3] << 16;
-        }
-    }
-    __device__ __forceinline__ float get(uint32_t c) const {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[c]);
-        const uint32_t h = c % 2 ? w[c / 2] >> 16 : w[c / 2] & 0xFFFFu;
-        if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
-        return __uint_as_float(h << 16);
-    }
-};
-
 template <typename P, typename Q>
 __global__ void __launch_bounds__(kThreads, sizeof(P) + sizeof(Q) > 4 ? 2 : 3) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ Shared sh;
@@ -455,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(P) + sizeof(Q) > 4 ? 2 : 3) v
         RawFour<P> raw[kGroups], next[kGroups];
         auto fetch = [&](uint32_t i0, RawFour<P>(&to)[kGroups]) {
 #pragma unroll
-            for (uint32_t j = 0; j < kGroups; ++j) to[j].load(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1);
+            for (uint32_t j = 0; j < kGroups; ++j) to[j].load(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1, -INFINITY);
         };
         fetch(run0, raw);
         const bool plain = p.low == -INFINITY && p.least == 0.0f && !p.infinite;
@@ -504,10 +472,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(P) + sizeof(Q) > 4 ? 2 : 3) v
         RawFour<Q> q_raw[kGroups], q_next[kGroups];
         auto fetch = [&](uint32_t i0, RawFour<P>(&to)[kGroups], RawFour<Q>(&q_to)[kGroups]) {
 #pragma unroll
-            for (uint32_t j = 0; j < kGroups; ++j) to[j].load(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1);
+            for (uint32_t j = 0; j < kGroups; ++j) to[j].load(z_row, a.wide[0], i0 + j * 128 + lane * 4, run1, -INFINITY);
             if (whole)
 #pragma unroll
-                for (uint32_t j = 0; j < kGroups; ++j) q_to[j].load(q_row, a.wide[1], i0 + j * 128 + lane * 4, run1);
+                for (uint32_t j = 0; j < kGroups; ++j) q_to[j].load(q_row, a.wide[1], i0 + j * 128 + lane * 4, run1, -INFINITY);
         };
         fetch(run0, raw, q_raw);
 #pragma unroll 1
