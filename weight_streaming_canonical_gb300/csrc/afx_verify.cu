@@ -292,8 +292,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(P) + sizeof(Q) > 4 ? 2 : 3) v
     const uint32_t r = blockIdx.x / ranks;
     const Side &target = a.side[0], &draft = a.side[1];
     auto started = cluster.barrier_arrive();  // a rank's memory may be written once its CTA runs
-    wait_for_earlier();
-    let_next_start();
+    // The scan's CTAs have all waited for the work before the call when this kernel starts, so the call's arguments are
+    // there; what the scan and the records leave is waited for below
+    if (a.n_tokens == 0) wait_for_earlier();
     const int32_t row0 = __ldg(a.starts + r), row1 = __ldg(a.starts + r + 1);
     const Kind p_kind(target, r, a.vocab), q_kind(draft, r, a.vocab);
     // all of the call or nothing: every CTA looks at all starts
@@ -304,6 +305,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(P) + sizeof(Q) > 4 ? 2 : 3) v
     }
     bad = __syncthreads_or(bad);
     cluster.barrier_wait(std::move(started));
+    if (!bad && row0 + static_cast<int32_t>(threadIdx.x) + 1 < row1) {  // the first tests' logits are on their way
+        const int32_t t = row0 + static_cast<int32_t>(threadIdx.x), d = draft_of(a.tokens, t, row1, a.vocab);
+        if (d >= 0) {
+            asm volatile("prefetch.global.L1 [%0];\n" ::"l"(static_cast<const P*>(target.logits) + t * target.row_stride + d));
+            if (draft.logits) asm volatile("prefetch.global.L1 [%0];\n" ::"l"(static_cast<const Q*>(draft.logits) + t * draft.row_stride + d));
+            asm volatile("prefetch.global.L1 [%0];\n" ::"l"(a.u + t));
+        }
+    }
+    wait_for_earlier();
+    let_next_start();
     if (bad || row0 == row1) {
         if (rank == 0 && threadIdx.x == 0) {
             a.counts[r] = 0;
