@@ -783,14 +783,14 @@ struct Launch {
         return AFX_OK;
     }
     // In cycles: a step of a tile (measured with other tiles on all SMs: 400 whatever the rows for up to 64 tokens,
-    // 430 and 500 for 64 and 128 rows by 128 tokens, 900 and 1000 for pairs of 192 and 256), a wave's
+    // 430 and 500 for 64 and 128 rows by 128 tokens, 900 and 970 for pairs of 192 and 256), a wave's
     // start and end and the join of a tile's CTAs.  700 tokens by 5120 rows of 17,408: pairs of 256 rows 70 us, CTAs of 128
     // 71; 300 by 17,408 of 5120: 46 and 35; 501 by 7168 of 5120: pairs of 192 rows 23.6, of 256 24.9; 1 by 5120 of 5120: three CTAs of 128 rows to a tile
     // 9.1 us, two 9.9, one 11.7, tiles of 64 rows 11.0.
     static void consider(const ProductArgs& a, int sms, Cut* best, double* least) {
         const uint32_t tokens = (kPair ? 2 : 1) * kTokens, tiles_m = ceil_div(a.n_tokens, tokens);
         const uint64_t tiles = static_cast<uint64_t>(tiles_m) * ceil_div(a.rows, T::kRows);
-        const double step = kPair ? (N == 96 ? 900.0 : 1000.0) : a.n_tokens <= 64 ? 400.0 : N == 64 ? 430.0 : 500.0;
+        const double step = kPair ? (N == 96 ? 900.0 : 970.0) : a.n_tokens <= 64 ? 400.0 : N == 64 ? 430.0 : 500.0;
         for (uint32_t split = 1; split <= (kPair ? 1 : kMostSplit) && split <= a.blocks; ++split) {
             const uint32_t slots = at_once(split, sms);
             if (slots == 0 || (split > 1 && tiles > slots)) continue;
