@@ -5,8 +5,8 @@
 // magnitude a, scale = max(a / 448, 2^-126), values E4M3(x / scale).  Half a
 // warp a block, eight elements a lane, four blocks in flight; the eight warps of a
 // CTA take eight tokens, whose scales share a sector.
-// Bound: HBM bandwidth for float32 (8191 tokens of 17,408: 104 us, 6.9 TB/s); for 16 bits the instructions of a block, of
-// which fewer than half depend on its elements (4096 of 17,408, BF16: 46 us, 4.7 TB/s; a warp a block took 65).
+// Bound: HBM bandwidth for float32 (8191 tokens of 17,408: 104 us, 6.9 TB/s); for 16 bits it is below that
+// (4096 of 17,408, BF16: 46.6 us, 4.6 TB/s; a warp a block took 65), with issue slots half busy and DRAM 28 % at 4096 of 5120.
 //
 // fp8_product_kernel: y = x W^T in steps of 128 columns, the block of the
 // scales.  A step of a tile is
@@ -37,7 +37,7 @@
 // Bound: for few tokens reading W (1 token by 17,408 rows of 5120: 16 us,
 // 5.4 TB/s; 64 by 5120 of 17,408: 20 us, 4.5 TB/s; the rest is the start and
 // the last steps' way to the sums); for many the sums: 4096 tokens by 17,408 of
-// 5120 in 316 us, 2.31 PFLOP/s, 215 us without reading the sums back, 165 with
+// 5120 in 316 to 328 us, 2.2 to 2.3 PFLOP/s, 215 us without reading the sums back, 165 with
 // the products alone.  A step of 128 x 256 takes 970 cycles, of which the products
 // take 520, while its sums are on their way: the wait for the products, 400 cycles of
 // loads from tensor memory and multiply-adds (two warps a quarter), the way back.
@@ -796,7 +796,8 @@ struct Launch {
     // In cycles: a step of a tile (measured with other tiles on all SMs: 400 whatever the rows for up to 64 tokens,
     // 430 and 500 for 64 and 128 rows by 128 tokens, 900 and 970 for pairs of 192 and 256), a wave's
     // start and end and the join of a tile's CTAs.  700 tokens by 5120 rows of 17,408: pairs of 256 rows 70 us, CTAs of 128
-    // 71; 300 by 17,408 of 5120: 46 and 35; 501 by 7168 of 5120: pairs of 192 rows 23.6, of 256 24.9; 1 by 5120 of 5120: three CTAs of 128 rows to a tile
+    // 71; 4096 by 17,408 of 5120, with the rounding: pairs 350 us, CTAs 358 a call at a time between other work, but 346
+    // and 341 back to back, 351 and 345 after a fill of 512 MB (why the order changes was not found); 300 by 17,408 of 5120: 46 and 35; 501 by 7168 of 5120: pairs of 192 rows 23.6, of 256 24.9; 1 by 5120 of 5120: three CTAs of 128 rows to a tile
     // 9.1 us, two 9.9, one 11.7, tiles of 64 rows 11.0.
     static void consider(const ProductArgs& a, int sms, Cut* best, double* least) {
         const uint32_t tokens = (kPair ? 2 : 1) * kTokens, tiles_m = ceil_div(a.n_tokens, tokens);
@@ -873,8 +874,8 @@ extern "C" afx_status afx_fp8_quantize(const void* x_dev, uint32_t type, uint64_
     a.blocks = ceil_div(cols, kBlock);
     const bool wide = !((reinterpret_cast<uintptr_t>(x_dev) | (n_tokens > 1 ? x_stride * size : 0)) & 15u) &&
                       !((reinterpret_cast<uintptr_t>(q_dev) | (n_tokens > 1 ? q_stride : 0)) & 7u);
-    // Eight tokens a CTA; their blocks over as many CTAs as fill the SMs ten times over (8191 tokens of 17,408: 110 us,
-    // 132 with CTAs for one filling, 124 with 40), in fours where there are many
+    // Eight tokens a CTA; their blocks over as many CTAs as fill the SMs ten times over (8191 tokens of 17,408 with a warp a block:
+    // 110 us, 132 with CTAs for one filling, 124 with 40), in fours where there are many
     const uint32_t groups = ceil_div(n_tokens, kQuantThreads / 32);
     uint32_t parts = ceil_div(static_cast<uint32_t>(sms) * 64, groups);
     a.per_cta = ceil_div(a.blocks, parts);

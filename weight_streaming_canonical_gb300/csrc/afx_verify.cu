@@ -27,11 +27,11 @@
 // first sums their masses.
 //
 // Bound: with looked-up drafts and no cuts reading the rows, and the row to draw from once
-// more: 200 requests of up to three drafts, 492 rows of 151,936, float32, 96 us, of
-// which the scan takes 58 (5.2 TB/s).  With top-k and top-p the records: 64
-// requests of up to five drafts with their logits, BF16, 261 us, of which 180 are the sampling kernel's for some 300
-// rows (its cluster barriers and passes over shared memory) and 50 the tests and
-// draws.  One request of four drafts: 26 us, three kernels one after the other.
+// more: 200 requests of up to three drafts, 492 rows of 151,936, float32, 96 us; by
+// itself on cold caches the scan takes 54 (5.6 TB/s) and the draws 53.  With top-k and top-p the records: 64
+// requests of up to five drafts with their logits, BF16, 261 to 292 us by the inputs; by themselves
+// 177 for the sampling kernel (barriers and passes over shared memory), 57 for the
+// tests and draws, 25 for the scan.  One request of four drafts: 26 us, three kernels one after the other.
 #include <cooperative_groups.h>
 
 #include <type_traits>
