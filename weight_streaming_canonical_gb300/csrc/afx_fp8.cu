@@ -56,6 +56,7 @@
 #include <cstdio>
 #include <type_traits>
 
+#include "afx_ring.h"
 #include "afx_tensor.cuh"
 
 namespace cg = cooperative_groups;
@@ -447,8 +448,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) fp8_product_kernel(const _
             for (uint32_t q = it > a.stages ? it - a.stages : 0; q < it; ++q)
                 if (!bar_drain(&ctl.full[q % a.stages], q / a.stages & 1u)) raise(a.status, AFX_DEV_UNDRAINED);
       } else if (warp < kLoadWarp) {
-        // of a pair's step a product each, else every second step: waiting and issuing take one warp longer than the
-        // products
+        // of a pair's step a product each, else every second step, whose slots are this warp's own (ring_stages): waiting
+        // and issuing take one warp longer than the products
         const uint32_t m = warp - kMmaWarp;
         if (side == 0) {
             // float32 sums of E4M3 by E4M3, both with their columns contiguous
@@ -825,8 +826,8 @@ struct Launch {
         a.tiles = static_cast<uint32_t>(tiles);
         a.box = kPair || a.n_tokens >= kTokens ? kTokens : ceil_div(a.n_tokens, 8) * 8;
         const uint32_t fixed = 1024 + kCtlBytes + (kTokens - a.box) * kBlock + (a.sectors || split > 1 ? 0 : kStagingBytes);
-        a.stages = (kSmemMost - fixed) / (T::kWBytes + a.box * kBlock);
-        if (a.stages > kMostStages) a.stages = kMostStages;
+        // a pair's warps each take every step, a CTA's every second one
+        a.stages = ring_stages(kSmemMost - fixed, T::kWBytes + a.box * kBlock, kMostStages, kPair ? 1 : 2);
         // the sums of a CTA of several lie over the ring, which holds as many steps with fewer tokens
         static_assert(kTokens * T::kPartRow * sizeof(float) <= (kSmemMost - 1024 - kCtlBytes) / (T::kWBytes + kTokens * kBlock) * (T::kWBytes + kTokens * kBlock),
                       "sums fit the ring");
