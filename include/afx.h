@@ -850,7 +850,7 @@ typedef struct afx_verify_args {
     uint32_t reserved;
     const int32_t* starts_dev;    /* [n_requests + 1] */
     const int32_t* tokens_dev;    /* [n_tokens] */
-    afx_sampling sampling, draft_sampling;
+    afx_sampling sampling, draft_sampling; /* draft_sampling: ignored without draft logits */
     const float* u_dev;           /* [n_tokens], in [0, 1): row t's draft */
     const float* draw_u_dev;      /* [n_requests], in [0, 1): the token behind the drafts that stand */
 } afx_verify_args;

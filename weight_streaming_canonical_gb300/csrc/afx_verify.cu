@@ -721,7 +721,9 @@ extern "C" afx_status afx_verify(const afx_verify_args* args, int32_t* out_token
     VerifyArgs a{};
     Kept* kept = static_cast<Kept*>(workspace_dev);
     a.side[0] = side_of(v.logits_dev, v.type, v.row_stride, v.sampling, kept);
-    a.side[1] = side_of(v.draft_logits_dev, v.draft_type, v.draft_row_stride, v.draft_sampling, kept + v.n_tokens);
+    // without drafts' logits their parameters mean nothing and have not been checked: the kernels, which read a side's by its
+    // pointers, get none
+    a.side[1] = side_of(v.draft_logits_dev, v.draft_type, v.draft_row_stride, v.draft_logits_dev ? v.draft_sampling : afx_sampling{}, kept + v.n_tokens);
     a.parts = reinterpret_cast<Part*>(kept + 2 * static_cast<uint64_t>(v.n_tokens));
     a.starts = v.starts_dev;
     a.tokens = v.tokens_dev;
