@@ -689,7 +689,8 @@ afx_status afx_rotary_plan(uint32_t head_dim, uint32_t rotary_dim, uint32_t pair
                            afx_rotary* out);
 
 /* y[t][h] = x[t][h] turned to positions_dev[axis * axis_stride + t], for
- * n_tokens tokens of heads heads: element i of head h of token t at
+ * n_tokens tokens of heads heads (any axis_stride: 0 where all axes have the same
+ * positions, as text has among images): element i of head h of token t at
  * t * token stride + h * head stride + i of x_dev (x_type) and y_dev (y_type).
  * Angles are held as 64-bit fractions of a turn, so that a position of any
  * size, negative ones too, loses no accuracy but that of its frequency in 53

@@ -808,7 +808,7 @@ def rotary(head_dim: int, rotary_dim: int | None = None, base: float = 10_000.0,
 
 
 def _positions(positions, axes: int, n_tokens: int) -> tuple:
-    """(address, axis stride) of int32 positions: [n_tokens], or [axes][n_tokens]."""
+    """(address, axis stride) of int32 positions: [n_tokens], or [axes][n_tokens], of one row for all axes too (expand)."""
     shape, strides = positions.shape, positions.stride()
     if len(shape) == 1:
         shape, strides = (1, *shape), (n_tokens, *strides)
@@ -829,7 +829,7 @@ def _heads(x, dim: int, name: str) -> tuple:
 
 def afx_rotate(plan: afx_rotary, positions, x, y, stream=None) -> None:
     """y = x turned by the tokens' positions: x, y [tokens][heads][head_dim] (views allowed; y may be x), positions
-    int32 [tokens] or [axes][tokens]."""
+    int32 [tokens] or [axes][tokens] (one row for all axes: positions.expand(axes, tokens))."""
     px, xt, xh, n, heads, kind = _heads(x, plan.head_dim, "x")
     py, yt, yh, y_n, y_heads, y_kind = _heads(y, plan.head_dim, "y")
     if y_n != n or y_heads != heads:

@@ -330,7 +330,6 @@ extern "C" afx_status afx_rotate(const afx_rotary* rotary, const int32_t* positi
     if (heads > 65536) return afx_fail(AFX_E_ARG, "up to 65536 heads", 0);
     if (n_tokens > INT32_MAX) return afx_fail(AFX_E_ARG, "too many tokens", 0);
     if (n_tokens == 0 || heads == 0) return AFX_OK;
-    if (rotary->n_axes > 1 && axis_stride < n_tokens) return afx_fail(AFX_E_ARG, "axes lie at least n_tokens apart", 0);
     if ((heads > 1 && y_head_stride < rotary->head_dim) || (n_tokens > 1 && y_token_stride < rotary->head_dim))
         return afx_fail(AFX_E_ARG, "rows of the result must not overlap", 0);
     if (x_dev == y_dev && (x_type != y_type || (n_tokens > 1 && x_token_stride != y_token_stride) || (heads > 1 && x_head_stride != y_head_stride)))
@@ -360,7 +359,6 @@ extern "C" afx_status afx_rotate_write(const afx_rotary* rotary, const int32_t* 
     if (in->q_heads > 65536) return afx_fail(AFX_E_ARG, "up to 65536 heads", 0);
     if (in->n_tokens > INT32_MAX) return afx_fail(AFX_E_ARG, "too many tokens", 0);
     if (in->n_tokens == 0) return AFX_OK;
-    if (rotary->n_axes > 1 && axis_stride < in->n_tokens) return afx_fail(AFX_E_ARG, "axes lie at least n_tokens apart", 0);
     const uint32_t dim = cache->head_dim, size = type_size(in->type), out = cache->format == AFX_FMT_BF16 ? AFX_TYPE_BF16 : AFX_TYPE_FP16;
     if (in->q_heads) {
         if ((in->q_heads > 1 && q_out_head_stride < dim) || (in->n_tokens > 1 && q_out_token_stride < dim))
