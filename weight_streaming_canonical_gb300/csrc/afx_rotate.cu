@@ -369,8 +369,8 @@ extern "C" afx_status afx_rotate_write(const afx_rotary* rotary, const int32_t* 
         if (!device_ptr_here(in->q_dev, size) || !device_ptr_here(q_out_dev, 2)) return afx_fail(AFX_E_ARG, "the queries must be memory of the current device", 0);
     }
     if (!device_ptr_here(positions_dev, 4) || !device_ptr_here(in->k_dev, size) || !device_ptr_here(in->v_dev, size) || !device_ptr_here(slots_dev, 4) ||
-        (status_dev && !device_ptr_here(status_dev, 4)))
-        return afx_fail(AFX_E_ARG, "positions, keys, values and slots must be memory of the current device", 0);
+        !device_ptr_here(cache->k_dev, 16) || !device_ptr_here(cache->v_dev, 16) || (status_dev && !device_ptr_here(status_dev, 4)))
+        return afx_fail(AFX_E_ARG, "positions, keys, values, slots and the cache must be memory of the current device", 0);
     a.plan = *rotary;
     a.positions = positions_dev;
     a.axis_stride = axis_stride;
