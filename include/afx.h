@@ -694,7 +694,7 @@ afx_status afx_rotary_plan(uint32_t head_dim, uint32_t rotary_dim, uint32_t pair
  * t * token stride + h * head stride + i of x_dev (x_type) and y_dev (y_type).
  * Angles are held as 64-bit fractions of a turn, so that a position of any
  * size, negative ones too, loses no accuracy but that of its frequency in 53
- * bits; sines and cosines are those of a 32-bit angle; the pair's products
+ * bits; sines and cosines are those angles', rounded to float32; the pair's products
  * and sums are float32, rounded once to y_type.  y may be x itself (the same
  * address, type and strides); otherwise they must not overlap.  Any strides and
  * alignment (16-byte aligned rows are fastest); y's rows must not overlap.
