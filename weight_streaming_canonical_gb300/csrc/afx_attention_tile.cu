@@ -40,7 +40,6 @@
 // flag that all roles poll, copies and products in flight are waited for,
 // and the CTA frees its tensor memory and ends.
 #include <cstdio>
-#include <mutex>
 
 #include "afx_attention.cuh"
 #include "afx_tensor.cuh"
@@ -743,15 +742,18 @@ afx_status pool_map(CUtensorMap* map, void* pool, const afx_kv_cache& c, const P
 template <typename T, int D>
 afx_status launch(const TileArgs& args, cudaStream_t s) {
     // the row warps wait for the registers that they ask for: they must be there
-    static std::once_flag once;
-    static int regs = 0;
-    std::call_once(once, [] {
+    static Known known;
+    uint64_t regs = 0;
+    cudaError_t err = cudaSuccess;
+    const bool told = known.get(&regs, [&](uint64_t* v) {
         cudaFuncAttributes at{};
-        if (cudaFuncGetAttributes(&at, attention_tile_kernel<T, D>) == cudaSuccess)
-            regs = at.numRegs;
-        else
-            cudaGetLastError();
+        if ((err = cudaFuncGetAttributes(&at, attention_tile_kernel<T, D>)) == cudaSuccess) *v = static_cast<uint64_t>(at.numRegs);
+        return err == cudaSuccess;
     });
+    if (!told) {
+        cudaGetLastError();
+        return afx_fail(AFX_E_CUDA, "cudaFuncGetAttributes", err);
+    }
     if (regs < kRegsLaunch) return afx_fail(AFX_E_CUDA, "attention_tile_kernel was built with too few registers", 0);
     AFX_SERVE_TRY(cudaFuncSetAttribute(attention_tile_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(Shape<D>::kSmem)),

@@ -52,10 +52,10 @@
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
-#include <atomic>
 #include <cstdio>
 #include <type_traits>
 
+#include "afx_known.h"
 #include "afx_ring.h"
 #include "afx_tensor.cuh"
 
@@ -739,29 +739,30 @@ template <uint32_t N, bool kPair>
 struct Launch {
     using T = Tile<N, kPair>;
 
-    // Clusters of this kernel that run at once on the current device; asked once a device.
+    // Clusters of this kernel that run at once on the current device; asked once a device.  0 where that cannot be told.
     static uint32_t at_once(uint32_t split, int sms) {
         constexpr int kDevices = 16;
-        static std::atomic<uint32_t> known[kDevices][kMostSplit + 1];
+        static Known known[kDevices][kMostSplit + 1];
         const uint32_t size = split * (kPair ? 2 : 1);
         if (size == 1) return sms;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-        std::atomic<uint32_t>* k = dev < kDevices ? &known[dev][split] : nullptr;
-        if (k)
-            if (const uint32_t v = k->load(std::memory_order_relaxed)) return v - 1;
-        int n = 0;
-        if (prepare() == AFX_OK) {
+        auto ask = [&](uint64_t* clusters) {
+            if (prepare() != AFX_OK) return false;
             cudaLaunchAttribute at[2];
             cudaLaunchConfig_t cfg = config(size, size, nullptr, at);
             cfg.numAttrs = 1;
+            int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, fp8_product_kernel<N, kPair>, &cfg) != cudaSuccess) {
                 cudaGetLastError();
-                n = 0;
+                return false;
             }
-        }
-        if (k) k->store(static_cast<uint32_t>(n) + 1, std::memory_order_relaxed);
-        return static_cast<uint32_t>(n);
+            *clusters = static_cast<uint64_t>(n);
+            return true;
+        };
+        uint64_t n = 0;
+        const bool told = dev < kDevices ? known[dev][split].get(&n, ask) : ask(&n);
+        return told ? static_cast<uint32_t>(n) : 0;
     }
     static cudaLaunchConfig_t config(uint32_t grid, uint32_t cluster, cudaStream_t s, cudaLaunchAttribute (&at)[2]) {
         cudaLaunchConfig_t cfg{};
@@ -780,15 +781,18 @@ struct Launch {
     }
     static afx_status prepare() {
         // the warps with the sums wait for the registers that they ask for: they must be there
-        static std::once_flag once;
-        static int regs = 0;
-        std::call_once(once, [] {
+        static Known known;
+        uint64_t regs = 0;
+        cudaError_t err = cudaSuccess;
+        const bool told = known.get(&regs, [&](uint64_t* v) {
             cudaFuncAttributes f{};
-            if (cudaFuncGetAttributes(&f, fp8_product_kernel<N, kPair>) == cudaSuccess)
-                regs = f.numRegs;
-            else
-                cudaGetLastError();
+            if ((err = cudaFuncGetAttributes(&f, fp8_product_kernel<N, kPair>)) == cudaSuccess) *v = static_cast<uint64_t>(f.numRegs);
+            return err == cudaSuccess;
         });
+        if (!told) {
+            cudaGetLastError();
+            return afx_fail(AFX_E_CUDA, "cudaFuncGetAttributes", err);
+        }
         if (regs < kRegsLaunch) return afx_fail(AFX_E_CUDA, "fp8_product_kernel was built with too few registers", 0);
         AFX_SERVE_TRY(cudaFuncSetAttribute(fp8_product_kernel<N, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMost)),
                       "cudaFuncSetAttribute");

@@ -7,8 +7,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <mutex>
 
+#include "afx_known.h"
 #include "afx_serving.cuh"
 
 namespace afx {
@@ -147,16 +147,19 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 inline EncodeFn encode_fn() {
-    static std::once_flag once;
-    static EncodeFn fn = nullptr;
-    std::call_once(once, [] {
+    static Known known;
+    uint64_t fn = 0;
+    known.get(&fn, [](uint64_t* v) {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeFn>(f);
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        *v = reinterpret_cast<uintptr_t>(f);
+        return q == cudaDriverEntryPointSuccess;
     });
-    return fn;
+    return reinterpret_cast<EncodeFn>(static_cast<uintptr_t>(fn));
 }
 
 }  // namespace serve
