@@ -565,10 +565,11 @@ afx_status afx_fp8_quantize(const void* x_dev, uint32_t type, uint64_t x_stride,
  * with w_stride and x_stride multiples of 16; cols itself may be any number;
  * y of any alignment (32 bytes, with rows that keep it, is fastest).  cols from
  * 1 on; n_tokens, rows and cols below 2^24; w_stride and x_stride below 2^32.
- * One launch, no workspace, asynchronous on stream.  A wait past its
- * limit sets AFX_DEV_TIMEOUT in *status_dev (nullable; the result is then
- * unspecified).  y must not overlap the inputs.  Errors: AFX_E_ARG,
- * AFX_E_CUDA. */
+ * One launch, no workspace, asynchronous on stream.  A product of more than
+ * 2^30 steps (128 columns of a tile) an SM, which no GPU's memory holds, is
+ * refused.  A wait past its limit sets AFX_DEV_TIMEOUT in *status_dev
+ * (nullable; the result is then unspecified).  y must not overlap the inputs.
+ * Errors: AFX_E_ARG, AFX_E_CUDA. */
 afx_status afx_fp8_product(const uint8_t* w_dev, uint64_t w_stride, const float* w_scales_dev, uint32_t rows,
                            uint32_t cols, const uint8_t* x_dev, uint64_t x_stride, const float* x_scales_dev,
                            uint64_t x_scale_stride, uint32_t n_tokens, void* y_dev, uint32_t y_type,
@@ -866,7 +867,9 @@ afx_status afx_verify_workspace(uint32_t n_tokens, uint32_t n_requests, uint64_t
  * where u_dev[t] * q_t(d) < p_t(d).  At the first row whose draft does not,
  * a token is drawn from max(p_t - q_t, 0); where the drafts end, from p_t. The
  * token drawn is the first, by index, at which the running sum exceeds
- * draw_u_dev[r] times the whole; weights are summed as integers of 2^-44.
+ * draw_u_dev[r] times the whole; a draw's weights are summed as integers of
+ * 2^-44, and where a row keeps all its tokens the tests and the drafts' log
+ * probabilities go by a float32 sum.
  * Where nothing is left of max(p_t - q_t, 0) (the draft was none that q_t
  * allows), the draw is from p_t.
  * Written for request r: out_tokens_dev[t], its new tokens, a row each: the
@@ -880,7 +883,10 @@ afx_status afx_verify_workspace(uint32_t n_tokens, uint32_t n_requests, uint64_t
  * workspace_dev: 256-byte aligned, of at least afx_verify_workspace bytes,
  * contents ignored; calls that overlap on the GPU need their own.  The
  * outputs must not overlap the inputs.  The same call gives the same bits.
- * Two to four launches, asynchronous on stream.
+ * Asynchronous on stream, in launches one behind the other: one that reads the
+ * rows of logits (two if the drafts' have another type; one more for each
+ * 65,535 rows past the first), with top-k, top-p or min-p one that records what rows
+ * keep (or two), and one that tests and draws, alone if there are no rows.
  * Errors: AFX_E_ARG, AFX_E_NOSPACE, AFX_E_CUDA. */
 afx_status afx_verify(const afx_verify_args* args, int32_t* out_tokens_dev, int32_t* counts_dev, float* logprobs_dev,
                       void* workspace_dev, uint64_t workspace_bytes, afx_stream_t stream, int32_t* status_dev);

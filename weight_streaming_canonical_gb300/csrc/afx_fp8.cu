@@ -37,7 +37,7 @@
 // Bound: for few tokens reading W (1 token by 17,408 rows of 5120: 16 us,
 // 5.4 TB/s; 64 by 5120 of 17,408: 20 us, 4.5 TB/s; the rest is the start and
 // the last steps' way to the sums); for many the sums: 4096 tokens by 17,408 of
-// 5120 in 316 to 328 us, 2.2 to 2.3 PFLOP/s, 215 us without reading the sums back, 165 with
+// 5120 in 316 to 339 us by the clock, 2.2 to 2.3 PFLOP/s, 215 us without reading the sums back, 165 with
 // the products alone.  A step of 128 x 256 takes 970 cycles, of which the products
 // take 520, while its sums are on their way: the wait for the products, 400 cycles of
 // loads from tensor memory and multiply-adds (two warps a quarter), the way back.
@@ -80,8 +80,11 @@ struct QuantArgs {
     uint32_t n_tokens, cols, blocks, per_cta;  // per_cta: blocks that a CTA does of its eight tokens
 };
 
-// x / scale, rounded to float32.  With r the rounded reciprocal and q = x r, q + r (x - q scale) is the rounded quotient
-// (Markstein's theorem) as long as x - q scale is exact, which tiny scales do not allow: those divide.
+// x / scale, rounded to float32 as far as its rounding to E4M3 can tell.  With r the rounded reciprocal and q = x r, the quotient is
+// q + r (x - q scale) (Markstein's correction) as long as x - q scale is exact, which tiny scales do not allow: those divide.
+// q may be two last places off, one more than the theorem allows, so this rests on all cases that count: for each of the 2^23
+// significands of a scale, each of the 16 of a border between two E4M3 values and the four float32 on either side
+// of their product, the result was the divided one; so it was for all 2^23 significands over 448 (scale_of).
 __device__ __forceinline__ void quotients(const float (&x)[8], float scale, float (&q)[8]) {
     if (scale < 0x1p-90f) {
 #pragma unroll
@@ -800,10 +803,12 @@ struct Launch {
     }
     // In cycles: a step of a tile (measured with other tiles on all SMs: 400 whatever the rows for up to 64 tokens,
     // 430 and 500 for 64 and 128 rows by 128 tokens, 900 and 970 for pairs of 192 and 256), a wave's
-    // start and end and the join of a tile's CTAs.  700 tokens by 5120 rows of 17,408: pairs of 256 rows 70 us, CTAs of 128
-    // 71; 4096 by 17,408 of 5120, with the rounding: pairs 350 us, CTAs 358 a call at a time between other work, but 346
-    // and 341 back to back, 351 and 345 after a fill of 512 MB (why the order changes was not found); 300 by 17,408 of 5120: 46 and 35; 501 by 7168 of 5120: pairs of 192 rows 23.6, of 256 24.9; 1 by 5120 of 5120: three CTAs of 128 rows to a tile
-    // 9.1 us, two 9.9, one 11.7, tiles of 64 rows 11.0.
+    // start and end and the join of a tile's CTAs.  Pairs against CTAs, each held to by turns, back to back, after a fill of
+    // 512 MB and with the rounding: 4096 tokens by 17,408 rows of 5120 331, 339 and 349 us, CTAs 335, 344 and 360; 300 by 17,408 of
+    // 5120 50, 54 and 50, CTAs 37, 45 and 38; 501 by 7168 of 5120 25, 29 and 26, CTAs 27, 31 and 28; 1000 by 7168 of
+    // 5120 44, 48 and 46, CTAs 38, 42 and 41.  It misses at times: 700 by 5120 of 17,408 gets pairs, 75, 78 and 84, CTAs
+    // 73, 78 and 81; 4096 by 7168 of 5120 CTAs, 155, 164 and 158, pairs 136, 141 and 150.  1 by 5120 of 5120: three CTAs of 128
+    // rows to a tile 9.1 us, two 9.9, one 11.7, tiles of 64 rows 11.0.
     static void consider(const ProductArgs& a, int sms, Cut* best, double* least) {
         const uint32_t tokens = (kPair ? 2 : 1) * kTokens, tiles_m = ceil_div(a.n_tokens, tokens);
         const uint64_t tiles = static_cast<uint64_t>(tiles_m) * ceil_div(a.rows, T::kRows);
