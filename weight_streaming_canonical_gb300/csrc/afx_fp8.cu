@@ -81,7 +81,7 @@ struct QuantArgs {
 };
 
 // x / scale, rounded to float32 as far as its rounding to E4M3 can tell.  With r the rounded reciprocal and q = x r, the quotient is
-// q + r (x - q scale) (Markstein's correction) as long as x - q scale is exact, which tiny scales do not allow: those divide.
+// q - r (q scale - x) (Markstein's correction) as long as q scale - x is exact, which tiny scales do not allow: those divide.
 // q may be two last places off, one more than the theorem allows, so this rests on all cases that count: for each of the 2^23
 // significands of a scale, each of the 16 of a border between two E4M3 values and the four float32 on either side
 // of their product, the result was the divided one; so it was for all 2^23 significands over 448 (scale_of).
@@ -95,7 +95,7 @@ __device__ __forceinline__ void quotients(const float (&x)[8], float scale, floa
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float near = x[i] * r;
-        q[i] = fmaf(r, fmaf(-near, scale, x[i]), near);
+        q[i] = fmaf(-r, fmaf(near, scale, -x[i]), near);  // this way round, what is left of -0 is +0, and -0 - r 0 is -0
     }
 }
 
